@@ -269,6 +269,137 @@ MLA_API int mla_decode_varlen(const void* q_lat, const void* q_pe, int64_t total
                               void* workspace, size_t workspace_bytes, int num_ctas, void* stream);
 
 /*
+ * mla_prefill - attention over whole prompts, before their latents are read
+ * back through the absorbed decode: queries and up-projected keys and values
+ * of a packed batch of sequences of different lengths. Sequence b has
+ * Lq = cu_q_lens[b+1] - cu_q_lens[b] query tokens, rows cu_q_lens[b] .. of q,
+ * and Lk = cu_k_lens[b+1] - cu_k_lens[b] keys, rows cu_k_lens[b] .. of k_nope,
+ * k_pe and v (Lk > Lq: the last Lq of a longer context, whose earlier rows come
+ * from the cache, for instance by mla_gather_upconvert). Head h < Hq reads key
+ * head g = h / (Hq / Hkv); the rotary key is shared by all heads:
+ *   s_j = scale * (q[h][0:128] . k_nope_j[g] + q[h][128:192] . k_pe_j)
+ *   out = sum_j softmax_j(s) v_j[g],   lse = ln sum_j exp(s_j)
+ * over keys 0 .. Lk - Lq + t for query t (causal != 0), or all Lk keys. A query
+ * that sees no key gets out = 0, lse = -inf.
+ *   q            device, bf16 [total_q, Hq, 192]: element strides q_stride_t
+ *                between tokens and q_stride_h between heads.
+ *   k_nope, v    device, bf16 [total_k, Hkv, 128], with strides likewise (the
+ *                two halves of one [total_k, Hkv, 256] up-projection may be
+ *                passed as they are).
+ *   k_pe         device, bf16 [total_k, 64], row stride k_pe_stride (columns
+ *                512 .. of 576-wide rows, say).
+ *                Bases 16-byte aligned; strides multiples of 8, at least the
+ *                width they step over.
+ *   cu_q_lens, cu_k_lens  device, int32 [B + 1], non-decreasing from 0, read on
+ *                the device only; entries are clamped to [0, total_q] and
+ *                [0, total_k], so no row past them is touched.
+ *   max_q_len    the longest Lq, >= 1 if total_q > 0 (a bound will do).
+ *   scale        > 0 and finite.
+ *   out          device, bf16 [total_q, Hq, 128], contiguous, 16-byte aligned.
+ *                Rows that no sequence names are not written.
+ *   lse          device, fp32 [total_q, Hq], natural log.
+ *   status       device int32 or NULL: ORed with 1 if a bounded internal wait
+ *                gave up (outputs are invalid).
+ * Scores, softmax sums and outputs accumulate in fp32; probabilities are
+ * rounded to bf16 for the product with v. A NaN or infinity in a key or value
+ * that a query does not see does not reach it (queries beside it are then
+ * formed again one by one, which is slow). Hq must be a multiple of Hkv. The
+ * result is the same bit for bit on every run.
+ */
+MLA_API int mla_prefill(const void* q, int64_t q_stride_t, int64_t q_stride_h, const void* k_nope,
+                        int64_t k_stride_t, int64_t k_stride_h, const void* k_pe, int64_t k_pe_stride, const void* v,
+                        int64_t v_stride_t, int64_t v_stride_h, const int32_t* cu_q_lens, const int32_t* cu_k_lens,
+                        int B, int64_t total_q, int64_t total_k, int max_q_len, int Hq, int Hkv, int causal,
+                        float scale, void* out, float* lse, int32_t* status, void* stream);
+
+/*
+ * mla_attn_weights - the attention that every cached token received from a
+ * step's queries, added into a running score per token: what an eviction
+ * (mla_cache_evict) goes by. After mla_decode of the same queries over the
+ * same cache has left lse, for request b < B and cached token
+ * j < min(seq_lens[b], max_len):
+ *   weights[b][j] = decay * weights[b][j]
+ *                 + sum over rows r = (b * q_len + t) * Hq + h that see j of
+ *                   exp(scale * (q_lat[r] . c_j + q_pe[r] . k_pe_j) - lse[r])
+ * (row r sees tokens 0 .. seq_lens[b] - q_len + t, as in mla_decode; a row
+ * whose lse is -inf adds nothing). Every row's terms sum to 1. Other entries
+ * of weights are not touched. With decay 0 the old values are not read, so the
+ * first call needs no initialised buffer.
+ *   q_lat, q_pe, cache, num_slots, page_size, block_table, seq_lens, scale
+ *                as for mla_decode. The queries whose attention counts need not
+ *                be the last decode's: any q_len queries at the end of the
+ *                requests with their lse (a prompt's last ones, say) will do.
+ *   lse          device, fp32 [B*q_len, Hq], natural log.
+ *   cache_kind, lat_dim   MLA_CACHE_BF16_576 with lat_dim 256, 512, 768 or 1792
+ *                (rows of 2 (lat_dim + 64) bytes), or MLA_CACHE_FP8_DS_MLA_656
+ *                with lat_dim 512.
+ *   weights      device, fp32 [B, weights_stride], weights_stride >= max_len.
+ *                Sums are fp32; scores of fp8 rows use the codes' exact values
+ *                times their fp32 scales.
+ *   decay        factor on the old scores, finite and >= 0 (1 accumulates).
+ *   status       device int32 or NULL: ORed with 1 if a bounded internal wait
+ *                gave up (weights are invalid), with 2 if a block-table entry
+ *                pointed outside the pool or past the table row (page 0 was
+ *                read instead, as in mla_decode). Never cleared.
+ *   num_ctas     CTAs sharing the tokens (0 = one per SM). The result does not
+ *                depend on it.
+ * The result has one order of additions and is the same bit for bit on every
+ * run. Calls on different streams may overlap if their weights differ.
+ */
+MLA_API int mla_attn_weights(const void* q_lat, const void* q_pe, const float* lse, const void* cache, int cache_kind,
+                             int lat_dim, int64_t num_slots, int page_size, const int32_t* block_table,
+                             int64_t block_table_stride, const int32_t* seq_lens, int B, int q_len, int Hq,
+                             float scale, float decay, float* weights, int64_t weights_stride, int max_len,
+                             int32_t* status, int num_ctas, void* stream);
+
+/*
+ * mla_cache_evict - keep the best-scored tokens of each request within a
+ * budget, and close the gaps in its pages. For request b < B with
+ * T = min(seq_lens[b], max_len, block_table_stride * page_size) cached tokens
+ * and K = min(max(budgets[b], 0), T):
+ *   kept      the K tokens with the largest scores, where a protected token
+ *             scores above all others: positions[b][j] < n_sink (the sequence's
+ *             first tokens) or positions[b][j] > newest - n_recent, newest the
+ *             largest position of the request. Equal scores (-0 and 0 are
+ *             equal): the lower place j first. A NaN score is below all others.
+ *   places    a kept token at j < K stays; the places below K whose token goes
+ *             are taken, in ascending order, by the kept tokens at j >= K, in
+ *             ascending order. So the fewest possible rows move, and the order
+ *             of the cached rows changes, which no decode depends on: the
+ *             positions move along with their tokens and keep the order in time.
+ * After the call the request's tokens are places 0 .. K - 1 of the same table
+ * row; pages past ceil(K / page_size) are free. Rows at places >= K keep their
+ * bytes, so the call may be repeated with the same result.
+ *   cache        device, num_slots rows of row_bytes bytes (a multiple of 16,
+ *                16 .. 65536), 16-byte aligned; written in place. Pages from
+ *                the first that loses a token on must not be shared with
+ *                another request: n_sink protects a shared prefix of that
+ *                many tokens.
+ *   weights, positions          device, fp32 / int32 [B, stride]: the score and
+ *                the position in its sequence of the token at each place.
+ *   new_weights, new_positions  device, [B, stride]: the same for the kept
+ *                tokens, places 0 .. K - 1; other entries are not written. Each
+ *                may be the input buffer itself, and may not overlap it otherwise.
+ *   stride       elements between requests, >= max_len.
+ *   budgets      device, int32 [B].
+ *   new_seq_lens device, int32 [B]: K. May be seq_lens.
+ *   moves        device, int32 [B, moves_stride], moves_stride >= max_len + 2:
+ *                moves[b][0] = n, [1] = K, then n pairs (from, to) of places, for
+ *                arrays of the caller's own that go along; entries past the
+ *                pairs are not written.
+ *   status       device int32 or NULL: ORed with 2 if a moved row's page lay
+ *                outside the pool (that row was not copied) or seq_lens[b]
+ *                passed max_len or the table row (the tokens past it are dropped).
+ * Two launches.
+ */
+MLA_API int mla_cache_evict(void* cache, int row_bytes, int64_t num_slots, int page_size, const int32_t* block_table,
+                            int64_t block_table_stride, const int32_t* seq_lens, const float* weights,
+                            const int32_t* positions, int64_t stride, int max_len, const int32_t* budgets, int B,
+                            int n_sink, int n_recent, int32_t* new_seq_lens, float* new_weights,
+                            int32_t* new_positions, int32_t* moves, int64_t moves_stride, int32_t* status,
+                            void* stream);
+
+/*
  * mla_merge_lse - combine S partial results of the same N rows computed over
  * disjoint token sets (flash-decoding split-KV / decode context parallel
  * combine; vLLM PR #55543 commit 5.1-5.4 "(0, -inf) per the DCP merge

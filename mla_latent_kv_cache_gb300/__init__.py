@@ -13,8 +13,9 @@ Entry points mirror ``include/mla.h``:
   mla_cache_write, mla_decode_workspace_bytes, mla_decode, mla_decode_varlen,
   mla_merge_lse, mla_gather_upconvert, mla_cache_write_latent,
   mla_decode_latent_workspace_bytes, mla_decode_latent,
-  mla_decode_static_scratch (+ mla_static_scratch_status), mla_num_sms,
-  mla_row_bytes, mla_status_string.
+  mla_decode_static_scratch (+ mla_static_scratch_status), mla_prefill,
+  mla_attn_weights, mla_cache_evict, mla_num_sms, mla_row_bytes,
+  mla_status_string.
 ``decode(...)`` is a convenience wrapper that allocates the outputs and the
 workspace with torch and calls ``mla_decode``.
 """
@@ -91,6 +92,15 @@ def load() -> ctypes.CDLL:
                                               vp, vp, sz, i32, vp]
             lib.mla_decode_latent.restype = i32
             lib.mla_merge_lse.restype = i32
+            lib.mla_prefill.argtypes = [vp, i64, i64, vp, i64, i64, vp, i64, vp, i64, i64, vp, vp, i32, i64, i64, i32,
+                                        i32, i32, i32, f32, vp, vp, vp, vp]
+            lib.mla_prefill.restype = i32
+            lib.mla_attn_weights.argtypes = [vp, vp, vp, vp, i32, i32, i64, i32, vp, i64, vp, i32, i32, i32, f32, f32,
+                                             vp, i64, i32, vp, i32, vp]
+            lib.mla_attn_weights.restype = i32
+            lib.mla_cache_evict.argtypes = [vp, i32, i64, i32, vp, i64, vp, vp, vp, i64, i32, vp, i32, i32, i32, vp,
+                                            vp, vp, vp, i64, vp, vp]
+            lib.mla_cache_evict.restype = i32
             _lib = lib
     return _lib
 
@@ -376,6 +386,156 @@ def mla_merge_lse(part_out: torch.Tensor, part_lse: torch.Tensor, out: torch.Ten
     out_dtype = MLA_OUT_F32 if out.dtype == torch.float32 else MLA_OUT_BF16
     _check(load().mla_merge_lse(part_out.data_ptr(), part_lse.data_ptr(), S, N, out.data_ptr(), out_dtype,
                                 lse.data_ptr() if lse is not None else None, _stream(stream)), "mla_merge_lse")
+
+
+def _row_bytes(where, cache_kind, lat_dim) -> int:
+    """Bytes of a cached row; bf16 rows may have another latent width."""
+    if cache_kind == MLA_CACHE_BF16_576:
+        _need(lat_dim > 0, where, f"lat_dim {lat_dim}")
+        return 2 * (lat_dim + 64)
+    rb = mla_row_bytes(cache_kind)
+    _need(rb > 0, where, f"unknown cache kind {cache_kind}")
+    _need(lat_dim == 512, where, "rows of this cache kind have lat_dim 512")
+    return rb
+
+
+def _current_device() -> int:
+    return torch.cuda.current_device()
+
+
+def _here(where, **tensors) -> None:
+    """_on_device, and that device is the current one (the library launches there)."""
+    _on_device(where, **tensors)
+    dev, cur = next(iter(tensors.values())).device, _current_device()
+    _need(dev.index == cur, where, f"the arguments are on {dev}, the current device is cuda:{cur}")
+
+
+def _rows_apart(t) -> bool:
+    """Contiguous rows of a 2-D tensor that do not share elements."""
+    return (t.stride(1) == 1 or t.shape[1] <= 1) and (t.stride(0) >= t.shape[1] or t.shape[0] <= 1)
+
+
+def _status_arg(where, status) -> None:
+    _need(status is None or (status.dtype == torch.int32 and status.numel() >= 1), where,
+          "status must be an int32 tensor")
+
+
+def _table_args(where, block_table, seq_lens, cache) -> int:
+    """Checks of a paged batch shared by the calls that keep the cache; the number of requests."""
+    _need(cache.is_contiguous(), where, "cache must be contiguous")
+    _need(block_table.dtype == torch.int32 and block_table.dim() == 2 and block_table.stride(1) == 1, where,
+          "block_table must be a 2-D int32 tensor with contiguous rows")
+    _need(seq_lens.dtype == torch.int32 and seq_lens.is_contiguous(), where, "seq_lens must be contiguous int32")
+    B = seq_lens.numel()
+    _need(block_table.shape[0] >= B, where, f"block_table has {block_table.shape[0]} rows for {B} requests")
+    return B
+
+
+def mla_prefill(q, k_nope, k_pe, v, cu_q_lens, cu_k_lens, max_q_len, scale, out, lse, causal: bool = True, status=None,
+                stream=None) -> None:
+    """Attention over whole packed prompts (include/mla.h): q [total_q, Hq, 192],
+    k_nope and v [total_k, Hkv, 128], k_pe [total_k, 64], all bf16 with
+    contiguous last dimensions (strided views allowed), cu_q_lens and cu_k_lens
+    int32 [B + 1] on the device, out bf16 [total_q, Hq, 128], lse fp32
+    [total_q, Hq]. `status` (a device int32 tensor) collects status bits."""
+    where = "mla_prefill"
+    _here(where, q=q, k_nope=k_nope, k_pe=k_pe, v=v, cu_q_lens=cu_q_lens, cu_k_lens=cu_k_lens, out=out, lse=lse,
+          status=status)
+    _need(q.dim() == 3 and q.shape[2] == 192, where, "q must be [total_q, Hq, 192]")
+    total_q, Hq = q.shape[0], q.shape[1]
+    _need(k_nope.dim() == 3 and k_nope.shape[2] == 128, where, "k_nope must be [total_k, Hkv, 128]")
+    total_k, Hkv = k_nope.shape[0], k_nope.shape[1]
+    _need(v.shape == k_nope.shape, where, "v must have k_nope's shape")
+    _need(k_pe.dim() == 2 and k_pe.shape[0] == total_k and k_pe.shape[1] == 64, where, f"k_pe must be [{total_k}, 64]")
+    for name, t in (("q", q), ("k_nope", k_nope), ("k_pe", k_pe), ("v", v)):
+        _need(t.dtype == torch.bfloat16 and t.stride(-1) == 1, where, f"{name} must be bf16 with a contiguous last dimension")
+    _need(out.dtype == torch.bfloat16 and out.is_contiguous() and out.shape == (total_q, Hq, 128), where,
+          f"out must be a contiguous bf16 [{total_q}, {Hq}, 128] tensor")
+    _need(lse.dtype == torch.float32 and lse.is_contiguous() and lse.shape == (total_q, Hq), where,
+          f"lse must be a contiguous fp32 [{total_q}, {Hq}] tensor")
+    B = cu_q_lens.numel() - 1
+    for name, t in (("cu_q_lens", cu_q_lens), ("cu_k_lens", cu_k_lens)):
+        _need(t.dtype == torch.int32 and t.is_contiguous() and t.numel() == B + 1 and B >= 0, where,
+              f"{name} must be contiguous int32 with B + 1 entries, as many as the other")
+    _status_arg(where, status)
+
+    def step(t, d, width):  # the stride of a dimension of one entry says nothing
+        return t.stride(d) if t.shape[d] > 1 else width
+
+    _check(load().mla_prefill(q.data_ptr(), step(q, 0, 192), step(q, 1, 192), k_nope.data_ptr(), step(k_nope, 0, 128),
+                              step(k_nope, 1, 128), k_pe.data_ptr(), step(k_pe, 0, 64), v.data_ptr(), step(v, 0, 128),
+                              step(v, 1, 128), cu_q_lens.data_ptr(), cu_k_lens.data_ptr(), B, total_q, total_k,
+                              int(max_q_len), Hq, Hkv, 1 if causal else 0, float(scale), out.data_ptr(),
+                              lse.data_ptr(), status.data_ptr() if status is not None else None, _stream(stream)),
+           where)
+
+
+def mla_attn_weights(q_lat, q_pe, lse, cache, cache_kind, page_size, block_table, seq_lens, q_len, scale, weights,
+                     decay: float = 0.0, lat_dim: int = 512, num_ctas: int = 0, status=None, stream=None) -> None:
+    """weights[b][j] = decay * weights[b][j] + the attention that token j of
+    request b received from the step's queries (include/mla.h): q_lat
+    [B*q_len, Hq, lat_dim] and q_pe [B*q_len, Hq, 64] bf16 as in mla_decode,
+    lse [B*q_len, Hq] fp32 from it, weights fp32 [>= B, max_len] with
+    contiguous rows. `status` (a device int32 tensor) collects status bits."""
+    where = "mla_attn_weights"
+    _here(where, q_lat=q_lat, q_pe=q_pe, lse=lse, cache=cache, block_table=block_table, seq_lens=seq_lens,
+          weights=weights, status=status)
+    B = _table_args(where, block_table, seq_lens, cache)
+    Hq = q_lat.shape[-2] if q_lat.dim() >= 2 else 0
+    rows = B * int(q_len) * Hq
+    _need(q_lat.dtype == torch.bfloat16 and q_pe.dtype == torch.bfloat16, where, "q_lat and q_pe must be bf16")
+    _need(q_lat.is_contiguous() and q_pe.is_contiguous(), where, "q_lat and q_pe must be contiguous")
+    _need(q_lat.numel() == rows * lat_dim and q_pe.numel() == rows * 64, where,
+          f"q_lat / q_pe hold {q_lat.numel()} / {q_pe.numel()} values, {rows} rows of {lat_dim} / 64 expected")
+    _need(lse.dtype == torch.float32 and lse.is_contiguous() and lse.numel() == rows, where,
+          f"lse must be a contiguous fp32 tensor of {rows} values")
+    _need(weights.dtype == torch.float32 and weights.dim() == 2 and weights.shape[0] >= B and _rows_apart(weights),
+          where, f"weights must be a fp32 [>= {B}, max_len] tensor with contiguous rows")
+    _status_arg(where, status)
+    rb = _row_bytes(where, cache_kind, lat_dim)
+    _check(load().mla_attn_weights(q_lat.data_ptr(), q_pe.data_ptr(), lse.data_ptr(), cache.data_ptr(),
+                                   int(cache_kind), int(lat_dim), _nbytes(cache) // rb, int(page_size),
+                                   block_table.data_ptr(), block_table.stride(0), seq_lens.data_ptr(), B, int(q_len),
+                                   Hq, float(scale), float(decay), weights.data_ptr(),
+                                   max(weights.stride(0), weights.shape[1]), weights.shape[1],
+                                   status.data_ptr() if status is not None else None, int(num_ctas), _stream(stream)),
+           where)
+
+
+def mla_cache_evict(cache, cache_kind, page_size, block_table, seq_lens, weights, positions, budgets, n_sink,
+                    n_recent, new_seq_lens, new_weights, new_positions, moves, lat_dim: int = 512, status=None,
+                    stream=None) -> None:
+    """Keep each request's budgets[b] best-scored tokens and close the gaps in
+    its pages, in place (include/mla.h): weights fp32 and positions int32
+    [>= B, max_len] with the same row stride, budgets int32 [B]; new_seq_lens
+    int32 [B], new_weights and new_positions shaped as the inputs (or the
+    inputs themselves), moves int32 [>= B, >= max_len + 2]."""
+    where = "mla_cache_evict"
+    _here(where, cache=cache, block_table=block_table, seq_lens=seq_lens, weights=weights, positions=positions,
+          budgets=budgets, new_seq_lens=new_seq_lens, new_weights=new_weights, new_positions=new_positions,
+          moves=moves, status=status)
+    B = _table_args(where, block_table, seq_lens, cache)
+    _need(weights.dim() == 2 and weights.shape[0] >= B and _rows_apart(weights), where,
+          f"weights must be [>= {B}, max_len] with contiguous rows")
+    stride, max_len = max(weights.stride(0), weights.shape[1]), weights.shape[1]
+    for name, t, dt in (("weights", weights, torch.float32), ("positions", positions, torch.int32),
+                        ("new_weights", new_weights, torch.float32), ("new_positions", new_positions, torch.int32)):
+        _need(t.dtype == dt and t.shape == weights.shape and _rows_apart(t) and
+              (t.stride(0) == weights.stride(0) or t.shape[0] == 1), where,
+              f"{name} must be a {dt} tensor of weights' shape and strides")
+    for name, t in (("budgets", budgets), ("new_seq_lens", new_seq_lens)):
+        _need(t.dtype == torch.int32 and t.is_contiguous() and t.numel() >= B, where,
+              f"{name} must be contiguous int32 of at least {B} values")
+    _need(moves.dtype == torch.int32 and moves.dim() == 2 and _rows_apart(moves) and moves.shape[0] >= B and
+          moves.shape[1] >= max_len + 2, where, f"moves must be an int32 [>= {B}, >= {max_len + 2}] tensor")
+    _status_arg(where, status)
+    rb = _row_bytes(where, cache_kind, lat_dim)
+    _check(load().mla_cache_evict(cache.data_ptr(), rb, _nbytes(cache) // rb, int(page_size), block_table.data_ptr(),
+                                  block_table.stride(0), seq_lens.data_ptr(), weights.data_ptr(),
+                                  positions.data_ptr(), stride, max_len, budgets.data_ptr(), B, int(n_sink),
+                                  int(n_recent), new_seq_lens.data_ptr(), new_weights.data_ptr(),
+                                  new_positions.data_ptr(), moves.data_ptr(), max(moves.stride(0), moves.shape[1]),
+                                  status.data_ptr() if status is not None else None, _stream(stream)), where)
 
 
 def decode(q_lat, q_pe, cache, cache_kind, page_size, block_table, seq_lens, q_len, scale,

@@ -16,7 +16,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIBDIR = os.path.join(HERE, "_lib")
 LIB = os.path.join(LIBDIR, "libmla_gb300.so")
-SOURCES = ["api.cu", "cache_write.cu", "decode.cu"]
+SOURCES = ["api.cu", "cache_write.cu", "decode.cu", "prefill.cu", "attn_weights.cu", "evict.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

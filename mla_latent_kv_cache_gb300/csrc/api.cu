@@ -4,6 +4,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <cfloat>
 #include <climits>
 #include <cstdint>
 #include <atomic>
@@ -20,6 +21,14 @@ namespace {
 constexpr size_t kWsHeader = 256;
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Two buffers of n bytes each: the same one, or apart.
+bool same_or_apart(const void* a, const void* b, size_t n) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x == y || x + n <= y || y + n <= x;
+}
 
 struct DevInfo {
     int sms = -1;
@@ -415,6 +424,215 @@ int mla_decode_varlen(const void* q_lat, const void* q_pe, int64_t total_q_token
     return decode_impl(q_lat, q_pe, total_q_tokens, cache, cache_kind, num_slots, page_size, block_table,
                        block_table_stride, seq_lens, cu_q_lens, B, max_q_len, Hq, scale, out, out_dtype, lse,
                        workspace, workspace_bytes, num_ctas, stream);
+}
+
+int mla_prefill(const void* q, int64_t q_stride_t, int64_t q_stride_h, const void* k_nope, int64_t k_stride_t,
+                int64_t k_stride_h, const void* k_pe, int64_t k_pe_stride, const void* v, int64_t v_stride_t,
+                int64_t v_stride_h, const int32_t* cu_q_lens, const int32_t* cu_k_lens, int B, int64_t total_q,
+                int64_t total_k, int max_q_len, int Hq, int Hkv, int causal, float scale, void* out, float* lse,
+                int32_t* status, void* stream) {
+    if (B < 0 || total_q < 0 || total_k < 0 || max_q_len < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv)
+        return MLA_ERR_INVALID_ARG;
+    if (!(scale > 0.f) || scale > FLT_MAX) return MLA_ERR_INVALID_ARG;
+    if (B == 0 || total_q == 0) return MLA_OK;
+    if (max_q_len < 1) return MLA_ERR_INVALID_ARG;
+    if (!q || !cu_q_lens || !cu_k_lens || !out || !lse) return MLA_ERR_INVALID_ARG;
+    if (total_k > 0 && (!k_nope || !k_pe || !v)) return MLA_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(k_nope) || !aligned16(k_pe) || !aligned16(v) || !aligned16(out))
+        return MLA_ERR_INVALID_ARG;
+    if (!aligned4(cu_q_lens) || !aligned4(cu_k_lens) || !aligned4(lse) || !aligned4(status)) return MLA_ERR_INVALID_ARG;
+    const int64_t strides[7] = {q_stride_t, q_stride_h, k_stride_t, k_stride_h, k_pe_stride, v_stride_t, v_stride_h};
+    const int64_t least[7] = {192, 192, 128, 128, 64, 128, 128};
+    for (int i = 0; i < 7; ++i)
+        if (strides[i] < least[i] || strides[i] % 8) return MLA_ERR_INVALID_ARG;
+    for (int i = 0; i < 7; ++i)
+        if (strides[i] >= (1LL << 38)) return MLA_ERR_UNSUPPORTED;  // TMA strides are below 2^40 bytes
+    // TMA coordinates are 32-bit, and a tile may pass the last row
+    if (total_q > INT32_MAX - 1024 || total_k > INT32_MAX - 1024) return MLA_ERR_UNSUPPORTED;
+    if ((total_q / 256 + B) * Hq > INT32_MAX) return MLA_ERR_UNSUPPORTED;  // grid size
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return MLA_ERR_CUDA;
+    const DevInfo di = dev_info(dev);
+    if (di.sms <= 0) return MLA_ERR_CUDA;
+    if (di.major != 10) return MLA_ERR_UNSUPPORTED;
+
+    mla::PrefillParams p;
+    p.q = static_cast<const __nv_bfloat16*>(q);
+    p.q_st = q_stride_t;
+    p.q_sh = q_stride_h;
+    p.k_nope = static_cast<const __nv_bfloat16*>(k_nope);
+    p.k_st = k_stride_t;
+    p.k_sh = k_stride_h;
+    p.k_pe = static_cast<const __nv_bfloat16*>(k_pe);
+    p.kp_st = k_pe_stride;
+    p.v = static_cast<const __nv_bfloat16*>(v);
+    p.v_st = v_stride_t;
+    p.v_sh = v_stride_h;
+    p.cu_q = cu_q_lens;
+    p.cu_k = cu_k_lens;
+    p.B = B;
+    p.total_q = static_cast<int>(total_q);
+    p.total_k = static_cast<int>(total_k);
+    p.Hq = Hq;
+    p.Hkv = Hkv;
+    p.causal = causal != 0;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    p.out = static_cast<__nv_bfloat16*>(out);
+    p.lse = lse;
+    p.status = status;
+    auto enc = encode_fn();
+    if (!enc) return MLA_ERR_CUDA;
+    mla::PrefillMaps maps;
+    std::memset(&maps, 0, sizeof(maps));
+    auto map = [&](CUtensorMap* m, const void* base, int width, int heads, int64_t tokens, int64_t sh, int64_t st) {
+        cuuint64_t gdim[3] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(heads),
+                              static_cast<cuuint64_t>(tokens)};
+        cuuint64_t gstride[2] = {static_cast<cuuint64_t>(sh) * 2, static_cast<cuuint64_t>(st) * 2};
+        cuuint32_t box[3] = {64u, 1u, 128u}, estride[3] = {1u, 1u, 1u};
+        return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), gdim, gstride, box, estride,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    };
+    // without keys no block is loaded: the maps then describe q's first row
+    const bool keys = total_k > 0;
+    if (!map(&maps.q, q, 192, Hq, total_q, q_stride_h, q_stride_t) ||
+        !map(&maps.k_nope, keys ? k_nope : q, 128, keys ? Hkv : 1, keys ? total_k : 1, k_stride_h, k_stride_t) ||
+        !map(&maps.k_pe, keys ? k_pe : q, 64, 1, keys ? total_k : 1, k_pe_stride, k_pe_stride) ||
+        !map(&maps.v, keys ? v : q, 128, keys ? Hkv : 1, keys ? total_k : 1, v_stride_h, v_stride_t))
+        return MLA_ERR_CUDA;
+    const cudaError_t e = mla::launch_prefill(maps, p, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+}
+
+int mla_attn_weights(const void* q_lat, const void* q_pe, const float* lse, const void* cache, int cache_kind,
+                     int lat_dim, int64_t num_slots, int page_size, const int32_t* block_table,
+                     int64_t block_table_stride, const int32_t* seq_lens, int B, int q_len, int Hq, float scale,
+                     float decay, float* weights, int64_t weights_stride, int max_len, int32_t* status, int num_ctas,
+                     void* stream) {
+    if (B < 0 || q_len <= 0 || Hq <= 0 || page_size <= 0 || num_slots <= 0 || max_len < 0 || num_ctas < 0)
+        return MLA_ERR_INVALID_ARG;
+    if (cache_kind != MLA_CACHE_BF16_576 && cache_kind != MLA_CACHE_FP8_DS_MLA_656) return MLA_ERR_INVALID_ARG;
+    const bool fp8 = cache_kind == MLA_CACHE_FP8_DS_MLA_656;
+    if (lat_dim != 512 && (fp8 || (lat_dim != 256 && lat_dim != 768 && lat_dim != 1792))) return MLA_ERR_UNSUPPORTED;
+    if (!(decay >= 0.f) || decay > FLT_MAX || scale != scale) return MLA_ERR_INVALID_ARG;
+    if (num_slots > 0x7fffffffLL) return MLA_ERR_UNSUPPORTED;  // TMA row coordinates are 32-bit
+    const int64_t HQ64 = static_cast<int64_t>(Hq) * q_len;
+    if (HQ64 > (1 << 20)) return MLA_ERR_UNSUPPORTED;
+    if (B == 0 || max_len == 0) return MLA_OK;
+    if (!q_lat || !q_pe || !lse || !cache || !block_table || !seq_lens || !weights) return MLA_ERR_INVALID_ARG;
+    if (!aligned16(q_lat) || !aligned16(q_pe) || !aligned16(cache)) return MLA_ERR_INVALID_ARG;
+    if (!aligned4(lse) || !aligned4(weights) || !aligned4(block_table) || !aligned4(seq_lens) || !aligned4(status))
+        return MLA_ERR_INVALID_ARG;
+    if (block_table_stride < 1 || weights_stride < max_len) return MLA_ERR_INVALID_ARG;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return MLA_ERR_CUDA;
+    const DevInfo di = dev_info(dev);
+    if (di.sms <= 0) return MLA_ERR_CUDA;
+    if (di.major != 10) return MLA_ERR_UNSUPPORTED;
+
+    mla::WeightsParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.q_lat = static_cast<const __nv_bfloat16*>(q_lat);
+    p.q_pe = static_cast<const __nv_bfloat16*>(q_pe);
+    p.lse = lse;
+    p.cache = static_cast<const uint8_t*>(cache);
+    p.num_slots = num_slots;
+    p.row_bytes = fp8 ? mla::kRowFp8 : 2 * (lat_dim + mla::kP);
+    p.block_table = block_table;
+    p.bt_stride = block_table_stride;
+    p.seq_lens = seq_lens;
+    p.weights = weights;
+    p.w_stride = weights_stride;
+    p.max_len = max_len;
+    p.decay = decay;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    p.page_size = page_size;
+    p.run_rows = gcd_int(page_size, 128);
+    p.B = B;
+    p.Qt = q_len;
+    p.Hq = Hq;
+    p.HQ = static_cast<int>(HQ64);
+    p.lat_dim = lat_dim;
+    p.status = status;
+    int smem = 0;
+    if (!mla::weights_plan(p.HQ, lat_dim, fp8, p, &smem)) return MLA_ERR_UNSUPPORTED;
+    // pages that are not a multiple of 8 rows are read row by row
+    const bool lsu = page_size % 8 != 0;
+    mla::WeightsMaps maps;
+    std::memset(&maps, 0, sizeof(maps));
+    if (!lsu) {
+        auto enc = encode_fn();
+        if (!enc) return MLA_ERR_CUDA;
+        const cuuint64_t rb = static_cast<cuuint64_t>(p.row_bytes);
+        const cuuint32_t br = static_cast<cuuint32_t>(p.run_rows);
+        auto map = [&](CUtensorMap* m, bool bytes, cuuint32_t width, bool swizzle) {
+            cuuint64_t gdim[2] = {bytes ? rb : rb / 2, static_cast<cuuint64_t>(num_slots)};
+            cuuint64_t gstride[1] = {rb};
+            cuuint32_t box[2] = {width, br}, estride[2] = {1u, 1u};
+            return enc(m, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+                       const_cast<void*>(cache), gdim, gstride, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                       swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                       CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+        };
+        if (!map(&maps.rows, fp8, fp8 ? 128u : 64u, true)) return MLA_ERR_CUDA;
+        if (fp8 && (!map(&maps.rope, false, 64u, true) || !map(&maps.scales, true, 16u, false))) return MLA_ERR_CUDA;
+    }
+    const cudaError_t e = mla::launch_attn_weights(maps, p, fp8, lsu, num_ctas > 0 ? num_ctas : di.sms, smem,
+                                                   static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+}
+
+int mla_cache_evict(void* cache, int row_bytes, int64_t num_slots, int page_size, const int32_t* block_table,
+                    int64_t block_table_stride, const int32_t* seq_lens, const float* weights,
+                    const int32_t* positions, int64_t stride, int max_len, const int32_t* budgets, int B, int n_sink,
+                    int n_recent, int32_t* new_seq_lens, float* new_weights, int32_t* new_positions, int32_t* moves,
+                    int64_t moves_stride, int32_t* status, void* stream) {
+    if (B < 0 || page_size <= 0 || num_slots <= 0 || max_len < 0 || n_sink < 0 || n_recent < 0)
+        return MLA_ERR_INVALID_ARG;
+    if (row_bytes < 16 || row_bytes > 65536 || row_bytes % 16) return MLA_ERR_INVALID_ARG;
+    if (max_len > (1 << 30) || B > (1 << 24)) return MLA_ERR_UNSUPPORTED;
+    if (block_table_stride < 1 || stride < max_len || moves_stride < static_cast<int64_t>(max_len) + 2)
+        return MLA_ERR_INVALID_ARG;
+    if (B == 0) return MLA_OK;
+    if (!cache || !block_table || !seq_lens || !budgets || !new_seq_lens || !moves) return MLA_ERR_INVALID_ARG;
+    if (max_len > 0 && (!weights || !positions || !new_weights || !new_positions)) return MLA_ERR_INVALID_ARG;
+    if (!aligned16(cache)) return MLA_ERR_INVALID_ARG;
+    if (!aligned4(block_table) || !aligned4(seq_lens) || !aligned4(weights) || !aligned4(positions) ||
+        !aligned4(budgets) || !aligned4(new_seq_lens) || !aligned4(new_weights) || !aligned4(new_positions) ||
+        !aligned4(moves) || !aligned4(status))
+        return MLA_ERR_INVALID_ARG;
+    const size_t held = max_len == 0 ? 0 : (static_cast<size_t>(B - 1) * stride + max_len) * 4;
+    if (!same_or_apart(weights, new_weights, held) || !same_or_apart(positions, new_positions, held))
+        return MLA_ERR_INVALID_ARG;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return MLA_ERR_CUDA;
+    const DevInfo di = dev_info(dev);
+    if (di.sms <= 0) return MLA_ERR_CUDA;
+    if (di.major != 10) return MLA_ERR_UNSUPPORTED;
+    mla::EvictParams p;
+    p.cache = static_cast<uint8_t*>(cache);
+    p.num_slots = num_slots;
+    p.row_bytes = row_bytes;
+    p.page_size = page_size;
+    p.block_table = block_table;
+    p.bt_stride = block_table_stride;
+    p.seq_lens = seq_lens;
+    p.weights = weights;
+    p.positions = positions;
+    p.stride = stride;
+    p.max_len = max_len;
+    p.budgets = budgets;
+    p.B = B;
+    p.n_sink = n_sink;
+    p.n_recent = n_recent;
+    p.new_lens = new_seq_lens;
+    p.new_weights = new_weights;
+    p.new_positions = new_positions;
+    p.moves = moves;
+    p.moves_stride = moves_stride;
+    p.status = status;
+    const cudaError_t e = mla::launch_evict(p, di.sms, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 
 int mla_decode_static_scratch(const void* q_lat, const void* q_pe, const void* cache, int cache_kind,

@@ -82,4 +82,89 @@ cudaError_t launch_decode(const DecodeMaps& maps, const DecodeParams& p, int NP,
 cudaError_t launch_merge_lse(const float* part_o, const float* part_lse, int S, int64_t N, void* out, int out_f32,
                              float* lse, cudaStream_t stream);
 
+// Attention weights per cached token (mla_attn_weights).
+struct WeightsParams {
+    const __nv_bfloat16* q_lat;
+    const __nv_bfloat16* q_pe;
+    const float* lse;
+    const uint8_t* cache;
+    int64_t num_slots;
+    int row_bytes;
+    const int32_t* block_table;
+    int64_t bt_stride;
+    const int32_t* seq_lens;
+    float* weights;
+    int64_t w_stride;
+    int max_len;       // weights kept per request
+    float decay;
+    float scale_log2;  // softmax scale * log2(e)
+    int page_size;
+    int run_rows;      // TMA box height: gcd(page_size, 128)
+    int B, Qt, Hq, HQ;
+    int lat_dim;
+    int np;            // query rows per group, padded (weights_plan)
+    int groups;
+    int slots;         // ring blocks
+    int* status;
+};
+// rows: 64-dim blocks of a bf16 row or 128-code blocks of an fp8 one (128-B
+// swizzle); fp8: rope = the 64 bf16 values at byte 528, scales = the 16 bytes
+// at 512.
+struct WeightsMaps {
+    CUtensorMap rows, rope, scales;
+};
+bool weights_plan(int HQ, int lat_dim, int kind, WeightsParams& p, int* smem_bytes);
+cudaError_t launch_attn_weights(const WeightsMaps& maps, const WeightsParams& p, int kind, bool lsu, int ctas,
+                                int smem_bytes, cudaStream_t stream);
+
+// Eviction by score (mla_cache_evict).
+struct EvictParams {
+    uint8_t* cache;
+    int64_t num_slots;
+    int row_bytes;
+    int page_size;
+    const int32_t* block_table;
+    int64_t bt_stride;
+    const int32_t* seq_lens;
+    const float* weights;
+    const int32_t* positions;
+    int64_t stride;    // of weights, positions and their new ones
+    int max_len;
+    const int32_t* budgets;
+    int B;
+    int n_sink, n_recent;
+    int32_t* new_lens;
+    float* new_weights;
+    int32_t* new_positions;
+    int32_t* moves;
+    int64_t moves_stride;
+    int* status;
+};
+cudaError_t launch_evict(const EvictParams& p, int sms, cudaStream_t stream);
+
+// Attention over whole prompts (mla_prefill); strides in elements.
+struct PrefillParams {
+    const __nv_bfloat16* q;
+    int64_t q_st, q_sh;
+    const __nv_bfloat16* k_nope;
+    int64_t k_st, k_sh;
+    const __nv_bfloat16* k_pe;
+    int64_t kp_st;
+    const __nv_bfloat16* v;
+    int64_t v_st, v_sh;
+    const int32_t* cu_q;
+    const int32_t* cu_k;
+    int B, total_q, total_k, Hq, Hkv;
+    int causal;
+    float scale_log2;  // softmax scale * log2(e)
+    __nv_bfloat16* out;
+    float* lse;
+    int* status;
+};
+// 64-value blocks of 128 tokens of one head (128-B swizzle).
+struct PrefillMaps {
+    CUtensorMap q, k_nope, k_pe, v;
+};
+cudaError_t launch_prefill(const PrefillMaps& maps, const PrefillParams& p, cudaStream_t stream);
+
 }  // namespace mla
