@@ -195,6 +195,13 @@ __device__ __forceinline__ void cluster_sync_all() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_lane() {
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
+    return ok != 0;
+}
+
 // ------------------------------------------------------------------ proxies
 
 __device__ __forceinline__ void fence_proxy_async_smem() {

@@ -256,75 +256,93 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                 }
             }
         } else if (warp == 8) {
-            if (lane == 0) {
-                // ------------------------------------------------ MMA issuer
-                const uint32_t idS = idesc_bf16(128, 128, false, false), idPV = idesc_bf16(128, 128, false, true),
-                               idPVh = idesc_bf16(128, 64, false, true);
-                bool ok = true;
-                auto wait_blk = [&](uint32_t u) {
-                    if (ok && !mbar_wait(&ctrl->blk_full[u % kSlots], (u / kSlots) & 1, abort)) ok = false;
-                };
-                auto scores = [&](int i, int j) {
-                    for (int c = 0; c < 3 && ok; ++c) {
-                        const uint32_t u = 5 * j + c;
-                        wait_blk(u);
-                        if (!ok) return;
-                        tc_fence_after();
-                        const uint64_t da = smem_desc(smem_u32(qs + (i * 3 + c) * kBlkP), 16, 1024, kSw128);
-                        const uint64_t db = smem_desc(smem_u32(ring + (u % kSlots) * kBlkP), 16, 1024, kSw128);
+            // ---------------------------------------------------- MMA issuer
+            // The whole warp walks the loop and one lane issues: descriptors are
+            // then warp-uniform values, which the instruction takes from uniform
+            // registers (formed by a single lane they cost a move each per product).
+            const bool leader = elect_lane();
+            const uint32_t idS = idesc_bf16(128, 128, false, false), idPV = idesc_bf16(128, 128, false, true),
+                           idPVh = idesc_bf16(128, 64, false, true);
+            const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+            const int n0 = __shfl_sync(0xffffffffu, n[0], 0), n1 = __shfl_sync(0xffffffffu, n[1], 0);
+            const uint64_t dQ = smem_desc(smem_u32(qs), 16, 1024, kSw128);
+            const uint64_t dK = smem_desc(smem_u32(ring), 16, 1024, kSw128);
+            const uint64_t dV = smem_desc(smem_u32(ring), kBlkP, 1024, kSw128);
+            constexpr uint32_t kBlkD = kBlkP >> 4;
+            bool ok = true;
+            auto wait_blk = [&](uint32_t u) {
+                if (ok && !mbar_wait(&ctrl->blk_full[u % kSlots], (u / kSlots) & 1, abort)) ok = false;
+            };
+            auto scores = [&](int i, int j) {
 #pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            umma_bf16(tmem + i * 128, da + 2 * kk, db + 2 * kk, idS, (c | kk) != 0);
-                    }
-                    umma_commit(&ctrl->s_full[i]);
-                    if (i == 1 || j >= n[1])
-                        for (int c = 0; c < 3; ++c) umma_commit(&ctrl->blk_empty[(5 * j + c) % kSlots]);
-                };
-                auto values = [&](int i, int j) {
-                    const uint32_t u = 5 * j + 3;
+                for (int c = 0; c < 3; ++c) {
+                    const uint32_t u = 5 * j + c;
                     wait_blk(u);
-                    wait_blk(u + 1);
                     if (!ok) return;
                     tc_fence_after();
-                    const uint32_t s0 = u % kSlots, s1 = (u + 1) % kSlots;
-                    const uint64_t d0 = smem_desc(smem_u32(ring + s0 * kBlkP), kBlkP, 1024, kSw128);
-                    const uint32_t tO = tmem + 256 + i * 128, tP = tmem + i * 128;
+                    const uint64_t da = dQ + (i * 3 + c) * kBlkD, db = dK + (u % kSlots) * kBlkD;
+                    if (leader) {
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk) umma_bf16(tm + i * 128, da + 2 * kk, db + 2 * kk, idS, (c | kk) != 0);
+                    }
+                }
+                if (leader) {
+                    umma_commit(&ctrl->s_full[i]);
+                    if (i == 1 || j >= n1)
+                        for (int c = 0; c < 3; ++c) umma_commit(&ctrl->blk_empty[(5 * j + c) % kSlots]);
+                }
+            };
+            auto values = [&](int i, int j) {
+                const uint32_t u = 5 * j + 3;
+                wait_blk(u);
+                wait_blk(u + 1);
+                if (!ok) return;
+                tc_fence_after();
+                const uint32_t s0 = u % kSlots, s1 = (u + 1) % kSlots;
+                const uint64_t d0 = dV + s0 * kBlkD, d1 = dV + s1 * kBlkD;
+                const uint32_t tO = tm + 256 + i * 128, tP = tm + i * 128;
+                if (leader) {
                     if (s1 == s0 + 1) {
 #pragma unroll
                         for (int kk = 0; kk < 8; ++kk)
                             umma_bf16_ta(tO, tP + 8 * kk, d0 + kk * (2048 >> 4), idPV, (j | kk) != 0);
                     } else {  // the two blocks are the ring's last and first
-                        const uint64_t d1 = smem_desc(smem_u32(ring + s1 * kBlkP), kBlkP, 1024, kSw128);
 #pragma unroll
                         for (int kk = 0; kk < 8; ++kk) {
                             umma_bf16_ta(tO, tP + 8 * kk, d0 + kk * (2048 >> 4), idPVh, (j | kk) != 0);
                             umma_bf16_ta(tO + 64, tP + 8 * kk, d1 + kk * (2048 >> 4), idPVh, (j | kk) != 0);
                         }
                     }
-                    if (i == 1 || j >= n[1]) {
+                    if (i == 1 || j >= n1) {
                         umma_commit(&ctrl->blk_empty[s0]);
                         umma_commit(&ctrl->blk_empty[s1]);
                     }
-                };
-                for (int i = 0; i < 2 && ok; ++i)
-                    if (n[i]) {
-                        if (!mbar_wait(&ctrl->q_full[i], 0, abort)) ok = false;
-                        else scores(i, 0);
-                    }
-                for (int j = 0; j < nk && ok; ++j)
-                    for (int i = 0; i < 2 && ok; ++i) {
-                        if (j >= n[i]) continue;
-                        if (!mbar_wait(&ctrl->p_full[i], j & 1, abort)) {
-                            ok = false;
-                            break;
-                        }
-                        tc_fence_after();
-                        values(i, j);
-                        if (!ok) break;
-                        // in order behind the product that reads P_i from the same columns
-                        if (j + 1 < n[i]) scores(i, j + 1);
-                        else umma_commit(&ctrl->o_full[i]);
-                    }
+                }
+            };
+            auto step = [&](int i, int j, int ni) {  // P_i(j) V, then the scores of the next key tile
+                if (!ok || j >= ni) return;
+                if (!mbar_wait(&ctrl->p_full[i], j & 1, abort)) {
+                    ok = false;
+                    return;
+                }
+                tc_fence_after();
+                values(i, j);
+                if (!ok) return;
+                // in order behind the product that reads P_i from the same columns
+                if (j + 1 < ni) scores(i, j + 1);
+                else if (leader) umma_commit(&ctrl->o_full[i]);
+            };
+            if (n0 && !mbar_wait(&ctrl->q_full[0], 0, abort)) ok = false;
+            if (ok && n0) scores(0, 0);
+            if (ok && n1 && !mbar_wait(&ctrl->q_full[1], 0, abort)) ok = false;
+            if (ok && n1) scores(1, 0);
+            const int most = max(n0, n1);
+            for (int j = 0; j < most && ok; ++j) {
+                step(0, j, n0);
+                step(1, j, n1);
+            }
+            ok = __all_sync(0xffffffffu, ok);
+            if (leader) {
                 if (!ok) p_fail(p, ctrl);
                 drain_mma(&ctrl->fin);
             }
