@@ -267,57 +267,72 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile int* abort = &ctrl->abort;
 
     if (warp == 0) {
-        if (lane == 0) {
-            // ------------------------------------------------ score products
-            int i = 0;       // S buffers filled
-            uint32_t u = 0;  // blocks used
-            bool ok = true;
-            const uint32_t id_b = (1u << 7) | (1u << 10) | idesc_f8(kTok, npg, 0, 0);
-            const uint32_t id_h = idesc_f8(kTok, npg, 0, 0), id_l = idesc_f8(kTok, npg, 0, 1);
-            while (ok && !wk.done()) {
-                if (wk.newq && !mbar_wait(&ctrl->q_full[wk.q % kQBufs], (wk.q / kQBufs) & 1, abort)) ok = false;
-                for (int sub = 0; ok && sub < subs; ++sub, ++i) {
-                    if (i >= 2 && !mbar_wait(&ctrl->s_free[i & 1], ((i >> 1) - 1) & 1, abort)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t tS = tmem + (i & 1) * buf_cols;
-                    for (int kb = 0; kb < NB; ++kb) {
-                        const uint32_t v = u + kb, slot = v % NS;
-                        if (sub == 0) {
-                            if (!mbar_wait(&ctrl->blk_full[slot], (v / NS) & 1, abort)) {
-                                ok = false;
-                                break;
-                            }
-                            tc_fence_after();
+        // ------------------------------------------------------ score products
+        // The whole warp walks the tiles and one lane issues: descriptors are then
+        // warp-uniform values, which the instruction takes from uniform registers.
+        const bool leader = elect_lane();
+        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+        int i = 0;                        // S buffers filled
+        uint32_t slot = 0, phase = 0;     // the next block's
+        bool ok = true;
+        const uint32_t id_b = (1u << 7) | (1u << 10) | idesc_f8(kTok, npg, 0, 0);
+        const uint32_t id_h = idesc_f8(kTok, npg, 0, 0), id_l = idesc_f8(kTok, npg, 0, 1);
+        const uint64_t dR = smem_desc(smem_u32(ring), 16, 1024, kSw128), dQ = smem_desc(smem_u32(qbuf), 16, 1024, kSw128);
+        const uint32_t q_step = static_cast<uint32_t>(qblk) >> 4;
+        while (ok && !wk.done()) {
+            if (wk.newq && !mbar_wait(&ctrl->q_full[wk.q % kQBufs], (wk.q / kQBufs) & 1, abort)) ok = false;
+            const uint32_t slot0 = slot;
+            for (int sub = 0; ok && sub < subs; ++sub, ++i) {
+                if (i >= 2 && !mbar_wait(&ctrl->s_free[i & 1], ((i >> 1) - 1) & 1, abort)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t tS = tm + (i & 1) * buf_cols;
+                uint64_t dq = dQ + static_cast<uint32_t>(sub * npg * 128 >> 4);
+                uint32_t at = slot0;
+                for (int kb = 0; kb < NB; ++kb) {
+                    if (sub == 0) {
+                        if (!mbar_wait(&ctrl->blk_full[slot], phase, abort)) {
+                            ok = false;
+                            break;
                         }
-                        const uint64_t da = smem_desc(smem_u32(ring + slot * kBlk), 16, 1024, kSw128);
-                        if (KIND == 1 && kb < NB - 1) {
-                            const uint64_t dh = smem_desc(smem_u32(qbuf + 2 * kb * qblk + sub * npg * 128), 16, 1024, kSw128);
-                            const uint64_t dl = dh + (qblk >> 4);
+                        tc_fence_after();
+                        if (++slot == static_cast<uint32_t>(NS)) {
+                            slot = 0;
+                            phase ^= 1;
+                        }
+                    }
+                    const uint64_t da = dR + at * static_cast<uint32_t>(kBlk >> 4);
+                    if (KIND == 1 && kb < NB - 1) {
+                        if (leader) {
 #pragma unroll
                             for (int kk = 0; kk < 4; ++kk) {
-                                umma_f8(tS + kb * npg, da + 2 * kk, dh + 2 * kk, id_h, kk != 0);
-                                umma_f8(tS + kb * npg, da + 2 * kk, dl + 2 * kk, id_l, 1u);
+                                umma_f8(tS + kb * npg, da + 2 * kk, dq + 2 * kk, id_h, kk != 0);
+                                umma_f8(tS + kb * npg, da + 2 * kk, dq + q_step + 2 * kk, id_l, 1u);
                             }
-                        } else {
-                            const uint64_t dq = smem_desc(
-                                smem_u32(qbuf + (KIND == 1 ? 2 * kb : kb) * qblk + sub * npg * 128), 16, 1024, kSw128);
-                            const uint32_t t = KIND == 1 ? tS + kb * npg : tS;
+                        }
+                        dq += 2 * q_step;
+                    } else {
+                        const uint32_t t = KIND == 1 ? tS + kb * npg : tS;
+                        if (leader) {
 #pragma unroll
                             for (int kk = 0; kk < 4; ++kk)
                                 umma_bf16(t, da + 2 * kk, dq + 2 * kk, id_b, KIND == 1 ? kk != 0 : (kb | kk) != 0);
                         }
-                        if (sub == subs - 1) umma_commit(&ctrl->blk_empty[slot]);
+                        dq += q_step;
                     }
-                    if (ok) umma_commit(&ctrl->s_full[i & 1]);
+                    if (sub == subs - 1 && leader) umma_commit(&ctrl->blk_empty[at]);
+                    if (++at == static_cast<uint32_t>(NS)) at = 0;
                 }
-                if (!ok) break;
-                if (wk.last_of_q()) umma_commit(&ctrl->q_empty);
-                u += NB;
-                wk.next(p);
+                if (ok && leader) umma_commit(&ctrl->s_full[i & 1]);
             }
+            if (!ok) break;
+            if (wk.last_of_q() && leader) umma_commit(&ctrl->q_empty);
+            wk.next(p);
+        }
+        ok = __all_sync(0xffffffffu, ok);
+        if (leader) {
             if (!ok) w_fail(p, ctrl);
             drain_mma(&ctrl->fin);
         }
