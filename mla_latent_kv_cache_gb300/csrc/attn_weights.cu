@@ -29,7 +29,7 @@
 // instructions, and half the shared-memory traffic of widened rows.
 //
 // Warp roles: 0 issues the products (and allocates TMEM), 1 and 2 load blocks
-// (even and odd ones), 4..7 weights, 8..11 queries (shared-memory layout, and
+// (row by row: 3 and 12 too), 4..7 weights, 8..11 queries (shared-memory layout, and
 // the split for fp8 rows). With more query rows than fit beside the ring they
 // are taken in groups over chunks of kChunk tiles, so that the groups after
 // the first find the rows in L2.
@@ -48,7 +48,7 @@ constexpr int kMaxSlots = 12;
 constexpr int kScSlots = 4;        // fp8: tiles' block scales
 constexpr int kQBufs = 4;          // generations of lse / query scales that may be in use at once
 constexpr int kChunk = 4;          // tiles per turn when the query rows take several groups
-constexpr int kThreads = 384;
+constexpr int kThreads = 416;
 constexpr int kLse = 128;
 constexpr int kSmemLimit = 232448;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -167,6 +167,10 @@ __device__ __forceinline__ int w_slot(const WeightsParams& p, int b, int tok, bo
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
+// bytes = 0 writes 16 zero bytes.
+__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
@@ -211,13 +215,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t* sc_ring = qbuf + n_qblk * qblk;
     uint8_t* ring = sc_ring + (KIND == 1 ? kScSlots * kTok * 16 : 0);
     const int NS = p.slots;
-    // columns of an S buffer: fp8 rows hold five sums (four blocks and the rope)
-    // for 16 or 32 query rows at a time
-    const int npg = KIND == 1 ? min(NP, 32) : NP;
-    const int subs = NP / npg;
-    const int buf_cols = KIND == 1 ? 5 * npg : npg;
-    const uint32_t tmem_cols = 2 * buf_cols <= 32 ? 32 : 2 * buf_cols <= 64 ? 64 : 2 * buf_cols <= 128 ? 128
-                               : 2 * buf_cols <= 256 ? 256 : 512;
+    // columns of an S buffer: fp8 rows hold five sums (four blocks and the rope);
+    // two buffers where TMEM holds them (fp8: up to 48 query rows)
+    const int buf_cols = KIND == 1 ? 5 * NP : NP;
+    const int nbuf = 2 * buf_cols <= 512 ? 2 : 1;
+    const int used = nbuf * buf_cols;
+    const uint32_t tmem_cols = used <= 32 ? 32 : used <= 64 ? 64 : used <= 128 ? 128 : used <= 256 ? 256 : 512;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
@@ -272,63 +275,57 @@ __global__ void __launch_bounds__(kThreads, 1)
         // warp-uniform values, which the instruction takes from uniform registers.
         const bool leader = elect_lane();
         const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-        int i = 0;                        // S buffers filled
+        int buf = 0, turn = 0;            // S buffer of the next tile, and its uses before
         uint32_t slot = 0, phase = 0;     // the next block's
         bool ok = true;
-        const uint32_t id_b = (1u << 7) | (1u << 10) | idesc_f8(kTok, npg, 0, 0);
-        const uint32_t id_h = idesc_f8(kTok, npg, 0, 0), id_l = idesc_f8(kTok, npg, 0, 1);
+        const uint32_t id_b = (1u << 7) | (1u << 10) | idesc_f8(kTok, NP, 0, 0);
+        const uint32_t id_h = idesc_f8(kTok, NP, 0, 0), id_l = idesc_f8(kTok, NP, 0, 1);
         const uint64_t dR = smem_desc(smem_u32(ring), 16, 1024, kSw128), dQ = smem_desc(smem_u32(qbuf), 16, 1024, kSw128);
         const uint32_t q_step = static_cast<uint32_t>(qblk) >> 4;
         while (ok && !wk.done()) {
             if (wk.newq && !mbar_wait(&ctrl->q_full[wk.q % kQBufs], (wk.q / kQBufs) & 1, abort)) ok = false;
-            const uint32_t slot0 = slot;
-            for (int sub = 0; ok && sub < subs; ++sub, ++i) {
-                if (i >= 2 && !mbar_wait(&ctrl->s_free[i & 1], ((i >> 1) - 1) & 1, abort)) {
+            if (ok && turn > 0 && !mbar_wait(&ctrl->s_free[buf], (turn - 1) & 1, abort)) ok = false;
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t tS = tm + buf * buf_cols;
+            uint64_t dq = dQ;
+            for (int kb = 0; kb < NB; ++kb) {
+                if (!mbar_wait(&ctrl->blk_full[slot], phase, abort)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const uint32_t tS = tm + (i & 1) * buf_cols;
-                uint64_t dq = dQ + static_cast<uint32_t>(sub * npg * 128 >> 4);
-                uint32_t at = slot0;
-                for (int kb = 0; kb < NB; ++kb) {
-                    if (sub == 0) {
-                        if (!mbar_wait(&ctrl->blk_full[slot], phase, abort)) {
-                            ok = false;
-                            break;
-                        }
-                        tc_fence_after();
-                        if (++slot == static_cast<uint32_t>(NS)) {
-                            slot = 0;
-                            phase ^= 1;
-                        }
-                    }
-                    const uint64_t da = dR + at * static_cast<uint32_t>(kBlk >> 4);
+                const uint64_t da = dR + slot * static_cast<uint32_t>(kBlk >> 4);
+                if (leader) {
                     if (KIND == 1 && kb < NB - 1) {
-                        if (leader) {
 #pragma unroll
-                            for (int kk = 0; kk < 4; ++kk) {
-                                umma_f8(tS + kb * npg, da + 2 * kk, dq + 2 * kk, id_h, kk != 0);
-                                umma_f8(tS + kb * npg, da + 2 * kk, dq + q_step + 2 * kk, id_l, 1u);
-                            }
+                        for (int kk = 0; kk < 4; ++kk) {
+                            umma_f8(tS + kb * NP, da + 2 * kk, dq + 2 * kk, id_h, kk != 0);
+                            umma_f8(tS + kb * NP, da + 2 * kk, dq + q_step + 2 * kk, id_l, 1u);
                         }
-                        dq += 2 * q_step;
                     } else {
-                        const uint32_t t = KIND == 1 ? tS + kb * npg : tS;
-                        if (leader) {
 #pragma unroll
-                            for (int kk = 0; kk < 4; ++kk)
-                                umma_bf16(t, da + 2 * kk, dq + 2 * kk, id_b, KIND == 1 ? kk != 0 : (kb | kk) != 0);
-                        }
-                        dq += q_step;
+                        for (int kk = 0; kk < 4; ++kk)
+                            umma_bf16(KIND == 1 ? tS + kb * NP : tS, da + 2 * kk, dq + 2 * kk, id_b,
+                                      KIND == 1 ? kk != 0 : (kb | kk) != 0);
                     }
-                    if (sub == subs - 1 && leader) umma_commit(&ctrl->blk_empty[at]);
-                    if (++at == static_cast<uint32_t>(NS)) at = 0;
+                    umma_commit(&ctrl->blk_empty[slot]);
                 }
-                if (ok && leader) umma_commit(&ctrl->s_full[i & 1]);
+                dq += KIND == 1 ? 2 * q_step : q_step;
+                if (++slot == static_cast<uint32_t>(NS)) {
+                    slot = 0;
+                    phase ^= 1;
+                }
             }
             if (!ok) break;
-            if (wk.last_of_q() && leader) umma_commit(&ctrl->q_empty);
+            if (leader) {
+                umma_commit(&ctrl->s_full[buf]);
+                if (wk.last_of_q()) umma_commit(&ctrl->q_empty);
+            }
+            if (++buf == nbuf) {
+                buf = 0;
+                ++turn;
+            }
             wk.next(p);
         }
         ok = __all_sync(0xffffffffu, ok);
@@ -336,10 +333,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) w_fail(p, ctrl);
             drain_mma(&ctrl->fin);
         }
-    } else if (warp == 1 || warp == 2) {
+    } else if (warp == 1 || warp == 2 || (LSU && (warp == 3 || warp == 12))) {
         // ---------------------------------------------------------- blocks
-        // (the ring has an even number of slots, so a slot always has the same loader)
-        const uint32_t me = warp - 1;
+        // Loader w takes every kLoaders-th block (TMA: the ring has an even number of
+        // slots, so a slot always has the same loader).
+        constexpr uint32_t kLoaders = LSU ? 4 : 2;
+        const uint32_t me = warp == 12 ? 3 : warp - 1;
         const int BR = p.run_rows;
         const uint64_t pol = l2_policy_evict_first();
         bool ok = true, bad = false;
@@ -349,7 +348,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t parity = 0;                 // and the parity of the last fill of each
         int sc_armed = 0;                    // TMA: tiles whose scales this warp has asked for
         uint32_t pend_slot = 0;              // LSU: the fill before, not yet handed over
-        int pend = 0, pend_sc = -1;
+        int pend = 0, pend_sc = -1, sc_new = -1;
+        auto hand_over = [&]() {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0 && pend) {
+                mbar_arrive(&ctrl->blk_full[pend_slot]);
+                if (pend_sc >= 0) mbar_arrive(&ctrl->sc_full[pend_sc]);
+            }
+            pend = 0;
+        };
+        // waits for a barrier; LSU: what waits behind it may need this warp's last fill first
+        auto wait_empty = [&](uint64_t* bar, uint32_t parity) -> bool {
+            if (LSU && pend && !__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) {
+                cp_async_wait<0>();
+                hand_over();
+            }
+            return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort));
+        };
         int y_next = 0;
         auto run_slot = [&]() -> int {
             if (wk.done()) return 0;
@@ -373,8 +389,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // this tile's block scales
             if (KIND == 1 && me == 0) {
                 const int sl = i % kScSlots;
-                if (i >= kScSlots &&
-                    !__all_sync(0xffffffffu, mbar_wait(&ctrl->sc_empty[sl], ((i / kScSlots) - 1) & 1, abort))) {
+                if (i >= kScSlots && !wait_empty(&ctrl->sc_empty[sl], ((i / kScSlots) - 1) & 1)) {
                     ok = false;
                     break;
                 }
@@ -390,14 +405,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (lane + 32 * q < valid)
                             cp_async16(smem_u32(dst + (lane + 32 * q) * 16),
                                        p.cache + static_cast<int64_t>(slot4[q]) * p.row_bytes + 512);
+                    sc_new = sl;
                 }
             }
             for (int kb = 0; kb < NB; ++kb) {
                 const uint32_t v = u + kb;
-                if ((v & 1) != me) continue;
+                if (v % kLoaders != me) continue;
                 const uint32_t slot = v % NS;
-                if (v >= static_cast<uint32_t>(NS) &&
-                    !__all_sync(0xffffffffu, mbar_wait(&ctrl->blk_empty[slot], ((v / NS) - 1) & 1, abort))) {
+                if (v >= static_cast<uint32_t>(NS) && !wait_empty(&ctrl->blk_empty[slot], ((v / NS) - 1) & 1)) {
                     ok = false;
                     break;
                 }
@@ -424,16 +439,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     cp_async_commit();
                     // the fill before this one has landed: hand it over
                     cp_async_wait<1>();
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0 && pend) {
-                        mbar_arrive(&ctrl->blk_full[pend_slot]);
-                        if (pend_sc >= 0) mbar_arrive(&ctrl->sc_full[pend_sc]);
-                    }
+                    hand_over();
                     pend = 1;
                     pend_slot = slot;
-                    // warp 1's first fill of a tile carries the tile's scales
-                    pend_sc = KIND == 1 && me == 0 && kb < 2 ? i % kScSlots : -1;
+                    // loader 0's first fill of a tile carries the tile's scales
+                    pend_sc = sc_new;
+                    sc_new = -1;
                 }
             }
             if (!ok) break;
@@ -445,12 +456,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok && lane == 0) w_fail(p, ctrl);
         if (LSU) {
             cp_async_wait<0>();
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0 && pend) {
-                mbar_arrive(&ctrl->blk_full[pend_slot]);
-                if (pend_sc >= 0) mbar_arrive(&ctrl->sc_full[pend_sc]);
-            }
+            hand_over();
         } else {
             // no copy may arrive after the CTA is gone: wait (bounded, whatever the
             // abort flag says) for the last fill of every barrier this warp armed
@@ -461,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_wait(&ctrl->sc_full[k % kScSlots], (k / kScSlots) & 1, &never);
         }
         if (bad && p.status) atomicOr(p.status, kErrBadBlock);
-    } else if (warp >= 8) {
+    } else if (warp >= 8 && warp < 12) {
         // --------------------------------------------------------- queries
         const int wq = warp - 8;
         const int D = p.lat_dim;
@@ -477,76 +483,91 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int gen = wk.q % kQBufs;
             const int r0 = wk.g * NP, rows = min(NP, p.HQ - r0);
             const int64_t row0 = static_cast<int64_t>(wk.b) * p.HQ + r0;
-            for (int r = wq; r < NP; r += 4) {
-                const bool real = r < rows;
-                const uint4* ql = reinterpret_cast<const uint4*>(p.q_lat + (row0 + r) * D);
-                const uint4* qp = reinterpret_cast<const uint4*>(p.q_pe + (row0 + r) * kP);
-                const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-                if (KIND == 0) {
-                    for (int un = lane; un < (D + kP) / 8; un += 32) {
-                        const uint4 x = !real ? z : un < D / 8 ? __ldg(ql + un) : __ldg(qp + un - D / 8);
-                        *reinterpret_cast<uint4*>(qbuf + (un >> 3) * qblk + r * 128 + (((un & 7) ^ (r & 7)) << 4)) = x;
-                    }
-                } else {
-                    // lane holds values 16 lane .. 16 lane + 15: unit lane % 8 of block lane / 8
-                    const uint4 x[2] = {real ? __ldg(ql + 2 * lane) : z, real ? __ldg(ql + 2 * lane + 1) : z};
-                    const __nv_bfloat162* xb = reinterpret_cast<const __nv_bfloat162*>(x);
-                    float2 f[8];
-                    float mx = 0.f;
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        f[k] = __bfloat1622float2(xb[k]);
-                        mx = fmaxf(mx, fmaxf(fabsf(f[k].x), fabsf(f[k].y)));
-                    }
-#pragma unroll
-                    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-                    // the power of two that brings the largest into [128, 256)
-                    const int e = static_cast<int>(__float_as_uint(mx) >> 23) - 127;
-                    const int k2 = max(-120, min(120, 7 - e));
-                    const float up = __uint_as_float(static_cast<uint32_t>(127 + k2) << 23);
-                    const float down = __uint_as_float(static_cast<uint32_t>(127 - k2) << 23);
-                    uint32_t h[4], l[4];
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const float2 s = make_float2(f[k].x * up, f[k].y * up);
-                        const uint32_t hc = __nv_cvt_float2_to_fp8x2(s, __NV_SATFINITE, __NV_E4M3);
-                        const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(hc), __NV_E4M3);
-                        const float2 hf = __half22float2(*reinterpret_cast<const __half2*>(&hr));
-                        // e4m3 has no infinity: NaN - finite = NaN and inf - 448 = inf
-                        // stay non-finite in e5m2 (no saturation)
-                        const float2 d = make_float2(s.x - hf.x, s.y - hf.y);
-                        const uint32_t lc = __nv_cvt_float2_to_fp8x2(d, __NV_NOSAT, __NV_E5M2);
-                        if (k & 1) {
-                            h[k >> 1] |= hc << 16;
-                            l[k >> 1] |= lc << 16;
-                        } else {
-                            h[k >> 1] = hc & 0xFFFFu;
-                            l[k >> 1] = lc & 0xFFFFu;
-                        }
-                    }
-                    uint8_t* at = qbuf + (lane >> 3) * 2 * qblk + r * 128 + (((lane & 7) ^ (r & 7)) << 4);
-                    *reinterpret_cast<uint4*>(at) = make_uint4(h[0], h[1], h[2], h[3]);
-                    *reinterpret_cast<uint4*>(at + qblk) = make_uint4(l[0], l[1], l[2], l[3]);
-                    if (lane < 8)
-                        *reinterpret_cast<uint4*>(qbuf + 8 * qblk + r * 128 + ((lane ^ (r & 7)) << 4)) =
-                            real ? __ldg(qp + lane) : z;
-                    if (lane == 0) ctrl->qs[gen][r] = down;
+            // everything in flight at once: a request's queries are one latency
+            const uint32_t q0 = smem_u32(qbuf);
+            if (KIND == 0) {
+                for (int r = wq; r < NP; r += 4) {
+                    const int64_t row = row0 + (r < rows ? r : 0);
+                    const __nv_bfloat16 *ql = p.q_lat + row * D, *qp = p.q_pe + row * kP;
+                    for (int un = lane; un < (D + kP) / 8; un += 32)
+                        cp_async16_or_zero(q0 + (un >> 3) * qblk + r * 128 + (((un & 7) ^ (r & 7)) << 4),
+                                           un < D / 8 ? ql + un * 8 : qp + (un * 8 - D), r < rows ? 16 : 0);
                 }
-                if (lane == 0) {
-                    const float L = real ? __ldg(p.lse + row0 + r) : INFINITY;
-                    ctrl->lse2[gen][r] = L == -INFINITY ? INFINITY : L * kLog2e;
+            } else {
+                if (lane < 8)
+                    for (int r = wq; r < NP; r += 4)
+                        cp_async16_or_zero(q0 + 8 * qblk + r * 128 + ((lane ^ (r & 7)) << 4),
+                                           p.q_pe + (row0 + (r < rows ? r : 0)) * kP + lane * 8, r < rows ? 16 : 0);
+                for (int r4 = wq; r4 < NP; r4 += 16) {  // four rows at a time; NP is a multiple of 16
+                    uint4 x[4][2];
+#pragma unroll
+                    for (int n = 0; n < 4; ++n) {
+                        const int r = r4 + 4 * n;
+                        // lane holds values 16 lane .. 16 lane + 15: unit lane % 8 of block lane / 8
+                        const uint4* ql = reinterpret_cast<const uint4*>(p.q_lat + (row0 + r) * D) + 2 * lane;
+                        x[n][0] = r < rows ? __ldg(ql) : make_uint4(0u, 0u, 0u, 0u);
+                        x[n][1] = r < rows ? __ldg(ql + 1) : make_uint4(0u, 0u, 0u, 0u);
+                    }
+#pragma unroll
+                    for (int n = 0; n < 4; ++n) {
+                        const int r = r4 + 4 * n;
+                        const __nv_bfloat162* xb = reinterpret_cast<const __nv_bfloat162*>(x[n]);
+                        float mx = 0.f;
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const float2 f = __bfloat1622float2(xb[k]);
+                            mx = fmaxf(mx, fmaxf(fabsf(f.x), fabsf(f.y)));
+                        }
+                        // (non-negative floats are ordered as their bits)
+                        mx = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mx)));
+                        // the power of two that brings the largest into [128, 256)
+                        const int e = static_cast<int>(__float_as_uint(mx) >> 23) - 127;
+                        const int k2 = max(-120, min(120, 7 - e));
+                        const float up = __uint_as_float(static_cast<uint32_t>(127 + k2) << 23);
+                        uint32_t h[4], l[4];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const float2 f = __bfloat1622float2(xb[k]);
+                            // (x - x is 0, and NaN for an infinity, which 8 bits do not hold)
+                            const float2 s = make_float2(fmaf(f.x, up, f.x - f.x), fmaf(f.y, up, f.y - f.y));
+                            const uint32_t hc = __nv_cvt_float2_to_fp8x2(s, __NV_SATFINITE, __NV_E4M3);
+                            const __half2_raw hr =
+                                __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(hc), __NV_E4M3);
+                            const float2 hf = __half22float2(*reinterpret_cast<const __half2*>(&hr));
+                            const float2 d = make_float2(s.x - hf.x, s.y - hf.y);
+                            const uint32_t lc = __nv_cvt_float2_to_fp8x2(d, __NV_SATFINITE, __NV_E5M2);
+                            if (k & 1) {
+                                h[k >> 1] |= hc << 16;
+                                l[k >> 1] |= lc << 16;
+                            } else {
+                                h[k >> 1] = hc & 0xFFFFu;
+                                l[k >> 1] = lc & 0xFFFFu;
+                            }
+                        }
+                        uint8_t* at = qbuf + (lane >> 3) * 2 * qblk + r * 128 + (((lane & 7) ^ (r & 7)) << 4);
+                        *reinterpret_cast<uint4*>(at) = make_uint4(h[0], h[1], h[2], h[3]);
+                        *reinterpret_cast<uint4*>(at + qblk) = make_uint4(l[0], l[1], l[2], l[3]);
+                        if (lane == 0) ctrl->qs[gen][r] = __uint_as_float(static_cast<uint32_t>(127 - k2) << 23);
+                    }
                 }
             }
+            const int own = wq * 32 + lane;
+            if (own < NP) {
+                const float L = own < rows ? __ldg(p.lse + row0 + own) : INFINITY;
+                ctrl->lse2[gen][own] = L == -INFINITY ? INFINITY : L * kLog2e;
+            }
+            cp_async_commit();
+            cp_async_wait<0>();
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&ctrl->q_full[gen]);
             wk.next(p);
         }
-    } else if (warp >= 4) {
+    } else if (warp >= 4 && warp < 8) {
         // --------------------------------------------------------- weights
         const int tk = (warp - 4) * 32 + lane;
         const uint32_t lane_base = static_cast<uint32_t>((warp - 4) * 32) << 16;
-        int i = 0, n = 0;  // S buffers, tiles
+        int n = 0, buf = 0, turn = 0;  // tiles, S buffer and its uses before
         bool ok = true;
         while (ok && !wk.done()) {
             const int tok = wk.j * kTok + tk;
@@ -575,47 +596,50 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&ctrl->sc_empty[sl]);
             }
-            float acc = 0.f;
-            for (int sub = 0; sub < subs; ++sub, ++i) {
-                if (!__all_sync(0xffffffffu, mbar_wait(&ctrl->s_full[i & 1], (i >> 1) & 1, abort))) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                const uint32_t tS = tmem + (i & 1) * buf_cols + lane_base;
-                for (int cc = 0; cc < npg; cc += 16) {
-                    uint32_t s[16];
-                    float x[16];
-                    tmem_ld_x16(tS + (KIND == 1 ? 4 * npg : 0) + cc, s);
-                    if (KIND == 1) {
-                        uint32_t a[16];
-                        tmem_ld_x16(tS + cc, a);
-#pragma unroll
-                        for (int k = 0; k < 16; ++k) x[k] = __uint_as_float(a[k]) * sc.x;
-                        tmem_ld_x16(tS + npg + cc, a);
-#pragma unroll
-                        for (int k = 0; k < 16; ++k) x[k] = fmaf(__uint_as_float(a[k]), sc.y, x[k]);
-                        tmem_ld_x16(tS + 2 * npg + cc, a);
-#pragma unroll
-                        for (int k = 0; k < 16; ++k) x[k] = fmaf(__uint_as_float(a[k]), sc.z, x[k]);
-                        tmem_ld_x16(tS + 3 * npg + cc, a);
-#pragma unroll
-                        for (int k = 0; k < 16; ++k) x[k] = fmaf(__uint_as_float(a[k]), sc.w, x[k]);
-                    }
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) {
-                        const int c = sub * npg + cc + k;
-                        float v = __uint_as_float(s[k]);
-                        if (KIND == 1) v = fmaf(x[k], qs[c], v);
-                        const float e = ex2(fmaf(v, p.scale_log2, -lse2[c]));
-                        acc += c >= c0 && c < c1 ? e : 0.f;
-                    }
-                }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&ctrl->s_free[i & 1]);
+            if (!__all_sync(0xffffffffu, mbar_wait(&ctrl->s_full[buf], turn & 1, abort))) {
+                ok = false;
+                break;
             }
-            if (!ok) break;
+            tc_fence_after();
+            const uint32_t tS = tmem + buf * buf_cols + lane_base;
+            float acc = 0.f;
+            for (int cc = 0; cc < NP; cc += 16) {
+                uint32_t s[16];
+                float x[16];
+                tmem_ld_x16(tS + (KIND == 1 ? 4 * NP : 0) + cc, s);
+                if (KIND == 1) {
+                    uint32_t a[16];
+                    tmem_ld_x16(tS + cc, a);
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) x[k] = __uint_as_float(a[k]) * sc.x;
+                    tmem_ld_x16(tS + NP + cc, a);
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) x[k] = fmaf(__uint_as_float(a[k]), sc.y, x[k]);
+                    tmem_ld_x16(tS + 2 * NP + cc, a);
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) x[k] = fmaf(__uint_as_float(a[k]), sc.z, x[k]);
+                    tmem_ld_x16(tS + 3 * NP + cc, a);
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) x[k] = fmaf(__uint_as_float(a[k]), sc.w, x[k]);
+                }
+                if (cc + 16 >= NP) {  // all of the buffer is read
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&ctrl->s_free[buf]);
+                }
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                    const int c = cc + k;
+                    float v = __uint_as_float(s[k]);
+                    if (KIND == 1) v = fmaf(x[k], qs[c], v);
+                    const float e = ex2(fmaf(v, p.scale_log2, -lse2[c]));
+                    acc += c >= c0 && c < c1 ? e : 0.f;
+                }
+            }
+            if (++buf == nbuf) {
+                buf = 0;
+                ++turn;
+            }
             if (mine) *wp = wk.g > 0 ? old + acc : keep ? fmaf(p.decay, old, acc) : acc;
             ++n;
             wk.next(p);
@@ -636,17 +660,14 @@ bool weights_plan(int HQ, int lat_dim, int kind, WeightsParams& p, int* smem_byt
     const int qrow = (lat_dim + kP) * 2;
     const int fixed = 1024 + kCtrlBytes + (kind == 1 ? kScSlots * kTok * 16 : 0);
     const int avail = kSmemLimit - fixed;
-    // query rows that leave four blocks; fp8: a whole tile (five, so six), which
-    // stays in the ring while the query rows are taken 32 at a time
-    int most = (avail - (kind == 1 ? 6 : 4) * kBlk) / qrow;
-    most = most > kLse ? kLse : most;
-    const int step = kind == 1 ? 32 : 16;
-    if (most < step) return false;
-    most = most / step * step;
+    // query rows that leave four blocks; fp8: and whose five sums fit TMEM
+    int most = (avail - 4 * kBlk) / qrow / 16 * 16;
+    const int cap = kind == 1 ? 96 : kLse;
+    most = most > cap ? cap : most;
+    if (most < 16) return false;
     const int groups = (HQ + most - 1) / most;
     const int per = (HQ + groups - 1) / groups;
-    // fp8 sums are taken 16 or 32 query rows at a time
-    p.np = kind == 1 && per > 16 ? (per + 31) / 32 * 32 : (per + 15) / 16 * 16;
+    p.np = (per + 15) / 16 * 16;
     p.groups = (HQ + p.np - 1) / p.np;
     p.slots = (avail - p.np * qrow) / kBlk;
     if (p.slots > kMaxSlots) p.slots = kMaxSlots;
