@@ -30,7 +30,7 @@
 //
 // Warp roles: 0 issues the products (and allocates TMEM), 1 and 2 load blocks
 // (row by row: 3 and 12 too), 4..7 weights, 8..11 queries (shared-memory layout, and
-// the split for fp8 rows). With more query rows than fit beside the ring they
+// the split for fp8 rows) and, from 32 query rows on, the second half of the columns. With more query rows than fit beside the ring they
 // are taken in groups over chunks of kChunk tiles, so that the groups after
 // the first find the rows in L2.
 #include <climits>
@@ -47,7 +47,8 @@ constexpr int kBlk = 128 * 128;    // bytes of a ring block
 constexpr int kMaxSlots = 12;
 constexpr int kScSlots = 4;        // fp8: tiles' block scales
 constexpr int kQBufs = 4;          // generations of lse / query scales that may be in use at once
-constexpr int kChunk = 4;          // tiles per turn when the query rows take several groups
+constexpr int kParts = 4;          // tiles whose second halves may be on their way
+constexpr int kChunk = 8;          // tiles per turn when the query rows take several groups
 constexpr int kThreads = 416;
 constexpr int kLse = 128;
 constexpr int kSmemLimit = 232448;
@@ -58,12 +59,14 @@ struct WCtrl {
     uint64_t s_full[2], s_free[2];
     uint64_t q_full[kQBufs], q_empty;
     uint64_t sc_full[kScSlots], sc_empty[kScSlots];
+    uint64_t part_full[kParts];
     uint64_t fin;
     uint32_t tmem_base;
     int abort;
     int n_items, b0, j0;
     alignas(16) float lse2[kQBufs][kLse];  // log-sum-exp in log2 units; +inf where a row adds nothing
     alignas(16) float qs[kQBufs][kLse];    // fp8: what undoes the row's power of two
+    float part[kParts][kTok];              // sums over the second half of the columns
 };
 constexpr int kCtrlBytes = (sizeof(WCtrl) + 1023) / 1024 * 1024;
 
@@ -216,9 +219,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t* ring = sc_ring + (KIND == 1 ? kScSlots * kTok * 16 : 0);
     const int NS = p.slots;
     // columns of an S buffer: fp8 rows hold five sums (four blocks and the rope);
-    // two buffers where TMEM holds them (fp8: up to 48 query rows)
-    const int buf_cols = KIND == 1 ? 5 * NP : NP;
+    // two buffers where TMEM holds them (fp8: up to 48 query rows). bf16 rows: the
+    // products are summed in up to four parts, which fp32 additions join, since
+    // the tensor core's running sum truncates (one part was off by 2e-6 in the
+    // weights, four by a quarter of that)
+    const int sums = KIND == 1 ? 5 : NP <= 64 ? 4 : 2;
+    const int buf_cols = sums * NP;
     const int nbuf = 2 * buf_cols <= 512 ? 2 : 1;
+    const bool two = NP >= 32;  // two groups of warps share a tile's columns
     const int used = nbuf * buf_cols;
     const uint32_t tmem_cols = used <= 32 ? 32 : used <= 64 ? 64 : used <= 128 ? 128 : used <= 256 ? 256 : 512;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -230,14 +238,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&ctrl->s_full[i], 1);
-            mbar_init(&ctrl->s_free[i], 4);
+            mbar_init(&ctrl->s_free[i], two ? 8 : 4);
         }
         for (int i = 0; i < kQBufs; ++i) mbar_init(&ctrl->q_full[i], 4);
         mbar_init(&ctrl->q_empty, 1);
         for (int i = 0; i < kScSlots; ++i) {
             mbar_init(&ctrl->sc_full[i], 1);
-            mbar_init(&ctrl->sc_empty[i], 4);
+            mbar_init(&ctrl->sc_empty[i], two ? 8 : 4);
         }
+        for (int i = 0; i < kParts; ++i) mbar_init(&ctrl->part_full[i], 4);
         mbar_init(&ctrl->fin, 1);
         ctrl->abort = 0;
         fence_mbar_init();
@@ -296,6 +305,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 tc_fence_after();
                 const uint64_t da = dR + slot * static_cast<uint32_t>(kBlk >> 4);
+                const int part = KIND == 1 ? kb : kb * sums / NB;  // the sum that this block goes into
+                const bool first = KIND == 1 || kb == 0 || part != (kb - 1) * sums / NB;
                 if (leader) {
                     if (KIND == 1 && kb < NB - 1) {
 #pragma unroll
@@ -306,8 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     } else {
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
-                            umma_bf16(KIND == 1 ? tS + kb * NP : tS, da + 2 * kk, dq + 2 * kk, id_b,
-                                      KIND == 1 ? kk != 0 : (kb | kk) != 0);
+                            umma_bf16(tS + part * NP, da + 2 * kk, dq + 2 * kk, id_b, kk != 0 || !first);
                     }
                     umma_commit(&ctrl->blk_empty[slot]);
                 }
@@ -467,19 +477,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_wait(&ctrl->sc_full[k % kScSlots], (k / kScSlots) & 1, &never);
         }
         if (bad && p.status) atomicOr(p.status, kErrBadBlock);
-    } else if (warp >= 8 && warp < 12) {
-        // --------------------------------------------------------- queries
-        const int wq = warp - 8;
-        const int D = p.lat_dim;
-        while (!wk.done()) {
-            if (!wk.newq) {
-                wk.next(p);
-                continue;
-            }
-            if (wk.q > 0 && !__all_sync(0xffffffffu, mbar_wait(&ctrl->q_empty, (wk.q - 1) & 1, abort))) {
-                if (lane == 0) w_fail(p, ctrl);
-                break;
-            }
+    } else if (warp >= 4 && warp < 12) {
+        // --------------------------------------------- weights; 8..11: queries
+        const int grp = warp >> 3;  // 0: warps 4..7
+        const int wq = warp & 3, tk = wq * 32 + lane, D = p.lat_dim;
+        const uint32_t lane_base = static_cast<uint32_t>(wq * 32) << 16;
+        // this group's columns: the first half (all, with one group) or the second
+        const int half = two ? (NP / 16 + 1) / 2 * 16 : NP;
+        const int cb = grp ? half : 0, ce = grp ? NP : half;
+        auto load_q = [&]() {
             const int gen = wk.q % kQBufs;
             const int r0 = wk.g * NP, rows = min(NP, p.HQ - r0);
             const int64_t row0 = static_cast<int64_t>(wk.b) * p.HQ + r0;
@@ -561,27 +567,33 @@ __global__ void __launch_bounds__(kThreads, 1)
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&ctrl->q_full[gen]);
-            wk.next(p);
-        }
-    } else if (warp >= 4 && warp < 8) {
-        // --------------------------------------------------------- weights
-        const int tk = (warp - 4) * 32 + lane;
-        const uint32_t lane_base = static_cast<uint32_t>((warp - 4) * 32) << 16;
+        };
         int n = 0, buf = 0, turn = 0;  // tiles, S buffer and its uses before
         bool ok = true;
         while (ok && !wk.done()) {
+            if (grp == 1 && wk.newq) {
+                if (wk.q > 0 && !__all_sync(0xffffffffu, mbar_wait(&ctrl->q_empty, (wk.q - 1) & 1, abort))) {
+                    ok = false;
+                    break;
+                }
+                load_q();
+            }
+            if (grp == 1 && !two) {
+                wk.next(p);
+                continue;
+            }
             const int tok = wk.j * kTok + tk;
             const bool mine = tok < wk.T && tok < p.max_len;
             float* wp = p.weights + wk.b * p.w_stride + tok;
             const bool keep = wk.g > 0 || p.decay != 0.f;
-            const float old = mine && keep ? *wp : 0.f;
+            const float old = grp == 0 && mine && keep ? *wp : 0.f;
             if (wk.newq && !__all_sync(0xffffffffu, mbar_wait(&ctrl->q_full[wk.q % kQBufs], (wk.q / kQBufs) & 1, abort))) {
                 ok = false;
                 break;
             }
             const float* lse2 = ctrl->lse2[wk.q % kQBufs];
             const float* qs = ctrl->qs[wk.q % kQBufs];
-            // columns [c0, c1) of this group see the token: query t sees tokens up to T - Qt + t
+            // columns [c0, c1) of these rows see the token: query t sees tokens up to T - Qt + t
             const int r0 = wk.g * NP;
             const int c1 = min(NP, p.HQ - r0);
             const int c0 = mine ? max(0, max(0, tok - (wk.T - p.Qt)) * p.Hq - r0) : 0;
@@ -603,26 +615,25 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             const uint32_t tS = tmem + buf * buf_cols + lane_base;
             float acc = 0.f;
-            for (int cc = 0; cc < NP; cc += 16) {
-                uint32_t s[16];
-                float x[16];
-                tmem_ld_x16(tS + (KIND == 1 ? 4 * NP : 0) + cc, s);
-                if (KIND == 1) {
-                    uint32_t a[16];
-                    tmem_ld_x16(tS + cc, a);
+            for (int cc = cb; cc < ce; cc += 16) {
+                float x[16];  // scores; fp8: the four block sums, each times its scale
+                uint32_t a[16];
+                tmem_ld_x16(tS + cc, a);
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) x[k] = __uint_as_float(a[k]) * sc.x;
-                    tmem_ld_x16(tS + NP + cc, a);
+                for (int k = 0; k < 16; ++k) x[k] = KIND == 1 ? __uint_as_float(a[k]) * sc.x : __uint_as_float(a[k]);
+                tmem_ld_x16(tS + NP + cc, a);
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) x[k] = fmaf(__uint_as_float(a[k]), sc.y, x[k]);
+                for (int k = 0; k < 16; ++k) x[k] = KIND == 1 ? fmaf(__uint_as_float(a[k]), sc.y, x[k]) : x[k] + __uint_as_float(a[k]);
+                if (sums > 2) {
                     tmem_ld_x16(tS + 2 * NP + cc, a);
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) x[k] = fmaf(__uint_as_float(a[k]), sc.z, x[k]);
+                    for (int k = 0; k < 16; ++k) x[k] = KIND == 1 ? fmaf(__uint_as_float(a[k]), sc.z, x[k]) : x[k] + __uint_as_float(a[k]);
                     tmem_ld_x16(tS + 3 * NP + cc, a);
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) x[k] = fmaf(__uint_as_float(a[k]), sc.w, x[k]);
+                    for (int k = 0; k < 16; ++k) x[k] = KIND == 1 ? fmaf(__uint_as_float(a[k]), sc.w, x[k]) : x[k] + __uint_as_float(a[k]);
                 }
-                if (cc + 16 >= NP) {  // all of the buffer is read
+                if (KIND == 1) tmem_ld_x16(tS + 4 * NP + cc, a);  // the rotary part
+                if (cc + 16 >= ce) {  // this group's share of the buffer is read
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&ctrl->s_free[buf]);
@@ -630,8 +641,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int k = 0; k < 16; ++k) {
                     const int c = cc + k;
-                    float v = __uint_as_float(s[k]);
-                    if (KIND == 1) v = fmaf(x[k], qs[c], v);
+                    const float v = KIND == 1 ? fmaf(x[k], qs[c], __uint_as_float(a[k])) : x[k];
                     const float e = ex2(fmaf(v, p.scale_log2, -lse2[c]));
                     acc += c >= c0 && c < c1 ? e : 0.f;
                 }
@@ -640,7 +650,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                 buf = 0;
                 ++turn;
             }
-            if (mine) *wp = wk.g > 0 ? old + acc : keep ? fmaf(p.decay, old, acc) : acc;
+            // the halves meet (a tile's S waits for both groups' reads of an earlier
+            // one, so the second group is never kParts tiles ahead of the first)
+            if (two && grp == 1) {
+                ctrl->part[n % kParts][tk] = acc;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctrl->part_full[n % kParts]);
+            } else {
+                if (two) {
+                    if (!__all_sync(0xffffffffu, mbar_wait(&ctrl->part_full[n % kParts], (n / kParts) & 1, abort))) {
+                        ok = false;
+                        break;
+                    }
+                    acc += ctrl->part[n % kParts][tk];
+                }
+                if (mine) *wp = wk.g > 0 ? old + acc : keep ? fmaf(p.decay, old, acc) : acc;
+            }
             ++n;
             wk.next(p);
         }
