@@ -48,6 +48,8 @@ class MlaError(RuntimeError):
 def load() -> ctypes.CDLL:
     """Load the compiled library (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -105,8 +107,14 @@ def load() -> ctypes.CDLL:
     return _lib
 
 
+# the current stream's handle without a Stream object around it (a few microseconds a call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> int:
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
@@ -388,14 +396,21 @@ def mla_merge_lse(part_out: torch.Tensor, part_lse: torch.Tensor, out: torch.Ten
                                 lse.data_ptr() if lse is not None else None, _stream(stream)), "mla_merge_lse")
 
 
+def _refuse(where, detail) -> None:
+    raise MlaError(MLA_ERR_INVALID_ARG, where, detail)
+
+
 def _row_bytes(where, cache_kind, lat_dim) -> int:
     """Bytes of a cached row; bf16 rows may have another latent width."""
     if cache_kind == MLA_CACHE_BF16_576:
-        _need(lat_dim > 0, where, f"lat_dim {lat_dim}")
+        if lat_dim <= 0:
+            _refuse(where, f"lat_dim {lat_dim}")
         return 2 * (lat_dim + 64)
     rb = mla_row_bytes(cache_kind)
-    _need(rb > 0, where, f"unknown cache kind {cache_kind}")
-    _need(lat_dim == 512, where, "rows of this cache kind have lat_dim 512")
+    if rb <= 0:
+        _refuse(where, f"unknown cache kind {cache_kind}")
+    if lat_dim != 512:
+        _refuse(where, "rows of this cache kind have lat_dim 512")
     return rb
 
 
@@ -403,32 +418,50 @@ def _current_device() -> int:
     return torch.cuda.current_device()
 
 
-def _here(where, **tensors) -> None:
-    """_on_device, and that device is the current one (the library launches there)."""
-    _on_device(where, **tensors)
-    dev, cur = next(iter(tensors.values())).device, _current_device()
-    _need(dev.index == cur, where, f"the arguments are on {dev}, the current device is cuda:{cur}")
+def _here(where, names, tensors) -> None:
+    """Every tensor (None: not given) is a CUDA tensor on the current device,
+    where the library launches. A call of a few microseconds is mostly its
+    checks, so the common case is a comparison of device numbers."""
+    dev = _current_device() if _is_cuda(tensors[0]) else -1
+    for t in tensors:
+        if t is not None and (not _is_cuda(t) or t.get_device() != dev):
+            break
+    else:
+        return
+    _on_device(where, **dict(zip(names, tensors)))
+    _refuse(where, f"the arguments are on {tensors[0].device}, the current device is cuda:{dev}")
 
 
 def _rows_apart(t) -> bool:
     """Contiguous rows of a 2-D tensor that do not share elements."""
-    return (t.stride(1) == 1 or t.shape[1] <= 1) and (t.stride(0) >= t.shape[1] or t.shape[0] <= 1)
+    rows, cols = t.shape
+    s0, s1 = t.stride()
+    return (s1 == 1 or cols <= 1) and (s0 >= cols or rows <= 1)
 
 
-def _status_arg(where, status) -> None:
-    _need(status is None or (status.dtype == torch.int32 and status.numel() >= 1), where,
-          "status must be an int32 tensor")
+def _status_ptr(where, status):
+    if status is None:
+        return None
+    if status.dtype is not torch.int32 or status.numel() < 1:
+        _refuse(where, "status must be an int32 tensor")
+    return status.data_ptr()
 
 
 def _table_args(where, block_table, seq_lens, cache) -> int:
     """Checks of a paged batch shared by the calls that keep the cache; the number of requests."""
-    _need(cache.is_contiguous(), where, "cache must be contiguous")
-    _need(block_table.dtype == torch.int32 and block_table.dim() == 2 and block_table.stride(1) == 1, where,
-          "block_table must be a 2-D int32 tensor with contiguous rows")
-    _need(seq_lens.dtype == torch.int32 and seq_lens.is_contiguous(), where, "seq_lens must be contiguous int32")
+    if not cache.is_contiguous():
+        _refuse(where, "cache must be contiguous")
+    if block_table.dtype is not torch.int32 or block_table.dim() != 2 or block_table.stride(1) != 1:
+        _refuse(where, "block_table must be a 2-D int32 tensor with contiguous rows")
+    if seq_lens.dtype is not torch.int32 or not seq_lens.is_contiguous():
+        _refuse(where, "seq_lens must be contiguous int32")
     B = seq_lens.numel()
-    _need(block_table.shape[0] >= B, where, f"block_table has {block_table.shape[0]} rows for {B} requests")
+    if block_table.shape[0] < B:
+        _refuse(where, f"block_table has {block_table.shape[0]} rows for {B} requests")
     return B
+
+
+_PREFILL_NAMES = ("q", "k_nope", "k_pe", "v", "cu_q_lens", "cu_k_lens", "out", "lse", "status")
 
 
 def mla_prefill(q, k_nope, k_pe, v, cu_q_lens, cu_k_lens, max_q_len, scale, out, lse, causal: bool = True, status=None,
@@ -439,35 +472,43 @@ def mla_prefill(q, k_nope, k_pe, v, cu_q_lens, cu_k_lens, max_q_len, scale, out,
     int32 [B + 1] on the device, out bf16 [total_q, Hq, 128], lse fp32
     [total_q, Hq]. `status` (a device int32 tensor) collects status bits."""
     where = "mla_prefill"
-    _here(where, q=q, k_nope=k_nope, k_pe=k_pe, v=v, cu_q_lens=cu_q_lens, cu_k_lens=cu_k_lens, out=out, lse=lse,
-          status=status)
-    _need(q.dim() == 3 and q.shape[2] == 192, where, "q must be [total_q, Hq, 192]")
-    total_q, Hq = q.shape[0], q.shape[1]
-    _need(k_nope.dim() == 3 and k_nope.shape[2] == 128, where, "k_nope must be [total_k, Hkv, 128]")
-    total_k, Hkv = k_nope.shape[0], k_nope.shape[1]
-    _need(v.shape == k_nope.shape, where, "v must have k_nope's shape")
-    _need(k_pe.dim() == 2 and k_pe.shape[0] == total_k and k_pe.shape[1] == 64, where, f"k_pe must be [{total_k}, 64]")
-    for name, t in (("q", q), ("k_nope", k_nope), ("k_pe", k_pe), ("v", v)):
-        _need(t.dtype == torch.bfloat16 and t.stride(-1) == 1, where, f"{name} must be bf16 with a contiguous last dimension")
-    _need(out.dtype == torch.bfloat16 and out.is_contiguous() and out.shape == (total_q, Hq, 128), where,
-          f"out must be a contiguous bf16 [{total_q}, {Hq}, 128] tensor")
-    _need(lse.dtype == torch.float32 and lse.is_contiguous() and lse.shape == (total_q, Hq), where,
-          f"lse must be a contiguous fp32 [{total_q}, {Hq}] tensor")
+    _here(where, _PREFILL_NAMES, (q, k_nope, k_pe, v, cu_q_lens, cu_k_lens, out, lse, status))
+    bf16 = torch.bfloat16
+    if q.dim() != 3 or q.shape[2] != 192:
+        _refuse(where, "q must be [total_q, Hq, 192]")
+    if k_nope.dim() != 3 or k_nope.shape[2] != 128:
+        _refuse(where, "k_nope must be [total_k, Hkv, 128]")
+    total_q, Hq, _ = q.shape
+    total_k, Hkv, _ = kv_shape = k_nope.shape
+    if v.shape != kv_shape:
+        _refuse(where, "v must have k_nope's shape")
+    if k_pe.shape != (total_k, 64):
+        _refuse(where, f"k_pe must be [{total_k}, 64]")
+    sq, sk, sp, sv = q.stride(), k_nope.stride(), k_pe.stride(), v.stride()
+    if (q.dtype is not bf16 or k_nope.dtype is not bf16 or k_pe.dtype is not bf16 or v.dtype is not bf16 or
+            sq[2] != 1 or sk[2] != 1 or sp[1] != 1 or sv[2] != 1):
+        _refuse(where, "q must be bf16 with a contiguous last dimension, and so must k_nope, k_pe and v")
+    if out.dtype is not bf16 or out.shape != (total_q, Hq, 128) or not out.is_contiguous():
+        _refuse(where, f"out must be a contiguous bf16 [{total_q}, {Hq}, 128] tensor")
+    if lse.dtype is not torch.float32 or lse.shape != (total_q, Hq) or not lse.is_contiguous():
+        _refuse(where, f"lse must be a contiguous fp32 [{total_q}, {Hq}] tensor")
     B = cu_q_lens.numel() - 1
-    for name, t in (("cu_q_lens", cu_q_lens), ("cu_k_lens", cu_k_lens)):
-        _need(t.dtype == torch.int32 and t.is_contiguous() and t.numel() == B + 1 and B >= 0, where,
-              f"{name} must be contiguous int32 with B + 1 entries, as many as the other")
-    _status_arg(where, status)
+    if cu_q_lens.dtype is not torch.int32 or not cu_q_lens.is_contiguous() or B < 0:
+        _refuse(where, "cu_q_lens must be contiguous int32 with B + 1 entries")
+    if cu_k_lens.dtype is not torch.int32 or not cu_k_lens.is_contiguous() or cu_k_lens.numel() != B + 1:
+        _refuse(where, "cu_k_lens must be contiguous int32 with as many entries as cu_q_lens")
+    st = _status_ptr(where, status)
+    # (the stride of a dimension of one entry says nothing)
+    one_q, one_k, one_h, one_g = total_q <= 1, total_k <= 1, Hq <= 1, Hkv <= 1
+    _check(load().mla_prefill(
+        q.data_ptr(), 192 if one_q else sq[0], 192 if one_h else sq[1],
+        k_nope.data_ptr(), 128 if one_k else sk[0], 128 if one_g else sk[1], k_pe.data_ptr(), 64 if one_k else sp[0],
+        v.data_ptr(), 128 if one_k else sv[0], 128 if one_g else sv[1], cu_q_lens.data_ptr(), cu_k_lens.data_ptr(), B,
+        total_q, total_k, int(max_q_len), Hq, Hkv, 1 if causal else 0, float(scale), out.data_ptr(), lse.data_ptr(), st,
+        _stream(stream)), where)
 
-    def step(t, d, width):  # the stride of a dimension of one entry says nothing
-        return t.stride(d) if t.shape[d] > 1 else width
 
-    _check(load().mla_prefill(q.data_ptr(), step(q, 0, 192), step(q, 1, 192), k_nope.data_ptr(), step(k_nope, 0, 128),
-                              step(k_nope, 1, 128), k_pe.data_ptr(), step(k_pe, 0, 64), v.data_ptr(), step(v, 0, 128),
-                              step(v, 1, 128), cu_q_lens.data_ptr(), cu_k_lens.data_ptr(), B, total_q, total_k,
-                              int(max_q_len), Hq, Hkv, 1 if causal else 0, float(scale), out.data_ptr(),
-                              lse.data_ptr(), status.data_ptr() if status is not None else None, _stream(stream)),
-           where)
+_WEIGHTS_NAMES = ("q_lat", "q_pe", "lse", "cache", "block_table", "seq_lens", "weights", "status")
 
 
 def mla_attn_weights(q_lat, q_pe, lse, cache, cache_kind, page_size, block_table, seq_lens, q_len, scale, weights,
@@ -478,28 +519,32 @@ def mla_attn_weights(q_lat, q_pe, lse, cache, cache_kind, page_size, block_table
     lse [B*q_len, Hq] fp32 from it, weights fp32 [>= B, max_len] with
     contiguous rows. `status` (a device int32 tensor) collects status bits."""
     where = "mla_attn_weights"
-    _here(where, q_lat=q_lat, q_pe=q_pe, lse=lse, cache=cache, block_table=block_table, seq_lens=seq_lens,
-          weights=weights, status=status)
+    _here(where, _WEIGHTS_NAMES, (q_lat, q_pe, lse, cache, block_table, seq_lens, weights, status))
     B = _table_args(where, block_table, seq_lens, cache)
     Hq = q_lat.shape[-2] if q_lat.dim() >= 2 else 0
     rows = B * int(q_len) * Hq
-    _need(q_lat.dtype == torch.bfloat16 and q_pe.dtype == torch.bfloat16, where, "q_lat and q_pe must be bf16")
-    _need(q_lat.is_contiguous() and q_pe.is_contiguous(), where, "q_lat and q_pe must be contiguous")
-    _need(q_lat.numel() == rows * lat_dim and q_pe.numel() == rows * 64, where,
-          f"q_lat / q_pe hold {q_lat.numel()} / {q_pe.numel()} values, {rows} rows of {lat_dim} / 64 expected")
-    _need(lse.dtype == torch.float32 and lse.is_contiguous() and lse.numel() == rows, where,
-          f"lse must be a contiguous fp32 tensor of {rows} values")
-    _need(weights.dtype == torch.float32 and weights.dim() == 2 and weights.shape[0] >= B and _rows_apart(weights),
-          where, f"weights must be a fp32 [>= {B}, max_len] tensor with contiguous rows")
-    _status_arg(where, status)
+    if q_lat.dtype is not torch.bfloat16 or q_pe.dtype is not torch.bfloat16:
+        _refuse(where, "q_lat and q_pe must be bf16")
+    if not q_lat.is_contiguous() or not q_pe.is_contiguous():
+        _refuse(where, "q_lat and q_pe must be contiguous")
+    if q_lat.numel() != rows * lat_dim or q_pe.numel() != rows * 64:
+        _refuse(where, f"q_lat / q_pe hold {q_lat.numel()} / {q_pe.numel()} values, {rows} rows of {lat_dim} / 64 expected")
+    if lse.dtype is not torch.float32 or not lse.is_contiguous() or lse.numel() != rows:
+        _refuse(where, f"lse must be a contiguous fp32 tensor of {rows} values")
+    if weights.dtype is not torch.float32 or weights.dim() != 2 or weights.shape[0] < B or not _rows_apart(weights):
+        _refuse(where, f"weights must be a fp32 [>= {B}, max_len] tensor with contiguous rows")
+    st = _status_ptr(where, status)
     rb = _row_bytes(where, cache_kind, lat_dim)
-    _check(load().mla_attn_weights(q_lat.data_ptr(), q_pe.data_ptr(), lse.data_ptr(), cache.data_ptr(),
-                                   int(cache_kind), int(lat_dim), _nbytes(cache) // rb, int(page_size),
-                                   block_table.data_ptr(), block_table.stride(0), seq_lens.data_ptr(), B, int(q_len),
-                                   Hq, float(scale), float(decay), weights.data_ptr(),
-                                   max(weights.stride(0), weights.shape[1]), weights.shape[1],
-                                   status.data_ptr() if status is not None else None, int(num_ctas), _stream(stream)),
-           where)
+    max_len = weights.shape[1]
+    _check(load().mla_attn_weights(
+        q_lat.data_ptr(), q_pe.data_ptr(), lse.data_ptr(), cache.data_ptr(), int(cache_kind), int(lat_dim),
+        cache.nbytes // rb, int(page_size), block_table.data_ptr(), block_table.stride(0), seq_lens.data_ptr(), B,
+        int(q_len), Hq, float(scale), float(decay),
+        weights.data_ptr(), max(weights.stride(0), max_len), max_len, st, int(num_ctas), _stream(stream)), where)
+
+
+_EVICT_NAMES = ("cache", "block_table", "seq_lens", "weights", "positions", "budgets", "new_seq_lens", "new_weights",
+                "new_positions", "moves", "status")
 
 
 def mla_cache_evict(cache, cache_kind, page_size, block_table, seq_lens, weights, positions, budgets, n_sink,
@@ -511,31 +556,32 @@ def mla_cache_evict(cache, cache_kind, page_size, block_table, seq_lens, weights
     int32 [B], new_weights and new_positions shaped as the inputs (or the
     inputs themselves), moves int32 [>= B, >= max_len + 2]."""
     where = "mla_cache_evict"
-    _here(where, cache=cache, block_table=block_table, seq_lens=seq_lens, weights=weights, positions=positions,
-          budgets=budgets, new_seq_lens=new_seq_lens, new_weights=new_weights, new_positions=new_positions,
-          moves=moves, status=status)
+    _here(where, _EVICT_NAMES, (cache, block_table, seq_lens, weights, positions, budgets, new_seq_lens, new_weights,
+                                new_positions, moves, status))
     B = _table_args(where, block_table, seq_lens, cache)
-    _need(weights.dim() == 2 and weights.shape[0] >= B and _rows_apart(weights), where,
-          f"weights must be [>= {B}, max_len] with contiguous rows")
-    stride, max_len = max(weights.stride(0), weights.shape[1]), weights.shape[1]
-    for name, t, dt in (("weights", weights, torch.float32), ("positions", positions, torch.int32),
-                        ("new_weights", new_weights, torch.float32), ("new_positions", new_positions, torch.int32)):
-        _need(t.dtype == dt and t.shape == weights.shape and _rows_apart(t) and
-              (t.stride(0) == weights.stride(0) or t.shape[0] == 1), where,
-              f"{name} must be a {dt} tensor of weights' shape and strides")
-    for name, t in (("budgets", budgets), ("new_seq_lens", new_seq_lens)):
-        _need(t.dtype == torch.int32 and t.is_contiguous() and t.numel() >= B, where,
-              f"{name} must be contiguous int32 of at least {B} values")
-    _need(moves.dtype == torch.int32 and moves.dim() == 2 and _rows_apart(moves) and moves.shape[0] >= B and
-          moves.shape[1] >= max_len + 2, where, f"moves must be an int32 [>= {B}, >= {max_len + 2}] tensor")
-    _status_arg(where, status)
+    if weights.dim() != 2 or weights.shape[0] < B or not _rows_apart(weights):
+        _refuse(where, f"weights must be [>= {B}, max_len] with contiguous rows")
+    shape, strides, f32, i32 = weights.shape, weights.stride(), torch.float32, torch.int32
+    max_len = shape[1]
+    if (weights.dtype is not f32 or positions.dtype is not i32 or new_weights.dtype is not f32 or
+            new_positions.dtype is not i32):
+        _refuse(where, "weights and new_weights must be fp32, positions and new_positions int32")
+    for name, t in (("positions", positions), ("new_weights", new_weights), ("new_positions", new_positions)):
+        if t.shape != shape or (t.stride() != strides and shape[0] > 1):
+            _refuse(where, f"{name} must be a tensor of weights' shape and strides")
+    if budgets.dtype is not i32 or not budgets.is_contiguous() or budgets.numel() < B:
+        _refuse(where, f"budgets must be contiguous int32 of at least {B} values")
+    if new_seq_lens.dtype is not i32 or not new_seq_lens.is_contiguous() or new_seq_lens.numel() < B:
+        _refuse(where, f"new_seq_lens must be contiguous int32 of at least {B} values")
+    if moves.dtype is not i32 or moves.dim() != 2 or moves.shape[0] < B or moves.shape[1] < max_len + 2 or not _rows_apart(moves):
+        _refuse(where, f"moves must be an int32 [>= {B}, >= {max_len + 2}] tensor")
+    st = _status_ptr(where, status)
     rb = _row_bytes(where, cache_kind, lat_dim)
-    _check(load().mla_cache_evict(cache.data_ptr(), rb, _nbytes(cache) // rb, int(page_size), block_table.data_ptr(),
-                                  block_table.stride(0), seq_lens.data_ptr(), weights.data_ptr(),
-                                  positions.data_ptr(), stride, max_len, budgets.data_ptr(), B, int(n_sink),
-                                  int(n_recent), new_seq_lens.data_ptr(), new_weights.data_ptr(),
-                                  new_positions.data_ptr(), moves.data_ptr(), max(moves.stride(0), moves.shape[1]),
-                                  status.data_ptr() if status is not None else None, _stream(stream)), where)
+    _check(load().mla_cache_evict(
+        cache.data_ptr(), int(rb), cache.nbytes // rb, int(page_size), block_table.data_ptr(), block_table.stride(0),
+        seq_lens.data_ptr(), weights.data_ptr(), positions.data_ptr(), max(strides[0], max_len), max_len,
+        budgets.data_ptr(), B, int(n_sink), int(n_recent), new_seq_lens.data_ptr(), new_weights.data_ptr(),
+        new_positions.data_ptr(), moves.data_ptr(), max(moves.stride(0), moves.shape[1]), st, _stream(stream)), where)
 
 
 def decode(q_lat, q_pe, cache, cache_kind, page_size, block_table, seq_lens, q_len, scale,

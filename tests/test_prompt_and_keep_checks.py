@@ -114,7 +114,7 @@ class _Recorder:
 def fake(monkeypatch, lib):
     rec = _Recorder(lib)
     monkeypatch.setattr(m, "_is_cuda", lambda t: isinstance(t, torch.Tensor))
-    monkeypatch.setattr(m, "_current_device", lambda: None)  # a host tensor's device has no index
+    monkeypatch.setattr(m, "_current_device", lambda: -1)  # what a host tensor gives as its device
     monkeypatch.setattr(m, "load", lambda: rec)
     monkeypatch.setattr(m, "_stream", lambda s: 0)
     return rec
