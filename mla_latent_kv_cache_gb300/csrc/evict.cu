@@ -18,11 +18,13 @@
 // the same result, and the rows moved are the fewest that any closing-up must
 // move: one per step in the steady state, where a shift would move them all.
 //
-// Two kernels. evict_select_kernel: a cluster of CL CTAs per request, each with
-// a contiguous part of the tokens whose keys stay in shared memory over all
-// passes; histograms and counts are combined through distributed shared
-// memory. evict_move_kernel: all SMs copy the listed rows, whatever request
-// they belong to.
+// Two kernels. The select kernel: a cluster of up to 8 CTAs per request, each
+// with a contiguous part of the tokens whose keys stay in the threads'
+// registers over all passes (evict_select_kernel; up to 262,144 tokens), or in
+// shared memory as far as they fit (evict_select_long_kernel); histograms and
+// counts are combined through distributed shared memory. evict_move_kernel:
+// all SMs copy the listed rows, whatever request they belong to, by bulk
+// copies through shared memory, with two batches of rows a warp in flight.
 #include <climits>
 
 #include <cooperative_groups.h>
@@ -87,7 +89,8 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* scan, uint3
     return r;
 }
 
-__global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const EvictParams p, int cap) {
+// Any number of tokens: keys in shared memory, formed again past `cap`.
+__global__ void __launch_bounds__(kSelThreads, 1) evict_select_long_kernel(const EvictParams p, int cap) {
     extern __shared__ uint32_t keys[];
     __shared__ SelectShared sh;
     cg::cluster_group cluster = cg::this_cluster();
@@ -293,23 +296,319 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Evic
     cluster.sync();  // no CTA leaves while another reads its counts
 }
 
-// Copies the listed rows. The moves of all requests form one sequence, dealt
-// out to warps four rows at a time; a warp has all its loads in flight before
-// the first store. UNITS: 16-byte units of a row (0: given at run time).
-constexpr int kMoveRows = 4;
-constexpr int kMoveThreads = 256;
-constexpr int kMoveReqs = 1024;  // requests whose counts a CTA holds at once
+// Sum over the warps before this one, and over all, of one value per warp
+// (given by every lane). One barrier; buf holds kSelWarps values.
+__device__ __forceinline__ uint32_t warps_before(uint32_t v, uint32_t* buf, uint32_t& total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (lane == 0) buf[warp] = v;
+    __syncthreads();
+    const uint32_t mine = buf[lane];
+    total = __reduce_add_sync(0xffffffffu, mine);
+    return __reduce_add_sync(0xffffffffu, lane < warp ? mine : 0u);
+}
 
-template <int UNITS>
-__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictParams p) {
-    __shared__ uint32_t first[kMoveReqs + 1];
-    __shared__ uint32_t wsum[kMoveThreads / 32];
+struct SelectRegShared {
+    uint32_t hist[3][kSelBins];   // this CTA's counts of each digit, read by the cluster
+    uint32_t warp[6][kSelWarps];  // per-warp values of the passes
+    int newest;
+    uint32_t ties, moves;         // this CTA's counts, read by the cluster
+    uint32_t bin[3], above[3], count[3];  // the chosen bin of each digit, the keys above it, and in it
+};
+
+// Up to KPT keys a thread, in registers: warp w of the CTA holds the span of
+// 32 kn consecutive tokens at t0 + 32 kn w, lane l its tokens l, l + 32, ...
+template <int KPT>
+__global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const EvictParams p) {
+    __shared__ __align__(16) SelectRegShared sh;
+    cg::cluster_group cluster = cg::this_cluster();
+    const int CL = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
+    const int b = static_cast<int>(blockIdx.x) / CL;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int units = UNITS > 0 ? UNITS : p.row_bytes / 16;
-    constexpr int kMaxPer = UNITS > 0 ? (kMoveRows * UNITS + 31) / 32 : 8;
+    auto meet = [&]() {
+        if (CL > 1) cluster.sync();
+        else __syncthreads();
+    };
+    if (tid == 0) griddep_launch_dependents();
+
+    const int T0 = max(__ldg(p.seq_lens + b), 0);
+    // tokens that neither the score rows nor the table row hold are not there
+    const int64_t held = min(static_cast<int64_t>(p.max_len), p.bt_stride * p.page_size);
+    const int T = static_cast<int>(min(static_cast<int64_t>(T0), held));
+    const int K = min(max(__ldg(p.budgets + b), 0), T);
+    const float* w = p.weights + b * p.stride;
+    const int32_t* pos = p.positions + b * p.stride;
+    float* nw = p.new_weights + b * p.stride;
+    int32_t* np = p.new_positions + b * p.stride;
+    int32_t* moves = p.moves + b * p.moves_stride;
+    const bool copy = nw != w, copyp = np != pos;
+
+    const int kn = ((T + CL - 1) / CL + kSelThreads - 1) / kSelThreads;  // keys a thread, <= KPT
+    const int t0 = min(rank * kn * kSelThreads, T), t1 = min(t0 + kn * kSelThreads, T);
+    const int at0 = t0 + warp * kn * 32 + lane;  // this thread's tokens: at0 + 32 k < t1
+
+    if (T <= K) {
+        // nothing goes
+        for (int i = t0 + tid; i < t1; i += kSelThreads) {
+            if (copy) nw[i] = w[i];
+            if (copyp) np[i] = pos[i];
+        }
+        meet();  // every part has read its length
+        if (rank == 0 && tid == 0) {
+            moves[0] = 0;
+            moves[1] = K;
+            p.new_lens[b] = K;
+            if (T0 > T && p.status) atomicOr(p.status, kErrBadBlock);
+        }
+        return;
+    }
+
+    // ---- the newest position, which the protected recent ones are counted from
+    int mx = INT_MIN;
+#pragma unroll
+    for (int k = 0; k < KPT; ++k) {
+        const int i = at0 + 32 * k;
+        mx = max(mx, k < kn && i < t1 ? pos[i] : INT_MIN);
+    }
+    for (int i = tid; i < 3 * kSelBins; i += kSelThreads) (&sh.hist[0][0])[i] = 0;
+    mx = __reduce_max_sync(0xffffffffu, mx);
+    if (lane == 0) sh.warp[0][warp] = static_cast<uint32_t>(mx);
+    __syncthreads();
+    int newest = __reduce_max_sync(0xffffffffu, static_cast<int>(sh.warp[0][lane]));
+    if (CL > 1) {
+        if (tid == 0) sh.newest = newest;
+        cluster.sync();
+        newest = __reduce_max_sync(0xffffffffu, lane < CL ? *cluster.map_shared_rank(&sh.newest, lane) : INT_MIN);
+    }
+    const int64_t recent_from = static_cast<int64_t>(newest) + 1 - p.n_recent;
+    // keys, with eight loads of each kind in flight. Entries below K go to the
+    // new arrays as they are: the places whose token goes are written again when
+    // their new token moves in.
+    uint32_t key[KPT];
+    constexpr int kIn = KPT < 8 ? KPT : 8;
+#pragma unroll
+    for (int k0 = 0; k0 < KPT; k0 += kIn) {
+        if (k0 >= kn) break;
+        float wv[kIn];
+        int ps[kIn];
+#pragma unroll
+        for (int k = 0; k < kIn; ++k) {
+            const int i = at0 + 32 * (k0 + k);
+            const bool in = k0 + k < kn && i < t1;
+            wv[k] = in ? w[i] : 0.f;
+            ps[k] = in ? pos[i] : 0;
+        }
+#pragma unroll
+        for (int k = 0; k < kIn; ++k) {
+            const int i = at0 + 32 * (k0 + k);
+            key[k0 + k] = evict_key(wv[k], ps[k] < p.n_sink || ps[k] >= recent_from);
+            if (k0 + k < kn && i < min(t1, K)) {
+                if (copy) nw[i] = wv[k];
+                if (copyp) np[i] = ps[k];
+            }
+        }
+    }
+
+    // ---- radix select of the K-th largest key; it ends early where all keys of a bin stay
+    uint32_t prefix = 0, want = static_cast<uint32_t>(K);  // the `want`-th largest among keys that start with prefix
+    int low = 32;                                          // bits not yet decided
+    bool rank_ties = false;                                // of the keys equal to the threshold only the first `want` stay
+    if (K > 0) {
+#pragma unroll 1
+        for (int pass = 0; pass < 3; ++pass) {
+            const int bits = pass == 2 ? 10 : 11, shift = low - bits;
+            const uint32_t mask = (1u << bits) - 1u;
+            uint32_t* hist = sh.hist[pass];
+#pragma unroll
+            for (int k = 0; k < KPT; ++k) {
+                if (k >= kn) break;
+                const bool hit = at0 + 32 * k < t1 && (pass == 0 || (key[k] >> low) == prefix);
+                const unsigned m = __ballot_sync(0xffffffffu, hit);
+                if (m == 0) continue;
+                const uint32_t d = (key[k] >> shift) & mask;
+                // equal digits all through the warp (decayed scores are often all
+                // zero) would queue up on one counter: count them at once
+                const uint32_t d0 = __shfl_sync(0xffffffffu, d, __ffs(m) - 1);
+                if (__all_sync(0xffffffffu, !hit || d == d0)) {
+                    if (lane == 0) atomicAdd(hist + d0, static_cast<uint32_t>(__popc(m)));
+                } else if (hit) {
+                    atomicAdd(hist + d, 1u);
+                }
+            }
+            meet();
+            // thread t holds the bins 2047 - 2t and 2046 - 2t, so that an ascending
+            // scan over threads counts keys from the top
+            const int hb = kSelBins - 1 - 2 * tid;
+            uint32_t c_hi = 0, c_lo = 0;
+            if (CL > 1) {
+                uint2 h[8];
+#pragma unroll
+                for (int c = 0; c < 8; ++c)
+                    h[c] = c < CL ? *reinterpret_cast<const uint2*>(cluster.map_shared_rank(hist + hb - 1, c))
+                                  : make_uint2(0u, 0u);
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    c_lo += h[c].x;
+                    c_hi += h[c].y;
+                }
+            } else {
+                c_lo = hist[hb - 1];
+                c_hi = hist[hb];
+            }
+            uint32_t x = c_hi + c_lo;  // inclusive scan over the warp
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
+                if (lane >= o) x += y;
+            }
+            uint32_t total;
+            const uint32_t base = warps_before(__shfl_sync(0xffffffffu, x, 31), sh.warp[1 + pass], total);
+            const uint32_t above = base + x - c_hi - c_lo;
+            if (above < want && want <= above + c_hi) {
+                sh.bin[pass] = hb;
+                sh.above[pass] = above;
+                sh.count[pass] = c_hi;
+            } else if (above + c_hi < want && want <= above + c_hi + c_lo) {
+                sh.bin[pass] = hb - 1;
+                sh.above[pass] = above + c_hi;
+                sh.count[pass] = c_lo;
+            }
+            __syncthreads();
+            prefix = (prefix << bits) | sh.bin[pass];
+            want -= sh.above[pass];
+            low = shift;
+            if (sh.count[pass] == want) break;
+            rank_ties = pass == 2;
+        }
+    }
+    const uint32_t thr = K > 0 ? prefix << low : 0u;
+
+    // ---- what stays, as bits: k of this thread
+    uint32_t keep = 0, tie = 0;
+#pragma unroll
+    for (int k = 0; k < KPT; ++k) {
+        const bool in = k < kn && at0 + 32 * k < t1 && K > 0;
+        keep |= (in && (rank_ties ? key[k] > thr : key[k] >= thr) ? 1u : 0u) << k;
+        tie |= (in && rank_ties && key[k] == thr ? 1u : 0u) << k;
+    }
+    if (rank_ties) {  // by place: ties in the CTAs, the warps and the groups of 32 before
+        uint32_t total;
+        uint32_t before = warps_before(__reduce_add_sync(0xffffffffu, __popc(tie)), sh.warp[4], total);
+        if (CL > 1) {
+            if (tid == 0) sh.ties = total;
+            cluster.sync();
+            const uint32_t t = lane < rank ? *cluster.map_shared_rank(&sh.ties, lane) : 0u;
+            before += __reduce_add_sync(0xffffffffu, t);
+        }
+        for (int k = 0; k < kn; ++k) {
+            const unsigned m = __ballot_sync(0xffffffffu, tie >> k & 1u);
+            if ((tie >> k & 1u) && before + __popc(m & ((1u << lane) - 1u)) < want) keep |= 1u << k;
+            before += __popc(m);
+        }
+    }
+
+    // ---- the free places below K, the kept tokens above, and how many lie before
+    uint32_t in_bits = 0, below = 0;  // this thread's tokens, and those at places below K
+#pragma unroll
+    for (int k = 0; k < KPT; ++k) {
+        const int i = at0 + 32 * k;
+        in_bits |= (k < kn && i < t1 ? 1u : 0u) << k;
+        below |= (k < kn && i < min(t1, K) ? 1u : 0u) << k;
+    }
+    const uint32_t holes = ~keep & below, srcs = keep & in_bits & ~below;
+    // (a CTA has at most 32,768 of either: two counts in one sum)
+    uint32_t total;
+    uint32_t n = warps_before(__reduce_add_sync(0xffffffffu, __popc(holes) | __popc(srcs) << 16), sh.warp[5], total);
+    uint32_t hole = n & 0xFFFFu, src = n >> 16, n_moves = total & 0xFFFFu;
+    if (CL > 1) {
+        if (tid == 0) sh.moves = total;
+        cluster.sync();
+        const uint32_t t = lane < CL ? *cluster.map_shared_rank(&sh.moves, lane) : 0u;
+        hole += __reduce_add_sync(0xffffffffu, lane < rank ? t & 0xFFFFu : 0u);
+        src += __reduce_add_sync(0xffffffffu, lane < rank ? t >> 16 : 0u);
+        n_moves = __reduce_add_sync(0xffffffffu, t & 0xFFFFu);
+    }
+
+    // ---- the lists: move r takes the token at moves[2 + 2r] to place moves[3 + 2r]
+    const unsigned lower = (1u << lane) - 1u;
+#pragma unroll
+    for (int k = 0; k < KPT; ++k) {
+        if (k >= kn) break;
+        const int i = at0 + 32 * k;
+        const bool is_hole = holes >> k & 1u, is_src = srcs >> k & 1u;
+        const unsigned mh = __ballot_sync(0xffffffffu, is_hole), ms = __ballot_sync(0xffffffffu, is_src);
+        if (is_src) moves[2 + 2 * static_cast<int64_t>(src + __popc(ms & lower))] = i;
+        if (is_hole) moves[3 + 2 * static_cast<int64_t>(hole + __popc(mh & lower))] = i;
+        src += __popc(ms);
+        hole += __popc(mh);
+    }
+    meet();  // every part has read its length and the others' counts
+    if (rank == 0 && tid == 0) {
+        moves[0] = static_cast<int32_t>(n_moves);
+        moves[1] = K;
+        p.new_lens[b] = K;
+        if (T0 > T && p.status) atomicOr(p.status, kErrBadBlock);
+    }
+}
+
+// Copies the listed rows. The moves of all requests form one sequence (of rows,
+// or of kStage-byte pieces of longer rows), dealt out to warps in batches of
+// what a stage holds: a lane looks one row up and copies it into shared memory
+// and out again by bulk copies. A warp loads a batch while the one before is
+// written.
+constexpr int kMoveThreads = 256;
+constexpr int kMoveWarps = kMoveThreads / 32;
+constexpr int kMoveReqs = 1024;  // requests whose counts a CTA holds at once
+constexpr int kStage = 9216;     // bytes of a batch: eight 1,152-byte rows
+
+struct MoveShared {
+    uint64_t full[kMoveWarps][2];
+    uint32_t first[kMoveReqs + 1];
+    uint32_t wsum[kMoveWarps];
+    int abort;
+};
+
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                     smem_u32(dst)),
+                 "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
+}
+__device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(reinterpret_cast<uint64_t>(dst)),
+                 "r"(smem_u32(src)), "r"(bytes)
+                 : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+// This thread's stores have read their shared memory.
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+
+__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictParams p) {
+    extern __shared__ __align__(128) uint8_t stages[];
+    __shared__ MoveShared sh;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     constexpr int kPer = kMoveReqs / kMoveThreads;
+    if (tid == 0) {
+        for (int i = 0; i < kMoveWarps; ++i)
+            for (int k = 0; k < 2; ++k) mbar_init(&sh.full[i][k], 1);
+        sh.abort = 0;
+        fence_mbar_init();
+    }
+    // pieces a row has, and rows or pieces of a batch (at most a warp's lanes)
+    const int pieces = (p.row_bytes + kStage - 1) / kStage;
+    const int batch = pieces > 1 ? 1 : min(32, kStage / p.row_bytes);
+    uint8_t* stage = stages + warp * 2 * kStage;
+    bool bad = false, ok = true;
+    uint32_t loads = 0;  // batches this warp has asked for
+    // the batch on its way: this lane's target and bytes
+    uint8_t* out = nullptr;
+    uint32_t out_bytes = 0;
+    auto write_last = [&]() {  // writes batch loads - 1 once it has landed
+        const uint32_t k = loads - 1;
+        if (ok && !__all_sync(0xffffffffu, mbar_wait(&sh.full[warp][k & 1], (k >> 1) & 1, &sh.abort))) ok = false;
+        if (ok && out_bytes) bulk_store(out, stage + (k & 1) * kStage + lane * (pieces > 1 ? 0 : p.row_bytes), out_bytes);
+        bulk_commit();
+    };
     griddep_wait();
-    bool bad = false;
     for (int b0 = 0; b0 < p.B; b0 += kMoveReqs) {
         const int nb = min(kMoveReqs, p.B - b0);
         // prefix sums of the counts of requests b0 .. b0 + nb (kPer a thread)
@@ -326,83 +625,99 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictPar
             const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
             if (lane >= o) x += y;
         }
-        if (lane == 31) wsum[warp] = x;
+        if (lane == 31) sh.wsum[warp] = x;
         __syncthreads();
         uint32_t run = x - sum;
-        for (int k = 0; k < warp; ++k) run += wsum[k];
+        for (int k = 0; k < warp; ++k) run += sh.wsum[k];
 #pragma unroll
         for (int k = 0; k < kPer; ++k) {
-            first[tid * kPer + k] = run;
+            sh.first[tid * kPer + k] = run;
             run += c[k];
         }
-        if (tid == kMoveThreads - 1) first[kMoveReqs] = run;
+        if (tid == kMoveThreads - 1) sh.first[kMoveReqs] = run;
         __syncthreads();
-        const uint32_t total = first[kMoveReqs];
-        const uint64_t step = static_cast<uint64_t>(gridDim.x) * (kMoveThreads / 32) * kMoveRows;
-        for (uint64_t m0 = static_cast<uint64_t>(blockIdx.x * (kMoveThreads / 32) + warp) * kMoveRows; m0 < total; m0 += step) {
-            const int n = static_cast<int>(min(static_cast<uint64_t>(kMoveRows), total - m0));
-            // lane r < n looks up move m0 + r
-            int64_t s_slot = -1, d_slot = -1;
-            if (lane < n) {
-                const uint32_t m = static_cast<uint32_t>(m0) + lane;
+        const uint64_t total = static_cast<uint64_t>(sh.first[kMoveReqs]) * pieces;
+        const uint64_t step = static_cast<uint64_t>(gridDim.x) * kMoveWarps * batch;
+        for (uint64_t m0 = (static_cast<uint64_t>(warp) * gridDim.x + blockIdx.x) * batch; m0 < total && ok; m0 += step) {
+            const uint64_t item = m0 + lane;
+            const uint8_t* from = nullptr;
+            uint8_t* to = nullptr;
+            uint32_t bytes = 0;
+            if (lane < batch && item < total) {
+                const uint32_t m = static_cast<uint32_t>(item / pieces), piece = static_cast<uint32_t>(item % pieces);
                 int lo = 0, hi = nb;  // the last request whose first move is <= m
                 while (hi - lo > 1) {
                     const int mid = (lo + hi) >> 1;
-                    if (first[mid] <= m) lo = mid;
+                    if (sh.first[mid] <= m) lo = mid;
                     else hi = mid;
                 }
                 const int64_t b = b0 + lo;
-                const int32_t* mv = p.moves + b * p.moves_stride + 2 + 2 * static_cast<int64_t>(m - first[lo]);
+                const int32_t* mv = p.moves + b * p.moves_stride + 2 + 2 * static_cast<int64_t>(m - sh.first[lo]);
                 const int s = mv[0], d = mv[1];
-                p.new_weights[b * p.stride + d] = p.weights[b * p.stride + s];
-                p.new_positions[b * p.stride + d] = p.positions[b * p.stride + s];
+                if (piece == 0) {
+                    p.new_weights[b * p.stride + d] = p.weights[b * p.stride + s];
+                    p.new_positions[b * p.stride + d] = p.positions[b * p.stride + s];
+                }
                 const int32_t* bt = p.block_table + b * p.bt_stride;
                 const int64_t sp = __ldg(bt + s / p.page_size), dp = __ldg(bt + d / p.page_size);
-                s_slot = sp * p.page_size + s % p.page_size;
-                d_slot = dp * p.page_size + d % p.page_size;
+                const int64_t ss = sp * p.page_size + s % p.page_size, ds = dp * p.page_size + d % p.page_size;
                 // a page outside the pool: the row is not moved
-                if (sp < 0 || dp < 0 || s_slot >= p.num_slots || d_slot >= p.num_slots) {
+                if (sp < 0 || dp < 0 || ss >= p.num_slots || ds >= p.num_slots) {
                     bad = true;
-                    s_slot = d_slot = -1;
+                } else {
+                    const int64_t off = static_cast<int64_t>(piece) * kStage;
+                    from = p.cache + ss * p.row_bytes + off;
+                    to = p.cache + ds * p.row_bytes + off;
+                    bytes = static_cast<uint32_t>(min(static_cast<int64_t>(kStage), p.row_bytes - off));
                 }
             }
-            const int all = n * units;
-            for (int u0 = 0; u0 < all; u0 += 32 * kMaxPer) {
-                uint4 v[kMaxPer];
-#pragma unroll
-                for (int k = 0; k < kMaxPer; ++k) {
-                    const int u = u0 + k * 32 + lane;
-                    const int r = min(u / units, kMoveRows - 1);
-                    const int64_t s = __shfl_sync(0xffffffffu, s_slot, r);
-                    if (u < all && s >= 0)
-                        v[k] = *reinterpret_cast<const uint4*>(p.cache + s * p.row_bytes + (u - r * units) * 16);
-                }
-#pragma unroll
-                for (int k = 0; k < kMaxPer; ++k) {
-                    const int u = u0 + k * 32 + lane;
-                    const int r = min(u / units, kMoveRows - 1);
-                    const int64_t d = __shfl_sync(0xffffffffu, d_slot, r);
-                    if (u < all && d >= 0)
-                        *reinterpret_cast<uint4*>(p.cache + d * p.row_bytes + (u - r * units) * 16) = v[k];
-                }
-            }
+            // the stores of batch loads - 2 have left its stage
+            bulk_wait_read();
+            __syncwarp();
+            const uint32_t all = __reduce_add_sync(0xffffffffu, bytes);
+            uint64_t* bar = &sh.full[warp][loads & 1];
+            if (lane == 0) mbar_arrive_expect_tx(bar, all);
+            __syncwarp();
+            if (bytes) bulk_load(stage + (loads & 1) * kStage + lane * (pieces > 1 ? 0 : p.row_bytes), from, bytes, bar);
+            if (loads > 0) write_last();
+            ++loads;
+            out = to;
+            out_bytes = bytes;
+        }
+        if (loads > 0) {
+            write_last();
+            // the next requests' batches count on: none is on its way
+            out_bytes = 0;
         }
         __syncthreads();
+    }
+    bulk_wait_read();
+    if (!ok) {
+        // no copy may arrive after the CTA is gone
+        volatile int never = 0;
+        for (uint32_t k = loads < 2 ? 0 : loads - 2; k < loads; ++k) mbar_wait(&sh.full[warp][k & 1], (k >> 1) & 1, &never);
+        if (lane == 0) {
+            sh.abort = 1;
+            if (p.status) atomicOr(p.status, kErrWaitTimeout);
+        }
     }
     if (bad && p.status) atomicOr(p.status, kErrBadBlock);
 }
 
-// CTAs that share a request's tokens.
-int select_cluster(int max_len) { return max_len <= 8192 ? 1 : max_len <= 16384 ? 2 : max_len <= 32768 ? 4 : 8; }
+template <int KPT>
+cudaError_t launch_select(const cudaLaunchConfig_t& cfg, const EvictParams& p) {
+    return cudaLaunchKernelEx(&cfg, evict_select_kernel<KPT>, p);
+}
 
 }  // namespace
 
 cudaError_t launch_evict(const EvictParams& p, int sms, cudaStream_t stream) {
-    const int CL = select_cluster(p.max_len);
-    const int per = ((p.max_len + CL - 1) / CL + kSelThreads - 1) / kSelThreads * kSelThreads;
-    const int cap = per < kSelCap ? per : kSelCap;
-    cudaError_t e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelCap * 4);
-    if (e != cudaSuccess) return e;
+    // CTAs that share a request's tokens: 8 keys a thread where there are SMs for
+    // it, up to 32 otherwise
+    int CL = p.max_len <= 8 * kSelThreads ? 1 : p.max_len <= 16 * kSelThreads ? 2 : p.max_len <= 32 * kSelThreads ? 4 : 8;
+    auto keys = [&](int cl) { return ((p.max_len + cl - 1) / cl + kSelThreads - 1) / kSelThreads; };
+    while (CL > 1 && static_cast<int64_t>(CL) * p.B > sms && keys(CL / 2) <= 32) CL /= 2;
+    const int kpt = keys(CL);
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -411,24 +726,40 @@ cudaError_t launch_evict(const EvictParams& p, int sms, cudaStream_t stream) {
     attr[0].val.clusterDim.z = 1;
     cfg.gridDim = dim3(static_cast<unsigned>(CL) * p.B);
     cfg.blockDim = dim3(kSelThreads);
-    cfg.dynamicSmemBytes = static_cast<size_t>(cap) * 4;
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, evict_select_kernel, p, cap);
+    cudaError_t e;
+    if (kpt <= 4) {
+        e = launch_select<4>(cfg, p);
+    } else if (kpt <= 8) {
+        e = launch_select<8>(cfg, p);
+    } else if (kpt <= 16) {
+        e = launch_select<16>(cfg, p);
+    } else if (kpt <= 32) {
+        e = launch_select<32>(cfg, p);
+    } else {
+        const int cap = kpt * kSelThreads < kSelCap ? kpt * kSelThreads : kSelCap;
+        e = cudaFuncSetAttribute(evict_select_long_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelCap * 4);
+        if (e != cudaSuccess) return e;
+        cfg.dynamicSmemBytes = static_cast<size_t>(cap) * 4;
+        e = cudaLaunchKernelEx(&cfg, evict_select_long_kernel, p, cap);
+    }
+    if (e != cudaSuccess) return e;
+    constexpr int kMoveSmem = kMoveWarps * 2 * kStage;
+    e = cudaFuncSetAttribute(evict_move_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMoveSmem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t mc = {};
     cudaLaunchAttribute ma[1];
     ma[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     ma[0].val.programmaticStreamSerializationAllowed = 1;
-    mc.gridDim = dim3(static_cast<unsigned>(4 * sms));
+    mc.gridDim = dim3(static_cast<unsigned>(sms));
     mc.blockDim = dim3(kMoveThreads);
+    mc.dynamicSmemBytes = kMoveSmem;
     mc.stream = stream;
     mc.attrs = ma;
     mc.numAttrs = 1;
-    return p.row_bytes == kRowBf16  ? cudaLaunchKernelEx(&mc, evict_move_kernel<kRowBf16 / 16>, p)
-           : p.row_bytes == kRowFp8 ? cudaLaunchKernelEx(&mc, evict_move_kernel<kRowFp8 / 16>, p)
-                                    : cudaLaunchKernelEx(&mc, evict_move_kernel<0>, p);
+    return cudaLaunchKernelEx(&mc, evict_move_kernel, p);
 }
 
 }  // namespace mla

@@ -114,13 +114,35 @@ def test_protected_ends(n_sink, n_recent):
     _go(*_case(LENS, 16, seed=3), budgets=333, n_sink=n_sink, n_recent=n_recent, page=16)
 
 
-@pytest.mark.parametrize("most", [9000, 20000, 40000])
+@pytest.mark.parametrize("most", [4097, 9000, 20000, 40000, 100000, 200000])
 def test_requests_that_several_ctas_share(most):
     r = np.random.default_rng(most)
     lens = [most, most // 2, 1, 0, most - 1]
     for scores in ("ties", "distinct"):
         _go(*_case(lens, 64, 1, seed=most, scores=scores), budgets=r.integers(0, most, size=5), n_sink=4,
             n_recent=100, page=64, kind=1)
+
+
+def test_many_requests_that_fewer_ctas_share_each():
+    r = np.random.default_rng(6)
+    lens = r.integers(0, 20000, size=100)
+    _go(*_case(lens, 16, 0, 256, seed=6), budgets=r.integers(0, 20000, size=100), n_sink=4, n_recent=64, page=16, lat_dim=256)
+
+
+@pytest.mark.parametrize("row_bytes", [16, 48, 9216, 9232, 20000, 65536])
+def test_any_row_size(row_bytes):
+    lens, bt, cache, w, pos = _case([300, 0, 77], 16, seed=row_bytes)
+    cache = np.random.default_rng(1).integers(0, 256, size=(len(cache), row_bytes), dtype=np.uint8)
+    ref_c, ref_l, _, _, _ = keep_ref.evict(cache, bt, lens, w, pos, np.array([100, 5, 40]), 2, 8, 16)
+    d = [_t(x) for x in (cache, bt, lens, w, pos, np.array([100, 5, 40], np.int32))]
+    nl, nw, npos = torch.zeros_like(d[2]), torch.zeros_like(d[3]), torch.zeros_like(d[4])
+    mv = torch.zeros((3, w.shape[1] + 2), dtype=torch.int32, device=DEV)
+    st = m.load().mla_cache_evict(d[0].data_ptr(), row_bytes, len(cache), 16, d[1].data_ptr(), bt.shape[1], d[2].data_ptr(),
+                                  d[3].data_ptr(), d[4].data_ptr(), w.shape[1], w.shape[1], d[5].data_ptr(), 3, 2, 8,
+                                  nl.data_ptr(), nw.data_ptr(), npos.data_ptr(), mv.data_ptr(), mv.shape[1], None, None)
+    torch.cuda.synchronize()
+    assert st == m.MLA_OK
+    assert np.array_equal(nl.cpu().numpy(), ref_l) and np.array_equal(d[0].cpu().numpy(), ref_c)
 
 
 def test_more_tokens_than_shared_memory_holds_keys():
