@@ -18,9 +18,9 @@
 // the same result, and the rows moved are the fewest that any closing-up must
 // move: one per step in the steady state, where a shift would move them all.
 //
-// Two kernels. The select kernel: a cluster of up to 8 CTAs per request, each
+// Two kernels. The select kernel: a cluster of up to 16 CTAs per request, each
 // with a contiguous part of the tokens whose keys stay in the threads'
-// registers over all passes (evict_select_kernel; up to 262,144 tokens), or in
+// registers over all passes (evict_select_kernel; up to 524,288 tokens), or in
 // shared memory as far as they fit (evict_select_long_kernel); histograms and
 // counts are combined through distributed shared memory. evict_move_kernel:
 // all SMs copy the listed rows, whatever request they belong to, by bulk
@@ -440,13 +440,13 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Evic
             const int hb = kSelBins - 1 - 2 * tid;
             uint32_t c_hi = 0, c_lo = 0;
             if (CL > 1) {
-                uint2 h[8];
+                uint2 h[16];
 #pragma unroll
-                for (int c = 0; c < 8; ++c)
+                for (int c = 0; c < 16; ++c)
                     h[c] = c < CL ? *reinterpret_cast<const uint2*>(cluster.map_shared_rank(hist + hb - 1, c))
                                   : make_uint2(0u, 0u);
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
+                for (int c = 0; c < 16; ++c) {
                     c_lo += h[c].x;
                     c_hi += h[c].y;
                 }
@@ -555,9 +555,9 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Evic
 // what a stage holds: a lane looks one row up and copies it into shared memory
 // and out again by bulk copies. A warp loads a batch while the one before is
 // written.
-constexpr int kMoveThreads = 256;
+constexpr int kMoveThreads = 384;
 constexpr int kMoveWarps = kMoveThreads / 32;
-constexpr int kMoveReqs = 1024;  // requests whose counts a CTA holds at once
+constexpr int kMoveReqs = 1536;  // requests whose counts a CTA holds at once
 constexpr int kStage = 9216;     // bytes of a batch: eight 1,152-byte rows
 
 struct MoveShared {
@@ -706,6 +706,9 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictPar
 
 template <int KPT>
 cudaError_t launch_select(const cudaLaunchConfig_t& cfg, const EvictParams& p) {
+    // clusters of 16
+    const cudaError_t e = cudaFuncSetAttribute(evict_select_kernel<KPT>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
     return cudaLaunchKernelEx(&cfg, evict_select_kernel<KPT>, p);
 }
 
@@ -714,10 +717,12 @@ cudaError_t launch_select(const cudaLaunchConfig_t& cfg, const EvictParams& p) {
 cudaError_t launch_evict(const EvictParams& p, int sms, cudaStream_t stream) {
     // CTAs that share a request's tokens: 8 keys a thread where there are SMs for
     // it, up to 32 otherwise
-    int CL = p.max_len <= 8 * kSelThreads ? 1 : p.max_len <= 16 * kSelThreads ? 2 : p.max_len <= 32 * kSelThreads ? 4 : 8;
+    int CL = 1;
+    while (CL < 16 && p.max_len > CL * 8 * kSelThreads) CL *= 2;
     auto keys = [&](int cl) { return ((p.max_len + cl - 1) / cl + kSelThreads - 1) / kSelThreads; };
     while (CL > 1 && static_cast<int64_t>(CL) * p.B > sms && keys(CL / 2) <= 32) CL /= 2;
     const int kpt = keys(CL);
+    if (kpt > 32) CL = 8;  // evict_select_long_kernel
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -739,11 +744,10 @@ cudaError_t launch_evict(const EvictParams& p, int sms, cudaStream_t stream) {
     } else if (kpt <= 32) {
         e = launch_select<32>(cfg, p);
     } else {
-        const int cap = kpt * kSelThreads < kSelCap ? kpt * kSelThreads : kSelCap;
         e = cudaFuncSetAttribute(evict_select_long_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelCap * 4);
         if (e != cudaSuccess) return e;
-        cfg.dynamicSmemBytes = static_cast<size_t>(cap) * 4;
-        e = cudaLaunchKernelEx(&cfg, evict_select_long_kernel, p, cap);
+        cfg.dynamicSmemBytes = kSelCap * 4;
+        e = cudaLaunchKernelEx(&cfg, evict_select_long_kernel, p, kSelCap);
     }
     if (e != cudaSuccess) return e;
     constexpr int kMoveSmem = kMoveWarps * 2 * kStage;

@@ -146,8 +146,10 @@ def test_any_row_size(row_bytes):
 
 
 def test_more_tokens_than_shared_memory_holds_keys():
-    # 8 CTAs of 49,152 keys: the rest is formed again on every pass
-    _go(*_case([400000, 5], 784, 0, 256, seed=1), budgets=[170001, 3], n_sink=4, n_recent=1000, page=784, lat_dim=256)
+    # 16 CTAs keep 524,288 keys in registers; past that 8 keep 393,216 in shared
+    # memory and form the rest again on every pass
+    for n in (400000, 600000):
+        _go(*_case([n, 5], 784, 0, 256, seed=1), budgets=[170001, 3], n_sink=4, n_recent=1000, page=784, lat_dim=256)
 
 
 def test_more_requests_than_a_cta_counts_at_once():
