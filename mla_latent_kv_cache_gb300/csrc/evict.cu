@@ -308,7 +308,9 @@ __device__ __forceinline__ uint32_t warps_before(uint32_t v, uint32_t* buf, uint
 }
 
 struct SelectRegShared {
-    uint32_t hist[3][kSelBins];   // this CTA's counts of each digit, read by the cluster
+    uint32_t hist[3][kSelBins];        // this CTA's counts of each digit, read by the cluster
+    uint32_t slice[3][kSelBins / 2];   // the cluster's counts of this CTA's slice of the bins
+    uint32_t slice_total[3];
     uint32_t warp[6][kSelWarps];  // per-warp values of the passes
     int newest;
     uint32_t ties, moves;         // this CTA's counts, read by the cluster
@@ -370,6 +372,8 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Evic
         mx = max(mx, k < kn && i < t1 ? pos[i] : INT_MIN);
     }
     for (int i = tid; i < 3 * kSelBins; i += kSelThreads) (&sh.hist[0][0])[i] = 0;
+    if (CL > 1)
+        for (int i = tid; i < 3 * (kSelBins / 2) + 3; i += kSelThreads) (&sh.slice[0][0])[i] = 0;  // and the totals
     mx = __reduce_max_sync(0xffffffffu, mx);
     if (lane == 0) sh.warp[0][warp] = static_cast<uint32_t>(mx);
     __syncthreads();
@@ -434,25 +438,40 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Evic
                     atomicAdd(hist + d, 1u);
                 }
             }
-            meet();
-            // thread t holds the bins 2047 - 2t and 2046 - 2t, so that an ascending
-            // scan over threads counts keys from the top
-            const int hb = kSelBins - 1 - 2 * tid;
-            uint32_t c_hi = 0, c_lo = 0;
+            // the bin in which the want-th largest falls: threads hold bins from the top
+            // down, so that a scan over threads counts keys from the top
+            uint32_t c_hi, c_lo = 0, above0 = 0;
+            int top;  // this thread's upper bin
             if (CL > 1) {
-                uint2 h[16];
+                // each CTA sums its slice of the bins over the cluster (every CTA
+                // reading all bins of all others is 16 times the traffic: 9 us a
+                // digit); the slices' totals then say which slice to look into
+                cluster.sync();
+                const int S = kSelBins / CL;
+                uint32_t* slice = sh.slice[pass];
+                const int from = tid / (S / 2), pair = tid % (S / 2) * 2;
+                const uint2 h = *reinterpret_cast<const uint2*>(cluster.map_shared_rank(hist + rank * S + pair, from));
+                if (h.x) atomicAdd(slice + pair, h.x);
+                if (h.y) atomicAdd(slice + pair + 1, h.y);
+                const uint32_t sum = __reduce_add_sync(0xffffffffu, h.x + h.y);
+                if (lane == 0 && sum) atomicAdd(&sh.slice_total[pass], sum);
+                cluster.sync();
+                const uint32_t mine = lane < CL ? *cluster.map_shared_rank(&sh.slice_total[pass], lane) : 0u;
+                uint32_t up = mine;  // keys in this slice and those above it
 #pragma unroll
-                for (int c = 0; c < 16; ++c)
-                    h[c] = c < CL ? *reinterpret_cast<const uint2*>(cluster.map_shared_rank(hist + hb - 1, c))
-                                  : make_uint2(0u, 0u);
-#pragma unroll
-                for (int c = 0; c < 16; ++c) {
-                    c_lo += h[c].x;
-                    c_hi += h[c].y;
+                for (int o = 1; o < 16; o <<= 1) {
+                    const uint32_t y = __shfl_down_sync(0xffffffffu, up, o);
+                    if (lane + o < 32) up += y;
                 }
+                const int owner = __ffs(__ballot_sync(0xffffffffu, up - mine < want && want <= up)) - 1;
+                above0 = __shfl_sync(0xffffffffu, up - mine, owner);
+                top = owner * S + S - 1 - tid;
+                c_hi = tid < S ? *cluster.map_shared_rank(slice + S - 1 - tid, owner) : 0u;
             } else {
-                c_lo = hist[hb - 1];
-                c_hi = hist[hb];
+                __syncthreads();
+                top = kSelBins - 1 - 2 * tid;
+                c_hi = hist[top];
+                c_lo = hist[top - 1];
             }
             uint32_t x = c_hi + c_lo;  // inclusive scan over the warp
 #pragma unroll
@@ -462,13 +481,13 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Evic
             }
             uint32_t total;
             const uint32_t base = warps_before(__shfl_sync(0xffffffffu, x, 31), sh.warp[1 + pass], total);
-            const uint32_t above = base + x - c_hi - c_lo;
+            const uint32_t above = above0 + base + x - c_hi - c_lo;
             if (above < want && want <= above + c_hi) {
-                sh.bin[pass] = hb;
+                sh.bin[pass] = top;
                 sh.above[pass] = above;
                 sh.count[pass] = c_hi;
             } else if (above + c_hi < want && want <= above + c_hi + c_lo) {
-                sh.bin[pass] = hb - 1;
+                sh.bin[pass] = top - 1;
                 sh.above[pass] = above + c_hi;
                 sh.count[pass] = c_lo;
             }
