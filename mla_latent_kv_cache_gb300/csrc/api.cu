@@ -500,7 +500,7 @@ int mla_prefill(const void* q, int64_t q_stride_t, int64_t q_stride_h, const voi
         !map(&maps.k_pe, keys ? k_pe : q, 64, 1, keys ? total_k : 1, k_pe_stride, k_pe_stride) ||
         !map(&maps.v, keys ? v : q, 128, keys ? Hkv : 1, keys ? total_k : 1, v_stride_h, v_stride_t))
         return MLA_ERR_CUDA;
-    const cudaError_t e = mla::launch_prefill(maps, p, static_cast<cudaStream_t>(stream));
+    const cudaError_t e = mla::launch_prefill(maps, p, di.sms, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 

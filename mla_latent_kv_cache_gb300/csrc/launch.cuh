@@ -165,6 +165,6 @@ struct PrefillParams {
 struct PrefillMaps {
     CUtensorMap q, k_nope, k_pe, v;
 };
-cudaError_t launch_prefill(const PrefillMaps& maps, const PrefillParams& p, cudaStream_t stream);
+cudaError_t launch_prefill(const PrefillMaps& maps, const PrefillParams& p, int sms, cudaStream_t stream);
 
 }  // namespace mla

@@ -20,6 +20,9 @@
 //   P_i             thread = row: no exchange between threads; bf16, written
 //                   over S_i in TMEM, where it is the next product's A operand
 //   O_i += P_i V    128 x 128 x 128, into TMEM
+// A CTA per SM goes through its share of these items (a scheduler warp finds
+// them, the longest first): the next item's Q, keys and scores are on their way
+// while the last one's output is written.
 // TMEM: S_0, S_1, O_0, O_1 of 128 columns each = all 512. Shared memory: Q
 // 96 KB, and a ring of eight 16-KB blocks (64 dims of 128 tokens) through which
 // K (two blocks of k_nope, one of k_pe) and V (two) stream by TMA.
@@ -42,17 +45,25 @@ constexpr int kKT = 128;                  // keys of a tile
 constexpr int kBlkP = 128 * 128;          // a block: 64 dims of 128 tokens
 constexpr int kSlots = 8;
 constexpr int kDv = 128;
-constexpr int kThreadsP = 320;            // 8 softmax warps, the MMA issuer, the loader
+constexpr int kThreadsP = 352;            // 8 softmax warps, the MMA issuer, the loader, the scheduler
+constexpr int kItems = 4;                 // items ahead of the slowest role
 constexpr int kQBytesP = 2 * 3 * kBlkP;
 constexpr int kSmemP = 1024 + 1024 + kQBytesP + kSlots * kBlkP;
 constexpr float kRaise = 8.f;             // log2 units
 
+// 256 queries of one head: query rows q_row .. of a sequence of q_len and k_len
+// tokens, from its query t0 on, and the key tiles that each half sees.
+struct PItem {
+    int h, q_row, k_row, q_len, k_len, t0, n0, n1;
+};
+
 struct PCtrl {
-    uint64_t q_full[2], blk_full[kSlots], blk_empty[kSlots];
+    uint64_t q_full[2], q_empty[2], blk_full[kSlots], blk_empty[kSlots];
     uint64_t s_full[2], p_full[2], o_full[2], fin;
+    uint64_t item_full[kItems], item_empty[kItems];
     uint32_t tmem_base;
     int abort;
-    int b, qt;  // this CTA's sequence (-1: none) and pair of query tiles
+    PItem item[kItems];  // h < 0: no more
 };
 static_assert(sizeof(PCtrl) <= 1024, "control block");
 
@@ -95,70 +106,100 @@ __device__ __forceinline__ int2 p_span(const int32_t* cu, int b, int total) {
     return make_int2(a, max(e - a, 0));
 }
 
-// The s-th pair of query tiles of all sequences, the last pairs (which see the
-// most keys) first: a whole warp. b = -1 if there are fewer.
-__device__ __forceinline__ void p_locate(const PrefillParams& p, int64_t s, int lane, int& b, int& qt) {
-    auto pairs = [&](int i) { return i < p.B ? (p_span(p.cu_q, i, p.total_q).y + 2 * kQT - 1) / (2 * kQT) : 0; };
-    const int mine = pairs(lane);  // of the first 32 sequences
-    int top = 0;
-    for (int base = 0; base < p.B; base += 32) top = max(top, base == 0 ? mine : pairs(base + lane));
-    top = __reduce_max_sync(0xffffffffu, top);
-    auto from = [&](int q) -> int64_t {  // pairs with index >= q
-        int64_t n = 0;
-        for (int base = 0; base < p.B; base += 32)
-            n += __reduce_add_sync(0xffffffffu, max(0, (base == 0 ? mine : pairs(base + lane)) - q));
-        return n;
-    };
-    b = -1;
-    qt = 0;
-    if (from(0) <= s) return;
-    int lo = 0, hi = top;  // from(lo) > s, from(hi) = 0
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (from(mid) > s) lo = mid;
-        else hi = mid;
-    }
-    int64_t r = s - from(lo + 1);
-    for (int base = 0; base < p.B; base += 32) {
-        unsigned m = __ballot_sync(0xffffffffu, (base == 0 ? mine : pairs(base + lane)) > lo);
-        const int n = __popc(m);
-        if (r < n) {
-            for (; r > 0; --r) m &= m - 1;
-            b = base + __ffs(m) - 1;
-            break;
-        }
-        r -= n;
-    }
-    qt = lo;
+// Keys that query t of a sequence sees.
+__device__ __forceinline__ int p_seen(int causal, int q_len, int k_len, int t) {
+    return causal ? min(k_len, max(0, k_len - q_len + t + 1)) : k_len;
 }
 
-// A row again from the keys that it sees alone, by its whole warp (q of the
-// row and V of a visible key may be non-finite, and then so is the row).
+// Finds pairs of query tiles by their number, the last pairs of all sequences
+// (which see the most keys) first; used by a whole warp.
+struct PFinder {
+    int mine, top;  // lane's pairs of the first 32 sequences; the most that a sequence has
+    __device__ __forceinline__ int pairs(const PrefillParams& p, int i) const {
+        return i < p.B ? (p_span(p.cu_q, i, p.total_q).y + 2 * kQT - 1) / (2 * kQT) : 0;
+    }
+    __device__ __forceinline__ int of(const PrefillParams& p, int base, int lane) const {
+        return base == 0 ? mine : pairs(p, base + lane);
+    }
+    __device__ __forceinline__ void init(const PrefillParams& p, int lane) {
+        mine = pairs(p, lane);
+        top = 0;
+        for (int base = 0; base < p.B; base += 32) top = max(top, of(p, base, lane));
+        top = __reduce_max_sync(0xffffffffu, top);
+    }
+    __device__ __forceinline__ int64_t from(const PrefillParams& p, int q, int lane) const {  // pairs with index >= q
+        int64_t n = 0;
+        for (int base = 0; base < p.B; base += 32) n += __reduce_add_sync(0xffffffffu, max(0, of(p, base, lane) - q));
+        return n;
+    }
+    // Sequence b and pair qt of the s-th; false if there are fewer.
+    __device__ __forceinline__ bool find(const PrefillParams& p, int64_t s, int lane, int& b, int& qt) const {
+        if (from(p, 0, lane) <= s) return false;
+        int lo = 0, hi = top;  // from(lo) > s, from(hi) = 0
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (from(p, mid, lane) > s) lo = mid;
+            else hi = mid;
+        }
+        int64_t r = s - from(p, lo + 1, lane);
+        for (int base = 0; base < p.B; base += 32) {
+            unsigned m = __ballot_sync(0xffffffffu, of(p, base, lane) > lo);
+            const int n = __popc(m);
+            if (r < n) {
+                for (; r > 0; --r) m &= m - 1;
+                b = base + __ffs(m) - 1;
+                break;
+            }
+            r -= n;
+        }
+        qt = lo;
+        return true;
+    }
+};
+
+// A row again from the keys that it sees alone, by its whole warp (V of a
+// visible key may be non-finite, and then so is the row): 32 keys at a time, a
+// lane forms the score of one, and four of the 128 sums over them.
 __device__ __noinline__ void p_row_again(const PrefillParams& p, int64_t qrow, int h, int hk, int64_t k0, int vis,
                                          float m2, float inv_l, int lane) {
     const __nv_bfloat16* q = p.q + qrow * p.q_st + h * p.q_sh;
-    float qv[6], acc[4] = {0.f, 0.f, 0.f, 0.f};
+    auto dot8 = [](const __nv_bfloat16* a, const __nv_bfloat16* b, float s) {
+        const uint4 x = *reinterpret_cast<const uint4*>(a), y = *reinterpret_cast<const uint4*>(b);
+        const __nv_bfloat162 *xa = reinterpret_cast<const __nv_bfloat162*>(&x), *yb = reinterpret_cast<const __nv_bfloat162*>(&y);
 #pragma unroll
-    for (int i = 0; i < 6; ++i) qv[i] = __bfloat162float(q[lane + 32 * i]);
-    for (int j = 0; j < vis; ++j) {
-        const int64_t kr = k0 + j;
-        const __nv_bfloat16* kn = p.k_nope + kr * p.k_st + hk * p.k_sh;
-        const __nv_bfloat16* kp = p.k_pe + kr * p.kp_st;
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = __bfloat1622float2(xa[i]), g = __bfloat1622float2(yb[i]);
+            s = fmaf(f.x, g.x, s);
+            s = fmaf(f.y, g.y, s);
+        }
+        return s;
+    };
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int j0 = 0; j0 < vis; j0 += 32) {
+        const int64_t kr = k0 + min(j0 + lane, vis - 1);
+        const __nv_bfloat16 *kn = p.k_nope + kr * p.k_st + hk * p.k_sh, *kp = p.k_pe + kr * p.kp_st;
         float s = 0.f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) s = fmaf(qv[i], __bfloat162float(kn[lane + 32 * i]), s);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) s = fmaf(qv[4 + i], __bfloat162float(kp[lane + 32 * i]), s);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+#pragma unroll 4
+        for (int i = 0; i < 16; ++i) s = dot8(q + 8 * i, kn + 8 * i, s);
+#pragma unroll 4
+        for (int i = 0; i < 8; ++i) s = dot8(q + 128 + 8 * i, kp + 8 * i, s);
         const float w = ex2(fmaf(s, p.scale_log2, -m2)) * inv_l;
-        const __nv_bfloat16* v = p.v + kr * p.v_st + hk * p.v_sh;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[i] = fmaf(w, __bfloat162float(v[lane + 32 * i]), acc[i]);
+        const int n = min(32, vis - j0);
+        const __nv_bfloat16* v = p.v + (k0 + j0) * p.v_st + hk * p.v_sh + 4 * lane;
+#pragma unroll 4
+        for (int j = 0; j < n; ++j) {
+            const float wj = __shfl_sync(0xffffffffu, w, j);
+            const uint2 x = *reinterpret_cast<const uint2*>(v + j * p.v_st);
+            const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&x.x)),
+                         g = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&x.y));
+            acc[0] = fmaf(wj, f.x, acc[0]);
+            acc[1] = fmaf(wj, f.y, acc[1]);
+            acc[2] = fmaf(wj, g.x, acc[2]);
+            acc[3] = fmaf(wj, g.y, acc[3]);
+        }
     }
-    __nv_bfloat16* o = p.out + (qrow * p.Hq + h) * kDv;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) o[lane + 32 * i] = __float2bfloat16(acc[i]);
+    *reinterpret_cast<uint2*>(p.out + (qrow * p.Hq + h) * kDv + 4 * lane) =
+        make_uint2(pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]));
 }
 
 __global__ void __launch_bounds__(kThreadsP, 1)
@@ -169,11 +210,11 @@ __global__ void __launch_bounds__(kThreadsP, 1)
     uint8_t* qs = smem + 1024;
     uint8_t* ring = qs + kQBytesP;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int h = blockIdx.x % p.Hq, hk = h / (p.Hq / p.Hkv);
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(&ctrl->q_full[i], 1);
+            mbar_init(&ctrl->q_empty[i], 1);
             mbar_init(&ctrl->s_full[i], 1);
             mbar_init(&ctrl->p_full[i], 4);
             mbar_init(&ctrl->o_full[i], 1);
@@ -181,6 +222,10 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         for (int i = 0; i < kSlots; ++i) {
             mbar_init(&ctrl->blk_full[i], 1);
             mbar_init(&ctrl->blk_empty[i], 1);
+        }
+        for (int i = 0; i < kItems; ++i) {
+            mbar_init(&ctrl->item_full[i], 1);
+            mbar_init(&ctrl->item_empty[i], 10);  // every warp but the scheduler
         }
         mbar_init(&ctrl->fin, 1);
         ctrl->abort = 0;
@@ -191,44 +236,93 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         tmem_relinquish();
         tc_fence_before();
     }
-    if (warp == 9) {
-        int b, qt;
-        p_locate(p, blockIdx.x / p.Hq, lane, b, qt);
-        if (lane == 0) {
-            ctrl->b = b;
-            ctrl->qt = qt;
-        }
-    }
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = ctrl->tmem_base;
     volatile int* abort = &ctrl->abort;
-    const int b = ctrl->b;
-    if (b >= 0) {
-        const int2 sq = p_span(p.cu_q, b, p.total_q), sk = p_span(p.cu_k, b, p.total_k);
-        const int t0 = ctrl->qt * 2 * kQT;
-        // keys that row t sees, and a tile's number of key tiles
-        auto seen = [&](int t) { return p.causal ? min(sk.y, max(0, sk.y - sq.y + t + 1)) : sk.y; };
-        int n[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int rows = min(kQT, sq.y - t0 - i * kQT);
-            n[i] = rows > 0 ? (seen(t0 + i * kQT + rows - 1) + kKT - 1) / kKT : 0;
-        }
-        const int nk = max(n[0], n[1]);
 
-        if (warp == 9) {
+    // The next item of this CTA, held by a whole warp until it gives it back;
+    // null at the end (or on failure).
+    int taken = 0;
+    bool ok = true;
+    auto take = [&]() -> const PItem* {
+        const int k = taken % kItems;
+        if (!__all_sync(0xffffffffu, mbar_wait(&ctrl->item_full[k], (taken / kItems) & 1, abort))) {
+            ok = false;
+            return nullptr;
+        }
+        return ctrl->item[k].h >= 0 ? &ctrl->item[k] : nullptr;
+    };
+    auto give_back = [&]() {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctrl->item_empty[taken % kItems]);
+        ++taken;
+    };
+    const int group = p.Hq / p.Hkv;
+
+    if (warp == 10) {
+        // ------------------------------------------------------------ scheduler
+        // Item k of all, in descending order of key tiles, goes to CTA k mod the
+        // grid in even rounds and from the other end in odd ones.
+        PFinder f;
+        f.init(p, lane);
+        const int64_t G = gridDim.x;
+        for (int64_t r = 0;; ++r) {
+            const int k = static_cast<int>(r % kItems);
+            if (r >= kItems &&
+                !__all_sync(0xffffffffu, mbar_wait(&ctrl->item_empty[k], static_cast<uint32_t>(r / kItems - 1) & 1, abort))) {
+                ok = false;
+                break;
+            }
+            const int64_t idx = r * G + (r & 1 ? G - 1 - blockIdx.x : blockIdx.x);
+            int b = 0, qt = 0;
+            PItem it = {-1, 0, 0, 0, 0, 0, 0, 0};
+            const bool any = f.find(p, idx / p.Hq, lane, b, qt);
+            if (any) {
+                const int2 sq = p_span(p.cu_q, b, p.total_q), sk = p_span(p.cu_k, b, p.total_k);
+                it.h = static_cast<int>(idx % p.Hq);
+                it.q_row = sq.x;
+                it.k_row = sk.x;
+                it.q_len = sq.y;
+                it.k_len = sk.y;
+                it.t0 = qt * 2 * kQT;
+                auto tiles = [&](int t) {
+                    const int rows = min(kQT, sq.y - t);
+                    return rows > 0 ? (p_seen(p.causal, sq.y, sk.y, t + rows - 1) + kKT - 1) / kKT : 0;
+                };
+                it.n0 = tiles(it.t0);
+                it.n1 = tiles(it.t0 + kQT);
+            }
             if (lane == 0) {
-                // ---------------------------------------------------- loader
-                uint32_t u = 0;
-                bool ok = true;
-                auto load_q = [&](int i) {
-                    if (n[i] == 0) return;
+                ctrl->item[k] = it;
+                mbar_arrive(&ctrl->item_full[k]);
+            }
+            // a round may be past the end at this end of the grid and not at the
+            // other: all later ones are past it
+            if (!any) break;
+        }
+        if (!ok && lane == 0) p_fail(p, ctrl);
+    } else if (warp == 9) {
+        // --------------------------------------------------------------- loader
+        uint32_t u = 0;         // blocks loaded
+        int nq[2] = {0, 0};     // items whose tile i was loaded
+        while (const PItem* item = take()) {
+            const PItem it = *item;
+            const int hk = it.h / group, nk = max(it.n0, it.n1);
+            if (lane == 0) {
+                auto load_q = [&](int i, int n) {
+                    if (n == 0 || !ok) return;
+                    if (nq[i] > 0 && !mbar_wait(&ctrl->q_empty[i], (nq[i] - 1) & 1, abort)) {
+                        ok = false;
+                        return;
+                    }
                     mbar_arrive_expect_tx(&ctrl->q_full[i], 3 * kBlkP);
                     for (int c = 0; c < 3; ++c)
-                        tma_load_3d(qs + (i * 3 + c) * kBlkP, &maps.q, &ctrl->q_full[i], 64 * c, h, sq.x + t0 + i * kQT);
+                        tma_load_3d(qs + (i * 3 + c) * kBlkP, &maps.q, &ctrl->q_full[i], 64 * c, it.h,
+                                    it.q_row + it.t0 + i * kQT);
+                    ++nq[i];
                 };
-                load_q(0);
+                load_q(0, it.n0);
                 for (int j = 0; j < nk && ok; ++j) {
                     for (int x = 0; x < 5; ++x, ++u) {
                         const uint32_t slot = u % kSlots;
@@ -238,126 +332,152 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                         }
                         mbar_arrive_expect_tx(&ctrl->blk_full[slot], kBlkP);
                         uint8_t* dst = ring + slot * kBlkP;
-                        const int kr = sk.x + j * kKT;
+                        const int kr = it.k_row + j * kKT;
                         if (x < 2) tma_load_3d(dst, &maps.k_nope, &ctrl->blk_full[slot], 64 * x, hk, kr);
                         else if (x == 2) tma_load_3d(dst, &maps.k_pe, &ctrl->blk_full[slot], 0, 0, kr);
                         else tma_load_3d(dst, &maps.v, &ctrl->blk_full[slot], 64 * (x - 3), hk, kr);
-                        if (u == 2) load_q(1);
+                        if (j == 0 && x == 2) load_q(1, it.n1);
                     }
-                }
-                if (!ok) {
-                    p_fail(p, ctrl);
-                    // no copy may arrive after the CTA is gone
-                    volatile int never = 0;
-                    for (uint32_t v = u < kSlots ? 0 : u - kSlots; v < u; ++v)
-                        mbar_wait(&ctrl->blk_full[v % kSlots], (v / kSlots) & 1, &never);
-                    for (int i = 0; i < 2; ++i)
-                        if (n[i]) mbar_wait(&ctrl->q_full[i], 0, &never);
                 }
             }
-        } else if (warp == 8) {
-            // ---------------------------------------------------- MMA issuer
-            // The whole warp walks the loop and one lane issues: descriptors are
-            // then warp-uniform values, which the instruction takes from uniform
-            // registers (formed by a single lane they cost a move each per product).
-            const bool leader = elect_lane();
-            const uint32_t idS = idesc_bf16(128, 128, false, false), idPV = idesc_bf16(128, 128, false, true),
-                           idPVh = idesc_bf16(128, 64, false, true);
-            const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-            const int n0 = __shfl_sync(0xffffffffu, n[0], 0), n1 = __shfl_sync(0xffffffffu, n[1], 0);
-            const uint64_t dQ = smem_desc(smem_u32(qs), 16, 1024, kSw128);
-            const uint64_t dK = smem_desc(smem_u32(ring), 16, 1024, kSw128);
-            const uint64_t dV = smem_desc(smem_u32(ring), kBlkP, 1024, kSw128);
-            constexpr uint32_t kBlkD = kBlkP >> 4;
-            bool ok = true;
-            auto wait_blk = [&](uint32_t u) {
-                if (ok && !mbar_wait(&ctrl->blk_full[u % kSlots], (u / kSlots) & 1, abort)) ok = false;
-            };
-            auto scores = [&](int i, int j) {
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+            if (!ok) break;
+            give_back();
+        }
+        if (!ok && lane == 0) {
+            p_fail(p, ctrl);
+            // no copy may arrive after the CTA is gone
+            volatile int never = 0;
+            for (uint32_t v = u < kSlots ? 0 : u - kSlots; v < u; ++v)
+                mbar_wait(&ctrl->blk_full[v % kSlots], (v / kSlots) & 1, &never);
+            for (int i = 0; i < 2; ++i)
+                if (nq[i]) mbar_wait(&ctrl->q_full[i], (nq[i] - 1) & 1, &never);
+        }
+    } else if (warp == 8) {
+        // ----------------------------------------------------------- MMA issuer
+        // The whole warp walks the loop and one lane issues: descriptors are then
+        // warp-uniform values, which the instruction takes from uniform registers
+        // (formed by a single lane they cost a move each per product: 4.6 against
+        // 3.4 ms for a causal prompt of 32,768 tokens and 16 heads).
+        const bool leader = elect_lane();
+        const uint32_t idS = idesc_bf16(128, 128, false, false), idPV = idesc_bf16(128, 128, false, true),
+                       idPVh = idesc_bf16(128, 64, false, true);
+        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+        const uint64_t dQ = smem_desc(smem_u32(qs), 16, 1024, kSw128);
+        const uint64_t dK = smem_desc(smem_u32(ring), 16, 1024, kSw128);
+        const uint64_t dV = smem_desc(smem_u32(ring), kBlkP, 1024, kSw128);
+        constexpr uint32_t kBlkD = kBlkP >> 4;
+        uint32_t u0 = 0;                 // the item's first block
+        uint32_t nq0 = 0, nq1 = 0;       // items with a tile 0, 1
+        uint32_t np0 = 0, np1 = 0;       // probabilities taken of each
+        int n0 = 0, n1 = 0;              // the item's key tiles
+        auto wait_blk = [&](uint32_t u) {
+            if (ok && !mbar_wait(&ctrl->blk_full[u % kSlots], (u / kSlots) & 1, abort)) ok = false;
+        };
+        auto scores = [&](int i, int j, int ni) {
 #pragma unroll
-                for (int c = 0; c < 3; ++c) {
-                    const uint32_t u = 5 * j + c;
-                    wait_blk(u);
-                    if (!ok) return;
-                    tc_fence_after();
-                    const uint64_t da = dQ + (i * 3 + c) * kBlkD, db = dK + (u % kSlots) * kBlkD;
-                    if (leader) {
-#pragma unroll
-                        for (int kk = 0; kk < 4; ++kk) umma_bf16(tm + i * 128, da + 2 * kk, db + 2 * kk, idS, (c | kk) != 0);
-                    }
-                }
-                if (leader) {
-                    umma_commit(&ctrl->s_full[i]);
-                    if (i == 1 || j >= n1)
-                        for (int c = 0; c < 3; ++c) umma_commit(&ctrl->blk_empty[(5 * j + c) % kSlots]);
-                }
-            };
-            auto values = [&](int i, int j) {
-                const uint32_t u = 5 * j + 3;
+            for (int c = 0; c < 3; ++c) {
+                const uint32_t u = u0 + 5 * j + c;
                 wait_blk(u);
-                wait_blk(u + 1);
                 if (!ok) return;
                 tc_fence_after();
-                const uint32_t s0 = u % kSlots, s1 = (u + 1) % kSlots;
-                const uint64_t d0 = dV + s0 * kBlkD, d1 = dV + s1 * kBlkD;
-                const uint32_t tO = tm + 256 + i * 128, tP = tm + i * 128;
+                const uint64_t da = dQ + (i * 3 + c) * kBlkD, db = dK + (u % kSlots) * kBlkD;
                 if (leader) {
-                    if (s1 == s0 + 1) {
 #pragma unroll
-                        for (int kk = 0; kk < 8; ++kk)
-                            umma_bf16_ta(tO, tP + 8 * kk, d0 + kk * (2048 >> 4), idPV, (j | kk) != 0);
-                    } else {  // the two blocks are the ring's last and first
+                    for (int kk = 0; kk < 4; ++kk) umma_bf16(tm + i * 128, da + 2 * kk, db + 2 * kk, idS, (c | kk) != 0);
+                }
+            }
+            if (leader) {
+                umma_commit(&ctrl->s_full[i]);
+                if (j + 1 == ni) umma_commit(&ctrl->q_empty[i]);
+                if (i == 1 || j >= n1)
+                    for (int c = 0; c < 3; ++c) umma_commit(&ctrl->blk_empty[(u0 + 5 * j + c) % kSlots]);
+            }
+        };
+        auto values = [&](int i, int j) {
+            const uint32_t u = u0 + 5 * j + 3;
+            wait_blk(u);
+            wait_blk(u + 1);
+            if (!ok) return;
+            tc_fence_after();
+            const uint32_t s0 = u % kSlots, s1 = (u + 1) % kSlots;
+            const uint64_t d0 = dV + s0 * kBlkD, d1 = dV + s1 * kBlkD;
+            const uint32_t tO = tm + 256 + i * 128, tP = tm + i * 128;
+            if (leader) {
+                if (s1 == s0 + 1) {
 #pragma unroll
-                        for (int kk = 0; kk < 8; ++kk) {
-                            umma_bf16_ta(tO, tP + 8 * kk, d0 + kk * (2048 >> 4), idPVh, (j | kk) != 0);
-                            umma_bf16_ta(tO + 64, tP + 8 * kk, d1 + kk * (2048 >> 4), idPVh, (j | kk) != 0);
-                        }
-                    }
-                    if (i == 1 || j >= n1) {
-                        umma_commit(&ctrl->blk_empty[s0]);
-                        umma_commit(&ctrl->blk_empty[s1]);
+                    for (int kk = 0; kk < 8; ++kk)
+                        umma_bf16_ta(tO, tP + 8 * kk, d0 + kk * (2048 >> 4), idPV, (j | kk) != 0);
+                } else {  // the two blocks are the ring's last and first
+#pragma unroll
+                    for (int kk = 0; kk < 8; ++kk) {
+                        umma_bf16_ta(tO, tP + 8 * kk, d0 + kk * (2048 >> 4), idPVh, (j | kk) != 0);
+                        umma_bf16_ta(tO + 64, tP + 8 * kk, d1 + kk * (2048 >> 4), idPVh, (j | kk) != 0);
                     }
                 }
-            };
-            auto step = [&](int i, int j, int ni) {  // P_i(j) V, then the scores of the next key tile
-                if (!ok || j >= ni) return;
-                if (!mbar_wait(&ctrl->p_full[i], j & 1, abort)) {
-                    ok = false;
-                    return;
+                if (i == 1 || j >= n1) {
+                    umma_commit(&ctrl->blk_empty[s0]);
+                    umma_commit(&ctrl->blk_empty[s1]);
                 }
-                tc_fence_after();
-                values(i, j);
-                if (!ok) return;
-                // in order behind the product that reads P_i from the same columns
-                if (j + 1 < ni) scores(i, j + 1);
-                else if (leader) umma_commit(&ctrl->o_full[i]);
-            };
-            if (n0 && !mbar_wait(&ctrl->q_full[0], 0, abort)) ok = false;
-            if (ok && n0) scores(0, 0);
-            if (ok && n1 && !mbar_wait(&ctrl->q_full[1], 0, abort)) ok = false;
-            if (ok && n1) scores(1, 0);
-            const int most = max(n0, n1);
-            for (int j = 0; j < most && ok; ++j) {
-                step(0, j, n0);
-                step(1, j, n1);
+            }
+        };
+        auto step = [&](int i, int j, int ni, uint32_t& np) {  // P_i(j) V, then the scores of the next key tile
+            if (!ok || j >= ni) return;
+            // (the item's first P_i comes after the last one's O_i was read)
+            if (!mbar_wait(&ctrl->p_full[i], np & 1, abort)) {
+                ok = false;
+                return;
+            }
+            ++np;
+            tc_fence_after();
+            values(i, j);
+            if (!ok) return;
+            // in order behind the product that reads P_i from the same columns
+            if (j + 1 < ni) scores(i, j + 1, ni);
+            else if (leader) umma_commit(&ctrl->o_full[i]);
+        };
+        auto start = [&](int i, int ni, uint32_t& nq) {
+            if (!ok || ni == 0) return;
+            if (!mbar_wait(&ctrl->q_full[i], nq & 1, abort)) {
+                ok = false;
+                return;
+            }
+            ++nq;
+            scores(i, 0, ni);
+        };
+        while (const PItem* item = take()) {
+            n0 = __shfl_sync(0xffffffffu, item->n0, 0);
+            n1 = __shfl_sync(0xffffffffu, item->n1, 0);
+            const int nk = max(n0, n1);
+            start(0, n0, nq0);
+            start(1, n1, nq1);
+            for (int j = 0; j < nk && ok; ++j) {
+                step(0, j, n0, np0);
+                step(1, j, n1, np1);
             }
             ok = __all_sync(0xffffffffu, ok);
-            if (leader) {
-                if (!ok) p_fail(p, ctrl);
-                drain_mma(&ctrl->fin);
-            }
-        } else {
-            // ------------------------------------------------------- softmax
-            const int i = warp >> 2;
-            const int row = (warp & 3) * 32 + lane, t = t0 + i * kQT + row;
-            const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-            const uint32_t tS = tmem + i * 128 + lanes, tO = tmem + 256 + i * 128 + lanes;
-            const int vis = seen(t);  // keys 0 .. vis - 1
-            float m = -INFINITY, l = 0.f;  // m in log2 units
-            bool ok = true;
-            const uint64_t c2 = pack2(p.scale_log2, p.scale_log2);
-            for (int j = 0; j < n[i] && ok; ++j) {
-                if (!__all_sync(0xffffffffu, mbar_wait(&ctrl->s_full[i], j & 1, abort))) {
+            if (!ok) break;
+            u0 += 5 * nk;
+            give_back();
+        }
+        if (leader) {
+            if (!ok) p_fail(p, ctrl);
+            drain_mma(&ctrl->fin);
+        }
+    } else {
+        // -------------------------------------------------------------- softmax
+        const int i = warp >> 2;
+        const int row = i * kQT + (warp & 3) * 32 + lane;
+        const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const uint32_t tS = tmem + i * 128 + lanes, tO = tmem + 256 + i * 128 + lanes;
+        const uint64_t c2 = pack2(p.scale_log2, p.scale_log2);
+        uint32_t ns = 0, no = 0;  // score tiles and outputs taken
+        while (const PItem* item = take()) {
+            const int n = i == 0 ? item->n0 : item->n1;
+            const int vis = p_seen(p.causal, item->q_len, item->k_len, item->t0 + row);  // keys 0 .. vis - 1
+            float m = -INFINITY, l = 0.f;                             // m in log2 units
+            for (int j = 0; j < n && ok; ++j, ++ns) {
+                if (!__all_sync(0xffffffffu, mbar_wait(&ctrl->s_full[i], ns & 1, abort))) {
                     ok = false;
                     break;
                 }
@@ -420,54 +540,61 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                 if (lane == 0) mbar_arrive(&ctrl->p_full[i]);
             }
             // ------------------------------------------------------ epilogue
-            if (ok && n[i] > 0 && !__all_sync(0xffffffffu, mbar_wait(&ctrl->o_full[i], 0, abort))) ok = false;
-            if (!ok && lane == 0) p_fail(p, ctrl);
-            if (ok) {
-                tc_fence_after();
-                const bool mine = t < sq.y;
-                const int64_t qrow = sq.x + t;
-                const float inv = l > 0.f ? 1.f / l : l;  // l = 0: nothing seen; NaN: the row is NaN
-                __nv_bfloat16* o = p.out + (qrow * p.Hq + h) * kDv;
-                bool fine = true;
+            if (ok && n > 0) {
+                if (!__all_sync(0xffffffffu, mbar_wait(&ctrl->o_full[i], no & 1, abort))) ok = false;
+                ++no;
+            }
+            if (!ok) break;
+            tc_fence_after();
+            const int t = item->t0 + row, h = item->h;
+            const bool mine = t < item->q_len;
+            const int64_t at = (static_cast<int64_t>(item->q_row) + t) * p.Hq + h;
+            const float inv = l > 0.f ? 1.f / l : l;  // l = 0: nothing seen; NaN: the row is NaN
+            __nv_bfloat16* o = p.out + at * kDv;
+            bool fine = true;
 #pragma unroll
-                for (int c = 0; c < 128; c += 32) {
-                    uint32_t v[32];
-                    if (n[i] > 0) {
-                        tmem_ld_x32(tO + c, v);
-                    } else {
+            for (int c = 0; c < 128; c += 32) {
+                uint32_t v[32];
+                if (n > 0) {
+                    tmem_ld_x32(tO + c, v);
+                } else {
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) v[k] = 0u;
-                    }
-                    if (vis <= 0) {  // sees nothing, beside rows that do
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) v[k] = 0u;
-                    }
-#pragma unroll
-                    for (int k = 0; k < 32; k += 8) {
-                        float f[8];
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            f[e] = __uint_as_float(v[k + e]) * inv;
-                            fine = fine && fabsf(f[e]) <= 3.0e38f;
-                        }
-                        if (mine)
-                            *reinterpret_cast<uint4*>(o + c + k) =
-                                make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                                           pack_bf16x2(f[6], f[7]));
-                    }
+                    for (int k = 0; k < 32; ++k) v[k] = 0u;
                 }
-                if (mine) p.lse[qrow * p.Hq + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
-                // rows to form again: O is not finite though the sums are
-                unsigned again = __ballot_sync(0xffffffffu, mine && !fine && l > 0.f && l < INFINITY && fabsf(m) < INFINITY);
-                while (again) {
-                    const int r = __ffs(again) - 1;
-                    again &= again - 1;
-                    __syncwarp();
-                    p_row_again(p, __shfl_sync(0xffffffffu, qrow, r), h, hk, sk.x, __shfl_sync(0xffffffffu, vis, r),
-                                __shfl_sync(0xffffffffu, m, r), __shfl_sync(0xffffffffu, inv, r), lane);
+                if (vis <= 0) {  // sees nothing, beside rows that do
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) v[k] = 0u;
+                }
+#pragma unroll
+                for (int k = 0; k < 32; k += 8) {
+                    float f[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        f[e] = __uint_as_float(v[k + e]) * inv;
+                        fine = fine && fabsf(f[e]) <= 3.0e38f;
+                    }
+                    if (mine)
+                        *reinterpret_cast<uint4*>(o + c + k) =
+                            make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                                       pack_bf16x2(f[6], f[7]));
                 }
             }
+            if (mine) p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
+            // rows to form again: O is not finite though the sums are
+            unsigned again = __ballot_sync(0xffffffffu, mine && !fine && l > 0.f && l < INFINITY && fabsf(m) < INFINITY);
+            while (again) {
+                const int r = __ffs(again) - 1;
+                again &= again - 1;
+                __syncwarp();
+                p_row_again(p, item->q_row + __shfl_sync(0xffffffffu, t, r), h, h / group, item->k_row,
+                            __shfl_sync(0xffffffffu, vis, r), __shfl_sync(0xffffffffu, m, r),
+                            __shfl_sync(0xffffffffu, inv, r), lane);
+            }
+            // O_i has been read before this warp's next P_i is handed over
+            tc_fence_before();
+            give_back();
         }
+        if (!ok && lane == 0) p_fail(p, ctrl);
     }
     tc_fence_before();
     __syncthreads();
@@ -479,12 +606,12 @@ __global__ void __launch_bounds__(kThreadsP, 1)
 
 }  // namespace
 
-cudaError_t launch_prefill(const PrefillMaps& maps, const PrefillParams& p, cudaStream_t stream) {
-    // sum of ceil(len / 256) <= total / 256 + B
-    const int64_t pairs = static_cast<int64_t>(p.total_q) / (2 * kQT) + p.B;
+cudaError_t launch_prefill(const PrefillMaps& maps, const PrefillParams& p, int sms, cudaStream_t stream) {
+    // items: sum of ceil(len / 256) <= total / 256 + B pairs of tiles, for every head
+    const int64_t items = (static_cast<int64_t>(p.total_q) / (2 * kQT) + p.B) * p.Hq;
     cudaError_t e = cudaFuncSetAttribute(prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemP);
     if (e != cudaSuccess) return e;
-    prefill_kernel<<<dim3(static_cast<unsigned>(pairs * p.Hq)), kThreadsP, kSmemP, stream>>>(maps, p);
+    prefill_kernel<<<dim3(static_cast<unsigned>(items < sms ? items : sms)), kThreadsP, kSmemP, stream>>>(maps, p);
     return cudaGetLastError();
 }
 
