@@ -449,7 +449,8 @@ int mla_prefill(const void* q, int64_t q_stride_t, int64_t q_stride_h, const voi
         if (strides[i] >= (1LL << 38)) return MLA_ERR_UNSUPPORTED;  // TMA strides are below 2^40 bytes
     // TMA coordinates are 32-bit, and a tile may pass the last row
     if (total_q > INT32_MAX - 1024 || total_k > INT32_MAX - 1024) return MLA_ERR_UNSUPPORTED;
-    if ((total_q / 256 + B) * Hq > INT32_MAX) return MLA_ERR_UNSUPPORTED;  // grid size
+    const int pack = mla::prefill_pack(Hq / Hkv);
+    if ((total_q / (2 * (128 / pack)) + B) * (Hq / pack) > INT32_MAX) return MLA_ERR_UNSUPPORTED;  // grid size
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return MLA_ERR_CUDA;
     const DevInfo di = dev_info(dev);
@@ -475,6 +476,8 @@ int mla_prefill(const void* q, int64_t q_stride_t, int64_t q_stride_h, const voi
     p.total_k = static_cast<int>(total_k);
     p.Hq = Hq;
     p.Hkv = Hkv;
+    p.pack = pack;
+    p.tile_tokens = 128 / pack;
     p.causal = causal != 0;
     p.scale_log2 = scale * 1.4426950408889634f;
     p.out = static_cast<__nv_bfloat16*>(out);
@@ -484,23 +487,25 @@ int mla_prefill(const void* q, int64_t q_stride_t, int64_t q_stride_h, const voi
     if (!enc) return MLA_ERR_CUDA;
     mla::PrefillMaps maps;
     std::memset(&maps, 0, sizeof(maps));
-    auto map = [&](CUtensorMap* m, const void* base, int width, int heads, int64_t tokens, int64_t sh, int64_t st) {
+    auto map = [&](CUtensorMap* m, const void* base, int width, int heads, int64_t tokens, int64_t sh, int64_t st,
+                   int box_heads = 1) {
         cuuint64_t gdim[3] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(heads),
                               static_cast<cuuint64_t>(tokens)};
         cuuint64_t gstride[2] = {static_cast<cuuint64_t>(sh) * 2, static_cast<cuuint64_t>(st) * 2};
-        cuuint32_t box[3] = {64u, 1u, 128u}, estride[3] = {1u, 1u, 1u};
+        cuuint32_t box[3] = {64u, static_cast<cuuint32_t>(box_heads), static_cast<cuuint32_t>(128 / box_heads)},
+                   estride[3] = {1u, 1u, 1u};
         return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), gdim, gstride, box, estride,
                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
     };
     // without keys no block is loaded: the maps then describe q's first row
     const bool keys = total_k > 0;
-    if (!map(&maps.q, q, 192, Hq, total_q, q_stride_h, q_stride_t) ||
+    if (!map(&maps.q, q, 192, Hq, total_q, q_stride_h, q_stride_t, pack) ||
         !map(&maps.k_nope, keys ? k_nope : q, 128, keys ? Hkv : 1, keys ? total_k : 1, k_stride_h, k_stride_t) ||
         !map(&maps.k_pe, keys ? k_pe : q, 64, 1, keys ? total_k : 1, k_pe_stride, k_pe_stride) ||
         !map(&maps.v, keys ? v : q, 128, keys ? Hkv : 1, keys ? total_k : 1, v_stride_h, v_stride_t))
         return MLA_ERR_CUDA;
-    const cudaError_t e = mla::launch_prefill(maps, p, di.sms, static_cast<cudaStream_t>(stream));
+    const cudaError_t e = mla::launch_prefill(maps, p, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 

@@ -155,16 +155,20 @@ struct PrefillParams {
     const int32_t* cu_q;
     const int32_t* cu_k;
     int B, total_q, total_k, Hq, Hkv;
+    int pack;          // query heads that share a tile (prefill_pack)
+    int tile_tokens;   // tokens of a tile: 128 / pack
     int causal;
     float scale_log2;  // softmax scale * log2(e)
     __nv_bfloat16* out;
     float* lse;
     int* status;
 };
-// 64-value blocks of 128 tokens of one head (128-B swizzle).
+// 64-value blocks (128-B swizzle): q of tile_tokens tokens of pack heads, the
+// others of 128 tokens of one head.
 struct PrefillMaps {
     CUtensorMap q, k_nope, k_pe, v;
 };
-cudaError_t launch_prefill(const PrefillMaps& maps, const PrefillParams& p, int sms, cudaStream_t stream);
+int prefill_pack(int group);
+cudaError_t launch_prefill(const PrefillMaps& maps, const PrefillParams& p, cudaStream_t stream);
 
 }  // namespace mla

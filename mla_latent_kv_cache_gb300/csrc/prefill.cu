@@ -12,16 +12,19 @@
 // them unrounded in fp32.
 //
 // Bound: the tensor cores. 640 flop per query, key and head against 2 (192 +
-// 128) bytes per key and head shared by 256 queries: far past the ridge for
-// prompts. A CTA takes 256 queries of one head as two tiles of 128 rows, each
-// with its own warpgroup of softmax threads, so that one tile's products run
-// while the other's probabilities are formed:
+// 128) bytes per key and head shared by 256 rows: far past the ridge for
+// prompts. An item is two tiles of 128 rows, each with its own warpgroup of
+// softmax threads, so that one tile's products run while the other's
+// probabilities are formed. The query heads that share a key head lie in one
+// tile (row = token x heads + head), which fills tiles for short sequences, wastes
+// less of the causal diagonal and reads the keys once for all of them:
 //   S_i = Q_i K^T   128 x 128 x 192, Q and K from shared memory, into TMEM
 //   P_i             thread = row: no exchange between threads; bf16, written
 //                   over S_i in TMEM, where it is the next product's A operand
 //   O_i += P_i V    128 x 128 x 128, into TMEM
-// A CTA per SM goes through its share of these items (a scheduler warp finds
-// them, the longest first): the next item's Q, keys and scores are on their way
+// The grid has a CTA for every item, longest first; a running CTA takes over
+// pending ones (cluster launch control) until there are none, so that SMs share
+// the items evenly, and the next item's Q, keys and scores are on their way
 // while the last one's output is written.
 // TMEM: S_0, S_1, O_0, O_1 of 128 columns each = all 512. Shared memory: Q
 // 96 KB, and a ring of eight 16-KB blocks (64 dims of 128 tokens) through which
@@ -51,8 +54,9 @@ constexpr int kQBytesP = 2 * 3 * kBlkP;
 constexpr int kSmemP = 1024 + 1024 + kQBytesP + kSlots * kBlkP;
 constexpr float kRaise = 8.f;             // log2 units
 
-// 256 queries of one head: query rows q_row .. of a sequence of q_len and k_len
-// tokens, from its query t0 on, and the key tiles that each half sees.
+// Two tiles of queries of heads h .. h + pack - 1: query rows q_row .. of a
+// sequence of q_len and k_len tokens, from its query t0 on, and the key tiles
+// that each tile sees.
 struct PItem {
     int h, q_row, k_row, q_len, k_len, t0, n0, n1;
 };
@@ -60,10 +64,11 @@ struct PItem {
 struct PCtrl {
     uint64_t q_full[2], q_empty[2], blk_full[kSlots], blk_empty[kSlots];
     uint64_t s_full[2], p_full[2], o_full[2], fin;
-    uint64_t item_full[kItems], item_empty[kItems];
+    uint64_t item_full[kItems], item_empty[kItems], more_full;
     uint32_t tmem_base;
     int abort;
     PItem item[kItems];  // h < 0: no more
+    alignas(16) uint4 more;  // what a request for a pending CTA answered
 };
 static_assert(sizeof(PCtrl) <= 1024, "control block");
 
@@ -111,51 +116,105 @@ __device__ __forceinline__ int p_seen(int causal, int q_len, int k_len, int t) {
     return causal ? min(k_len, max(0, k_len - q_len + t + 1)) : k_len;
 }
 
-// Finds pairs of query tiles by their number, the last pairs of all sequences
-// (which see the most keys) first; used by a whole warp.
+// Finds pairs of query tiles by their number in descending order of the key
+// tiles that they see; used by a whole warp.
 struct PFinder {
-    int mine, top;  // lane's pairs of the first 32 sequences; the most that a sequence has
-    __device__ __forceinline__ int pairs(const PrefillParams& p, int i) const {
-        return i < p.B ? (p_span(p.cu_q, i, p.total_q).y + 2 * kQT - 1) / (2 * kQT) : 0;
-    }
-    __device__ __forceinline__ int of(const PrefillParams& p, int base, int lane) const {
-        return base == 0 ? mine : pairs(p, base + lane);
+    int lq, lk, top;  // lane's lengths of the first 32 sequences; the most key tiles of any
+    int tokens;       // of a pair
+    __device__ __forceinline__ void lens(const PrefillParams& p, int i, int lane, int& q, int& k) const {
+        if (i < 32) {
+            q = lq;
+            k = lk;
+        } else {
+            q = i + lane < p.B ? p_span(p.cu_q, i + lane, p.total_q).y : 0;
+            k = i + lane < p.B ? p_span(p.cu_k, i + lane, p.total_k).y : 0;
+        }
     }
     __device__ __forceinline__ void init(const PrefillParams& p, int lane) {
-        mine = pairs(p, lane);
+        tokens = 2 * p.tile_tokens;
+        lq = lane < p.B ? p_span(p.cu_q, lane, p.total_q).y : 0;
+        lk = lane < p.B ? p_span(p.cu_k, lane, p.total_k).y : 0;
         top = 0;
-        for (int base = 0; base < p.B; base += 32) top = max(top, of(p, base, lane));
+        for (int i = 0; i < p.B; i += 32) {
+            int q, k;
+            lens(p, i, lane, q, k);
+            top = max(top, q > 0 ? (k + kKT - 1) / kKT : 0);
+        }
         top = __reduce_max_sync(0xffffffffu, top);
     }
-    __device__ __forceinline__ int64_t from(const PrefillParams& p, int q, int lane) const {  // pairs with index >= q
+    // Pairs of a sequence that see at least x key tiles: the last ones, and the
+    // very last sees all keys.
+    __device__ __forceinline__ int count(const PrefillParams& p, int q, int k, int x) const {
+        const int pairs = (q + tokens - 1) / tokens;
+        if (x == 0 || pairs == 0) return pairs;
+        if (x > (k + kKT - 1) / kKT) return 0;
+        if (!p.causal) return pairs;
+        const int64_t y = static_cast<int64_t>(x - 1) * kKT - (k - q);  // a pair ends past y
+        return y < 0 ? pairs : max(1, pairs - static_cast<int>(min(y / tokens, static_cast<int64_t>(pairs))));
+    }
+    __device__ __forceinline__ int64_t from(const PrefillParams& p, int x, int lane) const {
         int64_t n = 0;
-        for (int base = 0; base < p.B; base += 32) n += __reduce_add_sync(0xffffffffu, max(0, of(p, base, lane) - q));
+        for (int i = 0; i < p.B; i += 32) {
+            int q, k;
+            lens(p, i, lane, q, k);
+            n += __reduce_add_sync(0xffffffffu, count(p, q, k, x));
+        }
         return n;
     }
     // Sequence b and pair qt of the s-th; false if there are fewer.
     __device__ __forceinline__ bool find(const PrefillParams& p, int64_t s, int lane, int& b, int& qt) const {
         if (from(p, 0, lane) <= s) return false;
-        int lo = 0, hi = top;  // from(lo) > s, from(hi) = 0
+        int lo = 0, hi = top + 1;  // from(lo) > s, from(hi) = 0
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
             if (from(p, mid, lane) > s) lo = mid;
             else hi = mid;
         }
-        int64_t r = s - from(p, lo + 1, lane);
-        for (int base = 0; base < p.B; base += 32) {
-            unsigned m = __ballot_sync(0xffffffffu, of(p, base, lane) > lo);
-            const int n = __popc(m);
-            if (r < n) {
-                for (; r > 0; --r) m &= m - 1;
-                b = base + __ffs(m) - 1;
-                break;
+        int64_t r = s - from(p, lo + 1, lane);  // among the pairs that see exactly lo
+        for (int i = 0; i < p.B; i += 32) {
+            int q, k;
+            lens(p, i, lane, q, k);
+            const int all = count(p, q, k, lo), c = all - count(p, q, k, lo + 1);
+            int sum = c;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, sum, o);
+                if (lane >= o) sum += v;
             }
-            r -= n;
+            const unsigned hit = __ballot_sync(0xffffffffu, sum > r);
+            if (hit) {
+                const int L = __ffs(hit) - 1;
+                const int first = (q + tokens - 1) / tokens - all - (sum - c);
+                b = i + L;
+                qt = static_cast<int>(__shfl_sync(0xffffffffu, first, L) + r);
+                return true;
+            }
+            r -= __shfl_sync(0xffffffffu, sum, 31);
         }
-        qt = lo;
-        return true;
+        return false;
     }
 };
+
+// Asks for a pending CTA of this grid in this one's place; the answer lands at
+// `dst` (16 bytes) and completes on `bar`.
+__device__ __forceinline__ void ask_for_cta(uint4* dst, uint64_t* bar) {
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                     smem_u32(dst)),
+                 "r"(smem_u32(bar))
+                 : "memory");
+}
+// The block index that an answer gives, or -1 if none was pending.
+__device__ __forceinline__ int64_t answered_cta(const uint4* src) {
+    uint32_t got, x;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\tld.shared.b128 r, [%2];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\tselp.u32 %0, 1, 0, p;\n\tmov.u32 %1, 0;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n\t}"
+        : "=r"(got), "=r"(x)
+        : "r"(smem_u32(src))
+        : "memory");
+    return got ? static_cast<int64_t>(x) : -1;
+}
 
 // A row again from the keys that it sees alone, by its whole warp (V of a
 // visible key may be non-finite, and then so is the row): 32 keys at a time, a
@@ -227,6 +286,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
             mbar_init(&ctrl->item_full[i], 1);
             mbar_init(&ctrl->item_empty[i], 10);  // every warp but the scheduler
         }
+        mbar_init(&ctrl->more_full, 1);
         mbar_init(&ctrl->fin, 1);
         ctrl->abort = 0;
         fence_mbar_init();
@@ -262,46 +322,69 @@ __global__ void __launch_bounds__(kThreadsP, 1)
 
     if (warp == 10) {
         // ------------------------------------------------------------ scheduler
-        // Item k of all, in descending order of key tiles, goes to CTA k mod the
-        // grid in even rounds and from the other end in odd ones.
         PFinder f;
         f.init(p, lane);
-        const int64_t G = gridDim.x;
-        for (int64_t r = 0;; ++r) {
+        const int units = p.Hq / p.pack;  // head groups
+        int64_t idx = blockIdx.x;         // item: head group idx % units of pair idx / units
+        bool end = false;
+        uint32_t asked = 0;
+        // the next CTA's index in idx; at the end of the grid, end
+        auto next_cta = [&]() {
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&ctrl->more_full, 16);
+                ask_for_cta(&ctrl->more, &ctrl->more_full);
+            }
+            if (!__all_sync(0xffffffffu, mbar_wait(&ctrl->more_full, asked & 1, abort))) {
+                ok = false;
+                end = true;
+                return;
+            }
+            ++asked;
+            idx = answered_cta(&ctrl->more);
+            end = idx < 0;
+            fence_proxy_async_smem();  // read before the next answer is written
+            __syncwarp();
+        };
+        for (int64_t r = 0; ok; ++r) {
             const int k = static_cast<int>(r % kItems);
             if (r >= kItems &&
                 !__all_sync(0xffffffffu, mbar_wait(&ctrl->item_empty[k], static_cast<uint32_t>(r / kItems - 1) & 1, abort))) {
                 ok = false;
                 break;
             }
-            const int64_t idx = r * G + (r & 1 ? G - 1 - blockIdx.x : blockIdx.x);
             int b = 0, qt = 0;
             PItem it = {-1, 0, 0, 0, 0, 0, 0, 0};
-            const bool any = f.find(p, idx / p.Hq, lane, b, qt);
+            const bool any = !end && f.find(p, idx / units, lane, b, qt);
             if (any) {
                 const int2 sq = p_span(p.cu_q, b, p.total_q), sk = p_span(p.cu_k, b, p.total_k);
-                it.h = static_cast<int>(idx % p.Hq);
+                it.h = static_cast<int>(idx % units) * p.pack;
                 it.q_row = sq.x;
                 it.k_row = sk.x;
                 it.q_len = sq.y;
                 it.k_len = sk.y;
-                it.t0 = qt * 2 * kQT;
+                it.t0 = qt * 2 * p.tile_tokens;
                 auto tiles = [&](int t) {
-                    const int rows = min(kQT, sq.y - t);
-                    return rows > 0 ? (p_seen(p.causal, sq.y, sk.y, t + rows - 1) + kKT - 1) / kKT : 0;
+                    const int n = min(p.tile_tokens, sq.y - t);
+                    return n > 0 ? (p_seen(p.causal, sq.y, sk.y, t + n - 1) + kKT - 1) / kKT : 0;
                 };
                 it.n0 = tiles(it.t0);
-                it.n1 = tiles(it.t0 + kQT);
+                it.n1 = tiles(it.t0 + p.tile_tokens);
             }
             if (lane == 0) {
                 ctrl->item[k] = it;
                 mbar_arrive(&ctrl->item_full[k]);
             }
-            // a round may be past the end at this end of the grid and not at the
-            // other: all later ones are past it
             if (!any) break;
+            next_cta();
         }
-        if (!ok && lane == 0) p_fail(p, ctrl);
+        // past the last item the grid may hold CTAs that would find nothing
+        // (it is sized by a bound): taken here they need not start
+        while (ok && !end) next_cta();
+        if (!ok && lane == 0) {
+            p_fail(p, ctrl);
+            volatile int never = 0;
+            if (asked == 0 || !end) mbar_wait(&ctrl->more_full, asked & 1, &never);
+        }
     } else if (warp == 9) {
         // --------------------------------------------------------------- loader
         uint32_t u = 0;         // blocks loaded
@@ -316,10 +399,10 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                         ok = false;
                         return;
                     }
-                    mbar_arrive_expect_tx(&ctrl->q_full[i], 3 * kBlkP);
+                    mbar_arrive_expect_tx(&ctrl->q_full[i], 3 * p.pack * p.tile_tokens * 128);
                     for (int c = 0; c < 3; ++c)
                         tma_load_3d(qs + (i * 3 + c) * kBlkP, &maps.q, &ctrl->q_full[i], 64 * c, it.h,
-                                    it.q_row + it.t0 + i * kQT);
+                                    it.q_row + it.t0 + i * p.tile_tokens);
                     ++nq[i];
                 };
                 load_q(0, it.n0);
@@ -467,14 +550,17 @@ __global__ void __launch_bounds__(kThreadsP, 1)
     } else {
         // -------------------------------------------------------------- softmax
         const int i = warp >> 2;
-        const int row = i * kQT + (warp & 3) * 32 + lane;
+        // row of the tile: token row / pack, head row % pack (rows past the last token's are not used)
+        const int row = (warp & 3) * 32 + lane;
+        const int tok = i * p.tile_tokens + row / p.pack, head = row % p.pack;
+        const bool used = row < p.tile_tokens * p.pack;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t tS = tmem + i * 128 + lanes, tO = tmem + 256 + i * 128 + lanes;
         const uint64_t c2 = pack2(p.scale_log2, p.scale_log2);
         uint32_t ns = 0, no = 0;  // score tiles and outputs taken
         while (const PItem* item = take()) {
             const int n = i == 0 ? item->n0 : item->n1;
-            const int vis = p_seen(p.causal, item->q_len, item->k_len, item->t0 + row);  // keys 0 .. vis - 1
+            const int vis = p_seen(p.causal, item->q_len, item->k_len, item->t0 + tok);  // keys 0 .. vis - 1
             float m = -INFINITY, l = 0.f;                             // m in log2 units
             for (int j = 0; j < n && ok; ++j, ++ns) {
                 if (!__all_sync(0xffffffffu, mbar_wait(&ctrl->s_full[i], ns & 1, abort))) {
@@ -546,8 +632,8 @@ __global__ void __launch_bounds__(kThreadsP, 1)
             }
             if (!ok) break;
             tc_fence_after();
-            const int t = item->t0 + row, h = item->h;
-            const bool mine = t < item->q_len;
+            const int t = item->t0 + tok, h = item->h + head;
+            const bool mine = used && t < item->q_len;
             const int64_t at = (static_cast<int64_t>(item->q_row) + t) * p.Hq + h;
             const float inv = l > 0.f ? 1.f / l : l;  // l = 0: nothing seen; NaN: the row is NaN
             __nv_bfloat16* o = p.out + at * kDv;
@@ -586,7 +672,8 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                 const int r = __ffs(again) - 1;
                 again &= again - 1;
                 __syncwarp();
-                p_row_again(p, item->q_row + __shfl_sync(0xffffffffu, t, r), h, h / group, item->k_row,
+                const int hr = __shfl_sync(0xffffffffu, h, r);
+                p_row_again(p, item->q_row + __shfl_sync(0xffffffffu, t, r), hr, hr / group, item->k_row,
                             __shfl_sync(0xffffffffu, vis, r), __shfl_sync(0xffffffffu, m, r),
                             __shfl_sync(0xffffffffu, inv, r), lane);
             }
@@ -606,12 +693,20 @@ __global__ void __launch_bounds__(kThreadsP, 1)
 
 }  // namespace
 
-cudaError_t launch_prefill(const PrefillMaps& maps, const PrefillParams& p, int sms, cudaStream_t stream) {
-    // items: sum of ceil(len / 256) <= total / 256 + B pairs of tiles, for every head
-    const int64_t items = (static_cast<int64_t>(p.total_q) / (2 * kQT) + p.B) * p.Hq;
+// Query heads of a group that lie in one tile: the largest divisor of the group
+// whose whole tokens fill at least 124 of a tile's 128 rows.
+int prefill_pack(int group) {
+    for (int d = group < kQT ? group : kQT; d > 1; --d)
+        if (group % d == 0 && kQT / d * d >= 124) return d;
+    return 1;
+}
+
+cudaError_t launch_prefill(const PrefillMaps& maps, const PrefillParams& p, cudaStream_t stream) {
+    // items: sum of ceil(len / tokens) <= total / tokens + B pairs of tiles, for every head group
+    const int64_t items = (static_cast<int64_t>(p.total_q) / (2 * p.tile_tokens) + p.B) * (p.Hq / p.pack);
     cudaError_t e = cudaFuncSetAttribute(prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemP);
     if (e != cudaSuccess) return e;
-    prefill_kernel<<<dim3(static_cast<unsigned>(items < sms ? items : sms)), kThreadsP, kSmemP, stream>>>(maps, p);
+    prefill_kernel<<<dim3(static_cast<unsigned>(items)), kThreadsP, kSmemP, stream>>>(maps, p);
     return cudaGetLastError();
 }
 

@@ -119,6 +119,14 @@ def test_one_sequence(n):
     _check(_inputs([n], [n], 2, 2, seed=n))
 
 
+@pytest.mark.parametrize("Hq,Hkv", [(5, 1), (14, 2), (48, 1), (130, 1), (256, 2)])
+def test_group_sizes_that_do_not_divide_a_tile(Hq, Hkv):
+    # heads of a group share tiles of 128 rows: whole tokens of 5, 7, ... heads
+    q, k = [1, 40, 130, 0, 9], [1, 40, 150, 10, 300]
+    for causal in (True, False):
+        _check(_inputs(q, k, Hq, Hkv, seed=Hq), causal)
+
+
 def test_no_keys_at_all():
     a = _inputs([3, 300], [0, 0], 2, 1, seed=2)
     for causal in (True, False):
