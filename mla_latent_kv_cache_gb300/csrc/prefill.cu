@@ -49,7 +49,8 @@ constexpr int kBlkP = 128 * 128;          // a block: 64 dims of 128 tokens
 constexpr int kSlots = 8;
 constexpr int kDv = 128;
 constexpr int kThreadsP = 352;            // 8 softmax warps, the MMA issuer, the loader, the scheduler
-constexpr int kItems = 4;                 // items ahead of the slowest role
+constexpr int kItems = 4;                 // items between the scheduler and the slowest role
+constexpr int kAhead = 4;                 // key tiles before an item's last load at which the next is asked for
 constexpr int kQBytesP = 2 * 3 * kBlkP;
 constexpr int kSmemP = 1024 + 1024 + kQBytesP + kSlots * kBlkP;
 constexpr float kRaise = 8.f;             // log2 units
@@ -63,8 +64,8 @@ struct PItem {
 
 struct PCtrl {
     uint64_t q_full[2], q_empty[2], blk_full[kSlots], blk_empty[kSlots];
-    uint64_t s_full[2], p_full[2], o_full[2], fin;
-    uint64_t item_full[kItems], item_empty[kItems], more_full;
+    uint64_t s_full[2], p_half[2], p_full[2], o_full[2], fin;
+    uint64_t item_full[kItems], item_empty[kItems], more_full, want;
     uint32_t tmem_base;
     int abort;
     PItem item[kItems];  // h < 0: no more
@@ -98,6 +99,28 @@ __device__ __forceinline__ uint64_t pack2(float a, float b) {
 }
 __device__ __forceinline__ void unpack2(uint64_t d, float& a, float& b) {
     asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(d));
+}
+
+// 32 columns of TMEM on their way into r, which holds them after tmem_ld_end
+// (of every load begun before).
+__device__ __forceinline__ void tmem_ld_x32_begin(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,"
+                 "%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+                   "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+                   "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+                 : "r"(taddr)
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_ld_end(uint32_t (&r)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                   "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                   "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+                 :
+                 : "memory");
 }
 
 __device__ __forceinline__ void p_fail(const PrefillParams& p, PCtrl* c) {
@@ -149,8 +172,8 @@ struct PFinder {
         if (x == 0 || pairs == 0) return pairs;
         if (x > (k + kKT - 1) / kKT) return 0;
         if (!p.causal) return pairs;
-        const int64_t y = static_cast<int64_t>(x - 1) * kKT - (k - q);  // a pair ends past y
-        return y < 0 ? pairs : max(1, pairs - static_cast<int>(min(y / tokens, static_cast<int64_t>(pairs))));
+        const int y = (x - 1) * kKT - k + q;  // a pair ends past y; (x - 1) kKT < k, so y < q
+        return y < 0 ? pairs : max(1, pairs - y / tokens);
     }
     __device__ __forceinline__ int64_t from(const PrefillParams& p, int x, int lane) const {
         int64_t n = 0;
@@ -275,6 +298,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
             mbar_init(&ctrl->q_full[i], 1);
             mbar_init(&ctrl->q_empty[i], 1);
             mbar_init(&ctrl->s_full[i], 1);
+            mbar_init(&ctrl->p_half[i], 4);
             mbar_init(&ctrl->p_full[i], 4);
             mbar_init(&ctrl->o_full[i], 1);
         }
@@ -287,6 +311,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
             mbar_init(&ctrl->item_empty[i], 10);  // every warp but the scheduler
         }
         mbar_init(&ctrl->more_full, 1);
+        mbar_init(&ctrl->want, 1);
         mbar_init(&ctrl->fin, 1);
         ctrl->abort = 0;
         fence_mbar_init();
@@ -295,6 +320,33 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         tmem_alloc(&ctrl->tmem_base, 512);
         tmem_relinquish();
         tc_fence_before();
+    }
+    const int units = p.Hq / p.pack;  // head groups
+    int64_t idx = blockIdx.x;         // item: head group idx % units of pair idx / units
+    PFinder f;
+    PItem next = {-1, 0, 0, 0, 0, 0, 0, 0};
+    // item idx in `next` (h < 0: there is none), by the scheduler's whole warp
+    auto look_up = [&]() {
+        int b = 0, qt = 0;
+        next.h = -1;
+        if (!f.find(p, idx / units, lane, b, qt)) return;
+        const int2 sq = p_span(p.cu_q, b, p.total_q), sk = p_span(p.cu_k, b, p.total_k);
+        next.h = static_cast<int>(idx % units) * p.pack;
+        next.q_row = sq.x;
+        next.k_row = sk.x;
+        next.q_len = sq.y;
+        next.k_len = sk.y;
+        next.t0 = qt * 2 * p.tile_tokens;
+        auto tiles = [&](int t) {
+            const int n = min(p.tile_tokens, sq.y - t);
+            return n > 0 ? (p_seen(p.causal, sq.y, sk.y, t + n - 1) + kKT - 1) / kKT : 0;
+        };
+        next.n0 = tiles(next.t0);
+        next.n1 = tiles(next.t0 + p.tile_tokens);
+    };
+    if (warp == 10) {
+        f.init(p, lane);
+        look_up();
     }
     __syncthreads();
     tc_fence_after();
@@ -322,68 +374,57 @@ __global__ void __launch_bounds__(kThreadsP, 1)
 
     if (warp == 10) {
         // ------------------------------------------------------------ scheduler
-        PFinder f;
-        f.init(p, lane);
-        const int units = p.Hq / p.pack;  // head groups
-        int64_t idx = blockIdx.x;         // item: head group idx % units of pair idx / units
-        bool end = false;
-        uint32_t asked = 0;
-        // the next CTA's index in idx; at the end of the grid, end
+        // Finding an item takes a few microseconds (the code is cold each time), so
+        // it is done aside; but a CTA asks for the next one only a few key tiles
+        // before the loader is through with this one, so that it does not hold
+        // items that another could begin.
+        uint32_t asked = 0;  // answers taken
+        bool on_its_way = false;
         auto next_cta = [&]() {
             if (lane == 0) {
                 mbar_arrive_expect_tx(&ctrl->more_full, 16);
                 ask_for_cta(&ctrl->more, &ctrl->more_full);
             }
+            on_its_way = true;
             if (!__all_sync(0xffffffffu, mbar_wait(&ctrl->more_full, asked & 1, abort))) {
                 ok = false;
-                end = true;
                 return;
             }
+            on_its_way = false;
             ++asked;
             idx = answered_cta(&ctrl->more);
-            end = idx < 0;
             fence_proxy_async_smem();  // read before the next answer is written
             __syncwarp();
         };
-        for (int64_t r = 0; ok; ++r) {
-            const int k = static_cast<int>(r % kItems);
-            if (r >= kItems &&
-                !__all_sync(0xffffffffu, mbar_wait(&ctrl->item_empty[k], static_cast<uint32_t>(r / kItems - 1) & 1, abort))) {
+        while (ok) {
+            const int k = taken % kItems;
+            if (taken >= kItems &&
+                !__all_sync(0xffffffffu, mbar_wait(&ctrl->item_empty[k], static_cast<uint32_t>(taken / kItems - 1) & 1, abort))) {
                 ok = false;
                 break;
             }
-            int b = 0, qt = 0;
-            PItem it = {-1, 0, 0, 0, 0, 0, 0, 0};
-            const bool any = !end && f.find(p, idx / units, lane, b, qt);
-            if (any) {
-                const int2 sq = p_span(p.cu_q, b, p.total_q), sk = p_span(p.cu_k, b, p.total_k);
-                it.h = static_cast<int>(idx % units) * p.pack;
-                it.q_row = sq.x;
-                it.k_row = sk.x;
-                it.q_len = sq.y;
-                it.k_len = sk.y;
-                it.t0 = qt * 2 * p.tile_tokens;
-                auto tiles = [&](int t) {
-                    const int n = min(p.tile_tokens, sq.y - t);
-                    return n > 0 ? (p_seen(p.causal, sq.y, sk.y, t + n - 1) + kKT - 1) / kKT : 0;
-                };
-                it.n0 = tiles(it.t0);
-                it.n1 = tiles(it.t0 + p.tile_tokens);
-            }
             if (lane == 0) {
-                ctrl->item[k] = it;
+                ctrl->item[k] = next;
                 mbar_arrive(&ctrl->item_full[k]);
             }
-            if (!any) break;
+            if (next.h < 0) break;
+            if (!__all_sync(0xffffffffu, mbar_wait(&ctrl->want, taken & 1, abort))) {
+                ok = false;
+                break;
+            }
+            ++taken;
             next_cta();
+            if (!ok) break;
+            next.h = -1;
+            if (idx >= 0) look_up();
         }
-        // past the last item the grid may hold CTAs that would find nothing
-        // (it is sized by a bound): taken here they need not start
-        while (ok && !end) next_cta();
+        // past the last item the grid may hold CTAs that would find nothing (it is
+        // sized by a bound): taken here they need not start
+        while (ok && idx >= 0) next_cta();
         if (!ok && lane == 0) {
             p_fail(p, ctrl);
             volatile int never = 0;
-            if (asked == 0 || !end) mbar_wait(&ctrl->more_full, asked & 1, &never);
+            if (on_its_way) mbar_wait(&ctrl->more_full, asked & 1, &never);
         }
     } else if (warp == 9) {
         // --------------------------------------------------------------- loader
@@ -406,7 +447,9 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                     ++nq[i];
                 };
                 load_q(0, it.n0);
+                if (nk == 0) mbar_arrive(&ctrl->want);
                 for (int j = 0; j < nk && ok; ++j) {
+                    if (j == max(nk - kAhead, 0)) mbar_arrive(&ctrl->want);
                     for (int x = 0; x < 5; ++x, ++u) {
                         const uint32_t slot = u % kSlots;
                         if (u >= kSlots && !mbar_wait(&ctrl->blk_empty[slot], ((u / kSlots) - 1) & 1, abort)) {
@@ -477,28 +520,24 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                     for (int c = 0; c < 3; ++c) umma_commit(&ctrl->blk_empty[(u0 + 5 * j + c) % kSlots]);
             }
         };
-        auto values = [&](int i, int j) {
-            const uint32_t u = u0 + 5 * j + 3;
-            wait_blk(u);
-            wait_blk(u + 1);
-            if (!ok) return;
-            tc_fence_after();
-            const uint32_t s0 = u % kSlots, s1 = (u + 1) % kSlots;
-            const uint64_t d0 = dV + s0 * kBlkD, d1 = dV + s1 * kBlkD;
-            const uint32_t tO = tm + 256 + i * 128, tP = tm + i * 128;
+        // P_i(j) V over keys 64 half .. 64 half + 63 of the tile
+        auto values = [&](int i, int j, int half) {
+            const uint32_t u = u0 + 5 * j + 3, s0 = u % kSlots, s1 = (u + 1) % kSlots;
+            const uint64_t d0 = dV + s0 * kBlkD + half * (8192 >> 4), d1 = dV + s1 * kBlkD + half * (8192 >> 4);
+            const uint32_t tO = tm + 256 + i * 128, tP = tm + i * 128 + half * 32;
             if (leader) {
                 if (s1 == s0 + 1) {
 #pragma unroll
-                    for (int kk = 0; kk < 8; ++kk)
-                        umma_bf16_ta(tO, tP + 8 * kk, d0 + kk * (2048 >> 4), idPV, (j | kk) != 0);
+                    for (int kk = 0; kk < 4; ++kk)
+                        umma_bf16_ta(tO, tP + 8 * kk, d0 + kk * (2048 >> 4), idPV, (j | half | kk) != 0);
                 } else {  // the two blocks are the ring's last and first
 #pragma unroll
-                    for (int kk = 0; kk < 8; ++kk) {
-                        umma_bf16_ta(tO, tP + 8 * kk, d0 + kk * (2048 >> 4), idPVh, (j | kk) != 0);
-                        umma_bf16_ta(tO + 64, tP + 8 * kk, d1 + kk * (2048 >> 4), idPVh, (j | kk) != 0);
+                    for (int kk = 0; kk < 4; ++kk) {
+                        umma_bf16_ta(tO, tP + 8 * kk, d0 + kk * (2048 >> 4), idPVh, (j | half | kk) != 0);
+                        umma_bf16_ta(tO + 64, tP + 8 * kk, d1 + kk * (2048 >> 4), idPVh, (j | half | kk) != 0);
                     }
                 }
-                if (i == 1 || j >= n1) {
+                if (half == 1 && (i == 1 || j >= n1)) {
                     umma_commit(&ctrl->blk_empty[s0]);
                     umma_commit(&ctrl->blk_empty[s1]);
                 }
@@ -507,14 +546,19 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         auto step = [&](int i, int j, int ni, uint32_t& np) {  // P_i(j) V, then the scores of the next key tile
             if (!ok || j >= ni) return;
             // (the item's first P_i comes after the last one's O_i was read)
+            if (!mbar_wait(&ctrl->p_half[i], np & 1, abort)) ok = false;
+            wait_blk(u0 + 5 * j + 3);
+            wait_blk(u0 + 5 * j + 4);
+            if (!ok) return;
+            tc_fence_after();
+            values(i, j, 0);
             if (!mbar_wait(&ctrl->p_full[i], np & 1, abort)) {
                 ok = false;
                 return;
             }
             ++np;
             tc_fence_after();
-            values(i, j);
-            if (!ok) return;
+            values(i, j, 1);
             // in order behind the product that reads P_i from the same columns
             if (j + 1 < ni) scores(i, j + 1, ni);
             else if (leader) umma_commit(&ctrl->o_full[i]);
@@ -568,18 +612,29 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                     break;
                 }
                 tc_fence_after();
-                uint32_t s[128];
-                tmem_ld_x64(tS, *reinterpret_cast<uint32_t(*)[64]>(s));
-                tmem_ld_x64(tS + 64, *reinterpret_cast<uint32_t(*)[64]>(s + 64));
                 const int left = vis - j * kKT;  // visible keys of this tile
-                if (__any_sync(0xffffffffu, left < kKT)) {
+                const bool cut = __any_sync(0xffffffffu, left < kKT);
+                // the scores twice, 32 at a time and the next ones on their way: for
+                // the maximum and for the probabilities (128 at once would spill)
+                uint32_t s[2][32];
+                auto mask = [&](uint32_t(&x)[32], int c) {
+                    if (cut) {
 #pragma unroll
-                    for (int k = 0; k < 128; ++k)
-                        if (k >= left) s[k] = 0xff800000u;
-                }
+                        for (int k = 0; k < 32; ++k)
+                            if (32 * c + k >= left) x[k] = 0xff800000u;
+                    }
+                };
                 float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                tmem_ld_x32_begin(tS, s[0]);
 #pragma unroll
-                for (int k = 0; k < 128; ++k) mx[k & 3] = fmaxf(mx[k & 3], __uint_as_float(s[k]));
+                for (int c = 0; c < 4; ++c) {
+                    tmem_ld_end(s[c & 1]);
+                    if (c < 3) tmem_ld_x32_begin(tS + (c + 1) * 32, s[~c & 1]);
+                    mask(s[c & 1], c);
+#pragma unroll
+                    for (int k = 0; k < 32; k += 2)
+                        mx[k / 2 & 3] = fmaxf(mx[k / 2 & 3], fmaxf(__uint_as_float(s[c & 1][k]), __uint_as_float(s[c & 1][k + 1])));
+                }
                 const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
                 const bool raise = top > m + kRaise || (m == -INFINITY && top > m);
                 if (__any_sync(0xffffffffu, raise)) {
@@ -601,13 +656,17 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                 }
                 const float base = m == -INFINITY ? 0.f : m;
                 const uint64_t nb = pack2(-base, -base);
+                tmem_ld_x32_begin(tS, s[0]);
                 uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     uint32_t pk[16];
+                    tmem_ld_end(s[c & 1]);
+                    if (c < 3) tmem_ld_x32_begin(tS + (c + 1) * 32, s[~c & 1]);
+                    mask(s[c & 1], c);
 #pragma unroll
                     for (int k = 0; k < 16; ++k) {
-                        const uint64_t x = fma2(pack2(__uint_as_float(s[32 * c + 2 * k]), __uint_as_float(s[32 * c + 2 * k + 1])), c2, nb);
+                        const uint64_t x = fma2(pack2(__uint_as_float(s[c & 1][2 * k]), __uint_as_float(s[c & 1][2 * k + 1])), c2, nb);
                         float x0, x1;
                         unpack2(x, x0, x1);
                         x0 = ex2(x0);
@@ -615,7 +674,14 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                         sum[k & 1] = add2(sum[k & 1], pack2(x0, x1));
                         pk[k] = pack_bf16x2(x0, x1);
                     }
+                    // (over scores that have been read)
                     tmem_st_x16(tS + 16 * c, pk);
+                    if (c == 1) {  // the product with the first half of the keys may begin
+                        tmem_wait_st();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&ctrl->p_half[i]);
+                    }
                 }
                 float a0, a1;
                 unpack2(add2(sum[0], sum[1]), a0, a1);
@@ -635,35 +701,44 @@ __global__ void __launch_bounds__(kThreadsP, 1)
             const int t = item->t0 + tok, h = item->h + head;
             const bool mine = used && t < item->q_len;
             const int64_t at = (static_cast<int64_t>(item->q_row) + t) * p.Hq + h;
-            const float inv = l > 0.f ? 1.f / l : l;  // l = 0: nothing seen; NaN: the row is NaN
-            __nv_bfloat16* o = p.out + at * kDv;
+            const float inv = l > 0.f ? __fdividef(1.f, l) : l;  // l = 0: nothing seen; NaN: the row is NaN
             bool fine = true;
+            // Four lanes trade 16-byte units, so that lane j of them holds unit j of four
+            // rows and a store writes whole sectors. A loop, not unrolled: the code is
+            // cold at every item, and its length costs more than its steps.
+            const int64_t at_ = mine ? at : -1;
+            int64_t rows[4];
 #pragma unroll
+            for (int k = 0; k < 4; ++k) rows[k] = __shfl_sync(0xffffffffu, at_, (lane & 28) + k);
+            __nv_bfloat16* out = p.out + (lane & 3) * 8;
+#pragma unroll 1
             for (int c = 0; c < 128; c += 32) {
-                uint32_t v[32];
-                if (n > 0) {
-                    tmem_ld_x32(tO + c, v);
-                } else {
+                uint32_t v[32], x[4][4];
+                if (n > 0) tmem_ld_x32(tO + c, v);
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) v[k] = 0u;
-                }
-                if (vis <= 0) {  // sees nothing, beside rows that do
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) v[k] = 0u;
+                for (int k = 0; k < 32; k += 2) {
+                    // (a row that sees nothing may lie beside rows that do)
+                    const float f = vis > 0 ? __uint_as_float(v[k]) * inv : 0.f, g = vis > 0 ? __uint_as_float(v[k + 1]) * inv : 0.f;
+                    fine = fine && fabsf(f) <= 3.0e38f && fabsf(g) <= 3.0e38f;
+                    x[k / 8][k % 8 / 2] = pack_bf16x2(f, g);
                 }
 #pragma unroll
-                for (int k = 0; k < 32; k += 8) {
-                    float f[8];
+                for (int b = 2; b > 0; b >>= 1)
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        f[e] = __uint_as_float(v[k + e]) * inv;
-                        fine = fine && fabsf(f[e]) <= 3.0e38f;
-                    }
-                    if (mine)
-                        *reinterpret_cast<uint4*>(o + c + k) =
-                            make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                                       pack_bf16x2(f[6], f[7]));
-                }
+                    for (int q = 0; q < 4; ++q)
+                        if ((q & b) == 0) {
+                            const bool up = (lane & b) != 0;
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? x[q][e] : x[q | b][e], b);
+                                x[q][e] = up ? got : x[q][e];
+                                x[q | b][e] = up ? x[q | b][e] : got;
+                            }
+                        }
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (rows[k] >= 0)
+                        *reinterpret_cast<uint4*>(out + rows[k] * kDv + c) = make_uint4(x[k][0], x[k][1], x[k][2], x[k][3]);
             }
             if (mine) p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
             // rows to form again: O is not finite though the sums are
