@@ -488,11 +488,11 @@ int mla_prefill(const void* q, int64_t q_stride_t, int64_t q_stride_h, const voi
     mla::PrefillMaps maps;
     std::memset(&maps, 0, sizeof(maps));
     auto map = [&](CUtensorMap* m, const void* base, int width, int heads, int64_t tokens, int64_t sh, int64_t st,
-                   int box_heads = 1) {
+                   int box_heads, int box_tokens) {
         cuuint64_t gdim[3] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(heads),
                               static_cast<cuuint64_t>(tokens)};
         cuuint64_t gstride[2] = {static_cast<cuuint64_t>(sh) * 2, static_cast<cuuint64_t>(st) * 2};
-        cuuint32_t box[3] = {64u, static_cast<cuuint32_t>(box_heads), static_cast<cuuint32_t>(128 / box_heads)},
+        cuuint32_t box[3] = {64u, static_cast<cuuint32_t>(box_heads), static_cast<cuuint32_t>(box_tokens)},
                    estride[3] = {1u, 1u, 1u};
         return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), gdim, gstride, box, estride,
                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -500,10 +500,10 @@ int mla_prefill(const void* q, int64_t q_stride_t, int64_t q_stride_h, const voi
     };
     // without keys no block is loaded: the maps then describe q's first row
     const bool keys = total_k > 0;
-    if (!map(&maps.q, q, 192, Hq, total_q, q_stride_h, q_stride_t, pack) ||
-        !map(&maps.k_nope, keys ? k_nope : q, 128, keys ? Hkv : 1, keys ? total_k : 1, k_stride_h, k_stride_t) ||
-        !map(&maps.k_pe, keys ? k_pe : q, 64, 1, keys ? total_k : 1, k_pe_stride, k_pe_stride) ||
-        !map(&maps.v, keys ? v : q, 128, keys ? Hkv : 1, keys ? total_k : 1, v_stride_h, v_stride_t))
+    if (!map(&maps.q, q, 192, Hq, total_q, q_stride_h, q_stride_t, pack, p.tile_tokens) ||
+        !map(&maps.k_nope, keys ? k_nope : q, 128, keys ? Hkv : 1, keys ? total_k : 1, k_stride_h, k_stride_t, 1, 128) ||
+        !map(&maps.k_pe, keys ? k_pe : q, 64, 1, keys ? total_k : 1, k_pe_stride, k_pe_stride, 1, 128) ||
+        !map(&maps.v, keys ? v : q, 128, keys ? Hkv : 1, keys ? total_k : 1, v_stride_h, v_stride_t, 1, 64))
         return MLA_ERR_CUDA;
     const cudaError_t e = mla::launch_prefill(maps, p, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;

@@ -164,7 +164,7 @@ struct PrefillParams {
     int* status;
 };
 // 64-value blocks (128-B swizzle): q of tile_tokens tokens of pack heads, the
-// others of 128 tokens of one head.
+// others of one head: 128 tokens of keys, 64 of values.
 struct PrefillMaps {
     CUtensorMap q, k_nope, k_pe, v;
 };

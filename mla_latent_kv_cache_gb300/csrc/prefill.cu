@@ -27,8 +27,11 @@
 // the items evenly, and the next item's Q, keys and scores are on their way
 // while the last one's output is written.
 // TMEM: S_0, S_1, O_0, O_1 of 128 columns each = all 512. Shared memory: Q
-// 96 KB, and a ring of eight 16-KB blocks (64 dims of 128 tokens) through which
-// K (two blocks of k_nope, one of k_pe) and V (two) stream by TMA.
+// 96 KB, and a ring of eight 16-KB blocks through which K (two blocks of k_nope
+// and one of k_pe, 64 dims of 128 tokens) and V (two of 128 dims of 64 tokens)
+// stream by TMA. Eight blocks are 1.6 key tiles, so a block is given back when
+// its own last product is done: with V cut by dims and K given back by the tile
+// the issuer waited 945 of 3,700 cycles a key tile for blocks.
 //
 // Keys past a sequence's end and masked ones have probability 0, which keeps
 // finite values of theirs out of the sums. A NaN or infinity there would still
@@ -461,7 +464,9 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                         const int kr = it.k_row + j * kKT;
                         if (x < 2) tma_load_3d(dst, &maps.k_nope, &ctrl->blk_full[slot], 64 * x, hk, kr);
                         else if (x == 2) tma_load_3d(dst, &maps.k_pe, &ctrl->blk_full[slot], 0, 0, kr);
-                        else tma_load_3d(dst, &maps.v, &ctrl->blk_full[slot], 64 * (x - 3), hk, kr);
+                        else
+                            for (int d = 0; d < 2; ++d)
+                                tma_load_3d(dst + d * (kBlkP / 2), &maps.v, &ctrl->blk_full[slot], 64 * d, hk, kr + 64 * (x - 3));
                         if (j == 0 && x == 2) load_q(1, it.n1);
                     }
                 }
@@ -486,12 +491,11 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         // (formed by a single lane they cost a move each per product: 4.6 against
         // 3.4 ms for a causal prompt of 32,768 tokens and 16 heads).
         const bool leader = elect_lane();
-        const uint32_t idS = idesc_bf16(128, 128, false, false), idPV = idesc_bf16(128, 128, false, true),
-                       idPVh = idesc_bf16(128, 64, false, true);
+        const uint32_t idS = idesc_bf16(128, 128, false, false), idPV = idesc_bf16(128, 128, false, true);
         const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
         const uint64_t dQ = smem_desc(smem_u32(qs), 16, 1024, kSw128);
         const uint64_t dK = smem_desc(smem_u32(ring), 16, 1024, kSw128);
-        const uint64_t dV = smem_desc(smem_u32(ring), kBlkP, 1024, kSw128);
+        const uint64_t dV = smem_desc(smem_u32(ring), kBlkP / 2, 1024, kSw128);
         constexpr uint32_t kBlkD = kBlkP >> 4;
         uint32_t u0 = 0;                 // the item's first block
         uint32_t nq0 = 0, nq1 = 0;       // items with a tile 0, 1
@@ -511,36 +515,25 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                 if (leader) {
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk) umma_bf16(tm + i * 128, da + 2 * kk, db + 2 * kk, idS, (c | kk) != 0);
+                    // a block is free as soon as its last product is done, not the tile's
+                    if (i == 1 || j >= n1) umma_commit(&ctrl->blk_empty[u % kSlots]);
                 }
             }
             if (leader) {
                 umma_commit(&ctrl->s_full[i]);
                 if (j + 1 == ni) umma_commit(&ctrl->q_empty[i]);
-                if (i == 1 || j >= n1)
-                    for (int c = 0; c < 3; ++c) umma_commit(&ctrl->blk_empty[(u0 + 5 * j + c) % kSlots]);
             }
         };
         // P_i(j) V over keys 64 half .. 64 half + 63 of the tile
         auto values = [&](int i, int j, int half) {
-            const uint32_t u = u0 + 5 * j + 3, s0 = u % kSlots, s1 = (u + 1) % kSlots;
-            const uint64_t d0 = dV + s0 * kBlkD + half * (8192 >> 4), d1 = dV + s1 * kBlkD + half * (8192 >> 4);
-            const uint32_t tO = tm + 256 + i * 128, tP = tm + i * 128 + half * 32;
+            const uint32_t slot = (u0 + 5 * j + 3 + half) % kSlots;
+            const uint64_t dv = dV + slot * kBlkD;
             if (leader) {
-                if (s1 == s0 + 1) {
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        umma_bf16_ta(tO, tP + 8 * kk, d0 + kk * (2048 >> 4), idPV, (j | half | kk) != 0);
-                } else {  // the two blocks are the ring's last and first
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk) {
-                        umma_bf16_ta(tO, tP + 8 * kk, d0 + kk * (2048 >> 4), idPVh, (j | half | kk) != 0);
-                        umma_bf16_ta(tO + 64, tP + 8 * kk, d1 + kk * (2048 >> 4), idPVh, (j | half | kk) != 0);
-                    }
-                }
-                if (half == 1 && (i == 1 || j >= n1)) {
-                    umma_commit(&ctrl->blk_empty[s0]);
-                    umma_commit(&ctrl->blk_empty[s1]);
-                }
+                for (int kk = 0; kk < 4; ++kk)
+                    umma_bf16_ta(tm + 256 + i * 128, tm + i * 128 + half * 32 + 8 * kk, dv + kk * (2048 >> 4), idPV,
+                                 (j | half | kk) != 0);
+                if (i == 1 || j >= n1) umma_commit(&ctrl->blk_empty[slot]);
             }
         };
         auto step = [&](int i, int j, int ni, uint32_t& np) {  // P_i(j) V, then the scores of the next key tile
@@ -548,10 +541,10 @@ __global__ void __launch_bounds__(kThreadsP, 1)
             // (the item's first P_i comes after the last one's O_i was read)
             if (!mbar_wait(&ctrl->p_half[i], np & 1, abort)) ok = false;
             wait_blk(u0 + 5 * j + 3);
-            wait_blk(u0 + 5 * j + 4);
             if (!ok) return;
             tc_fence_after();
             values(i, j, 0);
+            wait_blk(u0 + 5 * j + 4);
             if (!mbar_wait(&ctrl->p_full[i], np & 1, abort)) {
                 ok = false;
                 return;
