@@ -293,7 +293,8 @@ MLA_API int mla_decode_varlen(const void* q_lat, const void* q_pe, int64_t total
  *   cu_q_lens, cu_k_lens  device, int32 [B + 1], non-decreasing from 0, read on
  *                the device only; entries are clamped to [0, total_q] and
  *                [0, total_k], so no row past them is touched.
- *   max_q_len    the longest Lq, >= 1 if total_q > 0 (a bound will do).
+ *   max_q_len    the longest Lq or a bound of it, >= 1 if total_q > 0: it sizes
+ *                the launch, and with a smaller value queries may be left out.
  *   scale        > 0 and finite.
  *   out          device, bf16 [total_q, Hq, 128], contiguous, 16-byte aligned.
  *                Rows that no sequence names are not written.

@@ -450,7 +450,8 @@ int mla_prefill(const void* q, int64_t q_stride_t, int64_t q_stride_h, const voi
     // TMA coordinates are 32-bit, and a tile may pass the last row
     if (total_q > INT32_MAX - 1024 || total_k > INT32_MAX - 1024) return MLA_ERR_UNSUPPORTED;
     const int pack = mla::prefill_pack(Hq / Hkv);
-    if ((total_q / (2 * (128 / pack)) + B) * (Hq / pack) > INT32_MAX) return MLA_ERR_UNSUPPORTED;  // grid size
+    if (mla::prefill_pairs(total_q, B, max_q_len, 128 / pack) * (Hq / pack) > INT32_MAX)
+        return MLA_ERR_UNSUPPORTED;  // grid size
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return MLA_ERR_CUDA;
     const DevInfo di = dev_info(dev);
@@ -505,7 +506,7 @@ int mla_prefill(const void* q, int64_t q_stride_t, int64_t q_stride_h, const voi
         !map(&maps.k_pe, keys ? k_pe : q, 64, 1, keys ? total_k : 1, k_pe_stride, k_pe_stride, 1, 128) ||
         !map(&maps.v, keys ? v : q, 128, keys ? Hkv : 1, keys ? total_k : 1, v_stride_h, v_stride_t, 1, 64))
         return MLA_ERR_CUDA;
-    const cudaError_t e = mla::launch_prefill(maps, p, static_cast<cudaStream_t>(stream));
+    const cudaError_t e = mla::launch_prefill(maps, p, max_q_len, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 

@@ -88,8 +88,9 @@ __device__ __forceinline__ uint32_t idesc_f8(int M, int N, uint32_t a_type, uint
 }
 
 __device__ __forceinline__ int w_tokens(const WeightsParams& p, int b) { return max(__ldg(p.seq_lens + b), 0); }
+// Tiles of the tokens whose weights are kept.
 __device__ __forceinline__ int w_tiles(const WeightsParams& p, int b) {
-    return static_cast<int>((static_cast<uint32_t>(w_tokens(p, b)) + kTok - 1) / kTok);
+    return static_cast<int>((static_cast<uint32_t>(min(w_tokens(p, b), p.max_len)) + kTok - 1) / kTok);
 }
 
 // The order in which every role walks this CTA's tiles: `rem` tiles from tile
@@ -379,12 +380,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         int y_next = 0;
         auto run_slot = [&]() -> int {
             if (wk.done()) return 0;
-            const int valid = min(kTok, wk.T - wk.j * kTok);
+            const int valid = min(kTok, min(wk.T, p.max_len) - wk.j * kTok);
             return lane * BR < valid ? w_slot(p, wk.b, wk.j * kTok + lane * BR, bad) : 0;
         };
         if (!LSU) y_next = run_slot();
         while (ok && !wk.done()) {
-            const int valid = min(kTok, wk.T - wk.j * kTok);
+            const int valid = min(kTok, min(wk.T, p.max_len) - wk.j * kTok);
             const int nruns = LSU ? 0 : (valid + BR - 1) / BR;
             const int y = y_next;
             int slot4[4] = {0, 0, 0, 0}, row_slot[LSU ? 32 : 1];

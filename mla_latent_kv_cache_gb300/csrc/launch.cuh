@@ -169,6 +169,7 @@ struct PrefillMaps {
     CUtensorMap q, k_nope, k_pe, v;
 };
 int prefill_pack(int group);
-cudaError_t launch_prefill(const PrefillMaps& maps, const PrefillParams& p, cudaStream_t stream);
+int64_t prefill_pairs(int64_t total_q, int B, int max_q_len, int tile_tokens);
+cudaError_t launch_prefill(const PrefillMaps& maps, const PrefillParams& p, int max_q_len, cudaStream_t stream);
 
 }  // namespace mla

@@ -769,9 +769,15 @@ int prefill_pack(int group) {
     return 1;
 }
 
-cudaError_t launch_prefill(const PrefillMaps& maps, const PrefillParams& p, cudaStream_t stream) {
-    // items: sum of ceil(len / tokens) <= total / tokens + B pairs of tiles, for every head group
-    const int64_t items = (static_cast<int64_t>(p.total_q) / (2 * p.tile_tokens) + p.B) * (p.Hq / p.pack);
+// A bound of the pairs of tiles that all sequences have.
+int64_t prefill_pairs(int64_t total_q, int B, int max_q_len, int tile_tokens) {
+    const int64_t t = 2 * tile_tokens, each = (static_cast<int64_t>(max_q_len) + t - 1) / t;
+    // sum of ceil(len / t) <= total / t + B, and B times the longest's
+    return each <= (total_q / t + B) / B ? each * B : total_q / t + B;
+}
+
+cudaError_t launch_prefill(const PrefillMaps& maps, const PrefillParams& p, int max_q_len, cudaStream_t stream) {
+    const int64_t items = prefill_pairs(p.total_q, p.B, max_q_len, p.tile_tokens) * (p.Hq / p.pack);
     cudaError_t e = cudaFuncSetAttribute(prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemP);
     if (e != cudaSuccess) return e;
     prefill_kernel<<<dim3(static_cast<unsigned>(items)), kThreadsP, kSmemP, stream>>>(maps, p);

@@ -158,6 +158,16 @@ def test_host_tensors_are_refused():
         _refused(call, "must be a CUDA tensor")
 
 
+def test_missing_tensors_are_refused(fake):
+    for name in ("q", "k_nope", "k_pe", "v", "cu_q_lens", "cu_k_lens", "out", "lse"):
+        _refused(lambda: _prefill(**{name: None}), f"{name} must be a CUDA tensor")
+    for name in ("q_lat", "lse", "cache", "block_table", "seq_lens", "weights"):
+        _refused(lambda: _weights(**{name: None}), f"{name} must be a CUDA tensor")
+    for name in ("cache", "positions", "budgets", "new_seq_lens", "new_weights", "moves"):
+        _refused(lambda: _evict(**{name: None}), f"{name} must be a CUDA tensor")
+    assert fake.calls == []
+
+
 def test_tensors_on_another_device_than_the_current_one_are_refused(fake, monkeypatch):
     monkeypatch.setattr(m, "_current_device", lambda: 1)
     for call in (_prefill, _weights, _evict):
