@@ -34,6 +34,7 @@
 // are taken in groups over chunks of kChunk tiles, so that the groups after
 // the first find the rows in L2.
 #include <climits>
+#include <type_traits>
 
 #include "launch.cuh"
 #include "mla_common.cuh"
@@ -251,6 +252,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&ctrl->fin, 1);
         ctrl->abort = 0;
         fence_mbar_init();
+    }
+    if (!LSU && warp == 1 && lane == 0) {
+        prefetch_tensormap(&maps.rows);
+        if (KIND == 1) {
+            prefetch_tensormap(&maps.rope);
+            prefetch_tensormap(&maps.scales);
+        }
     }
     if (warp == 0) {
         tmem_alloc(&ctrl->tmem_base, tmem_cols);
@@ -616,37 +624,47 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             const uint32_t tS = tmem + buf * buf_cols + lane_base;
             float acc = 0.f;
-            for (int cc = cb; cc < ce; cc += 16) {
-                float x[16];  // scores; fp8: the four block sums, each times its scale
-                uint32_t a[16];
-                tmem_ld_x16(tS + cc, a);
+            // W columns from cc on: their sums first (the buffer is free when the last
+            // are read), then the exponentials
+            auto columns = [&](auto width, int cc) {
+                constexpr int W = decltype(width)::value;
+                float x[W];  // scores; fp8: the four block sums, each times its scale
+                uint32_t a[W];
+                auto load = [&](int part) {
+                    if constexpr (W == 32) tmem_ld_x32(tS + part * NP + cc, a);
+                    else tmem_ld_x16(tS + part * NP + cc, a);
+                };
+                load(0);
 #pragma unroll
-                for (int k = 0; k < 16; ++k) x[k] = KIND == 1 ? __uint_as_float(a[k]) * sc.x : __uint_as_float(a[k]);
-                tmem_ld_x16(tS + NP + cc, a);
+                for (int k = 0; k < W; ++k) x[k] = KIND == 1 ? __uint_as_float(a[k]) * sc.x : __uint_as_float(a[k]);
+                load(1);
 #pragma unroll
-                for (int k = 0; k < 16; ++k) x[k] = KIND == 1 ? fmaf(__uint_as_float(a[k]), sc.y, x[k]) : x[k] + __uint_as_float(a[k]);
+                for (int k = 0; k < W; ++k) x[k] = KIND == 1 ? fmaf(__uint_as_float(a[k]), sc.y, x[k]) : x[k] + __uint_as_float(a[k]);
                 if (sums > 2) {
-                    tmem_ld_x16(tS + 2 * NP + cc, a);
+                    load(2);
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) x[k] = KIND == 1 ? fmaf(__uint_as_float(a[k]), sc.z, x[k]) : x[k] + __uint_as_float(a[k]);
-                    tmem_ld_x16(tS + 3 * NP + cc, a);
+                    for (int k = 0; k < W; ++k) x[k] = KIND == 1 ? fmaf(__uint_as_float(a[k]), sc.z, x[k]) : x[k] + __uint_as_float(a[k]);
+                    load(3);
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) x[k] = KIND == 1 ? fmaf(__uint_as_float(a[k]), sc.w, x[k]) : x[k] + __uint_as_float(a[k]);
+                    for (int k = 0; k < W; ++k) x[k] = KIND == 1 ? fmaf(__uint_as_float(a[k]), sc.w, x[k]) : x[k] + __uint_as_float(a[k]);
                 }
-                if (KIND == 1) tmem_ld_x16(tS + 4 * NP + cc, a);  // the rotary part
-                if (cc + 16 >= ce) {  // this group's share of the buffer is read
+                if (KIND == 1) load(4);  // the rotary part
+                if (cc + W >= ce) {      // this group's share of the buffer is read
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&ctrl->s_free[buf]);
                 }
 #pragma unroll
-                for (int k = 0; k < 16; ++k) {
+                for (int k = 0; k < W; ++k) {
                     const int c = cc + k;
                     const float v = KIND == 1 ? fmaf(x[k], qs[c], __uint_as_float(a[k])) : x[k];
                     const float e = ex2(fmaf(v, p.scale_log2, -lse2[c]));
                     acc += c >= c0 && c < c1 ? e : 0.f;
                 }
-            }
+            };
+            int cc = cb;
+            for (; cc + 32 <= ce; cc += 32) columns(std::integral_constant<int, 32>{}, cc);
+            if (cc < ce) columns(std::integral_constant<int, 16>{}, cc);
             if (++buf == nbuf) {
                 buf = 0;
                 ++turn;

@@ -657,39 +657,46 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictPar
         __syncthreads();
         const uint64_t total = static_cast<uint64_t>(sh.first[kMoveReqs]) * pieces;
         const uint64_t step = static_cast<uint64_t>(gridDim.x) * kMoveWarps * batch;
-        for (uint64_t m0 = (static_cast<uint64_t>(warp) * gridDim.x + blockIdx.x) * batch; m0 < total && ok; m0 += step) {
+        // this lane's row (or piece) of the batch at m0: looked up while the batch
+        // before is on its way
+        const uint8_t* from = nullptr;
+        uint8_t* to = nullptr;
+        uint32_t bytes = 0;
+        auto look_up = [&](uint64_t m0) {
             const uint64_t item = m0 + lane;
-            const uint8_t* from = nullptr;
-            uint8_t* to = nullptr;
-            uint32_t bytes = 0;
-            if (lane < batch && item < total) {
-                const uint32_t m = static_cast<uint32_t>(item / pieces), piece = static_cast<uint32_t>(item % pieces);
-                int lo = 0, hi = nb;  // the last request whose first move is <= m
-                while (hi - lo > 1) {
-                    const int mid = (lo + hi) >> 1;
-                    if (sh.first[mid] <= m) lo = mid;
-                    else hi = mid;
-                }
-                const int64_t b = b0 + lo;
-                const int32_t* mv = p.moves + b * p.moves_stride + 2 + 2 * static_cast<int64_t>(m - sh.first[lo]);
-                const int s = mv[0], d = mv[1];
-                if (piece == 0) {
-                    p.new_weights[b * p.stride + d] = p.weights[b * p.stride + s];
-                    p.new_positions[b * p.stride + d] = p.positions[b * p.stride + s];
-                }
-                const int32_t* bt = p.block_table + b * p.bt_stride;
-                const int64_t sp = __ldg(bt + s / p.page_size), dp = __ldg(bt + d / p.page_size);
-                const int64_t ss = sp * p.page_size + s % p.page_size, ds = dp * p.page_size + d % p.page_size;
-                // a page outside the pool: the row is not moved
-                if (sp < 0 || dp < 0 || ss >= p.num_slots || ds >= p.num_slots) {
-                    bad = true;
-                } else {
-                    const int64_t off = static_cast<int64_t>(piece) * kStage;
-                    from = p.cache + ss * p.row_bytes + off;
-                    to = p.cache + ds * p.row_bytes + off;
-                    bytes = static_cast<uint32_t>(min(static_cast<int64_t>(kStage), p.row_bytes - off));
-                }
+            bytes = 0;
+            if (lane >= batch || item >= total) return;
+            const uint32_t m = static_cast<uint32_t>(pieces > 1 ? item / pieces : item);
+            const uint32_t piece = static_cast<uint32_t>(item - static_cast<uint64_t>(m) * pieces);
+            int lo = 0, hi = nb;  // the last request whose first move is <= m
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (sh.first[mid] <= m) lo = mid;
+                else hi = mid;
             }
+            const int64_t b = b0 + lo;
+            const int32_t* mv = p.moves + b * p.moves_stride + 2 + 2 * static_cast<int64_t>(m - sh.first[lo]);
+            const int s = mv[0], d = mv[1];
+            if (piece == 0) {
+                p.new_weights[b * p.stride + d] = p.weights[b * p.stride + s];
+                p.new_positions[b * p.stride + d] = p.positions[b * p.stride + s];
+            }
+            const int32_t* bt = p.block_table + b * p.bt_stride;
+            const int64_t sp = __ldg(bt + s / p.page_size), dp = __ldg(bt + d / p.page_size);
+            const int64_t ss = sp * p.page_size + s % p.page_size, ds = dp * p.page_size + d % p.page_size;
+            // a page outside the pool: the row is not moved
+            if (sp < 0 || dp < 0 || ss >= p.num_slots || ds >= p.num_slots) {
+                bad = true;
+                return;
+            }
+            const int64_t off = static_cast<int64_t>(piece) * kStage;
+            from = p.cache + ss * p.row_bytes + off;
+            to = p.cache + ds * p.row_bytes + off;
+            bytes = static_cast<uint32_t>(min(static_cast<int64_t>(kStage), p.row_bytes - off));
+        };
+        uint64_t m0 = (static_cast<uint64_t>(warp) * gridDim.x + blockIdx.x) * batch;
+        if (m0 < total) look_up(m0);
+        for (; m0 < total && ok; m0 += step) {
             // the stores of batch loads - 2 have left its stage
             bulk_wait_read();
             __syncwarp();
@@ -702,6 +709,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictPar
             ++loads;
             out = to;
             out_bytes = bytes;
+            if (m0 + step < total) look_up(m0 + step);
         }
         if (loads > 0) {
             write_last();

@@ -324,6 +324,12 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         tmem_relinquish();
         tc_fence_before();
     }
+    if (warp == 9 && lane == 0) {
+        prefetch_tensormap(&maps.q);
+        prefetch_tensormap(&maps.k_nope);
+        prefetch_tensormap(&maps.k_pe);
+        prefetch_tensormap(&maps.v);
+    }
     const int units = p.Hq / p.pack;  // head groups
     int64_t idx = blockIdx.x;         // item: head group idx % units of pair idx / units
     PFinder f;

@@ -92,7 +92,7 @@ def _check(a, causal=True, scale=SCALE):
     got, glse = got.double().cpu().numpy(), glse.double().cpu().numpy()
     assert np.array_equal(np.isneginf(glse), ~fin)
     assert np.all(got[~fin] == 0)
-    assert np.all(np.abs(glse - lse)[fin] <= eps + lk * 2.0 ** -24 + 2.0 ** -22 * (1 + np.abs(lse[fin])))
+    assert np.all(np.abs(glse[fin] - lse[fin]) <= eps + lk * 2.0 ** -24 + 2.0 ** -22 * (1 + np.abs(lse[fin])))
     tol = (2.0 ** -8 + 2 * eps + lk * 2.0 ** -23) * A + 2.0 ** -8 * np.abs(out) + 1e-30
     assert np.all(np.abs(got - out) <= tol), np.abs(got - out).max()
     return got, glse
