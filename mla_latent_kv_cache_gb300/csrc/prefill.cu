@@ -143,10 +143,12 @@ __device__ __forceinline__ int p_seen(int causal, int q_len, int k_len, int t) {
 }
 
 // Finds pairs of query tiles by their number in descending order of the key
-// tiles that they see; used by a whole warp.
+// tiles that they see; used by a whole warp, mostly with ascending numbers.
 struct PFinder {
-    int lq, lk, top;  // lane's lengths of the first 32 sequences; the most key tiles of any
-    int tokens;       // of a pair
+    int lq, lk;            // lane's lengths of the first 32 sequences
+    int tokens;            // of a pair
+    int top, level;        // the most key tiles that a pair sees, and those of the last one found
+    int64_t above, upto;   // pairs that see more, and at least, level key tiles
     __device__ __forceinline__ void lens(const PrefillParams& p, int i, int lane, int& q, int& k) const {
         if (i < 32) {
             q = lq;
@@ -167,6 +169,8 @@ struct PFinder {
             top = max(top, q > 0 ? (k + kKT - 1) / kKT : 0);
         }
         top = __reduce_max_sync(0xffffffffu, top);
+        level = top + 1;
+        above = upto = 0;
     }
     // Pairs of a sequence that see at least x key tiles: the last ones, and the
     // very last sees all keys.
@@ -188,19 +192,31 @@ struct PFinder {
         return n;
     }
     // Sequence b and pair qt of the s-th; false if there are fewer.
-    __device__ __forceinline__ bool find(const PrefillParams& p, int64_t s, int lane, int& b, int& qt) const {
-        if (from(p, 0, lane) <= s) return false;
-        int lo = 0, hi = top + 1;  // from(lo) > s, from(hi) = 0
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (from(p, mid, lane) > s) lo = mid;
-            else hi = mid;
+    __device__ __forceinline__ bool find(const PrefillParams& p, int64_t s, int lane, int& b, int& qt) {
+        if (s < above || s >= upto) {  // another level: the highest whose pairs and those above pass s
+            int lo = 0, hi = s < above ? top + 1 : level;
+            int64_t n_lo = from(p, 0, lane), n_hi = s < above ? 0 : upto;  // n_lo > s >= n_hi
+            if (n_lo <= s) return false;
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                const int64_t n = from(p, mid, lane);
+                if (n > s) {
+                    lo = mid;
+                    n_lo = n;
+                } else {
+                    hi = mid;
+                    n_hi = n;
+                }
+            }
+            level = lo;
+            above = n_hi;
+            upto = n_lo;
         }
-        int64_t r = s - from(p, lo + 1, lane);  // among the pairs that see exactly lo
+        int64_t r = s - above;  // among the pairs that see exactly `level`
         for (int i = 0; i < p.B; i += 32) {
             int q, k;
             lens(p, i, lane, q, k);
-            const int all = count(p, q, k, lo), c = all - count(p, q, k, lo + 1);
+            const int all = count(p, q, k, level), c = all - count(p, q, k, level + 1);
             int sum = c;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
