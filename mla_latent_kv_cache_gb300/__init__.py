@@ -422,19 +422,22 @@ def _here(where, names, tensors) -> None:
     """Every tensor (but the last, which need not be given) is a CUDA tensor on
     the current device, where the library launches. A call of a few microseconds
     is mostly its checks, so the common case is a comparison of device numbers."""
-    dev = _current_device() if _is_cuda(tensors[0]) else -2
-    *needed, last = tensors
-    for t in needed:
-        if not _is_cuda(t) or t.get_device() != dev:
-            break
-    else:
-        if last is None or (_is_cuda(last) and last.get_device() == dev):
-            return
-    for name, t in zip(names, needed):
+    first = tensors[0]
+    if _is_cuda(first):
+        dev = _current_device()
+        try:
+            for t in tensors if tensors[-1] is not None else tensors[:-1]:
+                if t.get_device() != dev:
+                    break
+            else:
+                return
+        except AttributeError:  # not a tensor
+            pass
+    for name, t in zip(names, tensors[:-1]):
         if not _is_cuda(t):
             _refuse(where, f"{name} must be a CUDA tensor")
     _on_device(where, **dict(zip(names, tensors)))
-    _refuse(where, f"the arguments are on {tensors[0].device}, the current device is cuda:{dev}")
+    _refuse(where, f"the arguments are on {first.device}, the current device is cuda:{_current_device()}")
 
 
 def _rows_apart(t) -> bool:

@@ -722,8 +722,10 @@ bool weights_plan(int HQ, int lat_dim, int kind, WeightsParams& p, int* smem_byt
 
 cudaError_t launch_attn_weights(const WeightsMaps& maps, const WeightsParams& p, int kind, bool lsu, int ctas,
                                 int smem_bytes, cudaStream_t stream) {
+    static std::atomic<uint64_t> done[4];
     auto go = [&](auto* k) {
-        cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
+        const cudaError_t e = attribute_once(done[(kind == 1 ? 2 : 0) + (lsu ? 1 : 0)], reinterpret_cast<const void*>(k),
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
         if (e != cudaSuccess) return e;
         k<<<dim3(ctas), kThreads, smem_bytes, stream>>>(maps, p);
         return cudaGetLastError();

@@ -734,7 +734,9 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictPar
 template <int KPT>
 cudaError_t launch_select(const cudaLaunchConfig_t& cfg, const EvictParams& p) {
     // clusters of 16
-    const cudaError_t e = cudaFuncSetAttribute(evict_select_kernel<KPT>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = attribute_once(done, reinterpret_cast<const void*>(evict_select_kernel<KPT>),
+                                         cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     return cudaLaunchKernelEx(&cfg, evict_select_kernel<KPT>, p);
 }
@@ -771,14 +773,18 @@ cudaError_t launch_evict(const EvictParams& p, int sms, cudaStream_t stream) {
     } else if (kpt <= 32) {
         e = launch_select<32>(cfg, p);
     } else {
-        e = cudaFuncSetAttribute(evict_select_long_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelCap * 4);
+        static std::atomic<uint64_t> done{0};
+        e = attribute_once(done, reinterpret_cast<const void*>(evict_select_long_kernel),
+                           cudaFuncAttributeMaxDynamicSharedMemorySize, kSelCap * 4);
         if (e != cudaSuccess) return e;
         cfg.dynamicSmemBytes = kSelCap * 4;
         e = cudaLaunchKernelEx(&cfg, evict_select_long_kernel, p, kSelCap);
     }
     if (e != cudaSuccess) return e;
     constexpr int kMoveSmem = kMoveWarps * 2 * kStage;
-    e = cudaFuncSetAttribute(evict_move_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMoveSmem);
+    static std::atomic<uint64_t> move_done{0};
+    e = attribute_once(move_done, reinterpret_cast<const void*>(evict_move_kernel),
+                       cudaFuncAttributeMaxDynamicSharedMemorySize, kMoveSmem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t mc = {};
     cudaLaunchAttribute ma[1];

@@ -5,7 +5,22 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace mla {
+
+// Sets a kernel's attribute once per device (a driver call on every launch is a
+// fifth of a small call); `done` is the kernel's own, a bit for each device.
+inline cudaError_t attribute_once(std::atomic<uint64_t>& done, const void* kernel, cudaFuncAttribute attr, int value) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
+    if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, attr, value);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+    return e;
+}
 
 // Per-CTA status record (int32 words): 0 status bits, 1 first wait site,
 // 2 its tile, 4 + role: (site << 24) | tile where that role gave up.

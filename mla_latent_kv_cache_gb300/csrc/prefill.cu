@@ -800,7 +800,9 @@ int64_t prefill_pairs(int64_t total_q, int B, int max_q_len, int tile_tokens) {
 
 cudaError_t launch_prefill(const PrefillMaps& maps, const PrefillParams& p, int max_q_len, cudaStream_t stream) {
     const int64_t items = prefill_pairs(p.total_q, p.B, max_q_len, p.tile_tokens) * (p.Hq / p.pack);
-    cudaError_t e = cudaFuncSetAttribute(prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemP);
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = attribute_once(done, reinterpret_cast<const void*>(prefill_kernel),
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemP);
     if (e != cudaSuccess) return e;
     prefill_kernel<<<dim3(static_cast<unsigned>(items)), kThreadsP, kSmemP, stream>>>(maps, p);
     return cudaGetLastError();
