@@ -97,6 +97,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_long_kernel(const
     const int CL = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
     const int b = static_cast<int>(blockIdx.x) / CL;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    griddep_wait();  // the kernel before may still be writing the inputs
     if (tid == 0) griddep_launch_dependents();
 
     const int T0 = max(__ldg(p.seq_lens + b), 0);
@@ -330,6 +331,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Evic
         if (CL > 1) cluster.sync();
         else __syncthreads();
     };
+    griddep_wait();  // the kernel before may still be writing the inputs
     if (tid == 0) griddep_launch_dependents();
 
     const int T0 = max(__ldg(p.seq_lens + b), 0);
@@ -628,6 +630,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictPar
         bulk_commit();
     };
     griddep_wait();
+    if (tid == 0) griddep_launch_dependents();
     for (int b0 = 0; b0 < p.B; b0 += kMoveReqs) {
         const int nb = min(kMoveReqs, p.B - b0);
         // prefix sums of the counts of requests b0 .. b0 + nb (kPer a thread)
@@ -753,7 +756,9 @@ cudaError_t launch_evict(const EvictParams& p, int sms, cudaStream_t stream) {
     const int kpt = keys(CL);
     if (kpt > 32) CL = 8;  // evict_select_long_kernel
     cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = CL;
     attr[0].val.clusterDim.y = 1;
@@ -762,7 +767,7 @@ cudaError_t launch_evict(const EvictParams& p, int sms, cudaStream_t stream) {
     cfg.blockDim = dim3(kSelThreads);
     cfg.stream = stream;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     cudaError_t e;
     if (kpt <= 4) {
         e = launch_select<4>(cfg, p);
