@@ -323,9 +323,10 @@ MLA_API int mla_prefill(const void* q, int64_t q_stride_t, int64_t q_stride_h, c
  *                 + sum over rows r = (b * q_len + t) * Hq + h that see j of
  *                   exp(scale * (q_lat[r] . c_j + q_pe[r] . k_pe_j) - lse[r])
  * (row r sees tokens 0 .. seq_lens[b] - q_len + t, as in mla_decode; a row
- * whose lse is -inf adds nothing). Every row's terms sum to 1. Other entries
- * of weights are not touched. With decay 0 the old values are not read, so the
- * first call needs no initialised buffer.
+ * whose lse is -inf adds nothing). Every row's terms sum to 1, as nearly as its
+ * lse is that of its scores. Other entries of weights are not touched, and
+ * tokens at or past max_len are not read. With decay 0 the old values are not
+ * read, so the first call needs no initialised buffer.
  *   q_lat, q_pe, cache, num_slots, page_size, block_table, seq_lens, scale
  *                as for mla_decode. The queries whose attention counts need not
  *                be the last decode's: any q_len queries at the end of the

@@ -154,6 +154,29 @@ def test_prompt_to_bounded_cache(kind):
         assert set(range(min(4, n))) <= set(kept) and set(range(max(0, n + 3 - 16), n + 3)) <= set(kept)
 
 
+def test_calls_without_work():
+    e = lambda *n, dt=torch.bfloat16: torch.empty(n, dtype=dt, device=DEV)
+    i32 = torch.int32
+    m.mla_prefill(e(0, 8, 192), e(0, 2, 128), e(0, 64), e(0, 2, 128), torch.zeros(4, dtype=i32, device=DEV),
+                  torch.zeros(4, dtype=i32, device=DEV), 0, SCALE, e(0, 8, 128), e(0, 8, dt=torch.float32))
+    cache = torch.zeros((64, 1152), dtype=torch.uint8, device=DEV)
+    none = (e(0, 4, dt=i32), e(0, dt=i32))
+    m.mla_attn_weights(e(0, 8, 512), e(0, 8, 64), e(0, 8, dt=torch.float32), cache, 0, 16, *none, 1, SCALE,
+                       e(0, 50, dt=torch.float32))
+    m.mla_cache_evict(cache, 0, 16, *none, e(0, 50, dt=torch.float32), e(0, 50, dt=i32), e(0, dt=i32), 0, 0, e(0, dt=i32),
+                      e(0, 50, dt=torch.float32), e(0, 50, dt=i32), e(0, 52, dt=i32))
+    # requests without tokens, and score rows of no length
+    bt, sl = torch.zeros((2, 4), dtype=i32, device=DEV), torch.zeros(2, dtype=i32, device=DEV)
+    w, pos = torch.ones((2, 5), device=DEV), torch.ones((2, 5), dtype=i32, device=DEV)
+    m.mla_attn_weights(e(2, 8, 512), e(2, 8, 64), torch.zeros((2, 8), device=DEV), cache, 0, 16, bt, sl, 1, SCALE, w)
+    nl, mv = sl + 9, torch.full((2, 7), -1, dtype=i32, device=DEV)
+    m.mla_cache_evict(cache, 0, 16, bt, sl, w, pos, sl + 3, 0, 0, nl, w, pos, mv)
+    assert bool((w == 1).all()) and nl.tolist() == [0, 0] and mv[:, :2].tolist() == [[0, 0], [0, 0]]
+    m.mla_cache_evict(cache, 0, 16, bt, sl + 6, w[:, :0], pos[:, :0], sl + 3, 0, 0, nl, w[:, :0], pos[:, :0], mv)
+    torch.cuda.synchronize()
+    assert nl.tolist() == [0, 0] and not bool(cache.any())
+
+
 def test_two_streams_at_once():
     # the same kernels twice at the same time share nothing
     r = _Loop(0, [700, 900])

@@ -97,6 +97,16 @@ def test_page_sizes(kind, page):
     _check(_workload(kind, 16, 2, page, LENS, seed=page))
 
 
+@pytest.mark.parametrize("kind,page,Hq,Qt", [(0, 7, 128, 1), (0, 3, 100, 3), (1, 5, 96, 1), (1, 1, 64, 4)])
+def test_odd_pages_with_a_short_ring(kind, page, Hq, Qt):
+    # many query rows leave four blocks to the four warps that read odd pages
+    _check(_workload(kind, Hq, Qt, page, LENS + [1100], seed=page))
+
+
+def test_odd_pages_of_a_wide_row():
+    _check(_workload(0, 40, 1, 7, LENS, seed=3, lat_dim=1792))
+
+
 @pytest.mark.parametrize("lat_dim,Hq", [(256, 16), (256, 40), (768, 16), (768, 100), (1792, 8), (1792, 40)])
 def test_other_latent_widths(lat_dim, Hq):
     _check(_workload(0, Hq, 1, 16, LENS, seed=lat_dim, lat_dim=lat_dim))
