@@ -303,9 +303,11 @@ MLA_API int mla_decode_varlen(const void* q_lat, const void* q_pe, int64_t total
  *                gave up (outputs are invalid).
  * Scores, softmax sums and outputs accumulate in fp32; probabilities are
  * rounded to bf16 for the product with v. A NaN or infinity in a key or value
- * that a query does not see does not reach it (queries beside it are then
- * formed again one by one, which is slow). Hq must be a multiple of Hkv. The
- * result is the same bit for bit on every run.
+ * that a query does not see does not reach it: rows outside the sequence may
+ * hold anything, and where a later value of the sequence itself is not finite
+ * the queries less than a tile before it are formed again one by one, which is
+ * slow. Hq must be a multiple of Hkv. The result is the same bit for bit on
+ * every run.
  */
 MLA_API int mla_prefill(const void* q, int64_t q_stride_t, int64_t q_stride_h, const void* k_nope,
                         int64_t k_stride_t, int64_t k_stride_h, const void* k_pe, int64_t k_pe_stride, const void* v,

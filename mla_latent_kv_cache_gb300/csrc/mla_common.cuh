@@ -76,10 +76,12 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
 }
 
 // Slow path of the waits below: spins until the phase completes, `abort` is
-// raised by another role, or kWaitLimitNs passes (returns false then).
-template <bool kCluster>
+// raised by another role, or kWaitLimitNs passes (returns false then). kAlive:
+// the limit begins again whenever abort[1] has changed.
+template <bool kCluster, bool kAlive = false>
 static __device__ __noinline__ bool mbar_wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort) {
-    const unsigned long long t0 = globaltimer_ns();
+    unsigned long long t0 = globaltimer_ns();
+    int seen = kAlive ? abort[1] : 0;
     for (uint32_t i = 1;; ++i) {
         uint32_t ok;
         if (kCluster)
@@ -99,7 +101,11 @@ static __device__ __noinline__ bool mbar_wait_slow(uint64_t* bar, uint32_t parit
         if (ok) return true;
         if ((i & 63) == 0) {
             if (*abort) return false;
-            if (globaltimer_ns() - t0 > kWaitLimitNs) return false;
+            if (globaltimer_ns() - t0 > kWaitLimitNs) {
+                if (!kAlive || abort[1] == seen) return false;
+                seen = abort[1];
+                t0 = globaltimer_ns();
+            }
         }
     }
 }

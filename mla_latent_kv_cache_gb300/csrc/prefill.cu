@@ -35,8 +35,10 @@
 //
 // Keys past a sequence's end and masked ones have probability 0, which keeps
 // finite values of theirs out of the sums. A NaN or infinity there would still
-// spread (0 times it is NaN), so a row whose O comes out non-finite is formed
-// again by its warp from the keys that it sees alone.
+// spread (0 times it is NaN). So V past the sequence's end is cleared in shared
+// memory (a buffer longer than its sequences holds anything there), and a row
+// whose O comes out non-finite though the cause may lie behind what it sees is
+// formed again by its warp from the keys that it sees alone.
 #include <climits>
 
 #include "launch.cuh"
@@ -70,7 +72,7 @@ struct PCtrl {
     uint64_t s_full[2], p_half[2], p_full[2], o_full[2], fin;
     uint64_t item_full[kItems], item_empty[kItems], more_full, want;
     uint32_t tmem_base;
-    int abort;
+    int stop[2];             // abort flag, and a count that goes up while rows are formed again
     PItem item[kItems];  // h < 0: no more
     alignas(16) uint4 more;  // what a request for a pending CTA answered
 };
@@ -128,7 +130,14 @@ __device__ __forceinline__ void tmem_ld_end(uint32_t (&r)[32]) {
 
 __device__ __forceinline__ void p_fail(const PrefillParams& p, PCtrl* c) {
     if (p.status) atomicOr(p.status, kErrWaitTimeout);
-    *const_cast<volatile int*>(&c->abort) = 1;
+    *const_cast<volatile int*>(&c->stop[0]) = 1;
+}
+
+// mbar_wait that gives up only when nothing goes on: rows formed again over a
+// long context take longer than a wait's limit.
+__device__ __forceinline__ bool p_wait(uint64_t* bar, uint32_t parity, volatile int* stop) {
+    if (mbar_try_wait(bar, parity)) return true;
+    return mbar_wait_slow<false, true>(bar, parity, stop);
 }
 
 // A sequence's first row and its rows, of prefix sums clamped to [0, total].
@@ -258,14 +267,38 @@ __device__ __forceinline__ int64_t answered_cta(const uint4* src) {
     return got ? static_cast<int64_t>(x) : -1;
 }
 
+// The first (or last) of keys from .. to - 1 whose V is not finite, or INT_MAX
+// (-1); by a whole warp, 16 keys at a time.
+__device__ __noinline__ int p_bad_value(const PrefillParams& p, int hk, int64_t k0, int from, int to, bool last, int lane,
+                                        int* alive) {
+    const __nv_bfloat16* v = p.v + k0 * p.v_st + hk * p.v_sh + (lane & 15) * 8;
+    auto bad = [](uint32_t x) { return (x & 0x7f80u) == 0x7f80u || (x & 0x7f800000u) == 0x7f800000u; };
+    const int none = last ? -1 : INT_MAX;
+    for (int c = 0; c < to - from; c += 16) {
+        if (lane == 0 && c % 32768 == 0) atomicAdd(alive, 1);
+        const int j0 = last ? to - 16 - c : from + c;
+        int at = none;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int j = j0 + 2 * i + (lane >> 4);
+            const uint4 x = *reinterpret_cast<const uint4*>(v + min(max(j, from), to - 1) * p.v_st);
+            if (j >= from && j < to && (bad(x.x) || bad(x.y) || bad(x.z) || bad(x.w))) at = last ? max(at, j) : min(at, j);
+        }
+        at = last ? __reduce_max_sync(0xffffffffu, at) : __reduce_min_sync(0xffffffffu, at);
+        if (at != none) return at;
+    }
+    return none;
+}
+
 // A row again from the keys that it sees alone, by its whole warp (V of a
-// visible key may be non-finite, and then so is the row): 32 keys at a time, a
-// lane forms the score of one, and four of the 128 sums over them.
+// visible key may be non-finite, and then so is the row): 32 keys at a time.
+// Eight lanes form the score of one of four keys, each over 24 of its dims, and
+// a lane forms four of the 128 sums.
 __device__ __noinline__ void p_row_again(const PrefillParams& p, int64_t qrow, int h, int hk, int64_t k0, int vis,
-                                         float m2, float inv_l, int lane) {
+                                         float m2, float inv_l, int lane, int* alive) {
     const __nv_bfloat16* q = p.q + qrow * p.q_st + h * p.q_sh;
-    auto dot8 = [](const __nv_bfloat16* a, const __nv_bfloat16* b, float s) {
-        const uint4 x = *reinterpret_cast<const uint4*>(a), y = *reinterpret_cast<const uint4*>(b);
+    auto unit = [](const __nv_bfloat16* a) { return *reinterpret_cast<const uint4*>(a); };
+    auto dot8 = [](const uint4& x, const uint4& y, float s) {
         const __nv_bfloat162 *xa = reinterpret_cast<const __nv_bfloat162*>(&x), *yb = reinterpret_cast<const __nv_bfloat162*>(&y);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -275,19 +308,27 @@ __device__ __noinline__ void p_row_again(const PrefillParams& p, int64_t qrow, i
         }
         return s;
     };
+    const int u8 = (lane & 7) * 8;
+    const uint4 q0 = unit(q + u8), q1 = unit(q + 64 + u8), q2 = unit(q + 128 + u8);
     float acc[4] = {0.f, 0.f, 0.f, 0.f};
     for (int j0 = 0; j0 < vis; j0 += 32) {
-        const int64_t kr = k0 + min(j0 + lane, vis - 1);
-        const __nv_bfloat16 *kn = p.k_nope + kr * p.k_st + hk * p.k_sh, *kp = p.k_pe + kr * p.kp_st;
-        float s = 0.f;
-#pragma unroll 4
-        for (int i = 0; i < 16; ++i) s = dot8(q + 8 * i, kn + 8 * i, s);
-#pragma unroll 4
-        for (int i = 0; i < 8; ++i) s = dot8(q + 128 + 8 * i, kp + 8 * i, s);
+        if (lane == 0 && j0 % 32768 == 0) atomicAdd(alive, 1);
+        float s = 0.f;  // of key j0 + lane
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {  // keys j0 + 4 i .. j0 + 4 i + 3
+            const int64_t kr = k0 + min(j0 + 4 * i + (lane >> 3), vis - 1);
+            const __nv_bfloat16 *kn = p.k_nope + kr * p.k_st + hk * p.k_sh + u8, *kp = p.k_pe + kr * p.kp_st + u8;
+            float d = dot8(q2, unit(kp), dot8(q1, unit(kn + 64), dot8(q0, unit(kn), 0.f)));
+            d += __shfl_xor_sync(0xffffffffu, d, 1);
+            d += __shfl_xor_sync(0xffffffffu, d, 2);
+            d += __shfl_xor_sync(0xffffffffu, d, 4);
+            const float t = __shfl_sync(0xffffffffu, d, (lane & 3) * 8);
+            if (lane >> 2 == i) s = t;
+        }
         const float w = ex2(fmaf(s, p.scale_log2, -m2)) * inv_l;
         const int n = min(32, vis - j0);
         const __nv_bfloat16* v = p.v + (k0 + j0) * p.v_st + hk * p.v_sh + 4 * lane;
-#pragma unroll 4
+#pragma unroll 8
         for (int j = 0; j < n; ++j) {
             const float wj = __shfl_sync(0xffffffffu, w, j);
             const uint2 x = *reinterpret_cast<const uint2*>(v + j * p.v_st);
@@ -332,7 +373,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         mbar_init(&ctrl->more_full, 1);
         mbar_init(&ctrl->want, 1);
         mbar_init(&ctrl->fin, 1);
-        ctrl->abort = 0;
+        ctrl->stop[0] = ctrl->stop[1] = 0;
         fence_mbar_init();
     }
     if (warp == 8) {
@@ -376,7 +417,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = ctrl->tmem_base;
-    volatile int* abort = &ctrl->abort;
+    volatile int* abort = ctrl->stop;
 
     // The next item of this CTA, held by a whole warp until it gives it back;
     // null at the end (or on failure).
@@ -384,7 +425,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
     bool ok = true;
     auto take = [&]() -> const PItem* {
         const int k = taken % kItems;
-        if (!__all_sync(0xffffffffu, mbar_wait(&ctrl->item_full[k], (taken / kItems) & 1, abort))) {
+        if (!__all_sync(0xffffffffu, p_wait(&ctrl->item_full[k], (taken / kItems) & 1, abort))) {
             ok = false;
             return nullptr;
         }
@@ -411,7 +452,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                 ask_for_cta(&ctrl->more, &ctrl->more_full);
             }
             on_its_way = true;
-            if (!__all_sync(0xffffffffu, mbar_wait(&ctrl->more_full, asked & 1, abort))) {
+            if (!__all_sync(0xffffffffu, p_wait(&ctrl->more_full, asked & 1, abort))) {
                 ok = false;
                 return;
             }
@@ -424,7 +465,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         while (ok) {
             const int k = taken % kItems;
             if (taken >= kItems &&
-                !__all_sync(0xffffffffu, mbar_wait(&ctrl->item_empty[k], static_cast<uint32_t>(taken / kItems - 1) & 1, abort))) {
+                !__all_sync(0xffffffffu, p_wait(&ctrl->item_empty[k], static_cast<uint32_t>(taken / kItems - 1) & 1, abort))) {
                 ok = false;
                 break;
             }
@@ -433,7 +474,11 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                 mbar_arrive(&ctrl->item_full[k]);
             }
             if (next.h < 0) break;
-            if (!__all_sync(0xffffffffu, mbar_wait(&ctrl->want, taken & 1, abort))) {
+            // (an item may take long: as long as the loader, whose own waits end)
+            bool there;
+            do there = p_wait(&ctrl->want, taken & 1, abort);
+            while (!there && !*abort);
+            if (!__all_sync(0xffffffffu, there)) {
                 ok = false;
                 break;
             }
@@ -461,7 +506,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
             if (lane == 0) {
                 auto load_q = [&](int i, int n) {
                     if (n == 0 || !ok) return;
-                    if (nq[i] > 0 && !mbar_wait(&ctrl->q_empty[i], (nq[i] - 1) & 1, abort)) {
+                    if (nq[i] > 0 && !p_wait(&ctrl->q_empty[i], (nq[i] - 1) & 1, abort)) {
                         ok = false;
                         return;
                     }
@@ -477,7 +522,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                     if (j == max(nk - kAhead, 0)) mbar_arrive(&ctrl->want);
                     for (int x = 0; x < 5; ++x, ++u) {
                         const uint32_t slot = u % kSlots;
-                        if (u >= kSlots && !mbar_wait(&ctrl->blk_empty[slot], ((u / kSlots) - 1) & 1, abort)) {
+                        if (u >= kSlots && !p_wait(&ctrl->blk_empty[slot], ((u / kSlots) - 1) & 1, abort)) {
                             ok = false;
                             break;
                         }
@@ -524,7 +569,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         uint32_t np0 = 0, np1 = 0;       // probabilities taken of each
         int n0 = 0, n1 = 0;              // the item's key tiles
         auto wait_blk = [&](uint32_t u) {
-            if (ok && !mbar_wait(&ctrl->blk_full[u % kSlots], (u / kSlots) & 1, abort)) ok = false;
+            if (ok && !p_wait(&ctrl->blk_full[u % kSlots], (u / kSlots) & 1, abort)) ok = false;
         };
         auto scores = [&](int i, int j, int ni) {
 #pragma unroll
@@ -561,13 +606,13 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         auto step = [&](int i, int j, int ni, uint32_t& np) {  // P_i(j) V, then the scores of the next key tile
             if (!ok || j >= ni) return;
             // (the item's first P_i comes after the last one's O_i was read)
-            if (!mbar_wait(&ctrl->p_half[i], np & 1, abort)) ok = false;
+            if (!p_wait(&ctrl->p_half[i], np & 1, abort)) ok = false;
             wait_blk(u0 + 5 * j + 3);
             if (!ok) return;
             tc_fence_after();
             values(i, j, 0);
             wait_blk(u0 + 5 * j + 4);
-            if (!mbar_wait(&ctrl->p_full[i], np & 1, abort)) {
+            if (!p_wait(&ctrl->p_full[i], np & 1, abort)) {
                 ok = false;
                 return;
             }
@@ -580,7 +625,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         };
         auto start = [&](int i, int ni, uint32_t& nq) {
             if (!ok || ni == 0) return;
-            if (!mbar_wait(&ctrl->q_full[i], nq & 1, abort)) {
+            if (!p_wait(&ctrl->q_full[i], nq & 1, abort)) {
                 ok = false;
                 return;
             }
@@ -617,12 +662,13 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         const uint32_t tS = tmem + i * 128 + lanes, tO = tmem + 256 + i * 128 + lanes;
         const uint64_t c2 = pack2(p.scale_log2, p.scale_log2);
         uint32_t ns = 0, no = 0;  // score tiles and outputs taken
+        uint32_t u0 = 0;          // the item's first block
         while (const PItem* item = take()) {
             const int n = i == 0 ? item->n0 : item->n1;
             const int vis = p_seen(p.causal, item->q_len, item->k_len, item->t0 + tok);  // keys 0 .. vis - 1
             float m = -INFINITY, l = 0.f;                             // m in log2 units
             for (int j = 0; j < n && ok; ++j, ++ns) {
-                if (!__all_sync(0xffffffffu, mbar_wait(&ctrl->s_full[i], ns & 1, abort))) {
+                if (!__all_sync(0xffffffffu, p_wait(&ctrl->s_full[i], ns & 1, abort))) {
                     ok = false;
                     break;
                 }
@@ -669,6 +715,21 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                         }
                     }
                 }
+                if (cut && item->k_len < (j + 1) * kKT) {
+                    // V past the sequence's end: zeros (both tiles' threads write them)
+                    const uint32_t uv = u0 + 5 * j + 3;
+                    for (int h = 0; h < 2; ++h)
+                        if (!__all_sync(0xffffffffu, p_wait(&ctrl->blk_full[(uv + h) % kSlots], ((uv + h) / kSlots) & 1, abort)))
+                            ok = false;
+                    if (!ok) break;
+                    const int end = item->k_len - j * kKT;
+                    for (int x = row; x < (kKT - end) * 16; x += kQT) {
+                        const int r = end + x / 16;
+                        *reinterpret_cast<uint4*>(ring + (uv + r / 64) % kSlots * kBlkP + (x / 8 & 1) * (kBlkP / 2) +
+                                                  r % 64 * 128 + x % 8 * 16) = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    fence_proxy_async_smem();
+                }
                 const float base = m == -INFINITY ? 0.f : m;
                 const uint64_t nb = pack2(-base, -base);
                 tmem_ld_x32_begin(tS, s[0]);
@@ -708,7 +769,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
             }
             // ------------------------------------------------------ epilogue
             if (ok && n > 0) {
-                if (!__all_sync(0xffffffffu, mbar_wait(&ctrl->o_full[i], no & 1, abort))) ok = false;
+                if (!__all_sync(0xffffffffu, p_wait(&ctrl->o_full[i], no & 1, abort))) ok = false;
                 ++no;
             }
             if (!ok) break;
@@ -756,8 +817,18 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                         *reinterpret_cast<uint4*>(out + rows[k] * kDv + c) = make_uint4(x[k][0], x[k][1], x[k][2], x[k][3]);
             }
             if (mine) p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
-            // rows to form again: O is not finite though the sums are
+            // O is not finite though the sums are: form the row again if a value that is
+            // not lies in its last tile behind what it sees, or if none does that it sees
+            // (large values whose weighted sum passes fp32's range, though not their mean)
             unsigned again = __ballot_sync(0xffffffffu, mine && !fine && l > 0.f && l < INFINITY && fabsf(m) < INFINITY);
+            if (again) {
+                const int hk = item->h / group, end = min(n * kKT, item->k_len);
+                const bool these = again >> lane & 1u;
+                const int low = __reduce_min_sync(0xffffffffu, these ? vis : INT_MAX);
+                const int behind = p_bad_value(p, hk, item->k_row, low, end, true, lane, &ctrl->stop[1]);
+                const int first = p_bad_value(p, hk, item->k_row, 0, end, false, lane, &ctrl->stop[1]);
+                again = __ballot_sync(0xffffffffu, these && (behind >= vis || first >= vis));
+            }
             while (again) {
                 const int r = __ffs(again) - 1;
                 again &= again - 1;
@@ -765,10 +836,11 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                 const int hr = __shfl_sync(0xffffffffu, h, r);
                 p_row_again(p, item->q_row + __shfl_sync(0xffffffffu, t, r), hr, hr / group, item->k_row,
                             __shfl_sync(0xffffffffu, vis, r), __shfl_sync(0xffffffffu, m, r),
-                            __shfl_sync(0xffffffffu, inv, r), lane);
+                            __shfl_sync(0xffffffffu, inv, r), lane, &ctrl->stop[1]);
             }
             // O_i has been read before this warp's next P_i is handed over
             tc_fence_before();
+            u0 += 5 * max(item->n0, item->n1);
             give_back();
         }
         if (!ok && lane == 0) p_fail(p, ctrl);

@@ -218,6 +218,57 @@ def test_what_a_query_does_not_see_does_not_reach_it(where, bad):
         assert bool(near[:, :, other].all())
 
 
+def test_rows_formed_again_over_a_long_context():
+    # the last key's value is not finite and lies in the last key tile of every query:
+    # all but the last are formed again, for longer than the kernel's own waits
+    # last; heads of one group make more items than SMs, so that others wait for these
+    Lq, Lk, Hq = 127, 200063, 320
+    a = _inputs([Lq], [Lk], Hq, 1, seed=21)
+    clean, cl = _call(a)
+    a["v"][Lk - 1, 0, 5] = float("nan")
+    got, gl = _call(a)
+    assert torch.equal(gl, cl)
+    assert bool(torch.isnan(got[-1, :, 5]).all()) and int(torch.isnan(got).sum()) == Hq
+    k = torch.cat([a["k_nope"][:, 0], a["k_pe"]], 1).double()
+    for t, h in ((0, 0), (63, 177), (125, 319)):
+        n = Lk - Lq + t + 1
+        s = SCALE * (k[:n] @ a["q"][t, h].double())
+        A = torch.softmax(s, 0) @ a["v"][:n, 0].double().abs()
+        # rounded probabilities on one side, fp32 additions on both, and both outputs' rounding
+        tol = (2.0 ** -8 + 2 * n * 2.0 ** -24) * A + 2.0 ** -8 * (got[t, h].double().abs() + clean[t, h].double().abs())
+        assert bool(((got[t, h].double() - clean[t, h].double()).abs() <= tol).all())
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("Hq,Hkv", [(4, 4), (8, 2), (16, 1)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_what_lies_behind_a_sequence_changes_nothing(Hq, Hkv, bad, causal):
+    # rows of no sequence at the end of longer buffers, and those of the next sequence
+    q, k = [130, 1, 64, 300, 77], [130, 257, 63, 449, 640]
+    a = _inputs(q + [0], k + [200], Hq, Hkv, seed=22)
+    T = sum(k)
+    a["cu_q"], a["cu_k"] = a["cu_q"][:-1].contiguous(), a["cu_k"][:-1].contiguous()
+    clean, cl = _call(a, causal=causal)
+    for x in ("v", "k_nope", "k_pe"):
+        a[x][T:] = bad
+    got, gl = _call(a, causal=causal)
+    assert torch.equal(got, clean) and torch.equal(gl, cl)
+    a["v"][sum(k[:3]):] = bad  # the last two sequences' values
+    got, gl = _call(a, causal=causal)
+    n = sum(q[:3])
+    assert torch.equal(got[:n], clean[:n]) and torch.equal(gl, cl)
+    assert not bool(torch.isfinite(got[n:]).any())
+
+
+def test_values_whose_sum_passes_the_range():
+    # 2^127 under hundreds of weights near 1: past fp32, while their mean is not; the
+    # probabilities' rounding and the output's are off by 2^-8 at most each
+    a = _inputs([200], [600], 2, 1, seed=23)
+    a["v"].fill_(2.0 ** 127)
+    out, _ = _call(a)
+    assert bool(((out.double() / 2.0 ** 127 - 1).abs() <= 2.0 ** -7).all())
+
+
 def test_prefix_sums_past_the_rows_are_clamped():
     a = _inputs([100, 60], [100, 60], 2, 2, seed=11)
     want, wl = _call(a)
