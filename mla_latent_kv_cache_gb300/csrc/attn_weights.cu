@@ -581,9 +581,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = true;
         while (ok && !wk.done()) {
             if (grp == 1 && wk.newq) {
-                if (wk.q > 0 && !__all_sync(0xffffffffu, mbar_wait(&ctrl->q_empty, (wk.q - 1) & 1, abort))) {
-                    ok = false;
-                    break;
+                if (wk.q > 0) {
+                    // (the last queries may be in use for long: as long as the products, whose
+                    // own waits end)
+                    bool there;
+                    do there = mbar_wait(&ctrl->q_empty, (wk.q - 1) & 1, abort);
+                    while (!there && !*abort);
+                    if (!__all_sync(0xffffffffu, there)) {
+                        ok = false;
+                        break;
+                    }
                 }
                 load_q();
             }
@@ -602,10 +609,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             const float* lse2 = ctrl->lse2[wk.q % kQBufs];
             const float* qs = ctrl->qs[wk.q % kQBufs];
-            // columns [c0, c1) of these rows see the token: query t sees tokens up to T - Qt + t
-            const int r0 = wk.g * NP;
-            const int c1 = min(NP, p.HQ - r0);
-            const int c0 = mine ? max(0, max(0, tok - (wk.T - p.Qt)) * p.Hq - r0) : 0;
+            // columns from c0 on see the token: query t sees tokens up to T - Qt + t
+            const int c0 = mine ? max(0, max(0, tok - (wk.T - p.Qt)) * p.Hq - wk.g * NP) : 0;
             float4 sc = make_float4(0.f, 0.f, 0.f, 0.f);
             if (KIND == 1) {
                 const int sl = n % kScSlots;
@@ -654,12 +659,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&ctrl->s_free[buf]);
                 }
+                // columns that see the token and whose rows add (a NaN in the token stays
+                // out of the others)
+                uint32_t add = __ballot_sync(0xffffffffu, lane < W && !(lse2[cc + lane % W] == INFINITY));
+                add &= c0 - cc >= 32 ? 0u : 0xffffffffu << max(c0 - cc, 0);
 #pragma unroll
                 for (int k = 0; k < W; ++k) {
                     const int c = cc + k;
                     const float v = KIND == 1 ? fmaf(x[k], qs[c], __uint_as_float(a[k])) : x[k];
                     const float e = ex2(fmaf(v, p.scale_log2, -lse2[c]));
-                    acc += c >= c0 && c < c1 ? e : 0.f;
+                    acc += add >> k & 1u ? e : 0.f;
                 }
             };
             int cc = cb;

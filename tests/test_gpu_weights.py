@@ -191,6 +191,20 @@ def test_nan_in_one_token_stays_in_it(kind):
     assert torch.equal(got[0, keep], clean[0, keep])
 
 
+@pytest.mark.parametrize("kind", [0, 1])
+def test_rows_that_add_nothing_add_nothing_to_a_nan_token(kind):
+    wl = _workload(kind, 20, 2, 16, [200], seed=10)
+    lse = _lse(wl, keep_ref.scores(wl, wl.pool)[0])[1]
+    wl.pool[int(wl.block_table[0, 4]) * 16 + 6] = 0xFF  # token 70, NaN in every field of either kind
+    none = torch.full_like(lse, float("-inf"))
+    w, _ = _run(wl, none, torch.ones((1, 200), device=DEV), 1.0)
+    assert bool((w == 1).all())
+    some = none.clone()
+    some.view(-1)[7] = lse.view(-1)[7]
+    w, _ = _run(wl, some, torch.ones((1, 200), device=DEV), 1.0)
+    assert torch.isnan(w[0]).nonzero().view(-1).tolist() == [70]
+
+
 def test_fp8_queries_of_any_magnitude():
     # rows whose values span many powers of two, tiny rows, a zero row
     wl = _workload(1, 16, 1, 16, [200], seed=12)
