@@ -455,7 +455,7 @@ def _status_ptr(where, status):
     return status.data_ptr()
 
 
-def _table_args(where, block_table, seq_lens, cache) -> int:
+def _table_args(where, block_table, seq_lens, cache, max_len, page_size) -> int:
     """Checks of a paged batch shared by the calls that keep the cache; the number of requests."""
     if not cache.is_contiguous():
         _refuse(where, "cache must be contiguous")
@@ -466,6 +466,13 @@ def _table_args(where, block_table, seq_lens, cache) -> int:
     B = seq_lens.numel()
     if block_table.shape[0] < B:
         _refuse(where, f"block_table has {block_table.shape[0]} rows for {B} requests")
+    stride = block_table.stride(0)
+    if stride > block_table.shape[1] and B > 0 and page_size > 0:
+        # columns of a wider table: a row reaches to the next one, as far as max_len
+        # goes, and the last must lie in memory as well
+        last = (B - 1) * stride + min(stride, -(-max_len // page_size))
+        if last > block_table.untyped_storage().nbytes() // 4 - block_table.storage_offset():
+            _refuse(where, f"block_table's last row ends before the pages of {max_len} tokens")
     return B
 
 
@@ -528,7 +535,8 @@ def mla_attn_weights(q_lat, q_pe, lse, cache, cache_kind, page_size, block_table
     contiguous rows. `status` (a device int32 tensor) collects status bits."""
     where = "mla_attn_weights"
     _here(where, _WEIGHTS_NAMES, (q_lat, q_pe, lse, cache, block_table, seq_lens, weights, status))
-    B = _table_args(where, block_table, seq_lens, cache)
+    max_len = weights.shape[-1] if weights.dim() else 0
+    B = _table_args(where, block_table, seq_lens, cache, max_len, int(page_size))
     Hq = q_lat.shape[-2] if q_lat.dim() >= 2 else 0
     rows = B * int(q_len) * Hq
     if q_lat.dtype is not torch.bfloat16 or q_pe.dtype is not torch.bfloat16:
@@ -543,7 +551,6 @@ def mla_attn_weights(q_lat, q_pe, lse, cache, cache_kind, page_size, block_table
         _refuse(where, f"weights must be a fp32 [>= {B}, max_len] tensor with contiguous rows")
     st = _status_ptr(where, status)
     rb = _row_bytes(where, cache_kind, lat_dim)
-    max_len = weights.shape[1]
     _check(load().mla_attn_weights(
         q_lat.data_ptr(), q_pe.data_ptr(), lse.data_ptr(), cache.data_ptr(), int(cache_kind), int(lat_dim),
         cache.nbytes // rb, int(page_size), block_table.data_ptr(), block_table.stride(0), seq_lens.data_ptr(), B,
@@ -566,7 +573,7 @@ def mla_cache_evict(cache, cache_kind, page_size, block_table, seq_lens, weights
     where = "mla_cache_evict"
     _here(where, _EVICT_NAMES, (cache, block_table, seq_lens, weights, positions, budgets, new_seq_lens, new_weights,
                                 new_positions, moves, status))
-    B = _table_args(where, block_table, seq_lens, cache)
+    B = _table_args(where, block_table, seq_lens, cache, weights.shape[-1] if weights.dim() else 0, int(page_size))
     if weights.dim() != 2 or weights.shape[0] < B or not _rows_apart(weights):
         _refuse(where, f"weights must be [>= {B}, max_len] with contiguous rows")
     shape, strides, f32, i32 = weights.shape, weights.stride(), torch.float32, torch.int32

@@ -227,3 +227,15 @@ def test_weights_binding_refuses(fake, over, words):
 def test_evict_binding_refuses(fake, over, words):
     _refused(lambda: _evict(**over), words)
     assert fake.calls == []
+
+
+def test_columns_of_a_wider_table(fake):
+    table = i32(2, 8)[:, 4:]  # the last row ends four pages of 16 after it begins
+    _weights(block_table=table, weights=f32(2, 64))
+    _evict(block_table=table)
+    _weights(block_table=i32(2, 8)[:, :4], weights=f32(2, 999))
+    assert len(fake.calls) == 3
+    _refused(lambda: _weights(block_table=table, weights=f32(2, 65)), "block_table")
+    _refused(lambda: _evict(block_table=table, weights=f32(2, 65), positions=i32(2, 65), new_weights=f32(2, 65),
+                            new_positions=i32(2, 65), moves=i32(2, 67)), "block_table")
+    assert len(fake.calls) == 3
