@@ -309,7 +309,7 @@ __device__ __forceinline__ uint32_t warps_before(uint32_t v, uint32_t* buf, uint
 }
 
 struct SelectRegShared {
-    uint32_t hist[3][kSelBins];        // this CTA's counts of each digit, read by the cluster
+    uint32_t hist[3][kSelBins];        // this CTA's counts of each digit
     uint32_t slice[3][kSelBins / 2];   // the cluster's counts of this CTA's slice of the bins
     uint32_t slice_total[3];
     uint32_t warp[6][kSelWarps];  // per-warp values of the passes
@@ -367,11 +367,31 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Evic
     }
 
     // ---- the newest position, which the protected recent ones are counted from
-    int mx = INT_MIN;
+    // (few tokens a thread: their scores are asked for at once and both are held)
+    constexpr int kIn = KPT < 8 ? KPT : 8;
+    constexpr bool kHold = KPT <= kIn;
+    float wv[kIn];
+    int ps[kIn];
+    auto read = [&](int k0) {
 #pragma unroll
-    for (int k = 0; k < KPT; ++k) {
-        const int i = at0 + 32 * k;
-        mx = max(mx, k < kn && i < t1 ? pos[i] : INT_MIN);
+        for (int k = 0; k < kIn; ++k) {
+            const int i = at0 + 32 * (k0 + k);
+            const bool in = k0 + k < kn && i < t1;
+            wv[k] = in ? w[i] : 0.f;
+            ps[k] = in ? pos[i] : INT_MIN;
+        }
+    };
+    int mx = INT_MIN;
+    if (kHold) {
+        read(0);
+#pragma unroll
+        for (int k = 0; k < kIn; ++k) mx = max(mx, ps[k]);
+    } else {
+#pragma unroll
+        for (int k = 0; k < KPT; ++k) {
+            const int i = at0 + 32 * k;
+            mx = max(mx, k < kn && i < t1 ? pos[i] : INT_MIN);
+        }
     }
     for (int i = tid; i < 3 * kSelBins; i += kSelThreads) (&sh.hist[0][0])[i] = 0;
     if (CL > 1)
@@ -390,19 +410,10 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Evic
     // new arrays as they are: the places whose token goes are written again when
     // their new token moves in.
     uint32_t key[KPT];
-    constexpr int kIn = KPT < 8 ? KPT : 8;
 #pragma unroll
     for (int k0 = 0; k0 < KPT; k0 += kIn) {
         if (k0 >= kn) break;
-        float wv[kIn];
-        int ps[kIn];
-#pragma unroll
-        for (int k = 0; k < kIn; ++k) {
-            const int i = at0 + 32 * (k0 + k);
-            const bool in = k0 + k < kn && i < t1;
-            wv[k] = in ? w[i] : 0.f;
-            ps[k] = in ? pos[i] : 0;
-        }
+        if (!kHold) read(k0);
 #pragma unroll
         for (int k = 0; k < kIn; ++k) {
             const int i = at0 + 32 * (k0 + k);
@@ -445,18 +456,20 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Evic
             uint32_t c_hi, c_lo = 0, above0 = 0;
             int top;  // this thread's upper bin
             if (CL > 1) {
-                // each CTA sums its slice of the bins over the cluster (every CTA
-                // reading all bins of all others is 16 times the traffic: 9 us a
-                // digit); the slices' totals then say which slice to look into
-                cluster.sync();
+                // each CTA holds the cluster's sums of a slice of the bins, into which the
+                // others add theirs (every CTA reading all bins of all others is 16
+                // times the traffic: 9 us a digit); the slices' totals then say which
+                // slice to look into
+                __syncthreads();
                 const int S = kSelBins / CL;
                 uint32_t* slice = sh.slice[pass];
-                const int from = tid / (S / 2), pair = tid % (S / 2) * 2;
-                const uint2 h = *reinterpret_cast<const uint2*>(cluster.map_shared_rank(hist + rank * S + pair, from));
-                if (h.x) atomicAdd(slice + pair, h.x);
-                if (h.y) atomicAdd(slice + pair + 1, h.y);
+                const int bin = 2 * tid, to = bin / S;  // (a warp's 64 bins lie in one slice)
+                const uint2 h = *reinterpret_cast<const uint2*>(hist + bin);
+                uint32_t* sums = cluster.map_shared_rank(slice + bin % S, to);
+                if (h.x) atomicAdd(sums, h.x);
+                if (h.y) atomicAdd(sums + 1, h.y);
                 const uint32_t sum = __reduce_add_sync(0xffffffffu, h.x + h.y);
-                if (lane == 0 && sum) atomicAdd(&sh.slice_total[pass], sum);
+                if (lane == 0 && sum) atomicAdd(cluster.map_shared_rank(&sh.slice_total[pass], to), sum);
                 cluster.sync();
                 const uint32_t mine = lane < CL ? *cluster.map_shared_rank(&sh.slice_total[pass], lane) : 0u;
                 uint32_t up = mine;  // keys in this slice and those above it
