@@ -440,10 +440,12 @@ def _here(where, names, tensors) -> None:
     _refuse(where, f"the arguments are on {first.device}, the current device is cuda:{_current_device()}")
 
 
-def _rows_apart(t) -> bool:
-    """Contiguous rows of a 2-D tensor that do not share elements."""
-    rows, cols = t.shape
-    s0, s1 = t.stride()
+def _rows_apart(shape, strides) -> bool:
+    """Whether a tensor is 2-D with contiguous rows that do not share elements."""
+    if len(shape) != 2:
+        return False
+    rows, cols = shape
+    s0, s1 = strides
     return (s1 == 1 or cols <= 1) and (s0 >= cols or rows <= 1)
 
 
@@ -455,25 +457,28 @@ def _status_ptr(where, status):
     return status.data_ptr()
 
 
-def _table_args(where, block_table, seq_lens, cache, max_len, page_size) -> int:
-    """Checks of a paged batch shared by the calls that keep the cache; the number of requests."""
+def _table_args(where, block_table, seq_lens, cache, max_len, page_size):
+    """Checks of a paged batch shared by the calls that keep the cache: the number
+    of requests and the table's row stride."""
     if not cache.is_contiguous():
         _refuse(where, "cache must be contiguous")
-    if block_table.dtype is not torch.int32 or block_table.dim() != 2 or block_table.stride(1) != 1:
+    shape, strides, i32 = block_table.shape, block_table.stride(), torch.int32
+    if block_table.dtype is not i32 or len(shape) != 2 or strides[1] != 1:
         _refuse(where, "block_table must be a 2-D int32 tensor with contiguous rows")
-    if seq_lens.dtype is not torch.int32 or not seq_lens.is_contiguous():
+    if seq_lens.dtype is not i32 or not seq_lens.is_contiguous():
         _refuse(where, "seq_lens must be contiguous int32")
     B = seq_lens.numel()
-    if block_table.shape[0] < B:
-        _refuse(where, f"block_table has {block_table.shape[0]} rows for {B} requests")
-    stride = block_table.stride(0)
-    if stride > block_table.shape[1] and B > 0 and page_size > 0:
+    rows, cols = shape
+    if rows < B:
+        _refuse(where, f"block_table has {rows} rows for {B} requests")
+    stride = strides[0]
+    if stride > cols and B > 0 and page_size > 0:
         # columns of a wider table: a row reaches to the next one, as far as max_len
         # goes, and the last must lie in memory as well
         last = (B - 1) * stride + min(stride, -(-max_len // page_size))
         if last > block_table.untyped_storage().nbytes() // 4 - block_table.storage_offset():
             _refuse(where, f"block_table's last row ends before the pages of {max_len} tokens")
-    return B
+    return B, stride
 
 
 _PREFILL_NAMES = ("q", "k_nope", "k_pe", "v", "cu_q_lens", "cu_k_lens", "out", "lse", "status")
@@ -489,12 +494,13 @@ def mla_prefill(q, k_nope, k_pe, v, cu_q_lens, cu_k_lens, max_q_len, scale, out,
     where = "mla_prefill"
     _here(where, _PREFILL_NAMES, (q, k_nope, k_pe, v, cu_q_lens, cu_k_lens, out, lse, status))
     bf16 = torch.bfloat16
-    if q.dim() != 3 or q.shape[2] != 192:
+    q_shape, kv_shape = q.shape, k_nope.shape
+    if len(q_shape) != 3 or q_shape[2] != 192:
         _refuse(where, "q must be [total_q, Hq, 192]")
-    if k_nope.dim() != 3 or k_nope.shape[2] != 128:
+    if len(kv_shape) != 3 or kv_shape[2] != 128:
         _refuse(where, "k_nope must be [total_k, Hkv, 128]")
-    total_q, Hq, _ = q.shape
-    total_k, Hkv, _ = kv_shape = k_nope.shape
+    total_q, Hq, _ = q_shape
+    total_k, Hkv, _ = kv_shape
     if v.shape != kv_shape:
         _refuse(where, "v must have k_nope's shape")
     if k_pe.shape != (total_k, 64):
@@ -508,9 +514,10 @@ def mla_prefill(q, k_nope, k_pe, v, cu_q_lens, cu_k_lens, max_q_len, scale, out,
     if lse.dtype is not torch.float32 or lse.shape != (total_q, Hq) or not lse.is_contiguous():
         _refuse(where, f"lse must be a contiguous fp32 [{total_q}, {Hq}] tensor")
     B = cu_q_lens.numel() - 1
-    if cu_q_lens.dtype is not torch.int32 or not cu_q_lens.is_contiguous() or B < 0:
+    i32 = torch.int32
+    if cu_q_lens.dtype is not i32 or not cu_q_lens.is_contiguous() or B < 0:
         _refuse(where, "cu_q_lens must be contiguous int32 with B + 1 entries")
-    if cu_k_lens.dtype is not torch.int32 or not cu_k_lens.is_contiguous() or cu_k_lens.numel() != B + 1:
+    if cu_k_lens.dtype is not i32 or not cu_k_lens.is_contiguous() or cu_k_lens.numel() != B + 1:
         _refuse(where, "cu_k_lens must be contiguous int32 with as many entries as cu_q_lens")
     st = _status_ptr(where, status)
     # (the stride of a dimension of one entry says nothing)
@@ -535,27 +542,30 @@ def mla_attn_weights(q_lat, q_pe, lse, cache, cache_kind, page_size, block_table
     contiguous rows. `status` (a device int32 tensor) collects status bits."""
     where = "mla_attn_weights"
     _here(where, _WEIGHTS_NAMES, (q_lat, q_pe, lse, cache, block_table, seq_lens, weights, status))
-    max_len = weights.shape[-1] if weights.dim() else 0
-    B = _table_args(where, block_table, seq_lens, cache, max_len, int(page_size))
-    Hq = q_lat.shape[-2] if q_lat.dim() >= 2 else 0
+    w_shape, w_strides = weights.shape, weights.stride()
+    max_len = w_shape[-1] if w_shape else 0
+    B, bt_stride = _table_args(where, block_table, seq_lens, cache, max_len, int(page_size))
+    q_shape = q_lat.shape
+    Hq = q_shape[-2] if len(q_shape) >= 2 else 0
     rows = B * int(q_len) * Hq
-    if q_lat.dtype is not torch.bfloat16 or q_pe.dtype is not torch.bfloat16:
+    bf16, f32 = torch.bfloat16, torch.float32
+    if q_lat.dtype is not bf16 or q_pe.dtype is not bf16:
         _refuse(where, "q_lat and q_pe must be bf16")
     if not q_lat.is_contiguous() or not q_pe.is_contiguous():
         _refuse(where, "q_lat and q_pe must be contiguous")
     if q_lat.numel() != rows * lat_dim or q_pe.numel() != rows * 64:
         _refuse(where, f"q_lat / q_pe hold {q_lat.numel()} / {q_pe.numel()} values, {rows} rows of {lat_dim} / 64 expected")
-    if lse.dtype is not torch.float32 or not lse.is_contiguous() or lse.numel() != rows:
+    if lse.dtype is not f32 or not lse.is_contiguous() or lse.numel() != rows:
         _refuse(where, f"lse must be a contiguous fp32 tensor of {rows} values")
-    if weights.dtype is not torch.float32 or weights.dim() != 2 or weights.shape[0] < B or not _rows_apart(weights):
+    if weights.dtype is not f32 or not _rows_apart(w_shape, w_strides) or w_shape[0] < B:
         _refuse(where, f"weights must be a fp32 [>= {B}, max_len] tensor with contiguous rows")
     st = _status_ptr(where, status)
     rb = _row_bytes(where, cache_kind, lat_dim)
     _check(load().mla_attn_weights(
         q_lat.data_ptr(), q_pe.data_ptr(), lse.data_ptr(), cache.data_ptr(), int(cache_kind), int(lat_dim),
-        cache.nbytes // rb, int(page_size), block_table.data_ptr(), block_table.stride(0), seq_lens.data_ptr(), B,
+        cache.nbytes // rb, int(page_size), block_table.data_ptr(), bt_stride, seq_lens.data_ptr(), B,
         int(q_len), Hq, float(scale), float(decay),
-        weights.data_ptr(), max(weights.stride(0), max_len), max_len, st, int(num_ctas), _stream(stream)), where)
+        weights.data_ptr(), max(w_strides[0], max_len), max_len, st, int(num_ctas), _stream(stream)), where)
 
 
 _EVICT_NAMES = ("cache", "block_table", "seq_lens", "weights", "positions", "budgets", "new_seq_lens", "new_weights",
@@ -573,30 +583,32 @@ def mla_cache_evict(cache, cache_kind, page_size, block_table, seq_lens, weights
     where = "mla_cache_evict"
     _here(where, _EVICT_NAMES, (cache, block_table, seq_lens, weights, positions, budgets, new_seq_lens, new_weights,
                                 new_positions, moves, status))
-    B = _table_args(where, block_table, seq_lens, cache, weights.shape[-1] if weights.dim() else 0, int(page_size))
-    if weights.dim() != 2 or weights.shape[0] < B or not _rows_apart(weights):
-        _refuse(where, f"weights must be [>= {B}, max_len] with contiguous rows")
     shape, strides, f32, i32 = weights.shape, weights.stride(), torch.float32, torch.int32
-    max_len = shape[1]
+    max_len = shape[-1] if shape else 0
+    B, bt_stride = _table_args(where, block_table, seq_lens, cache, max_len, int(page_size))
+    if not _rows_apart(shape, strides) or shape[0] < B:
+        _refuse(where, f"weights must be [>= {B}, max_len] with contiguous rows")
     if (weights.dtype is not f32 or positions.dtype is not i32 or new_weights.dtype is not f32 or
             new_positions.dtype is not i32):
         _refuse(where, "weights and new_weights must be fp32, positions and new_positions int32")
+    one = shape[0] <= 1
     for name, t in (("positions", positions), ("new_weights", new_weights), ("new_positions", new_positions)):
-        if t.shape != shape or (t.stride() != strides and shape[0] > 1):
+        if t.shape != shape or (not one and t.stride() != strides):
             _refuse(where, f"{name} must be a tensor of weights' shape and strides")
     if budgets.dtype is not i32 or not budgets.is_contiguous() or budgets.numel() < B:
         _refuse(where, f"budgets must be contiguous int32 of at least {B} values")
     if new_seq_lens.dtype is not i32 or not new_seq_lens.is_contiguous() or new_seq_lens.numel() < B:
         _refuse(where, f"new_seq_lens must be contiguous int32 of at least {B} values")
-    if moves.dtype is not i32 or moves.dim() != 2 or moves.shape[0] < B or moves.shape[1] < max_len + 2 or not _rows_apart(moves):
+    m_shape, m_strides = moves.shape, moves.stride()
+    if moves.dtype is not i32 or not _rows_apart(m_shape, m_strides) or m_shape[0] < B or m_shape[1] < max_len + 2:
         _refuse(where, f"moves must be an int32 [>= {B}, >= {max_len + 2}] tensor")
     st = _status_ptr(where, status)
     rb = _row_bytes(where, cache_kind, lat_dim)
     _check(load().mla_cache_evict(
-        cache.data_ptr(), int(rb), cache.nbytes // rb, int(page_size), block_table.data_ptr(), block_table.stride(0),
+        cache.data_ptr(), int(rb), cache.nbytes // rb, int(page_size), block_table.data_ptr(), bt_stride,
         seq_lens.data_ptr(), weights.data_ptr(), positions.data_ptr(), max(strides[0], max_len), max_len,
         budgets.data_ptr(), B, int(n_sink), int(n_recent), new_seq_lens.data_ptr(), new_weights.data_ptr(),
-        new_positions.data_ptr(), moves.data_ptr(), max(moves.stride(0), moves.shape[1]), st, _stream(stream)), where)
+        new_positions.data_ptr(), moves.data_ptr(), max(m_strides[0], m_shape[1]), st, _stream(stream)), where)
 
 
 def decode(q_lat, q_pe, cache, cache_kind, page_size, block_table, seq_lens, q_len, scale,
