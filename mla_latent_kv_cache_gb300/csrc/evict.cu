@@ -367,17 +367,18 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Evic
     }
 
     // ---- the newest position, which the protected recent ones are counted from
-    // (few tokens a thread: their scores are asked for at once and both are held)
-    constexpr int kIn = KPT < 8 ? KPT : 8;
-    constexpr bool kHold = KPT <= kIn;
-    float wv[kIn];
+    // (up to 16 tokens a thread: their scores are asked for at once and both are held;
+    // else eight of each at a time)
+    constexpr bool kHold = KPT <= 16;
+    constexpr int kIn = kHold ? KPT : 8;
+    uint32_t key[KPT];  // a score's bits at first
     int ps[kIn];
     auto read = [&](int k0) {
 #pragma unroll
         for (int k = 0; k < kIn; ++k) {
             const int i = at0 + 32 * (k0 + k);
             const bool in = k0 + k < kn && i < t1;
-            wv[k] = in ? w[i] : 0.f;
+            key[k0 + k] = in ? __float_as_uint(w[i]) : 0u;
             ps[k] = in ? pos[i] : INT_MIN;
         }
     };
@@ -406,10 +407,8 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Evic
         newest = __reduce_max_sync(0xffffffffu, lane < CL ? *cluster.map_shared_rank(&sh.newest, lane) : INT_MIN);
     }
     const int64_t recent_from = static_cast<int64_t>(newest) + 1 - p.n_recent;
-    // keys, with eight loads of each kind in flight. Entries below K go to the
-    // new arrays as they are: the places whose token goes are written again when
-    // their new token moves in.
-    uint32_t key[KPT];
+    // keys. Entries below K go to the new arrays as they are: the places whose token
+    // goes are written again when their new token moves in.
 #pragma unroll
     for (int k0 = 0; k0 < KPT; k0 += kIn) {
         if (k0 >= kn) break;
@@ -417,9 +416,10 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Evic
 #pragma unroll
         for (int k = 0; k < kIn; ++k) {
             const int i = at0 + 32 * (k0 + k);
-            key[k0 + k] = evict_key(wv[k], ps[k] < p.n_sink || ps[k] >= recent_from);
+            const float wk = __uint_as_float(key[k0 + k]);
+            key[k0 + k] = evict_key(wk, ps[k] < p.n_sink || ps[k] >= recent_from);
             if (k0 + k < kn && i < min(t1, K)) {
-                if (copy) nw[i] = wv[k];
+                if (copy) nw[i] = wk;
                 if (copyp) np[i] = ps[k];
             }
         }
