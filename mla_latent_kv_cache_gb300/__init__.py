@@ -591,9 +591,10 @@ def mla_cache_evict(cache, cache_kind, page_size, block_table, seq_lens, weights
     if (weights.dtype is not f32 or positions.dtype is not i32 or new_weights.dtype is not f32 or
             new_positions.dtype is not i32):
         _refuse(where, "weights and new_weights must be fp32, positions and new_positions int32")
+    # (one row: its stride says nothing, but its values still have to follow each other)
     one = shape[0] <= 1
     for name, t in (("positions", positions), ("new_weights", new_weights), ("new_positions", new_positions)):
-        if t.shape != shape or (not one and t.stride() != strides):
+        if t.shape != shape or (not _rows_apart(shape, t.stride()) if one else t.stride() != strides):
             _refuse(where, f"{name} must be a tensor of weights' shape and strides")
     if budgets.dtype is not i32 or not budgets.is_contiguous() or budgets.numel() < B:
         _refuse(where, f"budgets must be contiguous int32 of at least {B} values")

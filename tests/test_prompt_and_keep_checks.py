@@ -239,3 +239,31 @@ def test_columns_of_a_wider_table(fake):
     _refused(lambda: _evict(block_table=table, weights=f32(2, 65), positions=i32(2, 65), new_weights=f32(2, 65),
                             new_positions=i32(2, 65), moves=i32(2, 67)), "block_table")
     assert len(fake.calls) == 3
+
+
+# One row: its stride says nothing, but the elements inside the row still have
+# to follow each other (the kernels walk a row as contiguous values).
+ONE_ROW = dict(block_table=i32(1, 4), seq_lens=i32(1), weights=f32(1, 50), positions=i32(1, 50), budgets=i32(1),
+               new_seq_lens=i32(1), new_weights=f32(1, 50), new_positions=i32(1, 50), moves=i32(1, 52))
+
+
+@pytest.mark.parametrize("name,view", [
+    (name, view(make))
+    for name, make in (("weights", f32), ("positions", i32), ("new_weights", f32), ("new_positions", i32))
+    for view in (lambda t: t(1, 100)[:, ::2], lambda t: t(50, 2).t()[:1], lambda t: t(1, 1).expand(1, 50))
+], ids=lambda x: x if isinstance(x, str) else f"strides{x.stride()}")
+def test_evict_refuses_one_row_whose_values_lie_apart(fake, name, view):
+    _refused(lambda: _evict(**{**ONE_ROW, name: view}), name)
+    assert fake.calls == []
+
+
+def test_evict_takes_one_row_of_any_row_stride(fake):
+    wide = lambda make: make(3, 99)[1:2, :50]
+    tall = lambda make: make(50, 1).t()  # strides (1, 1)
+    for view in (wide, tall):
+        _evict(**{**ONE_ROW, "weights": view(f32), "positions": view(i32), "new_weights": f32(1, 50), "new_positions": view(i32)})
+    _evict(**{**ONE_ROW, "weights": wide(f32), "positions": i32(1, 50)})
+    assert [c[1][9] >= 50 and c[1][10] == 50 for c in fake.calls] == [True] * 3
+    one = dict(weights=f32(1, 2)[:, ::2], positions=i32(1, 2)[:, ::2], new_weights=f32(1, 1), new_positions=i32(1, 1))
+    _evict(**{**ONE_ROW, **one})  # one value: its stride says nothing either
+    assert len(fake.calls) == 4
