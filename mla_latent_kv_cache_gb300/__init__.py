@@ -457,6 +457,14 @@ def _status_ptr(where, status):
     return status.data_ptr()
 
 
+def _one_row_stride(block_table, stride, cols) -> int:
+    """Entries that the only row of a table holds: its columns, or what follows
+    them in a wider row."""
+    if stride <= cols:
+        return cols
+    return max(cols, min(stride, block_table.untyped_storage().nbytes() // 4 - block_table.storage_offset()))
+
+
 def _table_args(where, block_table, seq_lens, cache, max_len, page_size):
     """Checks of a paged batch shared by the calls that keep the cache: the number
     of requests and the table's row stride."""
@@ -472,7 +480,14 @@ def _table_args(where, block_table, seq_lens, cache, max_len, page_size):
     if rows < B:
         _refuse(where, f"block_table has {rows} rows for {B} requests")
     stride = strides[0]
-    if stride > cols and B > 0 and page_size > 0:
+    if max_len == 0:
+        stride = max(stride, 1)  # nothing is read
+    elif rows == 1:
+        # (torch leaves the stride of a dimension of one entry as it comes)
+        stride = _one_row_stride(block_table, stride, cols)
+    elif stride < cols and rows > 0:
+        _refuse(where, "block_table's rows overlap")
+    elif stride > cols and B > 0 and page_size > 0:
         # columns of a wider table: a row reaches to the next one, as far as max_len
         # goes, and the last must lie in memory as well
         last = (B - 1) * stride + min(stride, -(-max_len // page_size))

@@ -267,3 +267,42 @@ def test_evict_takes_one_row_of_any_row_stride(fake):
     one = dict(weights=f32(1, 2)[:, ::2], positions=i32(1, 2)[:, ::2], new_weights=f32(1, 1), new_positions=i32(1, 1))
     _evict(**{**ONE_ROW, **one})  # one value: its stride says nothing either
     assert len(fake.calls) == 4
+
+
+def test_a_one_row_table_reaches_as_far_as_its_columns(fake):
+    # torch leaves the stride of a dimension of one entry as it comes: 1 here, and 0 for
+    # an expanded view
+    table = torch.arange(4, dtype=torch.int32).view(4, 1).t()
+    assert table.stride() == (1, 1) and table.is_contiguous()
+    narrow = (table, i32(4).as_strided((1, 4), (0, 1)), i32(4).as_strided((1, 4), (3, 1)))
+    for t in narrow:
+        _weights(block_table=t, seq_lens=i32(1), q_lat=bf(2, 8, 512), q_pe=bf(2, 8, 64), lse=f32(2, 8), weights=f32(1, 50))
+        assert fake.calls[-1][1][9] == 4
+        _evict(**{**ONE_ROW, "block_table": t})
+        assert fake.calls[-1][1][5] == 4
+    # columns of a wider row go on to its end, however large a stride the view has
+    _evict(**{**ONE_ROW, "block_table": i32(1, 8)[:, :4]})
+    assert fake.calls[-1][1][5] == 8
+    _evict(**{**ONE_ROW, "block_table": i32(6).as_strided((1, 4), (10 ** 6, 1), 1)})
+    assert fake.calls[-1][1][5] == 5
+
+
+@pytest.mark.parametrize("stride", [0, 1, 3])
+def test_tables_whose_rows_overlap_are_refused(fake, stride):
+    table = i32(8).as_strided((2, 4), (stride, 1))
+    _refused(lambda: _weights(block_table=table), "block_table")
+    _refused(lambda: _evict(block_table=table), "block_table")
+    assert fake.calls == []
+
+
+def test_tables_without_columns(fake):
+    # nothing is cached and nothing can be: the lengths still go over
+    for n in (1, 2):
+        empty = dict(seq_lens=i32(n), budgets=i32(n), weights=f32(n, 0), positions=i32(n, 0), new_weights=f32(n, 0),
+                     new_positions=i32(n, 0), new_seq_lens=i32(n), moves=i32(n, 2))
+        _evict(**{**empty, "block_table": i32(n, 0)})
+        assert fake.calls[-1][1][5] >= 1 and fake.calls[-1][1][10] == 0
+    # room for tokens but no table entry for them (one row: the library refuses a stride of 0)
+    _evict(**{**ONE_ROW, "block_table": i32(1, 0)})
+    assert fake.calls[-1][1][5] == 0
+    _refused(lambda: _evict(block_table=i32(2, 0)), "block_table")
