@@ -158,6 +158,15 @@ def _nbytes(t: torch.Tensor) -> int:
     return t.numel() * t.element_size()
 
 
+def _table_stride(block_table) -> int:
+    """A table's row stride for the library, which takes it as a row's length.
+    torch leaves the stride of a dimension of one entry as it comes (a [P, 1]
+    table transposed to [1, P] has strides (1, 1)), so a single row is at least
+    as long as its columns."""
+    rows, cols = block_table.shape
+    return max(block_table.stride(0), cols) if rows == 1 else block_table.stride(0)
+
+
 def _decode_args(where, q_lat, q_pe, cache, block_table, seq_lens, out, lse, workspace, rows, width):
     """Checks shared by the decode entry points: `rows` query rows of `width`
     latent values (query tokens x heads)."""
@@ -252,7 +261,7 @@ def mla_decode_varlen(q_lat, q_pe, cache, cache_kind, page_size, block_table, se
     odt = MLA_OUT_F32 if out.dtype == torch.float32 else MLA_OUT_BF16
     st = load().mla_decode_varlen(q_lat.data_ptr(), q_pe.data_ptr(), total_q, cache.data_ptr(), int(cache_kind),
                                   _nbytes(cache) // rb, int(page_size), block_table.data_ptr(),
-                                  block_table.stride(0), seq_lens.data_ptr(), cu_q_lens.data_ptr(), B,
+                                  _table_stride(block_table), seq_lens.data_ptr(), cu_q_lens.data_ptr(), B,
                                   int(max_q_len), Hq, float(scale), out.data_ptr(), odt, lse.data_ptr(),
                                   workspace.data_ptr(), _nbytes(workspace), int(num_ctas), _stream(stream))
     _check(st, "mla_decode_varlen")
@@ -275,7 +284,7 @@ def mla_gather_upconvert(cache: torch.Tensor, page_size: int, block_table: torch
     rows = dst.shape[0] if num_rows is None else int(num_rows)
     _need(0 <= rows <= dst.shape[0], where, f"num_rows {rows} outside [0, {dst.shape[0]}]")
     st = load().mla_gather_upconvert(cache.data_ptr(), cache.shape[0], int(page_size), block_table.data_ptr(),
-                                     block_table.stride(0), cu_seq_lens.data_ptr(), cu_seq_lens.shape[0] - 1, rows,
+                                     _table_stride(block_table), cu_seq_lens.data_ptr(), cu_seq_lens.shape[0] - 1, rows,
                                      dst.data_ptr(), dst.stride(0), _stream(stream))
     _check(st, "mla_gather_upconvert")
 
@@ -317,7 +326,7 @@ def mla_decode_latent(q_lat, q_pe, cache, lat_dim, page_size, block_table, seq_l
     nbytes = cache.numel() * cache.element_size()
     _check(load().mla_decode_latent(q_lat.data_ptr(), q_pe.data_ptr(), cache.data_ptr(), int(lat_dim),
                                     nbytes // row_bytes, int(page_size), block_table.data_ptr(),
-                                    block_table.stride(0), seq_lens.data_ptr(), B, int(q_len), Hq, float(scale),
+                                    _table_stride(block_table), seq_lens.data_ptr(), B, int(q_len), Hq, float(scale),
                                     out.data_ptr(), out_dtype, lse.data_ptr(), workspace.data_ptr(),
                                     workspace.numel() * workspace.element_size(), int(num_ctas), _stream(stream)),
            "mla_decode_latent")
@@ -342,7 +351,7 @@ def mla_decode(q_lat, q_pe, cache, cache_kind, page_size, block_table, seq_lens,
     rb = mla_row_bytes(cache_kind)
     _need(rb > 0, "mla_decode", f"unknown cache kind {cache_kind}")
     _check(load().mla_decode(q_lat.data_ptr(), q_pe.data_ptr(), cache.data_ptr(), cache_kind, nbytes // rb,
-                             page_size, block_table.data_ptr(), block_table.stride(0), seq_lens.data_ptr(), B, q_len,
+                             page_size, block_table.data_ptr(), _table_stride(block_table), seq_lens.data_ptr(), B, q_len,
                              Hq, float(scale), out.data_ptr(), out_dtype, lse.data_ptr(), workspace.data_ptr(),
                              workspace.numel() * workspace.element_size(), num_ctas, _stream(stream)),
            "mla_decode")
@@ -362,7 +371,7 @@ def mla_decode_static_scratch(q_lat, q_pe, cache, cache_kind, page_size, block_t
     rb = mla_row_bytes(cache_kind)
     _need(rb > 0, "mla_decode_static_scratch", f"unknown cache kind {cache_kind}")
     _check(load().mla_decode_static_scratch(q_lat.data_ptr(), q_pe.data_ptr(), cache.data_ptr(), cache_kind,
-                                            nbytes // rb, page_size, block_table.data_ptr(), block_table.stride(0),
+                                            nbytes // rb, page_size, block_table.data_ptr(), _table_stride(block_table),
                                             seq_lens.data_ptr(), B, q_len, Hq, float(scale), out.data_ptr(),
                                             out_dtype, lse.data_ptr(), num_ctas, _stream(stream)),
            "mla_decode_static_scratch")
@@ -458,8 +467,7 @@ def _status_ptr(where, status):
 
 
 def _one_row_stride(block_table, stride, cols) -> int:
-    """Entries that the only row of a table holds: its columns, or what follows
-    them in a wider row."""
+    """_table_stride of a table of one row, cut to what lies in memory."""
     if stride <= cols:
         return cols
     return max(cols, min(stride, block_table.untyped_storage().nbytes() // 4 - block_table.storage_offset()))
@@ -483,7 +491,6 @@ def _table_args(where, block_table, seq_lens, cache, max_len, page_size):
     if max_len == 0:
         stride = max(stride, 1)  # nothing is read
     elif rows == 1:
-        # (torch leaves the stride of a dimension of one entry as it comes)
         stride = _one_row_stride(block_table, stride, cols)
     elif stride < cols and rows > 0:
         _refuse(where, "block_table's rows overlap")

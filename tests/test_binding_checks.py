@@ -180,3 +180,29 @@ def test_gather_and_merge_checks(fake):
     _refused(lambda: m.mla_merge_lse(po[:, :2], pl, torch.empty((3, 512))), "part_out")
     _refused(lambda: m.mla_merge_lse(po, pl, torch.empty((2, 512))), "out must be")
     _refused(lambda: m.mla_merge_lse(po, pl, torch.empty((3, 512)), torch.empty(2)), "lse")
+
+
+def test_a_one_row_table_reaches_as_far_as_its_columns(fake):
+    # torch leaves the stride of a dimension of one entry as it comes
+    table = torch.arange(4, dtype=torch.int32).view(4, 1).t()
+    assert table.stride() == (1, 1) and table.is_contiguous()
+    a = _decode_inputs(B=1)
+    a["block_table"] = table
+    _decode(a)
+    assert fake.calls[-1][1][7] == 4
+    m.mla_decode_static_scratch(a["q_lat"], a["q_pe"], a["cache"], 0, 16, table, a["seq_lens"], 2, 0.1, a["out"], a["lse"])
+    assert fake.calls[-1][1][7] == 4
+    m.mla_decode_varlen(a["q_lat"], a["q_pe"], a["cache"], 0, 16, table, a["seq_lens"],
+                        torch.tensor([0, 2], dtype=torch.int32), 2, 0.1, a["out"], a["lse"], a["workspace"])
+    assert fake.calls[-1][1][8] == 4
+    w = _decode_inputs(B=1, D=768)
+    m.mla_decode_latent(w["q_lat"], w["q_pe"], w["cache"], 768, 16, table, w["seq_lens"], 2, 0.1, w["out"], w["lse"],
+                        w["workspace"])
+    assert fake.calls[-1][1][7] == 4
+    m.mla_gather_upconvert(torch.zeros((64, 656), dtype=torch.uint8), 16, table, torch.tensor([0, 40], dtype=torch.int32),
+                           torch.empty((40, 576), dtype=torch.bfloat16))
+    assert fake.calls[-1][1][4] == 4
+    # columns of a wider row, and more rows: the stride as it is
+    for t, want in ((torch.zeros((1, 8), dtype=torch.int32)[:, :4], 8), (torch.zeros((3, 4), dtype=torch.int32), 4)):
+        _decode(a, block_table=t)
+        assert fake.calls[-1][1][7] == want
