@@ -1495,9 +1495,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(decode_threads<LSU, 
 // Q's latent part in TMEM as its A operand; the ring has eleven K-block slots
 // and two rope slots, one S buffer, one P buffer and one O accumulator (a finished
 // segment is written out before the next segment's first value product).
-// 65..128 rows: the two 64-row groups of a worker run
-// as a cluster of two CTAs that share each tile through multicast TMA (each
-// issues half of the boxes into both), so the cache is read once per request.
+// 65..128 rows: the two 64-row groups of a worker are launched as a cluster of
+// two CTAs, so that they run at the same time over the same tiles: each loads
+// them for itself, the second from L2 (2.04 ms for 128 requests with up to 128
+// rows; one multicast copy for both was 2.03 ms, but has no place in a job of
+// several GPUs, which the library cannot tell from one).
 // fp8_ds_mla rows: TMA lands each K-block's e4m3 codes in the upper half of
 // its slot, four expand warps widen them in place to f16 (the queries' latent
 // part and P are f16 too). Latent width 1792: the two latent halves of every row in the two
@@ -1633,25 +1635,17 @@ struct FoldCtrl {
 };
 static_assert(sizeof(FoldCtrl) <= 3584, "control block");
 
-// MC: the two row groups of a worker (query rows 0..63 and 64..127 of each
-// request) are the two CTAs of a cluster; each CTA loads half of every tile's
-// boxes with multicast, so each cached row crosses HBM once for both groups,
-// and a ring slot is refilled only when both CTAs' value products have
-// released it.
 // KIND 1: fp8_ds_mla rows. TMA lands each K-block's e4m3 codes in the upper
 // half of its slot and each tile's block scales in a scale slot; two expand
 // warps widen the codes into the bf16 layout the products read, in place.
-template <int NP, int KB, bool PAIR, bool MC, int KIND>
+template <int NP, int KB, bool PAIR, int KIND>
 __global__ void __launch_bounds__(FoldCfg<NP, KB, PAIR, KIND>::kThreads, 1)
     mla_decode_fold_kernel(const __grid_constant__ DecodeMaps maps, const DecodeParams p) {
-    static_assert(!MC || (NP == 64 && !PAIR), "row-group pairs are 64-row CTAs");
-    static_assert(!(MC && KIND == 1), "fp8 rows: one row group per worker");
     using C = FoldCfg<NP, KB, PAIR, KIND>;
     // first expand warp (fp8 rows), after the softmax groups
     constexpr int kExp0 = 9 + 4 * (C::kSG - 1);
     // the rope's element column in a row: after the latent (bf16), or at byte 528 (fp8)
     constexpr int kRopeX = KIND == 1 ? 264 : C::kD;
-    constexpr uint16_t kPairMask = 0x3;
     constexpr int kT = C::kTok;
     using It = TileItT<6>;
     extern __shared__ uint8_t smem_raw[];
@@ -1674,20 +1668,17 @@ __global__ void __launch_bounds__(FoldCfg<NP, KB, PAIR, KIND>::kThreads, 1)
     const int gy = blockIdx.y;
     const int dbase = static_cast<int>(rank) * C::kDL;
     const bool has_rope = !PAIR || rank == 0;
-    // MC: which half of every box pair (and which rope half) this CTA issues
-    const int mrank = MC ? static_cast<int>(cluster_ctarank()) : 0;
     if (threadIdx.x == 0) MLA_KTRACE(0);
 
     if (threadIdx.x == 0) {
-        // MC: a slot is released by the value products of both CTAs
         for (int i = 0; i < C::kRL; ++i) {
             mbar_init(&ctrl->blk_full[i], 1);
-            mbar_init(&ctrl->blk_empty[i], MC ? 2 : 1);
+            mbar_init(&ctrl->blk_empty[i], 1);
         }
         // a rope slot is armed by both producer warps (one half each)
         for (int i = 0; i < C::kRR; ++i) {
             mbar_init(&ctrl->rope_full[i], C::kProducers);
-            mbar_init(&ctrl->rope_empty[i], MC ? 2 : 1);
+            mbar_init(&ctrl->rope_empty[i], 1);
         }
         for (int i = 0; i < 3; ++i) mbar_init(&ctrl->fin[i], 1);
         if constexpr (KIND == 1) {
@@ -1746,7 +1737,7 @@ __global__ void __launch_bounds__(FoldCfg<NP, KB, PAIR, KIND>::kThreads, 1)
         ctrl->m[c] = -INFINITY;
     }
     __syncthreads();
-    if constexpr (PAIR || MC) cluster_sync_all();  // the peer's barriers exist before any remote traffic
+    if constexpr (PAIR) cluster_sync_all();  // the peer's barriers exist before any remote traffic
     if (threadIdx.x == 0) {
         MLA_KTRACE(1);
 #ifdef MLA_TRACE
@@ -1821,8 +1812,7 @@ __global__ void __launch_bounds__(FoldCfg<NP, KB, PAIR, KIND>::kThreads, 1)
                             umma_bf16(tS, dr, dqr, idS, 0u);
                             umma_bf16(tS, dr + 2, dqr + 2, idS, 1u);
                         }
-                        if constexpr (MC) umma_commit_mc(&ctrl->rope_empty[rr], kPairMask);
-                        else umma_commit(&ctrl->rope_empty[rr]);
+                        umma_commit(&ctrl->rope_empty[rr]);
                     }
                 }
                 for (int kb = 0; kb < KB && ok; ++kb) {
@@ -1894,8 +1884,7 @@ __global__ void __launch_bounds__(FoldCfg<NP, KB, PAIR, KIND>::kThreads, 1)
                         umma_bf16(tO + kb * NP, da + ((kk * 2048) >> 4),
                                   dp + ((C::kTr ? kk * 32 : kk * 16 * NP * 2) >> 4), idPV,
                                   (new_seg && kk == 0) ? 0u : 1u);
-                    if constexpr (MC) umma_commit_mc(&ctrl->blk_empty[slot], kPairMask);
-                    else umma_commit(&ctrl->blk_empty[slot]);
+                    umma_commit(&ctrl->blk_empty[slot]);
                 }
                 umma_commit(&ctrl->o_done[i & 1]);
                 if (p.test_hold == 2 && mt == 1 && i < 32) spin_for_ns(20000);  // test hook: a lagging issuer
@@ -1962,15 +1951,8 @@ __global__ void __launch_bounds__(FoldCfg<NP, KB, PAIR, KIND>::kThreads, 1)
                                             &ctrl->rope_full[rr], kRopeX + 32 * rh, y, pol);
                         }
                     } else if (lane < nruns) {
-                        if constexpr (MC) {
-                            // rope half pp comes from the CTA of rank pp, into both CTAs
-                            if (pp == mrank)
-                                tma_load_2d_mc(rope_ring + rr * C::kRopeBytes + pp * 4096 + lane * BR * 64, &maps.rope,
-                                               &ctrl->rope_full[rr], kRopeX + 32 * pp, y, kPairMask, pol);
-                        } else {
-                            tma_load_2d(rope_ring + rr * C::kRopeBytes + pp * 4096 + lane * BR * 64, &maps.rope,
-                                        &ctrl->rope_full[rr], kRopeX + 32 * pp, y, pol);
-                        }
+                        tma_load_2d(rope_ring + rr * C::kRopeBytes + pp * 4096 + lane * BR * 64, &maps.rope,
+                                    &ctrl->rope_full[rr], kRopeX + 32 * pp, y, pol);
                     }
                     if (lane == 0 && pp == 0) MLA_TRACE_POINT(i, kTrProdIssued);
                 }
@@ -1985,15 +1967,6 @@ __global__ void __launch_bounds__(FoldCfg<NP, KB, PAIR, KIND>::kThreads, 1)
                         break;
                     }
                     if (lane == 0 && q == 0) MLA_TRACE_POINT(i, kTrEpiStart + pp);  // slot free
-                    if constexpr (MC) {
-                        // a peer that has given up may leave at any time: send it nothing more
-                        if (__shfl_sync(0xffffffffu, lane == 0 ? peer_aborted(&ctrl->abort, mrank ^ 1) : 0, 0)) {
-                            ok = false;
-                            fsite = kSiteTmaPairEmpty;
-                            ftile = i;
-                            break;
-                        }
-                    }
                     if constexpr (KIND == 1) {
                         // the codes of both halves (64 bytes a row each) into the slot's
                         // upper half: first-half rows at 8 KB, second-half rows at 12 KB
@@ -2013,17 +1986,10 @@ __global__ void __launch_bounds__(FoldCfg<NP, KB, PAIR, KIND>::kThreads, 1)
                     __syncwarp();
                     if (lane < nruns) {
                         uint8_t* dst = ring + slot * C::kBlkBytes + lane * BR * 128;
-                        if constexpr (MC) {
-                            // this CTA's half of the pair, into both CTAs
-                            const int hh = mrank;
-                            tma_load_2d_mc(dst + hh * 8192, &maps.lat, &ctrl->blk_full[slot], C::kHalf * hh + 64 * kb, y,
-                                           kPairMask, pol);
-                        } else {
 #pragma unroll
-                            for (int hh = 0; hh < 2; ++hh)
-                                tma_load_2d(dst + hh * 8192, &maps.lat, &ctrl->blk_full[slot],
-                                            dbase + C::kHalf * hh + 64 * kb, y, pol);
-                        }
+                        for (int hh = 0; hh < 2; ++hh)
+                            tma_load_2d(dst + hh * 8192, &maps.lat, &ctrl->blk_full[slot],
+                                        dbase + C::kHalf * hh + 64 * kb, y, pol);
                     }
                     armed = i * (C::prod_hi(pp) - C::prod_lo(pp)) + q + 1;
                 }
@@ -2831,7 +2797,7 @@ __global__ void __launch_bounds__(FoldCfg<NP, KB, PAIR, KIND>::kThreads, 1)
         }
     }
     __syncthreads();
-    if constexpr (PAIR || MC) cluster_sync_all();  // no remote traffic into this CTA after here
+    if constexpr (PAIR) cluster_sync_all();  // no remote traffic into this CTA after here
     if (threadIdx.x == 0) MLA_KTRACE(3);
     if (warp == 0) {
         __syncwarp();
@@ -3188,16 +3154,17 @@ cudaError_t launch_decode(const DecodeMaps& maps, const DecodeParams& p, int NP,
     return launch_decode_merge(p, G, 2 * G * GY, GY, stream);
 }
 
-template <int NP, int KB, bool PAIR = false, bool MC = false, int KIND = 0>
+template <int NP, int KB, bool PAIR = false, bool ROWS = false, int KIND = 0>
 struct FoldVariant {
     using C = FoldCfg<NP, KB, PAIR, KIND>;
-    static constexpr bool kCluster = PAIR || MC;
+    static constexpr bool kCluster = PAIR || ROWS;
     // cluster shape: the latent halves of a row (PAIR) side by side in x, the
-    // two row groups (MC) in y
+    // two row groups (ROWS) in y, which read the same tiles and so have to run at
+    // the same time
     static void cluster_attr(cudaLaunchAttribute& a) {
         a.id = cudaLaunchAttributeClusterDimension;
         a.val.clusterDim.x = PAIR ? 2 : 1;
-        a.val.clusterDim.y = MC ? 2 : 1;
+        a.val.clusterDim.y = ROWS ? 2 : 1;
         a.val.clusterDim.z = 1;
     }
     // Set the shared-memory attribute (once per device) and return how many
@@ -3208,14 +3175,14 @@ struct FoldVariant {
         int dev = 0;
         if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return -1;
         if (!done[dev]) {
-            auto k = mla_decode_fold_kernel<NP, KB, PAIR, MC, KIND>;
+            auto k = mla_decode_fold_kernel<NP, KB, PAIR, KIND>;
             if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes) != cudaSuccess)
                 return -1;
             if constexpr (kCluster) {
                 cudaLaunchConfig_t cfg = {};
                 cudaLaunchAttribute attr[1];
                 cluster_attr(attr[0]);
-                cfg.gridDim = dim3(PAIR ? 2 : 1, MC ? 2 : 1, 1);
+                cfg.gridDim = dim3(PAIR ? 2 : 1, ROWS ? 2 : 1, 1);
                 cfg.blockDim = dim3(C::kThreads, 1, 1);
                 cfg.dynamicSmemBytes = C::kSmemBytes;
                 cfg.attrs = attr;
@@ -3244,18 +3211,18 @@ struct FoldVariant {
             cluster_attr(attr[1]);
             cfg.numAttrs = 2;
         }
-        return cudaLaunchKernelEx(&cfg, mla_decode_fold_kernel<NP, KB, PAIR, MC, KIND>, maps, p);
+        return cudaLaunchKernelEx(&cfg, mla_decode_fold_kernel<NP, KB, PAIR, KIND>, maps, p);
     }
 };
 
 // The folded-tile variants: query rows padded to NP, latent width D (K-blocks
 // per tile 128 / D; 1792 splits the latent over a CTA pair); at 65 to 128
-// query rows of the 576-wide row the two row groups share each tile (MC);
+// query rows of the 576-wide row the two row groups run as a cluster (ROWS);
 // fp8_ds_mla rows (KINDV 1) at 64 rows.
-#define MLA_FOLD(NPV, DV, MCV, KINDV, EXPR)                                                                   \
+#define MLA_FOLD(NPV, DV, ROWSV, KINDV, EXPR)                                                                   \
     (DV == 512 ? (NPV == 16 ? (KINDV ? EXPR(16, 4, false, false, 1) : EXPR(16, 4, false, false, 0))             \
                             : NPV == 32 ? (KINDV ? EXPR(32, 4, false, false, 1) : EXPR(32, 4, false, false, 0)) \
-                                        : (MCV ? EXPR(64, 4, false, true, 0)                                   \
+                                        : (ROWSV ? EXPR(64, 4, false, true, 0)                                   \
                                                : KINDV ? EXPR(64, 4, false, false, 1) : EXPR(64, 4, false, false, 0))) \
                : DV == 256 ? (NPV == 16 ? EXPR(16, 2, false, false, 0) : EXPR(32, 2, false, false, 0))        \
                            : DV == 768 ? EXPR(16, 6, false, false, 0) : EXPR(16, 7, true, false, 0))
@@ -3273,23 +3240,23 @@ bool fold_is_row_pair(int NP, int lat_dim, int GY) { return NP == 64 && lat_dim 
 
 int decode_fold_ctas(int NP, int lat_dim, int kind, int GY, int requested_ctas) {
     if (!fold_supported(NP, lat_dim, kind, GY)) return -1;
-    const bool mc = kind == 0 && fold_is_row_pair(NP, lat_dim, GY);
+    const bool rows = kind == 0 && fold_is_row_pair(NP, lat_dim, GY);
 #define MLA_FOLD_WORKERS(a, b, c, d, e) FoldVariant<a, b, c, d, e>::max_workers()
-    const int mx = MLA_FOLD(NP, lat_dim, mc, kind == 1, MLA_FOLD_WORKERS);
+    const int mx = MLA_FOLD(NP, lat_dim, rows, kind == 1, MLA_FOLD_WORKERS);
 #undef MLA_FOLD_WORKERS
     if (mx <= 0) return -1;
     if (requested_ctas <= 0) return mx;
     if (fold_is_pair(lat_dim)) return requested_ctas >= 4 ? requested_ctas / 2 : 1;
-    if (mc) return requested_ctas >= 2 ? requested_ctas / 2 : 1;  // the grid has GY = 2 CTAs per worker
+    if (rows) return requested_ctas >= 2 ? requested_ctas / 2 : 1;  // the grid has GY = 2 CTAs per worker
     return requested_ctas;
 }
 
 cudaError_t launch_decode_fold(const DecodeMaps& maps, const DecodeParams& p, int NP, int kind, int W, int GY,
                                cudaStream_t stream) {
     if (!fold_supported(NP, p.lat_dim, kind, GY)) return cudaErrorInvalidValue;
-    const bool mc = kind == 0 && fold_is_row_pair(NP, p.lat_dim, GY);
+    const bool rows = kind == 0 && fold_is_row_pair(NP, p.lat_dim, GY);
 #define MLA_FOLD_LAUNCH(a, b, c, d, e) FoldVariant<a, b, c, d, e>::launch(maps, p, W, GY, stream)
-    cudaError_t e = MLA_FOLD(NP, p.lat_dim, mc, kind == 1, MLA_FOLD_LAUNCH);
+    cudaError_t e = MLA_FOLD(NP, p.lat_dim, rows, kind == 1, MLA_FOLD_LAUNCH);
 #undef MLA_FOLD_LAUNCH
     if (e != cudaSuccess) return e;
     // status records: one per CTA
