@@ -488,6 +488,14 @@ MLA_API void mla_test_hold_next_decode(void);
  */
 MLA_API void mla_test_slow_pv_next_decode(void);
 
+/*
+ * mla_test_limit_next_evict - test support for parts of a GPU on which no large
+ * cluster fits. The next mla_cache_evict call in this process that launches
+ * shares a request's tokens between at most `ctas` CTAs. Its results are the
+ * same. Nothing else sets it.
+ */
+MLA_API void mla_test_limit_next_evict(int ctas);
+
 /* Static English text for a status code. */
 MLA_API const char* mla_status_string(int status);
 

@@ -80,6 +80,8 @@ def load() -> ctypes.CDLL:
             lib.mla_test_hold_next_decode.restype = None
             lib.mla_test_slow_pv_next_decode.argtypes = []
             lib.mla_test_slow_pv_next_decode.restype = None
+            lib.mla_test_limit_next_evict.argtypes = [i32]
+            lib.mla_test_limit_next_evict.restype = None
             lib.mla_merge_lse.argtypes = [vp, vp, i32, i64, vp, i32, vp, vp]
             lib.mla_decode_varlen.argtypes = [vp, vp, i64, vp, i32, i64, i32, vp, i64, vp, vp, i32, i32, i32, f32,
                                               vp, i32, vp, vp, ctypes.c_size_t, i32, vp]
@@ -669,6 +671,12 @@ def test_slow_pv_next_decode() -> None:
     softmax warps by up to two tiles; its results are unchanged (see
     include/mla.h)."""
     load().mla_test_slow_pv_next_decode()
+
+
+def test_limit_next_evict(ctas: int) -> None:
+    """Test support: at most `ctas` CTAs share a request's tokens in the next
+    mla_cache_evict; its results are unchanged (see include/mla.h)."""
+    load().mla_test_limit_next_evict(int(ctas))
 
 
 def device_status(workspace: torch.Tensor) -> int:

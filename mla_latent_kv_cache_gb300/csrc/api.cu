@@ -106,6 +106,9 @@ size_t decode_ws_bytes(int B, int HQ, int ctas, int D = 512) { return decode_ws_
 // consumed by the next mla_decode.
 std::atomic<int> g_test_hold{0};
 
+// Set by mla_test_limit_next_evict, consumed by the next mla_cache_evict.
+std::atomic<int> g_test_evict_ctas{0};
+
 // Workspace of mla_decode_static_scratch: one array per device, placed when
 // this library's device code is loaded, for callers that cannot allocate.
 static __device__ __align__(256) unsigned char g_decode_scratch[MLA_STATIC_SCRATCH_BYTES];
@@ -637,7 +640,7 @@ int mla_cache_evict(void* cache, int row_bytes, int64_t num_slots, int page_size
     p.moves = moves;
     p.moves_stride = moves_stride;
     p.status = status;
-    const cudaError_t e = mla::launch_evict(p, di.sms, static_cast<cudaStream_t>(stream));
+    const cudaError_t e = mla::launch_evict(p, di.sms, g_test_evict_ctas.exchange(0), static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 
@@ -663,6 +666,8 @@ int mla_static_scratch_status(int32_t* dst, int n, void* stream) {
                                     static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
+
+void mla_test_limit_next_evict(int ctas) { g_test_evict_ctas.store(ctas); }
 
 void mla_test_hold_next_decode(void) { g_test_hold.store(1); }
 

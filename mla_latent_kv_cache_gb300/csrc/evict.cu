@@ -757,17 +757,49 @@ cudaError_t launch_select(const cudaLaunchConfig_t& cfg, const EvictParams& p) {
     return cudaLaunchKernelEx(&cfg, evict_select_kernel<KPT>, p);
 }
 
+// CTAs of the largest cluster of the select kernels that the current device can
+// run: 16 (which is not portable) on a whole GPU, fewer on a part of one. The
+// kernels' threads and registers leave one CTA to an SM, so one answers for all.
+int largest_cluster() {
+    static std::atomic<int> largest[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 1;
+    if (const int n = largest[dev].load(std::memory_order_relaxed)) return n;
+    auto* k = evict_select_kernel<32>;
+    int CL = 16;
+    if (cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) CL = 8;
+    for (; CL > 1; CL /= 2) {
+        cudaLaunchConfig_t cfg = {};
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = CL;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.gridDim = dim3(CL);
+        cfg.blockDim = dim3(kSelThreads);
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int n = 0;
+        if (cudaOccupancyMaxActiveClusters(&n, k, &cfg) == cudaSuccess && n > 0) break;
+    }
+    (void)cudaGetLastError();  // a size that does not fit is no error of a later launch
+    largest[dev].store(CL, std::memory_order_relaxed);
+    return CL;
+}
+
 }  // namespace
 
-cudaError_t launch_evict(const EvictParams& p, int sms, cudaStream_t stream) {
+cudaError_t launch_evict(const EvictParams& p, int sms, int most_ctas, cudaStream_t stream) {
+    int most = largest_cluster();
+    while (most > 1 && most_ctas > 0 && most > most_ctas) most /= 2;
     // CTAs that share a request's tokens: 8 keys a thread where there are SMs for
     // it, up to 32 otherwise
     int CL = 1;
-    while (CL < 16 && p.max_len > CL * 8 * kSelThreads) CL *= 2;
+    while (CL < most && p.max_len > CL * 8 * kSelThreads) CL *= 2;
     auto keys = [&](int cl) { return ((p.max_len + cl - 1) / cl + kSelThreads - 1) / kSelThreads; };
     while (CL > 1 && static_cast<int64_t>(CL) * p.B > sms && keys(CL / 2) <= 32) CL /= 2;
     const int kpt = keys(CL);
-    if (kpt > 32) CL = 8;  // evict_select_long_kernel
+    if (kpt > 32) CL = most < 8 ? most : 8;  // evict_select_long_kernel
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -155,7 +155,8 @@ struct EvictParams {
     int64_t moves_stride;
     int* status;
 };
-cudaError_t launch_evict(const EvictParams& p, int sms, cudaStream_t stream);
+// most_ctas > 0: no more CTAs share a request's tokens (a test's; else as many as the device can run).
+cudaError_t launch_evict(const EvictParams& p, int sms, int most_ctas, cudaStream_t stream);
 
 // Attention over whole prompts (mla_prefill); strides in elements.
 struct PrefillParams {

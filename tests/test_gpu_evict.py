@@ -209,3 +209,25 @@ def test_graph_replay_and_rows_of_wider_buffers():
             assert np.array_equal(nw[b, :ref_l[b]].cpu().numpy(), ref_w[b])
             assert np.array_equal(npos[b, :ref_l[b]].cpu().numpy(), ref_p[b])
             assert not bool(nw[b, n:].any())
+
+
+@pytest.mark.parametrize("ctas", [1, 2, 4, 8])
+@pytest.mark.parametrize("most", [5000, 40000, 300000])
+def test_where_no_large_cluster_fits(ctas, most):
+    # a part of a GPU may hold fewer than 16 CTAs of a cluster: fewer share a request, or the
+    # keys that no longer fit registers go to shared memory (and past that are formed again)
+    lens, bt, cache, w, pos = _case([most, most // 3, 7], 64, 1, seed=most + ctas)
+    bud = np.array([most // 2, most // 3, 3], dtype=np.int32)
+    ref_c, ref_l, ref_w, ref_p, ref_m = keep_ref.evict(cache, bt, lens, w, pos, bud, 4, 100, 64)
+    d = [_t(x) for x in (cache, bt, lens, w, pos, bud)]
+    nl, nw, npos = torch.zeros_like(d[2]), torch.zeros_like(d[3]), torch.zeros_like(d[4])
+    moves = torch.zeros((3, w.shape[1] + 2), dtype=torch.int32, device=DEV)
+    m.test_limit_next_evict(ctas)
+    m.mla_cache_evict(d[0], 1, 64, d[1], d[2], d[3], d[4], d[5], 4, 100, nl, nw, npos, moves)
+    torch.cuda.synchronize()
+    assert np.array_equal(nl.cpu().numpy(), ref_l) and np.array_equal(d[0].cpu().numpy(), ref_c)
+    for b in range(3):
+        n, K = len(ref_m[b]), int(ref_l[b])
+        mv = moves[b].cpu().numpy()
+        assert mv[0] == n and mv[1] == K and np.array_equal(mv[2:2 + 2 * n].reshape(n, 2), ref_m[b])
+        assert np.array_equal(nw[b, :K].cpu().numpy(), ref_w[b]) and np.array_equal(npos[b, :K].cpu().numpy(), ref_p[b])
