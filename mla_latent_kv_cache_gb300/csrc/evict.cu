@@ -591,7 +591,6 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Evic
 // written.
 constexpr int kMoveThreads = 384;
 constexpr int kMoveWarps = kMoveThreads / 32;
-constexpr int kMoveReqs = 1536;  // requests whose counts a CTA holds at once
 constexpr int kStage = 9216;     // bytes of a batch: eight 1,152-byte rows
 
 struct MoveShared {
@@ -616,7 +615,7 @@ __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.comm
 // This thread's stores have read their shared memory.
 __device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 
-__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictParams p) {
+__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictParams p, int reqs) {
     extern __shared__ __align__(128) uint8_t stages[];
     __shared__ MoveShared sh;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -644,8 +643,8 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictPar
     };
     griddep_wait();
     if (tid == 0) griddep_launch_dependents();
-    for (int b0 = 0; b0 < p.B; b0 += kMoveReqs) {
-        const int nb = min(kMoveReqs, p.B - b0);
+    for (int b0 = 0; b0 < p.B; b0 += reqs) {
+        const int nb = min(reqs, p.B - b0);
         // prefix sums of the counts of requests b0 .. b0 + nb (kPer a thread)
         uint32_t c[kPer], sum = 0;
 #pragma unroll
@@ -846,7 +845,7 @@ cudaError_t launch_evict(const EvictParams& p, int sms, int most_ctas, cudaStrea
     mc.stream = stream;
     mc.attrs = ma;
     mc.numAttrs = 1;
-    return cudaLaunchKernelEx(&mc, evict_move_kernel, p);
+    return cudaLaunchKernelEx(&mc, evict_move_kernel, p, evict_requests_at_once(p.max_len));
 }
 
 }  // namespace mla

@@ -155,6 +155,13 @@ struct EvictParams {
     int64_t moves_stride;
     int* status;
 };
+constexpr int kMoveReqs = 1536;  // requests whose counts of moves a CTA of the move kernel holds at once
+// Requests whose moves are counted at once: so many that 32 bits hold the sum.
+// (A request moves at most min(K, T - K) <= max_len / 2 rows.)
+constexpr int evict_requests_at_once(int max_len) {
+    const uint32_t each = static_cast<uint32_t>(max_len) / 2;
+    return each <= UINT32_MAX / kMoveReqs ? kMoveReqs : static_cast<int>(UINT32_MAX / each);
+}
 // most_ctas > 0: no more CTAs share a request's tokens (a test's; else as many as the device can run).
 cudaError_t launch_evict(const EvictParams& p, int sms, int most_ctas, cudaStream_t stream);
 
