@@ -24,8 +24,9 @@
 // rest, at most 8 units of its last place, so 3 bits), and the tensor cores
 // multiply the e4m3 codes with both: each 128-code block has its own
 // accumulator, and its fp32 scale is applied to the finished sum. Only
-// elements below 2^-14 of their row's largest are rounded (by at most 2^-21 of
-// it). The codes go from HBM to the tensor core untouched: no conversion
+// elements below 2^-13 of their row's largest are rounded, by at most 2^-21 of
+// it: scaled, they lie below 2^-6, where e4m3's step stays at 2^-9 and the rest
+// may have more bits than e5m2. The codes go from HBM to the tensor core untouched: no conversion
 // instructions, and half the shared-memory traffic of widened rows.
 //
 // Warp roles: 0 issues the products (and allocates TMEM), 1 and 2 load blocks

@@ -246,3 +246,68 @@ def test_graph_replay_and_side_stream():
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(w, want)
+
+
+# fp8 rows multiply a query in two parts, e4m3 and e5m2, of its values times the power of
+# two that brings the row's largest, mx, into [128, 256). A scaled value x >= 2^-6 is held
+# exactly: in e4m3's normal range the rest is at most 8 units of the value's last place,
+# 3 bits, and those are e5m2's. Below 2^-6 (2^-13 of 128) e4m3's step stays at 2^-9, so the
+# rest is up to 2^-10 and may have more bits than e5m2 holds: it is off by at most half a
+# step of e5m2 in [2^-11, 2^-10], 2^-14 = 2^-21 of 128. So a score is off by at most
+# scale 2^-21 mx sum |k_d| over the values under 2^-13 mx (all of them at worst).
+
+def _wide_rows(seed):
+    """Rows of one large value (in each of the four blocks in turn) and small ones from 2^-10 to 2^-20 of it."""
+    wl = _workload(1, 16, 1, 16, [200, 37], seed=seed)
+    g = torch.Generator().manual_seed(seed)
+    shape = tuple(wl.q_lat.shape)
+    x = torch.exp2(-10 - 10 * torch.rand(shape, generator=g)) * (torch.randint(0, 2, shape, generator=g) * 2 - 1)
+    for r in range(shape[0]):
+        for h in range(shape[1]):
+            x[r, h, (h * 32 + 7 * r) % 512] = 1 + float(torch.rand((), generator=g))
+    x *= torch.exp2(torch.arange(16).float() % 5 - 2)[None, :, None]
+    wl.q_lat.copy_(x.to(torch.bfloat16))
+    return wl
+
+
+def _split(q):
+    """The two parts of a row's values added up (bf16 rows, CPU), in fp64."""
+    x = q.double()
+    e = torch.floor(torch.log2(x.abs().amax(-1, keepdim=True)))
+    up = torch.exp2(7 - e)
+    s = (x * up).float()
+    h = s.to(torch.float8_e4m3fn).float()
+    lo = (s - h).to(torch.float8_e5m2).float()
+    return (h.double() + lo.double()) / up
+
+
+@pytest.mark.parametrize("seed", [21, 22])
+def test_fp8_queries_whose_values_span_many_powers_of_two(seed):
+    wl = _wide_rows(seed)
+    q = wl.q_lat.cpu()
+    held, mx = _split(q), q.double().abs().amax(-1, keepdim=True)
+    off = (held - q.double()).abs()
+    assert bool((off <= 2.0 ** -21 * mx).all()) and bool((off[q.double().abs() >= 2.0 ** -13 * mx] == 0).all())
+    assert bool((off > 0).any())  # the rounded range is exercised
+
+    # against the definition: the bound above
+    sc, mag = keep_ref.scores(wl, wl.pool)
+    L, lse = _lse(wl, sc)
+    got, st = _run(wl, lse, torch.zeros((2, 200), device=DEV), 0.0)
+    assert st == 0
+    got = got.cpu().double().numpy()
+    lse64 = lse.reshape(-1).double().cpu().numpy()
+    want = keep_ref.attn_weights(sc, lse64, 16, np.zeros((2, 200)), 0.0)
+    ksum = np.abs(keep_ref.rows_f64(wl.pool, 1)[:, :512]).sum(axis=1)
+    ksum = ksum[np.isfinite(ksum)].max()
+    n = 2 * (512 // 32) + 4 + 5
+    eps = (n + 4) * 2.0 ** -23 * (2 * mag + np.abs(L).max()) + 2.0 ** -22 + 16 * 2.0 ** -24
+    split = wl.scale * 2.0 ** -21 * float(mx.max()) * ksum
+    assert eps + split < 5e-3
+    assert np.all(np.abs(got - want) <= (eps + split) * want + 2.0 ** -126)
+
+    # and against the two parts as they are held, without any allowance for the rounding
+    wl.q_lat = held.to(DEV)
+    sc, _ = keep_ref.scores(wl, wl.pool)
+    want = keep_ref.attn_weights(sc, lse64, 16, np.zeros((2, 200)), 0.0)
+    assert np.all(np.abs(got - want) <= eps * want + 2.0 ** -126)
