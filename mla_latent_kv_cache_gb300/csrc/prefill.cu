@@ -56,6 +56,7 @@ constexpr int kDv = 128;
 constexpr int kThreadsP = 352;            // 8 softmax warps, the MMA issuer, the loader, the scheduler
 constexpr int kItems = 4;                 // items between the scheduler and the slowest role
 constexpr int kAhead = 4;                 // key tiles before an item's last load at which the next is asked for
+constexpr int kAliveTiles = 4096;         // key tiles (about 7 ms) after which the loader shows that it goes on
 constexpr int kQBytesP = 2 * 3 * kBlkP;
 constexpr int kSmemP = 1024 + 1024 + kQBytesP + kSlots * kBlkP;
 constexpr float kRaise = 8.f;             // log2 units
@@ -72,7 +73,7 @@ struct PCtrl {
     uint64_t s_full[2], p_half[2], p_full[2], o_full[2], fin;
     uint64_t item_full[kItems], item_empty[kItems], more_full, want;
     uint32_t tmem_base;
-    int stop[2];             // abort flag, and a count that goes up while rows are formed again
+    int stop[2];             // abort flag, and a count that goes up while long work goes on
     PItem item[kItems];  // h < 0: no more
     alignas(16) uint4 more;  // what a request for a pending CTA answered
 };
@@ -134,7 +135,8 @@ __device__ __forceinline__ void p_fail(const PrefillParams& p, PCtrl* c) {
 }
 
 // mbar_wait that gives up only when nothing goes on: rows formed again over a
-// long context take longer than a wait's limit.
+// long context take longer than a wait's limit, and so does an item of 80 million
+// keys, during which a tile without queries waits for the next one.
 __device__ __forceinline__ bool p_wait(uint64_t* bar, uint32_t parity, volatile int* stop) {
     if (mbar_try_wait(bar, parity)) return true;
     return mbar_wait_slow<false, true>(bar, parity, stop);
@@ -520,6 +522,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                 if (nk == 0) mbar_arrive(&ctrl->want);
                 for (int j = 0; j < nk && ok; ++j) {
                     if (j == max(nk - kAhead, 0)) mbar_arrive(&ctrl->want);
+                    if (j % kAliveTiles == kAliveTiles - 1) atomicAdd(&ctrl->stop[1], 1);
                     for (int x = 0; x < 5; ++x, ++u) {
                         const uint32_t slot = u % kSlots;
                         if (u >= kSlots && !p_wait(&ctrl->blk_empty[slot], ((u / kSlots) - 1) & 1, abort)) {

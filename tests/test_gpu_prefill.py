@@ -302,3 +302,22 @@ def test_repeats_bit_for_bit_on_a_side_stream_and_from_a_graph():
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, want) and torch.equal(lse, wl)
+
+
+def test_a_query_whose_keys_take_longer_than_a_wait():
+    # one query over 120 million keys: 1.5 s of one CTA, whose other tile and scheduler have
+    # nothing to do until the next item. Two keys, at both ends, hold all the weight but 5e-10.
+    Lk = 120_000_000
+    k = torch.zeros((Lk, 1, 128), dtype=torch.bfloat16, device=DEV)  # 31 GB; the values and rotary keys are views of it
+    q = torch.zeros((1, 1, 192), dtype=torch.bfloat16, device=DEV)
+    q[0, 0, 0] = 8
+    k[5, 0, 0] = k[Lk - 10, 0, 0] = 5
+    k[5, 0, 70], k[Lk - 10, 0, 9] = 3, 1
+    cu = lambda n: torch.tensor([0, n], dtype=torch.int32, device=DEV)
+    a = dict(q=q, k_nope=k, k_pe=k[:, 0, 64:], v=k, cu_q=cu(1), cu_k=cu(Lk), q_lens=[1], k_lens=[Lk], Hq=1, Hkv=1)
+    out, lse = _call(a, scale=1.0)
+    want = torch.zeros(128, dtype=torch.bfloat16)
+    want[0], want[70], want[9] = 5, 1.5, 0.5
+    assert torch.equal(out[0, 0].cpu(), want)  # probabilities of 1 and 2^-58: no rounding is left
+    L = 40 + np.log(2.0)
+    assert abs(float(lse) - L) <= 4 * 2.0 ** -23 * (2 * 40 + L) + 2.0 ** -22 * (1 + L)
