@@ -295,7 +295,8 @@ MLA_API int mla_decode_varlen(const void* q_lat, const void* q_pe, int64_t total
  *                [0, total_k], so no row past them is touched.
  *   max_q_len    the longest Lq or a bound of it, >= 1 if total_q > 0: it sizes
  *                the launch, and with a smaller value queries may be left out.
- *   scale        > 0 and finite.
+ *   scale        > 0 and below 2^127. A row whose scores pass 2^30 in magnitude
+ *                may come out NaN (the maximum in log2 units is held in fp32).
  *   out          device, bf16 [total_q, Hq, 128], contiguous, 16-byte aligned.
  *                Rows that no sequence names are not written.
  *   lse          device, fp32 [total_q, Hq], natural log.

@@ -436,7 +436,7 @@ int mla_prefill(const void* q, int64_t q_stride_t, int64_t q_stride_h, const voi
                 int32_t* status, void* stream) {
     if (B < 0 || total_q < 0 || total_k < 0 || max_q_len < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv)
         return MLA_ERR_INVALID_ARG;
-    if (!(scale > 0.f) || scale > FLT_MAX) return MLA_ERR_INVALID_ARG;
+    if (!(scale > 0.f) || scale >= 0x1p127f) return MLA_ERR_INVALID_ARG;  // in log2 units it is finite as well
     if (B == 0 || total_q == 0) return MLA_OK;
     if (max_q_len < 1) return MLA_ERR_INVALID_ARG;
     if (!q || !cu_q_lens || !cu_k_lens || !out || !lse) return MLA_ERR_INVALID_ARG;

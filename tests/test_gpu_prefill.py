@@ -321,3 +321,26 @@ def test_a_query_whose_keys_take_longer_than_a_wait():
     assert torch.equal(out[0, 0].cpu(), want)  # probabilities of 1 and 2^-58: no rounding is left
     L = 40 + np.log(2.0)
     assert abs(float(lse) - L) <= 4 * 2.0 ** -23 * (2 * 40 + L) + 2.0 ** -22 * (1 + L)
+
+
+def test_scores_of_any_magnitude_that_is_allowed():
+    # multiples of 2^24 up to 2^30: a row is the mean of the values with the largest it sees
+    n, H = 300, 2
+    a = _inputs([n], [n], H, 1, seed=31)
+    g = torch.Generator().manual_seed(31)
+    r = torch.randint(-64, 65, (n,), generator=g)
+    for x in ("q", "k_nope", "k_pe"):
+        a[x] = torch.zeros_like(a[x])
+    a["q"][:, :, 3] = 2.0 ** 15
+    a["k_nope"][:, 0, 3] = (r * 2.0 ** 9).to(torch.bfloat16).to(DEV)  # (at most 7 bits)
+    out, lse = _call(a, scale=1.0)
+    out, lse, v = out.double().cpu(), lse.double().cpu(), a["v"][:, 0].double().cpu()
+    for t in range(n):
+        top = int(r[:t + 1].max())
+        best = (r[:t + 1] == top).nonzero()[:, 0]
+        want, A = v[best].mean(0), v[best].abs().mean(0)
+        tol = 2.0 ** -8 * A + 2.0 ** -8 * want.abs() + n * 2.0 ** -23 * A
+        assert bool(((out[t] - want).abs() <= tol).all())
+        L = top * 2.0 ** 24 + np.log(len(best))
+        M = 2.0 ** 30
+        assert bool(((lse[t] - L).abs() <= 4 * 2.0 ** -23 * (2 * M + abs(L)) + 2.0 ** -22 * (1 + abs(L))).all())

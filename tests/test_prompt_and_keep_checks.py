@@ -306,3 +306,8 @@ def test_tables_without_columns(fake):
     _evict(**{**ONE_ROW, "block_table": i32(1, 0)})
     assert fake.calls[-1][1][5] == 0
     _refused(lambda: _evict(block_table=i32(2, 0)), "block_table")
+
+
+@pytest.mark.parametrize("scale", [2.0 ** 127, 3e38])
+def test_prefill_refuses_a_scale_that_log2_units_cannot_hold(lib, scale):
+    assert lib.mla_prefill(*_with(PREFILL, scale=scale)) == INVALID
