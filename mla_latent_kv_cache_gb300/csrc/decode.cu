@@ -1497,9 +1497,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(decode_threads<LSU, 
 // segment is written out before the next segment's first value product).
 // 65..128 rows: the two 64-row groups of a worker are launched as a cluster of
 // two CTAs, so that they run at the same time over the same tiles: each loads
-// them for itself, the second from L2 (2.04 ms for 128 requests with up to 128
-// rows; one multicast copy for both was 2.03 ms, but has no place in a job of
-// several GPUs, which the library cannot tell from one).
+// them for itself, the second from L2 as a rule (2.04 ms for 128 requests with
+// up to 128 rows; one multicast copy for both was 2.02 ms, but has no place in a
+// job of several GPUs, which the library cannot tell from one).
 // fp8_ds_mla rows: TMA lands each K-block's e4m3 codes in the upper half of
 // its slot, four expand warps widen them in place to f16 (the queries' latent
 // part and P are f16 too). Latent width 1792: the two latent halves of every row in the two
@@ -1904,7 +1904,9 @@ __global__ void __launch_bounds__(FoldCfg<NP, KB, PAIR, KIND>::kThreads, 1)
             const int pp = warp == 1 ? 0 : 1;
             It it;
             it.init(p.seq_lens, ctrl->b0, ctrl->j0);
-            const uint64_t pol = l2_policy_evict_first();
+            // a row is read once, and twice by a pair of row groups: there it may stay
+            // until the second has it (reads of HBM 1.12 times the cache -> 1.06)
+            const uint64_t pol = gridDim.y == 2 ? l2_policy_evict_normal() : l2_policy_evict_first();
             const int BR = p.run_rows;
             bool bad = false, ok = true;
             int fsite = 0, ftile = 0;
