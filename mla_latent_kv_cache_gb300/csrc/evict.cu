@@ -766,7 +766,11 @@ int largest_cluster() {
     if (const int n = largest[dev].load(std::memory_order_relaxed)) return n;
     auto* k = evict_select_kernel<32>;
     int CL = 16;
-    if (cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) CL = 8;
+    // (a size that does not fit is no error of a later launch)
+    if (cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) {
+        (void)cudaGetLastError();
+        CL = 8;
+    }
     for (; CL > 1; CL /= 2) {
         cudaLaunchConfig_t cfg = {};
         cudaLaunchAttribute attr[1];
@@ -779,9 +783,10 @@ int largest_cluster() {
         cfg.attrs = attr;
         cfg.numAttrs = 1;
         int n = 0;
-        if (cudaOccupancyMaxActiveClusters(&n, k, &cfg) == cudaSuccess && n > 0) break;
+        const cudaError_t e = cudaOccupancyMaxActiveClusters(&n, k, &cfg);
+        if (e == cudaSuccess && n > 0) break;
+        if (e != cudaSuccess) (void)cudaGetLastError();
     }
-    (void)cudaGetLastError();  // a size that does not fit is no error of a later launch
     largest[dev].store(CL, std::memory_order_relaxed);
     return CL;
 }
