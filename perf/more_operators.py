@@ -154,9 +154,9 @@ def _pages(t, page, gen):
 
 
 def _pow2(top):
-    """The least power of two s with top <= 448 s, within 2^-64 .. 2^64."""
+    """The least power of two s with top <= 448 s, within 2^-40 .. 2^40."""
     m, e = torch.frexp(top)
-    e = torch.where(top > 0, torch.where(m > 0.875, e - 8, e - 9), -64).clamp(-64, 64)
+    e = torch.where(top > 0, torch.where(m > 0.875, e - 8, e - 9), -40).clamp(-40, 40)
     return ((e + 127) << 23).to(torch.int32).view(torch.float32)  # the power itself, exactly
 
 
@@ -394,7 +394,7 @@ def exact(case, seed):
                 here, first = s["table"][b].long()[p // page:(p + m - 1) // page + 1], p // page
                 top = torch.zeros(len(here), dtype=torch.float64, device="cuda")
                 top.index_reduce_(0, place // page - first, row.abs().amax(1), "amax")
-                scale = torch.exp2(torch.ceil(torch.log2(top / 448)).clamp(-64, 64))
+                scale = torch.exp2(torch.ceil(torch.log2(top / 448)).clamp(-40, 40))
                 if p % page:
                     was = got["scales"][here[0]].item()
                     if was < scale[0].item():
