@@ -55,7 +55,17 @@ typedef enum {
 enum { MLA_CACHE_BF16_576 = 0, MLA_CACHE_FP8_DS_MLA_656 = 1 };
 enum { MLA_OUT_BF16 = 0, MLA_OUT_F32 = 1 };
 
-/* Bytes of one cached row for a cache kind (1152 or 656), or 0 if unknown. */
+/*
+ * A third kind of rows, with the scale outside of them (mla_cache_append and
+ * mla_decode_fp8_page alone take it; the other calls refuse it):
+ *   MLA_CACHE_FP8_PAGE_576   576 bytes: the e4m3 codes of c[0:512] / s and
+ *                            k_pe[0:64] / s, with one fp32 scale s for all rows
+ *                            of a page, in an array [pages] of the caller's. s
+ *                            is a power of two, 2^-40 .. 2^40.
+ */
+enum { MLA_CACHE_FP8_PAGE_576 = 2 };
+
+/* Bytes of one cached row for a cache kind (1152, 656 or 576), or 0 if unknown. */
 MLA_API int mla_row_bytes(int cache_kind);
 
 /*
@@ -403,6 +413,118 @@ MLA_API int mla_cache_evict(void* cache, int row_bytes, int64_t num_slots, int p
                             int n_sink, int n_recent, int32_t* new_seq_lens, float* new_weights,
                             int32_t* new_positions, int32_t* moves, int64_t moves_stride, int32_t* status,
                             void* stream);
+
+/*
+ * mla_rope - rotary positions: the pairs (a, b) of every head's rotary part
+ * become
+ *   (a cos u - b sin u, a sin u + b cos u) * mscale,   u = 2 pi positions[t] steps[i] / 2^64
+ * for token t and pair i < rot_dim / 2: values (i, i + rot_dim / 2), or (2i, 2i + 1)
+ * with interleaved != 0. In 32 bits, rounded once to the values' type.
+ *   x, out       device, [T, H, rot_dim]: bf16, or fp32 with f32 != 0; strides
+ *                in elements between tokens and heads (the rotary part of wider
+ *                heads is passed as it lies), at least rot_dim where there is
+ *                more than one head or token. out may be x itself, with its
+ *                strides, and may not overlap it otherwise, except as another
+ *                range of values of the same heads. 16-byte aligned bases and
+ *                strides with rot_dim a multiple of 16 up to 256 are fast; any
+ *                other alignment and even rot_dim is taken as well.
+ *   positions    device, int32 [T] (negative ones turn back).
+ *   steps        device, int64 [rot_dim / 2], 8-byte aligned: how far a pair
+ *                turns for each position, as a fraction of a turn times 2^64
+ *                (modulo 2^64), so far positions lose nothing. Frequencies
+ *                scaled for long contexts are other steps (rope_steps in the
+ *                Python module makes them); the gradient, or the way back, is
+ *                the call with -steps.
+ *   mscale       factor on the rotated values, finite.
+ */
+MLA_API int mla_rope(const void* x, int64_t x_stride_t, int64_t x_stride_h, const int32_t* positions,
+                     const int64_t* steps, int64_t T, int H, int rot_dim, int f32, int interleaved, float mscale,
+                     void* out, int64_t out_stride_t, int64_t out_stride_h, void* stream);
+
+/*
+ * mla_cache_append - new tokens of a batch, from the projection's output to rows
+ * of the paged cache: the latent's norm, the rotation of the shared key and the
+ * write, in one launch. Request b has n = cu_new_lens[b+1] - cu_new_lens[b] new
+ * tokens, rows cu_new_lens[b] .. of the inputs, which are the last n of its
+ * seq_lens[b]: token i of them has place j = seq_lens[b] - n + i, in slot
+ * block_table[b][j / page_size] * page_size + j % page_size, and
+ *   c' = c * rsqrt(mean(c^2) + eps) * norm_weight      (c itself without a weight)
+ *   k' = k_pe turned as in mla_rope by positions[row]  (by j without positions;
+ *        k_pe itself without steps)
+ * in 32 bits; each cached value is rounded once:
+ *   MLA_CACHE_BF16_576        (c', k') in bf16; lat_dim 256, 512, 768 or 1792.
+ *   MLA_CACHE_FP8_DS_MLA_656  as mla_cache_write quantises, from the 32-bit values.
+ *   MLA_CACHE_FP8_PAGE_576    codes e4m3(x / s), saturated, s the page's scale: the
+ *       least power of two with |x| <= 448 s for every finite new value of the
+ *       page, and not less than 2^-40. A page entered behind earlier rows keeps
+ *       its scale, or if the new one is larger, takes that and has the codes of
+ *       its earlier rows multiplied by old / new and rounded (a power of two: only
+ *       those that become subnormal change their value).
+ *   latent, k_pe  device, bf16 [total, lat_dim] and [total, 64], row strides in
+ *                elements, multiples of 8, 16-byte aligned (columns of one
+ *                projection may be passed as they lie).
+ *   cu_new_lens  device, int32 [B + 1], non-decreasing; entries are clamped to
+ *                [0, total]. Rows of the inputs that no request names are left out.
+ *   seq_lens     device, int32 [B], the new tokens counted.
+ *   block_table  device, int32 [B, block_table_cols], block_table_stride >=
+ *                block_table_cols elements between rows. Pages that get new
+ *                tokens are not shared between requests.
+ *   positions    device, int32 [total], or NULL.
+ *   steps        device, int64 [32], 8-byte aligned, or NULL; interleaved and
+ *                mscale as in mla_rope.
+ *   norm_weight  device, bf16 [lat_dim], 16-byte aligned, or NULL. eps >= 0.
+ *   cache        device, num_slots rows of the kind, 16-byte aligned. Slots that
+ *                no new token names are left as they were, but for the rescaled
+ *                ones above.
+ *   scales       MLA_CACHE_FP8_PAGE_576: device, fp32 [num_slots / page_size].
+ *                Entries of pages without new tokens are left as they were.
+ *   rows         device, bf16 [total, >= lat_dim + 64], or NULL: (c', k') of
+ *                every named token besides, for the up-projection and
+ *                mla_prefill. Row stride rows_stride, a multiple of 8, 16-byte
+ *                aligned. May be the inputs' own memory if these are its columns.
+ *   status       device int32 or NULL: ORed with 2 if a token had no place (a
+ *                request shorter than its new tokens) or its page lay outside
+ *                the pool or the table row. Such a token is not cached.
+ */
+MLA_API int mla_cache_append(const void* latent, int64_t latent_stride, const void* k_pe, int64_t k_pe_stride,
+                             const int32_t* cu_new_lens, const int32_t* seq_lens, const int32_t* block_table,
+                             int64_t block_table_stride, int64_t block_table_cols, int B, int64_t total, int page_size,
+                             const int32_t* positions,
+                             const int64_t* steps, int interleaved, float mscale, const void* norm_weight, float eps,
+                             void* cache, int cache_kind, int lat_dim, int64_t num_slots, float* scales, void* rows,
+                             int64_t rows_stride, int32_t* status, void* stream);
+
+/*
+ * mla_decode_fp8_page - mla_decode over MLA_CACHE_FP8_PAGE_576 rows: with s(j) the
+ * scale of token j's page and code_j its 576 values,
+ *   score_j = scale * s(j) * (q_lat[r] . code_j[0:512] + q_pe[r] . code_j[512:576])
+ *   out[r]  = sum_j softmax_j(score) s(j) code_j[0:512],   lse[r] = ln sum_j exp(score_j).
+ * The codes go to the tensor cores as they are. A query value is the sum of two
+ * e4m3 values of different scale: those below 2^-15 of their row's largest are
+ * rounded, by at most 2^-22 of it. A probability times s(j) is held likewise
+ * (up to 32 query rows: rounded by at most 2^-8 of itself or 2^-20 of the largest;
+ * above, 2^-8 or 2^-16). Sums are fp32.
+ *   scales       device, fp32 [num_slots / page_size], positive; one outside 2^-40 ..
+ *                2^40 counts as the nearer bound.
+ *   block_table  device, int32 [B, block_table_cols], block_table_stride >=
+ *                block_table_cols elements between rows; a page index past the
+ *                columns counts as an entry outside the pool.
+ *   cu_q_lens    device, int32 [B + 1], or NULL: with it, each request has its own
+ *                number of query tokens, at most q_len, as in mla_decode_varlen.
+ *   total_q_tokens  query tokens in q_lat, q_pe, out and lse (B * q_len without
+ *                cu_q_lens).
+ * A NaN in a row makes NaN of the query rows that see it, and of no others. Every
+ * other argument, the rows without a visible token, the workspace
+ * (mla_decode_workspace_bytes(B, q_len, Hq, num_ctas)) and the status words are as
+ * in mla_decode and mla_decode_varlen. Up to 64 query rows (Hq * q_len) the cache
+ * is read once per request; each further 64 rows read it again, at the same time.
+ */
+MLA_API int mla_decode_fp8_page(const void* q_lat, const void* q_pe, int64_t total_q_tokens, const void* cache,
+                                const float* scales, int64_t num_slots, int page_size, const int32_t* block_table,
+                                int64_t block_table_stride, int64_t block_table_cols, const int32_t* seq_lens,
+                                const int32_t* cu_q_lens, int B, int q_len, int Hq, float scale, void* out, int out_dtype,
+                                float* lse, void* workspace,
+                                size_t workspace_bytes, int num_ctas, void* stream);
 
 /*
  * mla_merge_lse - combine S partial results of the same N rows computed over

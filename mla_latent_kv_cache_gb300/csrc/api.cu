@@ -5,6 +5,7 @@
 
 #include <algorithm>
 #include <cfloat>
+#include <cmath>
 #include <climits>
 #include <cstdint>
 #include <atomic>
@@ -133,7 +134,10 @@ void* decode_scratch_ptr() {
 extern "C" {
 
 int mla_row_bytes(int cache_kind) {
-    return cache_kind == MLA_CACHE_BF16_576 ? mla::kRowBf16 : cache_kind == MLA_CACHE_FP8_DS_MLA_656 ? mla::kRowFp8 : 0;
+    return cache_kind == MLA_CACHE_BF16_576         ? mla::kRowBf16
+           : cache_kind == MLA_CACHE_FP8_DS_MLA_656 ? mla::kRowFp8
+           : cache_kind == MLA_CACHE_FP8_PAGE_576   ? mla::kRowPage
+                                                    : 0;
 }
 
 const char* mla_status_string(int status) {
@@ -641,6 +645,220 @@ int mla_cache_evict(void* cache, int row_bytes, int64_t num_slots, int page_size
     p.moves_stride = moves_stride;
     p.status = status;
     const cudaError_t e = mla::launch_evict(p, di.sms, g_test_evict_ctas.exchange(0), static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+}
+
+int mla_rope(const void* x, int64_t x_stride_t, int64_t x_stride_h, const int32_t* positions, const int64_t* steps,
+             int64_t T, int H, int rot_dim, int f32, int interleaved, float mscale, void* out, int64_t out_stride_t,
+             int64_t out_stride_h, void* stream) {
+    if (T < 0 || H < 0 || rot_dim <= 0 || rot_dim % 2 || !(std::fabs(mscale) <= FLT_MAX)) return MLA_ERR_INVALID_ARG;
+    if (T == 0 || H == 0) return MLA_OK;
+    if (!x || !out || !positions || !steps) return MLA_ERR_INVALID_ARG;
+    const uintptr_t es = f32 ? 4 : 2, xa = reinterpret_cast<uintptr_t>(x), oa = reinterpret_cast<uintptr_t>(out);
+    if (xa % es || oa % es || !aligned4(positions) || (reinterpret_cast<uintptr_t>(steps) & 7u)) return MLA_ERR_INVALID_ARG;
+    // a grid has a CTA for at least 256 pairs, or for four tokens
+    if (T > INT32_MAX || rot_dim > (1 << 20) || H > (1 << 20) || T * H > (256LL * INT32_MAX) / rot_dim)
+        return MLA_ERR_UNSUPPORTED;
+    mla::RopeParams p;
+    // (the stride of a dimension of one entry says nothing)
+    p.x_h = H > 1 ? x_stride_h : rot_dim;
+    p.o_h = H > 1 ? out_stride_h : rot_dim;
+    p.x_t = T > 1 ? x_stride_t : p.x_h * H;
+    p.o_t = T > 1 ? out_stride_t : p.o_h * H;
+    for (const int64_t s : {p.x_h, p.x_t, p.o_h, p.o_t}) {
+        if (s < rot_dim) return MLA_ERR_INVALID_ARG;
+        if (s > (1LL << 30)) return MLA_ERR_UNSUPPORTED;
+    }
+    // heads of a token, then tokens, or the other way round: rows apart either way
+    auto rows_apart = [&](int64_t st, int64_t sh) {
+        return T == 1 || H == 1 || st >= sh * (H - 1) + rot_dim || sh >= st * (T - 1) + rot_dim;
+    };
+    if (!rows_apart(p.x_t, p.x_h) || !rows_apart(p.o_t, p.o_h)) return MLA_ERR_INVALID_ARG;
+    if (xa != oa || p.x_t != p.o_t || p.x_h != p.o_h) {
+        // not the same view: apart, or other values of the same heads
+        const uintptr_t xe = xa + es * ((T - 1) * p.x_t + (H - 1) * p.x_h + rot_dim);
+        const uintptr_t oe = oa + es * ((T - 1) * p.o_t + (H - 1) * p.o_h + rot_dim);
+        if (xa < oe && oa < xe) {
+            const uintptr_t d = (xa > oa ? xa - oa : oa - xa) / es;
+            const int64_t step = H > 1 ? (T > 1 ? std::min(p.x_t, p.x_h) : p.x_h) : p.x_t;
+            if (p.x_t != p.o_t || p.x_h != p.o_h || (xa - oa) % es || d < static_cast<uintptr_t>(rot_dim) ||
+                d + rot_dim > static_cast<uintptr_t>(step))
+                return MLA_ERR_INVALID_ARG;
+        }
+    }
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return MLA_ERR_CUDA;
+    const DevInfo di = dev_info(dev);
+    if (di.sms <= 0) return MLA_ERR_CUDA;
+    if (di.major != 10) return MLA_ERR_UNSUPPORTED;
+    p.x = x;
+    p.out = out;
+    p.positions = positions;
+    p.steps = steps;
+    p.T = T;
+    p.H = H;
+    p.R = rot_dim;
+    p.interleaved = interleaved != 0;
+    p.mscale = mscale;
+    p.chunks = p.items_chunk = 1;
+    const cudaError_t e = mla::launch_rope(p, f32 != 0, di.sms, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+}
+
+int mla_cache_append(const void* latent, int64_t latent_stride, const void* k_pe, int64_t k_pe_stride,
+                     const int32_t* cu_new_lens, const int32_t* seq_lens, const int32_t* block_table,
+                     int64_t block_table_stride, int64_t block_table_cols, int B, int64_t total, int page_size,
+                     const int32_t* positions, const int64_t* steps, int interleaved, float mscale, const void* norm_weight, float eps, void* cache,
+                     int cache_kind, int lat_dim, int64_t num_slots, float* scales, void* rows, int64_t rows_stride,
+                     int32_t* status, void* stream) {
+    if (B < 0 || total < 0 || page_size <= 0 || num_slots < 0) return MLA_ERR_INVALID_ARG;
+    if (mla_row_bytes(cache_kind) == 0) return MLA_ERR_INVALID_ARG;
+    const bool bf16 = cache_kind == MLA_CACHE_BF16_576;
+    if (lat_dim != 512 && (!bf16 || (lat_dim != 256 && lat_dim != 768 && lat_dim != 1792))) return MLA_ERR_UNSUPPORTED;
+    if (!(eps >= 0.f) || eps > FLT_MAX || !(std::fabs(mscale) <= FLT_MAX)) return MLA_ERR_INVALID_ARG;
+    if (B == 0 || total == 0) return MLA_OK;
+    if (!latent || !k_pe || !cu_new_lens || !seq_lens || !block_table || !cache) return MLA_ERR_INVALID_ARG;
+    if ((cache_kind == MLA_CACHE_FP8_PAGE_576) != (scales != nullptr)) return MLA_ERR_INVALID_ARG;
+    if (!aligned16(latent) || !aligned16(k_pe) || !aligned16(cache) || !aligned16(norm_weight) || !aligned16(rows))
+        return MLA_ERR_INVALID_ARG;
+    if (!aligned4(cu_new_lens) || !aligned4(seq_lens) || !aligned4(block_table) || !aligned4(positions) ||
+        !aligned4(scales) || !aligned4(status) || (reinterpret_cast<uintptr_t>(steps) & 7u))
+        return MLA_ERR_INVALID_ARG;
+    if (latent_stride < lat_dim || latent_stride % 8 || k_pe_stride < mla::kP || k_pe_stride % 8 || block_table_cols < 0 ||
+        block_table_stride < block_table_cols)
+        return MLA_ERR_INVALID_ARG;
+    const int64_t width = lat_dim + mla::kP;
+    if (rows && (rows_stride < width || rows_stride % 8)) return MLA_ERR_INVALID_ARG;
+    // prefix sums are 32-bit; a grid has a CTA for eight tokens, or two and one for each page
+    if (total > INT32_MAX || B > (1 << 28)) return MLA_ERR_UNSUPPORTED;
+    if (latent_stride > (1LL << 30) || k_pe_stride > (1LL << 30) || (rows && rows_stride > (1LL << 30)))
+        return MLA_ERR_UNSUPPORTED;
+    if (rows) {
+        const uintptr_t r = reinterpret_cast<uintptr_t>(rows), re = r + 2 * ((total - 1) * rows_stride + width);
+        auto apart_or_column = [&](const void* in, int64_t stride, int64_t w, int64_t col) {
+            const uintptr_t a = reinterpret_cast<uintptr_t>(in), ae = a + 2 * ((total - 1) * stride + w);
+            return ae <= r || re <= a || (a == r + 2 * col && (stride == rows_stride || total == 1));
+        };
+        if (!apart_or_column(latent, latent_stride, lat_dim, 0) || !apart_or_column(k_pe, k_pe_stride, mla::kP, lat_dim))
+            return MLA_ERR_INVALID_ARG;
+    }
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return MLA_ERR_CUDA;
+    const DevInfo di = dev_info(dev);
+    if (di.sms <= 0) return MLA_ERR_CUDA;
+    if (di.major != 10) return MLA_ERR_UNSUPPORTED;
+    mla::AppendParams p;
+    p.latent = static_cast<const __nv_bfloat16*>(latent);
+    p.lat_st = latent_stride;
+    p.k_pe = static_cast<const __nv_bfloat16*>(k_pe);
+    p.pe_st = k_pe_stride;
+    p.cu = cu_new_lens;
+    p.seq_lens = seq_lens;
+    p.B = B;
+    p.total = total;
+    p.block_table = block_table;
+    p.bt_stride = block_table_stride;
+    p.bt_cols = block_table_cols;
+    p.page_size = page_size;
+    p.positions = positions;
+    p.steps = steps;
+    p.interleaved = interleaved != 0;
+    p.mscale = mscale;
+    p.norm = static_cast<const __nv_bfloat16*>(norm_weight);
+    p.eps = eps;
+    p.cache = static_cast<uint8_t*>(cache);
+    p.num_slots = num_slots;
+    p.scales = scales;
+    p.rows = static_cast<__nv_bfloat16*>(rows);
+    p.rows_st = rows_stride;
+    p.status = status;
+    const cudaError_t e = mla::launch_append(p, cache_kind, lat_dim, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+}
+
+int mla_decode_fp8_page(const void* q_lat, const void* q_pe, int64_t total_q_tokens, const void* cache,
+                        const float* scales, int64_t num_slots, int page_size, const int32_t* block_table,
+                        int64_t block_table_stride, int64_t block_table_cols, const int32_t* seq_lens,
+                        const int32_t* cu_q_lens, int B, int q_len, int Hq, float scale, void* out, int out_dtype,
+                        float* lse, void* workspace, size_t workspace_bytes, int num_ctas, void* stream) {
+    if (B <= 0 || q_len <= 0 || Hq <= 0 || page_size <= 0 || num_slots <= 0 || num_ctas < 0 || total_q_tokens <= 0)
+        return MLA_ERR_INVALID_ARG;
+    if (!cu_q_lens && total_q_tokens != static_cast<int64_t>(B) * q_len) return MLA_ERR_INVALID_ARG;
+    if (out_dtype != MLA_OUT_BF16 && out_dtype != MLA_OUT_F32) return MLA_ERR_INVALID_ARG;
+    if (!q_lat || !q_pe || !cache || !scales || !block_table || !seq_lens || !out || !lse || !workspace)
+        return MLA_ERR_INVALID_ARG;
+    if (!aligned16(q_lat) || !aligned16(q_pe) || !aligned16(cache) || !aligned16(out) ||
+        (reinterpret_cast<uintptr_t>(workspace) & 255u))
+        return MLA_ERR_INVALID_ARG;
+    if (!aligned4(scales) || !aligned4(block_table) || !aligned4(seq_lens) || !aligned4(cu_q_lens) || !aligned4(lse))
+        return MLA_ERR_INVALID_ARG;
+    if (block_table_cols < 0 || block_table_stride < block_table_cols || scale != scale) return MLA_ERR_INVALID_ARG;
+    if (num_slots > 0x7fffffffLL) return MLA_ERR_UNSUPPORTED;  // TMA row coordinates are 32-bit
+    const int64_t HQ64 = static_cast<int64_t>(Hq) * q_len;
+    if (HQ64 > (1 << 20) || total_q_tokens * Hq > INT32_MAX) return MLA_ERR_UNSUPPORTED;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return MLA_ERR_CUDA;
+    const DevInfo di = dev_info(dev);
+    if (di.sms <= 0) return MLA_ERR_CUDA;
+    if (di.major != 10) return MLA_ERR_UNSUPPORTED;
+    const int HQ = static_cast<int>(HQ64), GY = (HQ + 63) / 64, NP = rows_padded(HQ < 64 ? HQ : 64);
+    const int nctas = ws_ctas(num_ctas, di.sms);
+    const WsLayout wl = decode_ws_layout(B, HQ, nctas, mla::kD);
+    if (workspace_bytes < wl.total) return MLA_ERR_WORKSPACE;
+    // the row groups of a worker run at the same time, so that the later ones find the tiles in L2
+    const int W = std::max(1, std::min(num_ctas > 0 ? num_ctas : di.sms / GY, nctas));
+    const bool lsu = page_size % 8 != 0;  // such pages cannot be fetched as boxes of 8 rows
+
+    mla::DecodeParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.run_rows = gcd_int(page_size, 128);
+    mla::DecodeMaps maps;
+    std::memset(&maps, 0, sizeof(maps));
+    if (!lsu) {
+        auto enc = encode_fn();
+        if (!enc) return MLA_ERR_CUDA;
+        auto map = [&](CUtensorMap* m, cuuint32_t width, CUtensorMapSwizzle swizzle) {
+            cuuint64_t gdim[2] = {static_cast<cuuint64_t>(mla::kRowPage), static_cast<cuuint64_t>(num_slots)};
+            cuuint64_t gstride[1] = {static_cast<cuuint64_t>(mla::kRowPage)};
+            cuuint32_t box[2] = {width, static_cast<cuuint32_t>(p.run_rows)}, estride[2] = {1u, 1u};
+            return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(cache), gdim, gstride, box, estride,
+                       CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+        };
+        if (!map(&maps.lat, 128u, CU_TENSOR_MAP_SWIZZLE_128B) || !map(&maps.rope, 64u, CU_TENSOR_MAP_SWIZZLE_64B))
+            return MLA_ERR_CUDA;
+    }
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    p.q_lat = static_cast<const __nv_bfloat16*>(q_lat);
+    p.q_pe = static_cast<const __nv_bfloat16*>(q_pe);
+    p.cache = static_cast<const uint8_t*>(cache);
+    p.num_slots = num_slots;
+    p.block_table = block_table;
+    p.bt_stride = block_table_stride;
+    p.bt_cols = block_table_cols;
+    p.scales = scales;
+    p.seq_lens = seq_lens;
+    p.out = out;
+    p.lse = lse;
+    p.status = reinterpret_cast<int*>(ws);
+    p.rec = reinterpret_cast<int*>(ws + wl.rec_off);
+    p.part_lse = reinterpret_cast<float*>(ws + wl.lse_off);
+    p.part_o = reinterpret_cast<float*>(ws + wl.o_off);
+    p.scale_log2 = scale * 1.4426950408889634f;
+    p.page_size = page_size;
+    p.tile_shift = 7;
+    p.B = B;
+    p.Qt = q_len;
+    p.Hq = Hq;
+    p.HQ = HQ;
+    p.out_f32 = out_dtype == MLA_OUT_F32;
+    p.SPG = W + B;
+    p.wseg = 2;  // what a request boundary costs a worker, in tiles: its queries, the drain before them
+    p.cu_q = cu_q_lens;
+    p.total_q = static_cast<int>(total_q_tokens);
+    p.lat_dim = mla::kD;
+    p.rope_dim = mla::kP;
+    const cudaError_t e = mla::launch_decode_page8(maps, p, NP, lsu, W, GY, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 

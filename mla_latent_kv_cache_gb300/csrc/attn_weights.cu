@@ -72,23 +72,6 @@ struct WCtrl {
 };
 constexpr int kCtrlBytes = (sizeof(WCtrl) + 1023) / 1024 * 1024;
 
-// D(tmem) (+)= A(smem, e4m3) * B(smem, 8-bit type of idesc), fp32 accumulate, K = 32.
-__device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                        uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-
-// Instruction descriptors with N known at run time, both operands K-major:
-// kind::f8f6f4 (types 0 = e4m3, 1 = e5m2) and kind::f16 with bf16 operands.
-__device__ __forceinline__ uint32_t idesc_f8(int M, int N, uint32_t a_type, uint32_t b_type) {
-    return (1u << 4) | (a_type << 7) | (b_type << 10) | (static_cast<uint32_t>(N >> 3) << 17) |
-           (static_cast<uint32_t>(M >> 4) << 24);
-}
-
 __device__ __forceinline__ int w_tokens(const WeightsParams& p, int b) { return max(__ldg(p.seq_lens + b), 0); }
 // Tiles of the tokens whose weights are kept.
 __device__ __forceinline__ int w_tiles(const WeightsParams& p, int b) {

@@ -1,0 +1,848 @@
+// Paged MLA decode over 8-bit rows with one scale for each page
+// (mla_decode_fp8_page): tcgen05 products on the codes as they are.
+//
+// Mathematics. With code_j the 576 e4m3 codes of token j and s_j = s(page of j):
+//   score_j = scale s_j (q . code_j),   out = sum_j p_j s_j code_j / sum_j p_j.
+// The scale is the same for all of a row, so it never meets a code: it is one
+// factor on the finished score, and it goes into the weight of the value
+// product. In log2 units, x_j = log2(e) score_j + log2(s_j) and a running
+// maximum m over x (not over the scores) give
+//   P_j = 2^(x_j - m),   O += P_j code_j,   l += P_j / s_j,
+//   out = O / l,   lse = (m + log2 l) ln 2,
+// and P_j lies in a known range whatever the scales are, as 8 bits need it.
+//
+// 8-bit operands. A bf16 query value, scaled by a power of two per row to have
+// the row's largest in [128, 256), is h + l / 32: h the nearest e4m3 value, l the
+// nearest to 32 times the rest (the rest is at most 8, and has at most 3 more
+// bits). h and l are two columns of the B operand, so the score product reads
+// the tile once, and the two sums meet in fp32. P in (0, 256] is split the same
+// way. Up to 32 query rows its two parts are columns too, with accumulators of
+// their own; at 64 rows TMEM has no room for them, and the parts (l not scaled
+// there) go into the same accumulator one after the other.
+//
+// Bound: HBM, 576 bytes a token; at 16 query rows the products take a third of
+// the time the bytes do, at 64 rows about as long. So the kernel is a stream:
+// 128-token tiles arrive by TMA as four blocks of 128 dims (16 KB, one 128-byte
+// swizzle row a token) and the rotary part (8 KB). A block is the K-major A
+// operand of S = C Q^T (thread = token = TMEM lane) and the MN-major A operand of
+// O^T += C^T P, and its ring slot is free when its own value product is done.
+//
+// Warps: 0 issues S, 3 the value product, 1 loads; 4..7 (and 8..11 from 32 rows
+// on, each group half of the columns) softmax, P and output; the last four turn
+// a request's queries into h and l. Pages that are not a multiple of 8 rows are
+// read row by row by those last four. The split of the work between CTAs, the
+// partial results and their merge are those of the other decode kernels.
+#include <climits>
+
+#include "decode_split.cuh"
+#include "launch.cuh"
+#include "mla_common.cuh"
+
+namespace mla {
+
+namespace {
+
+constexpr int kTok = 128;             // tokens a tile
+constexpr int kBlk = kTok * 128;      // bytes of a latent block
+constexpr int kRopeBlk = kTok * 64;   // and of the rotary part
+constexpr int kRopes = 2;
+constexpr int kQGens = 4;             // generations of query scales that may be in use at once
+constexpr int kScs = 4;               // tiles' scales
+constexpr float kTop = 6.f;           // P of the maximum itself is 2^6
+constexpr float kSlack = 2.f;         // which a score may pass by so much before the maximum is raised: P <= 2^8
+constexpr float kNoMax = -1e30f;
+constexpr float kLn2f = 0.69314718055994530942f;
+
+template <int NP>
+struct P8Cfg {
+    static constexpr bool kStack = NP <= 32;            // P's parts in columns of their own
+    static constexpr int kSlots = NP == 16 ? 11 : NP == 32 ? 9 : 7;
+    static constexpr int kPBufs = NP == 64 ? 1 : 2;
+    static constexpr int kGroups = NP == 16 ? 1 : 2;    // softmax groups of four warps
+    static constexpr int kCW = NP / kGroups;            // columns of a group
+    static constexpr int kQBlk = 2 * NP * 128;          // a 128-dim block of the queries: h rows, then l rows
+    static constexpr int kQBytes = 4 * kQBlk + 2 * NP * 64;
+    static constexpr int kPRow = kStack ? 2 * NP : NP;  // bytes of a token's row of P (one swizzle row)
+    static constexpr int kPBytes = 2 * NP * kTok;
+    static constexpr uint32_t kPSw = kPRow == 32 ? kSw32 : kSw64;
+    static constexpr int kOffRope = kSlots * kBlk;
+    static constexpr int kOffQ = kOffRope + kRopes * kRopeBlk;
+    static constexpr int kOffP = kOffQ + kQBytes;
+    static constexpr int kOffCtrl = kOffP + kPBufs * kPBytes;
+    static constexpr int kQWarp = 4 + 4 * kGroups;      // first of the four query warps
+    static constexpr int kThreads = 32 * (kQWarp + 4);
+    static constexpr int kOCols = 4 * (kStack ? 2 * NP : NP);
+    static constexpr int kColS = kOCols;                // two S buffers of 2 NP columns
+    static_assert(kPRow == 32 || kPRow == 64, "one swizzle row");
+    static_assert(kColS + 4 * NP <= 512, "tmem");
+    static_assert(kQBlk % 1024 == 0 && (2 * NP * 64) % 1024 == 0 && kPBytes % 1024 == 0, "alignment of the swizzle atoms");
+};
+
+struct P8Ctrl {
+    uint64_t blk_full[12], blk_empty[12];
+    uint64_t rope_full[kRopes], rope_empty[kRopes];
+    uint64_t s_full[2], s_free[2];
+    // tile t's hand-off is p_full[t & 1], its products' end o_done[t & 1]: the
+    // softmax may be a tile ahead of a slow issuer, which a single barrier's
+    // parity could not tell
+    uint64_t p_full[2], o_done[2];
+    uint64_t q_full[kQGens], q_empty;
+    uint64_t sc_full[kScs];
+    uint64_t fin[2];
+    uint32_t tmem_base;
+    int abort;
+    int t_begin, t_end, b0, j0;
+    alignas(16) float sc[kScs][kTok];   // scales of a tile: one for each run of rows in a page, or each row
+    alignas(16) float kq[kQGens][64];   // what turns a column's sum into log2 units (without the token's scale)
+    alignas(16) float mm[64];           // running maximum - kTop
+    alignas(16) float alpha[64];
+    alignas(16) float red[4][64];
+    alignas(16) float inv[64];
+};
+
+template <int NP>
+constexpr int p8_smem() {
+    return P8Cfg<NP>::kOffCtrl + (static_cast<int>(sizeof(P8Ctrl)) + 15) / 16 * 16 + 1024;
+}
+static_assert(p8_smem<16>() <= 232448 && p8_smem<32>() <= 232448 && p8_smem<64>() <= 232448, "shared memory");
+
+// Page and slot of token tok of the request with this table row; page 0 and a
+// flag for an entry outside the pool or the row.
+__device__ __forceinline__ int p8_slot(const DecodeParams& p, const int32_t* btr, int tok, int& page, bool& bad) {
+    const int pi = tok / p.page_size;
+    int64_t pg = pi < p.bt_cols ? __ldg(btr + pi) : -1;
+    if (pg < 0 || (pg + 1) * p.page_size > p.num_slots) {
+        bad = true;
+        pg = 0;
+    }
+    page = static_cast<int>(pg);
+    const int64_t s = pg * p.page_size + tok % p.page_size;
+    return static_cast<int>(s < p.num_slots ? s : 0);
+}
+
+// A page's scale. A pool smaller than a page has no scales (and no rows that count).
+__device__ __forceinline__ float p8_scale(const DecodeParams& p, int page) {
+    if (p.num_slots < p.page_size) return 1.f;
+    const float s = __ldg(p.scales + page);
+    return s < 0x1p-40f ? 0x1p-40f : s > 0x1p40f ? 0x1p40f : s;  // (NaN stays)
+}
+
+__device__ __forceinline__ void p8_cp16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// Two values as e4m3 codes (low byte the first) and what is left of them.
+__device__ __forceinline__ uint32_t p8_split(float a, float b, float& ra, float& rb) {
+    const uint32_t h = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+    const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(h), __NV_E4M3);
+    const float2 hf = __half22float2(*reinterpret_cast<const __half2*>(&hr));
+    ra = a - hf.x;
+    rb = b - hf.y;
+    return h & 0xFFFFu;
+}
+__device__ __forceinline__ uint32_t p8_codes(float a, float b) {
+    return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3) & 0xFFFFu;
+}
+
+template <int NP, bool LSU>
+__global__ void __launch_bounds__(P8Cfg<NP>::kThreads, 1)
+    mla_decode_page8_kernel(const __grid_constant__ DecodeMaps maps, const DecodeParams p) {
+    using C = P8Cfg<NP>;
+    using It = TileItT<7>;
+    constexpr int CW = C::kCW;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    uint8_t* ring = smem;
+    uint8_t* rope_ring = smem + C::kOffRope;
+    uint8_t* qs = smem + C::kOffQ;
+    uint8_t* pbufs = smem + C::kOffP;
+    P8Ctrl* ctrl = reinterpret_cast<P8Ctrl*>(smem + C::kOffCtrl);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int g = blockIdx.x, G = gridDim.x, gy = blockIdx.y;
+    volatile int* abort = &ctrl->abort;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::kSlots; ++i) {
+            mbar_init(&ctrl->blk_full[i], LSU ? 4 : 1);
+            mbar_init(&ctrl->blk_empty[i], 1);
+        }
+        for (int i = 0; i < kRopes; ++i) {
+            mbar_init(&ctrl->rope_full[i], LSU ? 4 : 1);
+            mbar_init(&ctrl->rope_empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&ctrl->s_full[i], 1);
+            mbar_init(&ctrl->s_free[i], 4 * C::kGroups);
+            mbar_init(&ctrl->p_full[i], 4 * C::kGroups);
+            mbar_init(&ctrl->o_done[i], 1);
+            mbar_init(&ctrl->fin[i], 1);
+        }
+        for (int i = 0; i < kQGens; ++i) mbar_init(&ctrl->q_full[i], 4);
+        mbar_init(&ctrl->q_empty, 1);
+        for (int i = 0; i < kScs; ++i) mbar_init(&ctrl->sc_full[i], LSU ? 4 : 1);
+        ctrl->abort = 0;
+        fence_mbar_init();
+    }
+    if (!LSU && warp == 1 && lane == 0) {
+        prefetch_tensormap(&maps.lat);
+        prefetch_tensormap(&maps.rope);
+    }
+    // the previous kernel in the stream may still be writing the inputs or
+    // reading the workspace
+    griddep_wait();
+    if (threadIdx.x == 0) {
+        int4* r = reinterpret_cast<int4*>(status_rec(p));
+#pragma unroll
+        for (int k = 0; k < kStatusRecWords / 4; ++k) r[k] = make_int4(0, 0, 0, 0);
+    }
+    if (warp == 0) {
+        tmem_alloc(&ctrl->tmem_base, 512);
+        tmem_relinquish();
+        tc_fence_before();
+    }
+    if (warp == 2) {
+        const TileRange r = scan_range<7>(p, g, G, lane);
+        if (lane == 0) {
+            ctrl->t_begin = r.tb;
+            ctrl->t_end = r.te;
+            ctrl->b0 = r.b0;
+            ctrl->j0 = r.j0;
+        }
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) griddep_launch_dependents();  // the merge grid may be scheduled as CTAs retire
+    tc_fence_after();
+    const uint32_t tmem = ctrl->tmem_base;
+    const int ntiles = ctrl->t_end - ctrl->t_begin;
+    if (ntiles == 0 && ctrl->j0 > 0 && threadIdx.x < 64) {
+        // an empty range strictly inside request b0 (more workers than tiles):
+        // the merge of b0 counts this worker's slot, so mark it empty
+        p.part_lse[(static_cast<int64_t>(gy) * p.SPG + g + ctrl->b0) * 64 + threadIdx.x] = -INFINITY;
+    }
+    It it;
+    if (ntiles > 0) it.init(p.seq_lens, ctrl->b0, ctrl->j0);
+
+    // the query rows of request b in this row group as h and l codes, and their scales; four warps
+    auto load_q = [&](int b, int gen) {
+        const int wq = warp - C::kQWarp;
+        const int rows = req_rows_in_group(p, b, gy);
+        const int64_t row0 = req_row0(p, b) + gy * 64;
+        uint8_t* qr = qs + 4 * C::kQBlk;
+#pragma unroll 1
+        for (int r4 = wq; r4 < NP; r4 += 16) {  // four rows at a time, loads first
+            uint4 x[4][2];
+            uint32_t e[4];
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                const int r = r4 + 4 * n;
+                const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+                // lane holds latent values 16 lane .. 16 lane + 15 and rotary values 2 lane, 2 lane + 1
+                const uint4* ql = reinterpret_cast<const uint4*>(p.q_lat + (row0 + r) * kD) + 2 * lane;
+                x[n][0] = r < rows ? __ldg(ql) : z;
+                x[n][1] = r < rows ? __ldg(ql + 1) : z;
+                e[n] = r < rows ? __ldg(reinterpret_cast<const uint32_t*>(p.q_pe + (row0 + r) * kP) + lane) : 0u;
+            }
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                const int r = r4 + 4 * n;
+                const __nv_bfloat162* xb = reinterpret_cast<const __nv_bfloat162*>(x[n]);
+                const float2 pe = make_float2(__uint_as_float(e[n] << 16), __uint_as_float(e[n] & 0xFFFF0000u));
+                float mx = fmaxf(fabsf(pe.x), fabsf(pe.y));
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const float2 f = __bfloat1622float2(xb[k]);
+                    mx = fmaxf(mx, fmaxf(fabsf(f.x), fabsf(f.y)));
+                }
+                // (non-negative floats are ordered as their bits)
+                mx = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mx)));
+                // the power of two that brings the largest into [128, 256)
+                const int ex = static_cast<int>(__float_as_uint(mx) >> 23) - 127;
+                const int k2 = max(-120, min(120, 7 - ex));
+                const float up = __uint_as_float(static_cast<uint32_t>(127 + k2) << 23);
+                // (x - x is 0, and NaN for an infinity, which 8 bits do not hold)
+                auto scaled = [&](float v) { return fmaf(v, up, v - v); };
+                uint32_t h[4], l[4];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const float2 f = __bfloat1622float2(xb[k]);
+                    float ra, rb;
+                    const uint32_t hc = p8_split(scaled(f.x), scaled(f.y), ra, rb);
+                    const uint32_t lc = p8_codes(ra * 32.f, rb * 32.f);
+                    if (k & 1) {
+                        h[k >> 1] |= hc << 16;
+                        l[k >> 1] |= lc << 16;
+                    } else {
+                        h[k >> 1] = hc;
+                        l[k >> 1] = lc;
+                    }
+                }
+                // unit lane % 8 of row r, block lane / 8 (NP is a multiple of 8: rows NP + r swizzle alike)
+                uint8_t* at = qs + (lane >> 3) * C::kQBlk + r * 128 + (((lane & 7) ^ (r & 7)) << 4);
+                *reinterpret_cast<uint4*>(at) = make_uint4(h[0], h[1], h[2], h[3]);
+                *reinterpret_cast<uint4*>(at + NP * 128) = make_uint4(l[0], l[1], l[2], l[3]);
+                float ra, rb;
+                const uint32_t hc = p8_split(scaled(pe.x), scaled(pe.y), ra, rb);
+                const uint32_t lc = p8_codes(ra * 32.f, rb * 32.f);
+                uint8_t* ar = qr + r * 64 + (((lane >> 3) ^ ((r >> 1) & 3)) << 4) + (lane & 7) * 2;
+                *reinterpret_cast<uint16_t*>(ar) = static_cast<uint16_t>(hc);
+                *reinterpret_cast<uint16_t*>(ar + NP * 64) = static_cast<uint16_t>(lc);
+                if (lane == 0)
+                    ctrl->kq[gen][r] = __uint_as_float(static_cast<uint32_t>(127 - k2) << 23) * p.scale_log2;
+            }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctrl->q_full[gen]);
+    };
+
+    if (ntiles > 0) {
+        if (warp == 0) {
+            // ---------------------------------------------------------- scores
+            // The whole warp walks the tiles and one lane issues, so descriptors are
+            // warp-uniform values. The rotary part first: its slot is free soonest.
+            const bool leader = elect_lane();
+            const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+            const uint32_t id = idesc_f8(kTok, 2 * NP, 0, 0);
+            const uint64_t dq = smem_desc(smem_u32(qs), 16, 1024, kSw128);
+            const uint64_t dqr = smem_desc(smem_u32(qs) + 4 * C::kQBlk, 16, 512, kSw64);
+            const uint64_t dring = smem_desc(smem_u32(ring), 16, 1024, kSw128);
+            const uint64_t drope = smem_desc(smem_u32(rope_ring), 16, 512, kSw64);
+            uint32_t slot = 0, phase = 0;
+            int seg = -1, site = 0, i = 0;
+            for (; i < ntiles; ++i) {
+                if (i == 0 || it.j == 0) {
+                    ++seg;
+                    if (!mbar_wait(&ctrl->q_full[seg % kQGens], (seg / kQGens) & 1, abort)) {
+                        site = kSiteQFull;
+                        break;
+                    }
+                }
+                if (i >= 2 && !mbar_wait(&ctrl->s_free[i & 1], ((i >> 1) - 1) & 1, abort)) {
+                    site = kSiteSFree;
+                    break;
+                }
+                const int rr = i % kRopes;
+                if (!mbar_wait(&ctrl->rope_full[rr], (i / kRopes) & 1, abort)) {
+                    site = kSiteRopeFull;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t tS = tm + C::kColS + (i & 1) * 2 * NP;
+                if (leader) {
+                    const uint64_t da = drope + rr * static_cast<uint32_t>(kRopeBlk >> 4);
+                    umma_f8(tS, da, dqr, id, 0u);
+                    umma_f8(tS, da + 2, dqr + 2, id, 1u);
+                    umma_commit(&ctrl->rope_empty[rr]);
+                }
+                for (int kb = 0; kb < 4; ++kb) {
+                    if (!mbar_wait(&ctrl->blk_full[slot], phase, abort)) {
+                        site = kSitePairFull;
+                        break;
+                    }
+                    tc_fence_after();
+                    if (leader) {
+                        const uint64_t da = dring + slot * static_cast<uint32_t>(kBlk >> 4);
+                        const uint64_t db = dq + kb * static_cast<uint32_t>(C::kQBlk >> 4);
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk) umma_f8(tS, da + 2 * kk, db + 2 * kk, id, 1u);
+                    }
+                    if (++slot == static_cast<uint32_t>(C::kSlots)) {
+                        slot = 0;
+                        phase ^= 1;
+                    }
+                }
+                if (site) break;
+                It nx = it;
+                nx.next(p.seq_lens, p.B);
+                if (leader) {
+                    umma_commit(&ctrl->s_full[i & 1]);
+                    if (i + 1 == ntiles || nx.j == 0) umma_commit(&ctrl->q_empty);
+                }
+                it = nx;
+            }
+            __syncwarp();
+            if (leader) {
+                if (site) {
+                    fail(p, ctrl, kErrWaitTimeout, site, i);
+                    report(p, kRoleS, site, i);
+                }
+                // every product issued here completes before the CTA may release TMEM or exit
+                drain_mma(&ctrl->fin[0]);
+            }
+        } else if (warp == 3) {
+            // --------------------------------------------------- value product
+            const bool leader = elect_lane();
+            const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+            const uint32_t id = idesc_f8(128, C::kPRow, 0, 0, true);
+            const uint64_t dring = smem_desc(smem_u32(ring), kBlk, 1024, kSw128);
+            const uint64_t dp0 = smem_desc(smem_u32(pbufs), C::kPBytes, 8 * C::kPRow, C::kPSw);
+            uint32_t slot = 0;
+            int site = 0, i = 0;
+            for (; i < ntiles; ++i) {
+                const bool fresh = i == 0 || it.j == 0;
+                if (!mbar_wait(&ctrl->p_full[i & 1], (i >> 1) & 1, abort)) {
+                    site = kSitePFull;
+                    break;
+                }
+                tc_fence_after();
+                const uint64_t dp = dp0 + (i % C::kPBufs) * static_cast<uint32_t>(C::kPBytes >> 4);
+                for (int kb = 0; kb < 4; ++kb) {
+                    if (leader) {
+                        const uint64_t da = dring + slot * static_cast<uint32_t>(kBlk >> 4);
+                        const uint32_t tO = tm + kb * C::kPRow;
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk) {
+                            // tokens 32 kk .. 32 kk + 31
+                            umma_f8(tO, da + kk * (32 * 128 >> 4), dp + kk * (32 * C::kPRow >> 4), id, !(fresh && kk == 0));
+                            if (!C::kStack)
+                                umma_f8(tO, da + kk * (32 * 128 >> 4), dp + ((NP * kTok + kk * 32 * C::kPRow) >> 4), id, 1u);
+                        }
+                        umma_commit(&ctrl->blk_empty[slot]);
+                    }
+                    if (++slot == static_cast<uint32_t>(C::kSlots)) slot = 0;
+                }
+                if (leader) umma_commit(&ctrl->o_done[i & 1]);
+                it.next(p.seq_lens, p.B);
+            }
+            __syncwarp();
+            if (leader) {
+                if (site) {
+                    fail(p, ctrl, kErrWaitTimeout, site, i);
+                    report(p, kRolePV, site, i);
+                }
+                drain_mma(&ctrl->fin[1]);
+            }
+        } else if (!LSU && warp == 1) {
+            // ------------------------------------------------------------ loads
+            // Lane r owns run r of a tile: BR rows that lie next to each other in a page.
+            const int BR = p.run_rows;
+            const uint64_t pol = gridDim.y > 1 ? l2_policy_evict_normal() : l2_policy_evict_first();
+            bool bad = false, ok = true;
+            int site = 0, i = 0;
+            auto run_of = [&](const It& t, int& page) -> int {
+                page = 0;
+                const int valid = min(kTok, t.T - t.j * kTok);
+                if (lane * BR >= valid) return 0;
+                return p8_slot(p, p.block_table + static_cast<int64_t>(t.b) * p.bt_stride, t.j * kTok + lane * BR, page, bad);
+            };
+            int page_next, y_next = run_of(it, page_next);
+            float s_next = p8_scale(p, page_next);
+            uint32_t u = 0, armed = 0, parity = 0;  // blocks so far; slots whose barrier is armed, and their last parity
+            int rope_armed = 0;
+            for (; i < ntiles && ok; ++i) {
+                const int valid = min(kTok, it.T - it.j * kTok);
+                const int nruns = (valid + BR - 1) / BR;
+                const int y = y_next;
+                // (its slot: the loads of tile i are behind the value product of tile i - 3,
+                // which read nothing later than the scales of tile i - 3 did)
+                if (lane < nruns) ctrl->sc[i % kScs][lane] = s_next;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctrl->sc_full[i % kScs]);
+                it.next(p.seq_lens, p.B);
+                if (i + 1 < ntiles) {
+                    y_next = run_of(it, page_next);
+                    s_next = p8_scale(p, page_next);
+                }
+                const int rr = i % kRopes;
+                if (i >= kRopes && !__all_sync(0xffffffffu, mbar_wait(&ctrl->rope_empty[rr], ((i / kRopes) - 1) & 1, abort))) {
+                    ok = false;
+                    site = kSiteTmaRopeEmpty;
+                    break;
+                }
+                if (lane == 0) mbar_arrive_expect_tx(&ctrl->rope_full[rr], static_cast<uint32_t>(nruns * BR * 64));
+                __syncwarp();
+                rope_armed = i + 1;
+                if (lane < nruns)
+                    tma_load_2d(rope_ring + rr * kRopeBlk + lane * BR * 64, &maps.rope, &ctrl->rope_full[rr], kD, y, pol);
+                for (int kb = 0; kb < 4; ++kb, ++u) {
+                    const uint32_t slot = u % C::kSlots, fill = u / C::kSlots;
+                    if (fill > 0 && !__all_sync(0xffffffffu, mbar_wait(&ctrl->blk_empty[slot], (fill - 1) & 1, abort))) {
+                        ok = false;
+                        site = kSiteTmaPairEmpty;
+                        break;
+                    }
+                    if (lane == 0) mbar_arrive_expect_tx(&ctrl->blk_full[slot], static_cast<uint32_t>(nruns * BR * 128));
+                    __syncwarp();
+                    armed |= 1u << slot;
+                    parity = (parity & ~(1u << slot)) | ((fill & 1u) << slot);
+                    if (lane < nruns)
+                        tma_load_2d(ring + slot * kBlk + lane * BR * 128, &maps.lat, &ctrl->blk_full[slot], kb * 128, y, pol);
+                }
+            }
+            if (!ok && lane == 0) {
+                fail(p, ctrl, kErrWaitTimeout, site, i);
+                report(p, kRoleTma, site, i);
+            }
+            // no copy may arrive after the CTA is gone: wait (bounded, whatever the abort
+            // flag says) for the last fill of every barrier armed here
+            volatile int never = 0;
+            for (int s = 0; s < C::kSlots; ++s)
+                if (armed >> s & 1) mbar_wait(&ctrl->blk_full[s], parity >> s & 1, &never);
+            for (int k = max(0, rope_armed - kRopes); k < rope_armed; ++k)
+                mbar_wait(&ctrl->rope_full[k % kRopes], (k / kRopes) & 1, &never);
+            if (bad) atomicOr(status_rec(p), kErrBadBlock);
+        } else if (warp >= C::kQWarp) {
+            // ---------------------------------------------------------- queries
+            // (and LSU: the rows, warp w's being 32 w .. 32 w + 31 of a tile)
+            bool ok = true, bad = false;
+            int seg = -1, site = 0, i = 0;
+            const int w = warp - C::kQWarp;
+            uint64_t *pend = nullptr, *pend2 = nullptr;  // LSU: barriers of the fill before, not yet handed over
+            uint32_t u = 0;
+            auto hand_over = [&]() {
+                if (!pend) return;
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(pend);
+                    if (pend2) mbar_arrive(pend2);
+                }
+                pend = pend2 = nullptr;
+            };
+            // LSU: what waits behind a barrier may need this warp's last fill first
+            auto wait = [&](uint64_t* bar, uint32_t par, int where) {
+                if (LSU && pend && !__all_sync(0xffffffffu, mbar_try_wait(bar, par))) {
+                    asm volatile("cp.async.wait_group 0;" ::: "memory");
+                    hand_over();
+                }
+                if (__all_sync(0xffffffffu, mbar_wait(bar, par, abort))) return true;
+                site = where;
+                return false;
+            };
+            auto filled = [&](uint64_t* bar, uint64_t* bar2) {  // the fill before this one has landed: hand it over
+                asm volatile("cp.async.commit_group;" ::: "memory");
+                asm volatile("cp.async.wait_group 1;" ::: "memory");
+                hand_over();
+                pend = bar;
+                pend2 = bar2;
+            };
+            for (; i < ntiles; ++i) {
+                if (i == 0 || it.j == 0) {
+                    ++seg;
+                    if (seg > 0) {
+                        // (the last queries may be in use for long: as long as the products, whose
+                        // own waits end)
+                        if (LSU && pend) {
+                            asm volatile("cp.async.wait_group 0;" ::: "memory");
+                            hand_over();
+                        }
+                        do ok = __all_sync(0xffffffffu, mbar_wait(&ctrl->q_empty, (seg - 1) & 1, abort));
+                        while (!ok && !__any_sync(0xffffffffu, *abort));
+                        if (!ok) break;  // (another role has said why)
+                    }
+                    load_q(it.b, seg % kQGens);
+                }
+                if constexpr (LSU) {
+                    const int valid = min(kTok, it.T - it.j * kTok);
+                    const int row = w * 32 + lane;
+                    const int32_t* btr = p.block_table + static_cast<int64_t>(it.b) * p.bt_stride;
+                    int page = 0, slot_of = 0;
+                    if (row < valid) slot_of = p8_slot(p, btr, it.j * kTok + row, page, bad);
+                    ctrl->sc[i % kScs][row] = row < valid ? p8_scale(p, page) : 1.f;
+                    const int rr = i % kRopes;
+                    if (i >= kRopes && !wait(&ctrl->rope_empty[rr], ((i / kRopes) - 1) & 1, kSiteLsuRopeEmpty)) break;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {  // 8 rows of four 16-byte units at a time
+                        const int r = w * 32 + 8 * k + (lane >> 2), un = lane & 3;
+                        const int s = __shfl_sync(0xffffffffu, slot_of, 8 * k + (lane >> 2));
+                        if (r < valid)
+                            p8_cp16(smem_u32(rope_ring + rr * kRopeBlk + r * 64 + ((un ^ ((r >> 1) & 3)) << 4)),
+                                    p.cache + static_cast<int64_t>(s) * kRowPage + kD + un * 16);
+                    }
+                    filled(&ctrl->rope_full[rr], &ctrl->sc_full[i % kScs]);
+                    bool stop = false;
+                    for (int kb = 0; kb < 4; ++kb, ++u) {
+                        const uint32_t slot = u % C::kSlots, fill = u / C::kSlots;
+                        if (fill > 0 && !wait(&ctrl->blk_empty[slot], (fill - 1) & 1, kSiteLsuPairEmpty)) {
+                            stop = true;
+                            break;
+                        }
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {  // 4 rows of eight units at a time
+                            const int r = w * 32 + 4 * k + (lane >> 3), un = lane & 7;
+                            const int s = __shfl_sync(0xffffffffu, slot_of, 4 * k + (lane >> 3));
+                            if (r < valid)
+                                p8_cp16(smem_u32(ring + slot * kBlk + r * 128 + ((un ^ (r & 7)) << 4)),
+                                        p.cache + static_cast<int64_t>(s) * kRowPage + kb * 128 + un * 16);
+                        }
+                        filled(&ctrl->blk_full[slot], nullptr);
+                    }
+                    if (stop) break;
+                }
+                it.next(p.seq_lens, p.B);
+            }
+            if (LSU) {
+                asm volatile("cp.async.wait_group 0;" ::: "memory");
+                hand_over();
+            }
+            if (site && lane == 0) {
+                fail(p, ctrl, kErrWaitTimeout, site, i);
+                report(p, kRoleLsu0, site, i);
+            }
+            if (bad) atomicOr(status_rec(p), kErrBadBlock);
+        } else if (warp >= 4) {
+            // ------------------------------------------ softmax, P and output
+            // Thread tk holds token tk of the tile (TMEM lane tk), for the group's columns cb .. cb + CW.
+            const int grp = (warp - 4) >> 2, wq = warp & 3, tk = wq * 32 + lane;
+            const int cb = grp * CW;
+            const int bar = 1 + grp;
+            const uint32_t lane_base = static_cast<uint32_t>(wq * 32) << 16;
+            const int run_shift = LSU ? 0 : 31 - __clz(p.run_rows);  // (a power of two)
+            float l[CW];
+            int seg = -1, start_j = 0, T = 0, qt = 0, rows = 0;
+            bool failed = false;
+            int site = 0, i = 0;
+            auto wait = [&](uint64_t* b, uint32_t par, int where) {
+                if (!mbar_wait(b, par, abort)) {
+                    if (!failed) site = where;
+                    failed = true;
+                }
+            };
+            for (; i < ntiles; ++i) {
+                const bool fresh = i == 0 || it.j == 0;
+                if (fresh) {
+                    ++seg;
+                    start_j = it.j;
+                    T = it.T;
+                    qt = req_qt(p, it.b);
+                    rows = req_rows_in_group(p, it.b, gy);
+#pragma unroll
+                    for (int c = 0; c < CW; ++c) l[c] = 0.f;
+                    wait(&ctrl->q_full[seg % kQGens], (seg / kQGens) & 1, kSiteQFull);
+                }
+                const float* kq = ctrl->kq[seg % kQGens] + cb;
+                const int tok = it.j * kTok + tk, valid = min(kTok, T - it.j * kTok);
+                wait(&ctrl->sc_full[i % kScs], (i / kScs) & 1, kSiteSFull);
+                const float vs = tk < valid ? ctrl->sc[i % kScs][tk >> run_shift] : 1.f;
+                const float lv = log2f(vs), inv_vs = 1.f / vs;
+                wait(&ctrl->s_full[i & 1], (i >> 1) & 1, kSiteSFull);
+                tc_fence_after();
+                float x[CW];
+                {
+                    const uint32_t tS = tmem + C::kColS + (i & 1) * 2 * NP + lane_base + cb;
+#pragma unroll
+                    for (int c0 = 0; c0 < CW; c0 += 16) {
+                        uint32_t h[16], lo[16];
+                        tmem_ld_x16(tS + c0, h);
+                        tmem_ld_x16(tS + NP + c0, lo);
+#pragma unroll
+                        for (int c = 0; c < 16; ++c) x[c0 + c] = fmaf(__uint_as_float(lo[c]), 0x1p-5f, __uint_as_float(h[c]));
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctrl->s_free[i & 1]);
+                bool clear = tk >= valid;  // the row's codes must not meet the value product
+#pragma unroll
+                for (int c = 0; c < CW; ++c) x[c] = fmaf(x[c] * vs, kq[c], lv);
+                if (it.j * kTok + valid > T - qt || valid < kTok) {
+                    // columns from c0 on see the token: query t sees tokens up to T - qt + t
+                    const int c0 = tk < valid ? max(0, tok - (T - qt)) * p.Hq - gy * 64 - cb : INT_MAX;
+                    bool nan = true;
+#pragma unroll
+                    for (int c = 0; c < CW; ++c) {
+                        nan = nan && x[c] != x[c];
+                        if (c < c0) x[c] = -INFINITY;
+                    }
+                    // a NaN code would pass a weight of 0: rows that some queries do not see are
+                    // cleared if they hold one (those that do see it have NaN for a weight)
+                    if (tk < valid && c0 > -cb && nan && tok > T - qt) {
+                        const uint32_t s0 = (4u * i) % C::kSlots;
+                        for (int kb = 0; kb < 4 && !clear; ++kb) {
+                            const uint8_t* blk = ring + (s0 + kb) % C::kSlots * kBlk + tk * 128;
+                            for (int un = 0; un < 32; ++un) {
+                                const uint32_t v = reinterpret_cast<const uint32_t*>(blk)[un] & 0x7F7F7F7Fu;
+                                if (((v + 0x01010101u) & 0x80808080u) != 0) clear = true;
+                            }
+                        }
+                    }
+                }
+                bool need = fresh || failed;
+#pragma unroll
+                for (int c = 0; c < CW; ++c) need = need || x[c] > ctrl->mm[cb + c] + (kTop + kSlack);
+                if (named_bar_or(bar, 128, need)) {
+                    // the maxima move: every column's goes to the tile's if that is larger
+                    float most[CW];
+#pragma unroll
+                    for (int c = 0; c < CW; ++c) {
+                        // order-preserving whole numbers; NaN counts as nothing
+                        const float v = fmaxf(x[c], kNoMax);
+                        const int k = __float_as_int(v);
+                        const int r = __reduce_max_sync(0xffffffffu, k < 0 ? k ^ 0x7FFFFFFF : k);
+                        most[c] = __int_as_float(r < 0 ? r ^ 0x7FFFFFFF : r);
+                    }
+                    if (lane == 0) {
+#pragma unroll
+                        for (int c = 0; c < CW; ++c) ctrl->red[wq][cb + c] = most[c];
+                    }
+                    named_bar_sync(bar, 128);
+                    if (tk < CW) {
+                        const int c = cb + tk;
+                        const float old = fresh ? kNoMax : ctrl->mm[c] + kTop;
+                        const float top = fmaxf(fmaxf(ctrl->red[0][c], ctrl->red[1][c]), fmaxf(ctrl->red[2][c], ctrl->red[3][c]));
+                        const float m = fmaxf(old, top);
+                        ctrl->mm[c] = m - kTop;
+                        ctrl->alpha[c] = ex2(old - m);
+                    }
+                    if (named_bar_or(bar, 128, failed)) break;
+                    if (!fresh) {
+                        wait(&ctrl->o_done[(i - 1) & 1], ((i - 1) >> 1) & 1, kSiteORescale);
+                        tc_fence_after();
+                        __syncwarp();
+#pragma unroll 1
+                        for (int part = 0; part < (C::kStack ? 2 : 1); ++part)
+#pragma unroll 1
+                            for (int mt = 0; mt < 4; ++mt)
+#pragma unroll 1
+                                for (int c0 = 0; c0 < CW; c0 += 16) {
+                                    const uint32_t at = tmem + lane_base + mt * C::kPRow + part * NP + cb + c0;
+                                    uint32_t o[16];
+                                    tmem_ld_x16(at, o);
+#pragma unroll
+                                    for (int c = 0; c < 16; ++c)
+                                        o[c] = __float_as_uint(__uint_as_float(o[c]) * ctrl->alpha[cb + c0 + c]);
+                                    tmem_st_x16(at, o);
+                                }
+                        tmem_wait_st();
+#pragma unroll
+                        for (int c = 0; c < CW; ++c) l[c] *= ctrl->alpha[cb + c];
+                    }
+                }
+                // P and its place: free when the value product that read it last is done
+                if (i >= C::kPBufs)
+                    wait(&ctrl->o_done[(i - C::kPBufs) & 1], ((i - C::kPBufs) >> 1) & 1, kSiteOPbuf);
+                uint32_t hc[CW / 4], lc[CW / 4];
+#pragma unroll
+                for (int c = 0; c < CW; c += 2) {
+                    const float a = ex2(x[c] - ctrl->mm[cb + c]), b = ex2(x[c + 1] - ctrl->mm[cb + c + 1]);
+                    l[c] = fmaf(a, inv_vs, l[c]);
+                    l[c + 1] = fmaf(b, inv_vs, l[c + 1]);
+                    float ra, rb;
+                    const uint32_t h = p8_split(a, b, ra, rb);
+                    const uint32_t lo = C::kStack ? p8_codes(ra * 32.f, rb * 32.f) : p8_codes(ra, rb);
+                    if (c & 2) {
+                        hc[c >> 2] |= h << 16;
+                        lc[c >> 2] |= lo << 16;
+                    } else {
+                        hc[c >> 2] = h;
+                        lc[c >> 2] = lo;
+                    }
+                }
+                uint8_t* prow = pbufs + (i % C::kPBufs) * C::kPBytes + tk * C::kPRow;
+                const int sw = swz_p(tk, C::kPSw);
+#pragma unroll
+                for (int n = 0; n < CW / 16; ++n) {
+                    const int un = cb / 16 + n;
+                    *reinterpret_cast<uint4*>(prow + ((un ^ sw) << 4)) =
+                        make_uint4(hc[4 * n], hc[4 * n + 1], hc[4 * n + 2], hc[4 * n + 3]);
+                    uint8_t* lrow = C::kStack ? prow + (((NP / 16 + un) ^ sw) << 4) : prow + NP * kTok + ((un ^ sw) << 4);
+                    *reinterpret_cast<uint4*>(lrow) = make_uint4(lc[4 * n], lc[4 * n + 1], lc[4 * n + 2], lc[4 * n + 3]);
+                }
+                if (clear) {
+                    const uint32_t s0 = (4u * i) % C::kSlots;
+                    for (int kb = grp; kb < 4; kb += C::kGroups) {
+                        uint4* row = reinterpret_cast<uint4*>(ring + (s0 + kb) % C::kSlots * kBlk + tk * 128);
+#pragma unroll
+                        for (int un = 0; un < 8; ++un) row[un ^ (tk & 7)] = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                }
+                fence_proxy_async_smem();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctrl->p_full[i & 1]);
+                const int b = it.b, tiles = it.tiles, j = it.j;
+                it.next(p.seq_lens, p.B);
+                if (i + 1 < ntiles && j + 1 < tiles) continue;
+                // ------------------------------------------- the segment's end
+                float sum[CW];
+#pragma unroll
+                for (int c = 0; c < CW; ++c) sum[c] = warp_sum(l[c]);
+                if (lane == 0) {
+#pragma unroll
+                    for (int c = 0; c < CW; ++c) ctrl->red[wq][cb + c] = sum[c];
+                }
+                named_bar_sync(bar, 128);
+                const bool whole = start_j == 0 && j + 1 == tiles;
+                const int64_t row0 = req_row0(p, b) + gy * 64;
+                const int64_t slot0 = (static_cast<int64_t>(gy) * p.SPG + g + b) * 64;
+                if (tk < CW) {
+                    const int c = cb + tk;
+                    const float s = ctrl->red[0][c] + ctrl->red[1][c] + ctrl->red[2][c] + ctrl->red[3][c];
+                    // (a NaN sum is not nothing)
+                    ctrl->inv[c] = s == 0.f ? 0.f : 1.f / s;
+                    const float L = s == 0.f ? -INFINITY : (ctrl->mm[c] + log2f(s)) * kLn2f;
+                    if (c < rows) {
+                        if (whole) p.lse[row0 + c] = L;
+                        // (the merge leaves a NaN out of its maximum, and of an infinity it makes NaN)
+                        else p.part_lse[slot0 + c] = L != L ? INFINITY : L;
+                    }
+                }
+                wait(&ctrl->o_done[i & 1], (i >> 1) & 1, kSiteOFinal);
+                named_bar_sync(bar, 128);
+                tc_fence_after();
+                __syncwarp();
+#pragma unroll 1
+                for (int mt = 0; mt < 4; ++mt) {
+                    const int d = mt * 128 + tk;  // (lane tk holds a dim here)
+#pragma unroll 1
+                    for (int c0 = 0; c0 < CW; c0 += 16) {
+                        const uint32_t at = tmem + lane_base + mt * C::kPRow + cb + c0;
+                        uint32_t o[16];
+                        tmem_ld_x16(at, o);
+                        if (C::kStack) {
+                            uint32_t lo[16];
+                            tmem_ld_x16(at + NP, lo);
+#pragma unroll
+                            for (int c = 0; c < 16; ++c)
+                                o[c] = __float_as_uint(fmaf(__uint_as_float(lo[c]), 0x1p-5f, __uint_as_float(o[c])));
+                        }
+#pragma unroll
+                        for (int c = 0; c < 16; ++c) {
+                            const int r = cb + c0 + c;
+                            if (r >= rows) continue;
+                            const float v = __uint_as_float(o[c]) * ctrl->inv[r];
+                            if (!whole) p.part_o[(slot0 + r) * kD + d] = v;
+                            else if (p.out_f32) static_cast<float*>(p.out)[(row0 + r) * kD + d] = v;
+                            else static_cast<__nv_bfloat16*>(p.out)[(row0 + r) * kD + d] = __float2bfloat16_rn(v);
+                        }
+                    }
+                }
+                tc_fence_before();
+            }
+            if (failed) {
+                fail(p, ctrl, kErrWaitTimeout, site, i);
+                report(p, kRoleSoftmax, site, i);
+            }
+        }
+    }
+    __syncthreads();
+    if (warp == 0) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+template <int NP, bool LSU>
+cudaError_t go(const DecodeMaps& maps, const DecodeParams& p, int W, int GY, cudaStream_t stream) {
+    static std::atomic<uint64_t> done;
+    const auto k = mla_decode_page8_kernel<NP, LSU>;
+    const cudaError_t e = attribute_once(done, reinterpret_cast<const void*>(k), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         p8_smem<NP>());
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute attr[1];
+    cudaLaunchConfig_t cfg = pdl_config(dim3(W, GY), P8Cfg<NP>::kThreads, p8_smem<NP>(), stream, attr);
+    return cudaLaunchKernelEx(&cfg, k, maps, p);
+}
+
+}  // namespace
+
+cudaError_t launch_decode_page8(const DecodeMaps& maps, const DecodeParams& p, int NP, bool lsu, int W, int GY,
+                                cudaStream_t stream) {
+    const cudaError_t e = NP == 16   ? (lsu ? go<16, true>(maps, p, W, GY, stream) : go<16, false>(maps, p, W, GY, stream))
+                          : NP == 32 ? (lsu ? go<32, true>(maps, p, W, GY, stream) : go<32, false>(maps, p, W, GY, stream))
+                                     : (lsu ? go<64, true>(maps, p, W, GY, stream) : go<64, false>(maps, p, W, GY, stream));
+    return e == cudaSuccess ? launch_decode_merge(p, W, W * GY, GY, stream) : e;
+}
+
+}  // namespace mla

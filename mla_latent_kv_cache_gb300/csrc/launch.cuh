@@ -22,6 +22,23 @@ inline cudaError_t attribute_once(std::atomic<uint64_t>& done, const void* kerne
     return e;
 }
 
+// Launch configuration that lets the grid start while the previous kernel
+// in the stream drains (the kernel calls griddep_wait() before touching
+// global memory that kernel may use).
+inline cudaLaunchConfig_t pdl_config(dim3 grid, int threads, size_t smem, cudaStream_t stream,
+                                     cudaLaunchAttribute* attr) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cfg;
+}
+
 // Per-CTA status record (int32 words): 0 status bits, 1 first wait site,
 // 2 its tile, 4 + role: (site << 24) | tile where that role gave up.
 constexpr int kStatusRecWords = 16;
@@ -55,6 +72,8 @@ struct DecodeParams {
     int total_q;          // query tokens in q_lat, q_pe, out and lse; cu_q is clamped to [0, total_q]
     int lat_dim;       // latent width D: 512 (576-value rows), or 256 / 768 / 1792 (folded tiles, bf16)
     int rope_dim;      // rotary width P: 64
+    int64_t bt_cols;       // page-scaled rows: columns of the table
+    const float* scales;   // and the pages' scales
 };
 
 cudaError_t launch_cache_write(const void* latent, int64_t latent_stride, const void* k_pe, int64_t k_pe_stride,
@@ -94,6 +113,13 @@ cudaError_t launch_decode_fold(const DecodeMaps& maps, const DecodeParams& p, in
                                cudaStream_t stream);
 cudaError_t launch_decode(const DecodeMaps& maps, const DecodeParams& p, int NP, bool lsu, int kind, int G, int GY,
                           cudaStream_t stream);
+// The merge of a decode's partial results over W workers (nrec status records).
+cudaError_t launch_decode_merge(const DecodeParams& p, int W, int nrec, int GY, cudaStream_t stream);
+// Rows with one scale for each page (mla_decode_fp8_page): maps.lat = 128 codes
+// of a row (128-B swizzle), maps.rope = its 64 rotary codes (64-B swizzle), both
+// gcd(page_size, 128) rows high; lsu: pages read row by row.
+cudaError_t launch_decode_page8(const DecodeMaps& maps, const DecodeParams& p, int NP, bool lsu, int W, int GY,
+                                cudaStream_t stream);
 cudaError_t launch_merge_lse(const float* part_o, const float* part_lse, int S, int64_t N, void* out, int out_f32,
                              float* lse, cudaStream_t stream);
 
@@ -194,5 +220,49 @@ struct PrefillMaps {
 int prefill_pack(int group);
 int64_t prefill_pairs(int64_t total_q, int B, int max_q_len, int tile_tokens);
 cudaError_t launch_prefill(const PrefillMaps& maps, const PrefillParams& p, int max_q_len, cudaStream_t stream);
+
+// Rotary positions (mla_rope); strides in elements.
+struct RopeParams {
+    const void* x;
+    int64_t x_t, x_h;
+    void* out;
+    int64_t o_t, o_h;
+    const int32_t* positions;
+    const int64_t* steps;
+    int64_t T;
+    int H, R;
+    int interleaved;
+    float mscale;
+    int chunks, items_chunk;  // set by launch_rope: warps a token, 16-value items a warp
+};
+cudaError_t launch_rope(RopeParams p, int f32, int sms, cudaStream_t stream);
+
+// New tokens into the paged cache (mla_cache_append); strides in elements.
+struct AppendParams {
+    const __nv_bfloat16* latent;
+    int64_t lat_st;
+    const __nv_bfloat16* k_pe;
+    int64_t pe_st;
+    const int32_t* cu;
+    const int32_t* seq_lens;
+    int B;
+    int64_t total;
+    const int32_t* block_table;
+    int64_t bt_stride, bt_cols;
+    int page_size;
+    const int32_t* positions;   // or null: the place
+    const int64_t* steps;       // or null: no rotation
+    int interleaved;
+    float mscale;
+    const __nv_bfloat16* norm;  // or null
+    float eps;
+    uint8_t* cache;
+    int64_t num_slots;
+    float* scales;              // page rows
+    __nv_bfloat16* rows;        // or null
+    int64_t rows_st;
+    int* status;
+};
+cudaError_t launch_append(const AppendParams& p, int kind, int lat_dim, cudaStream_t stream);
 
 }  // namespace mla

@@ -15,6 +15,7 @@ constexpr int kP = 64;           // shared rotary key width
 constexpr int kW = 576;          // values per cached token
 constexpr int kRowBf16 = 1152;   // bytes per bf16 row
 constexpr int kRowFp8 = 656;     // bytes per fp8_ds_mla row
+constexpr int kRowPage = 576;    // bytes per page-scaled 8-bit row
 constexpr int kTile = 128;       // tokens per decode tile (UMMA M)
 
 // Device-side status bits written to the first word of the decode workspace.
@@ -314,6 +315,24 @@ __device__ __forceinline__ void umma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, u
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
         "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
+}
+
+// D(tmem) (+)= A(smem, e4m3) * B(smem, 8-bit type of idesc), fp32 accumulate, K = 32.
+__device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                        uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Instruction descriptors with N known at run time: kind::f8f6f4 (types 0 =
+// e4m3, 1 = e5m2; K-major unless said otherwise) and kind::f16 with bf16
+// operands.
+__host__ __device__ constexpr uint32_t idesc_f8(int M, int N, uint32_t a_type, uint32_t b_type, bool mn_major = false) {
+    return (1u << 4) | (a_type << 7) | (b_type << 10) | (mn_major ? 3u << 15 : 0u) | (static_cast<uint32_t>(N >> 3) << 17) |
+           (static_cast<uint32_t>(M >> 4) << 24);
 }
 
 // Arrive once on `bar` when every tcgen05.mma issued so far by this thread
