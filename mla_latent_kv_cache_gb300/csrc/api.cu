@@ -772,7 +772,7 @@ int mla_cache_append(const void* latent, int64_t latent_stride, const void* k_pe
     p.rows = static_cast<__nv_bfloat16*>(rows);
     p.rows_st = rows_stride;
     p.status = status;
-    const cudaError_t e = mla::launch_append(p, cache_kind, lat_dim, static_cast<cudaStream_t>(stream));
+    const cudaError_t e = mla::launch_append(p, cache_kind, lat_dim, di.sms, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 

@@ -29,82 +29,112 @@ __device__ __forceinline__ int a_cu(const AppendParams& p, int b) {
     return static_cast<int>(min(static_cast<int64_t>(max(__ldg(p.cu + b), 0)), p.total));
 }
 
-// (Plain loads: the dense rows may be written over the input they came from.)
-// A token's input as a lane holds it: 16-byte units lane, lane + 32, .. of the
-// latent, and pair `lane` of the rotary key.
-template <int D>
-struct Raw {
-    static constexpr int kU = D / 256;
-    uint4 lat[kU];
-    uint32_t pe;  // two bf16 values, the pair's first in the low half
-};
-
-template <int D>
-__device__ __forceinline__ void load_raw(const AppendParams& p, int64_t t, int lane, Raw<D>& r) {
-    const uint4* src = reinterpret_cast<const uint4*>(p.latent + t * p.lat_st);
-#pragma unroll
-    for (int k = 0; k < Raw<D>::kU; ++k) r.lat[k] = src[lane + 32 * k];
-    const __nv_bfloat16* pe = p.k_pe + t * p.pe_st;
-    if (p.interleaved) {
-        r.pe = reinterpret_cast<const uint32_t*>(pe)[lane];
-    } else {
-        const uint32_t a = reinterpret_cast<const unsigned short*>(pe)[lane];
-        const uint32_t b = reinterpret_cast<const unsigned short*>(pe)[lane + 32];
-        r.pe = a | b << 16;
-    }
+// Two fp32 values in one register pair, for the packed instructions (the
+// kernels are near the rate at which instructions issue).
+using F2 = unsigned long long;
+__device__ __forceinline__ F2 f2(float a, float b) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 un2(F2 v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
 }
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
-__device__ __forceinline__ void unpack8(const uint4& u, float (&f)[8]) {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+__device__ __forceinline__ void unpack8(const uint4& u, F2 (&f)[4]) {
+    f[0] = f2(bf16_lo(u.x), bf16_hi(u.x));
+    f[1] = f2(bf16_lo(u.y), bf16_hi(u.y));
+    f[2] = f2(bf16_lo(u.z), bf16_hi(u.z));
+    f[3] = f2(bf16_lo(u.w), bf16_hi(u.w));
+}
+
+__device__ __forceinline__ uint32_t bf16x2(F2 v) {
+    const float2 f = un2(v);
+    return pack_bf16x2(f.x, f.y);
+}
+__device__ __forceinline__ uint4 pack8(const F2 (&f)[4]) {
+    return make_uint4(bf16x2(f[0]), bf16x2(f[1]), bf16x2(f[2]), bf16x2(f[3]));
+}
+
+__device__ __forceinline__ float most_abs(float a, const F2 (&f)[4]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        f[2 * i] = bf16_lo(w[i]);
-        f[2 * i + 1] = bf16_hi(w[i]);
+        const float2 v = un2(f[i]);
+        a = fmaxf(a, fmaxf(fabsf(v.x), fabsf(v.y)));
     }
+    return a;
 }
 
-// 1 / rms of the token's latent (1 without a norm); a whole warp.
-template <int D>
-__device__ __forceinline__ float norm_factor(const AppendParams& p, const Raw<D>& r) {
-    if (!p.norm) return 1.f;
-    float s = 0.f;
+// The sum of squares of 8 values, by pairs.
+__device__ __forceinline__ F2 squares(F2 s, const F2 (&f)[4]) {
 #pragma unroll
-    for (int k = 0; k < Raw<D>::kU; ++k) {
-        float f[8];
-        unpack8(r.lat[k], f);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) s = fmaf(f[i], f[i], s);
-    }
+    for (int i = 0; i < 4; ++i) s = fma2(f[i], f[i], s);
+    return s;
+}
+
+// 1 / rms from a lane's sum of squares; a whole warp.
+__device__ __forceinline__ float norm_factor(F2 squares, float per, float eps) {
+    const float2 v = un2(squares);
+    float s = v.x + v.y;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    return rsqrtf(s * (1.f / D) + p.eps);
+    return rsqrtf(s * per + eps);
 }
 
-// Unit k of the lane's latent values, normalised.
-template <int D>
-__device__ __forceinline__ void latent8(const AppendParams& p, const Raw<D>& r, int k, int lane, float factor, float (&f)[8]) {
-    unpack8(r.lat[k], f);
-    if (!p.norm) return;
-    float w[8];
-    unpack8(__ldg(reinterpret_cast<const uint4*>(p.norm) + lane + 32 * k), w);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = f[i] * factor * w[i];
+// A lane's norm weights of the 16-byte unit u (1 without a norm).
+__device__ __forceinline__ void weights8(const AppendParams& p, int u, F2 (&w)[4]) {
+    if (p.norm) unpack8(__ldg(reinterpret_cast<const uint4*>(p.norm) + u), w);
+    else w[0] = w[1] = w[2] = w[3] = f2(1.f, 1.f);
 }
 
-// The lane's pair of the rotary key, turned.
-__device__ __forceinline__ float2 turned(const AppendParams& p, uint32_t pe, int64_t pos, int lane) {
-    const float a = bf16_lo(pe), b = bf16_hi(pe);
-    if (!p.steps) return make_float2(a, b);
-    const float2 cs = rope_cos_sin(pos, __ldg(p.steps + lane), p.mscale);
-    return make_float2(a * cs.x - b * cs.y, a * cs.y + b * cs.x);
+// Pair `lane` of the rotary key at pe, as two bf16 values, the first in the low
+// half. (Plain loads: the dense rows may be written over the input they came from.)
+__device__ __forceinline__ uint32_t load_pair(const void* pe, int interleaved, int lane) {
+    if (interleaved) return static_cast<const uint32_t*>(pe)[lane];
+    const uint32_t a = static_cast<const unsigned short*>(pe)[lane], b = static_cast<const unsigned short*>(pe)[lane + 32];
+    return a | b << 16;
 }
 
-__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
-    return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
-}
+// The angles of a warp's tokens, every DELTA-th, for the lane's pair. Most
+// positions follow each other, and a turn by DELTA positions more is four
+// instructions instead of another sine and cosine. It is off by some 2^-22 each
+// time, so every fourth is formed anew.
+template <int DELTA>
+struct Angle {
+    int pos;
+    float2 cs, step;
+    int left = -1;  // turns before the next one is formed anew
+    __device__ __forceinline__ float2 turn(const AppendParams& p, uint32_t pe, int at, int lane) {
+        const float a = bf16_lo(pe), b = bf16_hi(pe);
+        if (!p.steps) return make_float2(a, b);
+        if (left > 0 && at == pos + DELTA) {
+            cs = make_float2(cs.x * step.x - cs.y * step.y, cs.x * step.y + cs.y * step.x);
+            --left;
+        } else {
+            const int64_t f = __ldg(p.steps + lane);
+            cs = rope_cos_sin(at, f, p.mscale);
+            if (left < 0) step = rope_cos_sin(DELTA, f, 1.f);
+            left = 3;
+        }
+        pos = at;
+        return make_float2(a * cs.x - b * cs.y, a * cs.y + b * cs.x);
+    }
+};
 
 // The turned pair as bf16 into the 64 values at dst.
 __device__ __forceinline__ void store_pe(const AppendParams& p, void* dst, float2 r, int lane) {
@@ -118,10 +148,20 @@ __device__ __forceinline__ void store_pe(const AppendParams& p, void* dst, float
 }
 
 // Four values as e4m3 codes, saturated.
-__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
-    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+__device__ __forceinline__ uint32_t codes4(F2 a, F2 b) {
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(un2(a), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(un2(b), __NV_SATFINITE, __NV_E4M3);
     return lo | hi << 16;
+}
+
+// x / s correctly rounded for s within 2^-100 .. 2^100, with y = 1 / s correctly
+// rounded, by Markstein's correction (P. Markstein, Computation of elementary
+// functions on the IBM RISC System/6000 processor, 1990): the remainder of
+// x y is exact in one fused step. It is taken as q s - x, so that a zero keeps its
+// sign. (Where x is so small that the remainder underflows, the code is 0 anyway.)
+__device__ __forceinline__ F2 div2(F2 x, F2 minus_x, F2 s, F2 y, F2 minus_y) {
+    const F2 q = mul2(x, y);
+    return fma2(fma2(q, s, minus_x), minus_y, q);
 }
 
 // The page of table column pi of request b, or -1 (outside the pool or the row).
@@ -131,66 +171,204 @@ __device__ __forceinline__ int64_t a_page(const AppendParams& p, int b, int64_t 
     return page >= 0 && (page + 1) * p.page_size <= p.num_slots ? page : -1;
 }
 
+__device__ __forceinline__ void a_cp16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// Where a token goes: the first byte of its row in the pool (-1: nowhere) and its
+// position; named: a request names it.
+struct Where {
+    int64_t row;
+    int pos;
+    int named;
+};
 template <int KIND, int D>
-__global__ void __launch_bounds__(32 * kAppendWarps) append_kernel(const AppendParams p) {
-    griddep_wait();
-    griddep_launch_dependents();
-    const int64_t t = static_cast<int64_t>(blockIdx.x) * kAppendWarps + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
-    if (t >= p.total) return;
-    Raw<D> raw;
-    load_raw<D>(p, t, lane, raw);
-    // the request: the last b with cu[b] <= t
+__device__ __forceinline__ Where locate(const AppendParams& p, int64_t t) {
+    constexpr int row_bytes = KIND == MLA_CACHE_FP8_DS_MLA_656 ? kRowFp8 : 2 * (D + kP);
+    // the last b with cu[b] <= t
     int lo = 0, hi = p.B;
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (a_cu(p, mid) <= t) lo = mid;
         else hi = mid;
     }
-    const int b = lo, c0 = a_cu(p, b), c1 = a_cu(p, b + 1);
-    if (t < c0 || t >= c1) return;  // a row that no request names
-    const int64_t place = static_cast<int64_t>(max(__ldg(p.seq_lens + b), 0)) - c1 + t;
-    const int64_t page = place >= 0 ? a_page(p, b, place / p.page_size) : -1;
-    const int64_t pos = p.positions ? __ldg(p.positions + t) : place;
-    if (page < 0 && lane == 0 && p.status) atomicOr(p.status, kErrBadBlock);
-    const float factor = norm_factor<D>(p, raw);
-    const float2 pe = turned(p, raw.pe, pos, lane);
-    constexpr int row_bytes = KIND == MLA_CACHE_FP8_DS_MLA_656 ? kRowFp8 : 2 * (D + kP);
-    uint8_t* row = p.cache + (page * p.page_size + place % p.page_size) * row_bytes;
-    __nv_bfloat16* dense = p.rows ? p.rows + t * p.rows_st : nullptr;
+    const int c0 = a_cu(p, lo), c1 = a_cu(p, lo + 1);
+    Where w;
+    w.named = t >= c0 && t < c1;
+    const int place = max(__ldg(p.seq_lens + lo), 0) - c1 + static_cast<int>(t);
+    const int64_t page = w.named && place >= 0 ? a_page(p, lo, place / p.page_size) : -1;
+    w.row = page >= 0 ? (page * p.page_size + place % p.page_size) * row_bytes : -1;
+    w.pos = p.positions && w.named ? __ldg(p.positions + t) : place;
+    return w;
+}
+
+// A lane's 16-byte units of the latent: lane, lane + 32, ..; of fp8_ds_mla rows
+// 2 lane and 2 lane + 1, so that it has one block's scale to find, with seven
+// other lanes.
+template <int KIND>
+__device__ __forceinline__ int a_unit(int lane, int k) {
+    return KIND == MLA_CACHE_FP8_DS_MLA_656 ? 2 * lane + k : lane + 32 * k;
+}
+
+// Token t from its units and its turned pair to its row and its dense row.
+template <int KIND, int D>
+__device__ __forceinline__ void put_token(const AppendParams& p, int64_t t, const Where& at, const uint4 (&lat)[D / 256],
+                                          const F2 (&w)[D / 256][4], float2 pe, int lane) {
+    constexpr bool kFp8 = KIND == MLA_CACHE_FP8_DS_MLA_656;
+    constexpr int U = D / 256;
+    F2 f[U][4];
+    F2 sq = f2(0.f, 0.f);
 #pragma unroll
-    for (int k = 0; k < Raw<D>::kU; ++k) {
-        float f[8];
-        latent8<D>(p, raw, k, lane, factor, f);
-        if (dense || KIND == MLA_CACHE_BF16_576) {
-            const uint4 v = pack8(f);
-            if (dense) reinterpret_cast<uint4*>(dense)[lane + 32 * k] = v;
-            if (KIND == MLA_CACHE_BF16_576 && page >= 0) reinterpret_cast<uint4*>(row)[lane + 32 * k] = v;
+    for (int k = 0; k < U; ++k) {
+        unpack8(lat[k], f[k]);
+        sq = squares(sq, f[k]);
+    }
+    float c = 1.f;  // f times c are the normalised values
+    if (p.norm) {
+        c = norm_factor(sq, 1.f / D, p.eps);
+#pragma unroll
+        for (int k = 0; k < U; ++k)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f[k][i] = mul2(f[k][i], w[k][i]);
+    }
+    uint8_t* row = p.cache + at.row;
+    const bool put = at.row >= 0;
+    if (p.rows || !kFp8) {
+        uint4* dense = p.rows ? reinterpret_cast<uint4*>(p.rows + t * p.rows_st) : nullptr;
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            F2 y[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) y[i] = mul2(f[k][i], f2(c, c));
+            const uint4 v = pack8(y);
+            if (dense) dense[a_unit<KIND>(lane, k)] = v;
+            if (!kFp8 && put) reinterpret_cast<uint4*>(row)[a_unit<KIND>(lane, k)] = v;
         }
-        if constexpr (KIND == MLA_CACHE_FP8_DS_MLA_656) {
-            // lanes 0..15 hold block 2k, 16..31 block 2k + 1
-            float top = 0.f;
+        if (dense) store_pe(p, dense + D / 8, pe, lane);
+    }
+    if constexpr (kFp8) {
+        float top = most_abs(most_abs(0.f, f[0]), f[U - 1]) * c;  // (rounding keeps the order)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(f[i]));
+        for (int o = 1; o < 8; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        float scale;
+        uint32_t code[4];
+        if (top > 0x1p-90f && top < 0x1p90f) {
+            const float q = top * (1.f / 448.f);
+            scale = fmaf(fmaf(q, 448.f, -top), -1.f / 448.f, q);  // top / 448, correctly rounded (see div2)
+            if (p.norm) {
+                // values and factor in one: a quotient within two units of its last place
+                const float r = __fdividef(c, scale);
+                const F2 r2 = f2(r, r);
 #pragma unroll
-            for (int o = 1; o < 16; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-            const float scale = top == 0.f ? 1.f : __fdiv_rn(top, 448.f);
+                for (int i = 0; i < 4; ++i)
+                    code[i] = codes4(mul2(f[i >> 1][2 * (i & 1)], r2), mul2(f[i >> 1][2 * (i & 1) + 1], r2));
+            } else {
+                // the codes of mla_cache_write, bit for bit
+                const float y = __frcp_rn(scale);
+                const F2 s2 = f2(scale, scale), y2 = f2(y, y), my2 = f2(-y, -y), m1 = f2(-1.f, -1.f);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) f[i] = __fdiv_rn(f[i], scale);
-            if (page >= 0) {
-                reinterpret_cast<uint2*>(row)[lane + 32 * k] =
-                    make_uint2(codes4(f[0], f[1], f[2], f[3]), codes4(f[4], f[5], f[6], f[7]));
-                if ((lane & 15) == 0) reinterpret_cast<float*>(row + kD)[2 * k + (lane >> 4)] = scale;
+                for (int i = 0; i < 4; ++i) {
+                    const F2 a = f[i >> 1][2 * (i & 1)], b = f[i >> 1][2 * (i & 1) + 1];
+                    code[i] = codes4(div2(a, mul2(a, m1), s2, y2, my2), div2(b, mul2(b, m1), s2, y2, my2));
+                }
+            }
+        } else {
+            scale = top == 0.f ? 1.f : __fdiv_rn(top, 448.f);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 a = un2(f[i >> 1][2 * (i & 1)]), b = un2(f[i >> 1][2 * (i & 1) + 1]);
+                code[i] = codes4(f2(__fdiv_rn(a.x * c, scale), __fdiv_rn(a.y * c, scale)),
+                                 f2(__fdiv_rn(b.x * c, scale), __fdiv_rn(b.y * c, scale)));
             }
         }
+        if (put) {
+            reinterpret_cast<uint4*>(row)[lane] = make_uint4(code[0], code[1], code[2], code[3]);
+            if ((lane & 7) == 0) reinterpret_cast<float*>(row + kD)[lane >> 3] = scale;
+        }
     }
-    if (dense) store_pe(p, dense + D, pe, lane);
-    if (page >= 0) store_pe(p, row + (KIND == MLA_CACHE_FP8_DS_MLA_656 ? kD + 16 : 2 * D), pe, lane);
+    if (put) store_pe(p, row + (kFp8 ? kD + 16 : 2 * D), pe, lane);
+}
+
+// A warp a token.
+template <int KIND, int D>
+__global__ void __launch_bounds__(32 * kAppendWarps) append_kernel(const AppendParams p) {
+    constexpr int U = D / 256;
+    griddep_wait();
+    griddep_launch_dependents();
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * kAppendWarps + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    if (t >= p.total) return;
+    uint4 lat[U];
+    const uint4* src = reinterpret_cast<const uint4*>(p.latent + t * p.lat_st);
+#pragma unroll
+    for (int k = 0; k < U; ++k) lat[k] = src[a_unit<KIND>(lane, k)];
+    const uint32_t pair = load_pair(p.k_pe + t * p.pe_st, p.interleaved, lane);
+    F2 w[U][4];
+#pragma unroll
+    for (int k = 0; k < U; ++k) weights8(p, a_unit<KIND>(lane, k), w[k]);
+    const Where at = locate<KIND, D>(p, t);
+    if (!at.named) return;
+    if (at.row < 0 && lane == 0 && p.status) atomicOr(p.status, kErrBadBlock);
+    Angle<1> angle;
+    put_token<KIND, D>(p, t, at, lat, w, angle.turn(p, pair, at.pos, lane), lane);
+}
+
+// Prompts: a warp kMany consecutive tokens, all of them on their way to shared
+// memory while lane n looks up where the n-th goes.
+constexpr int kMany = 8;
+template <int D>
+constexpr int many_smem() {
+    return kAppendWarps * kMany * 2 * (D + kP);
+}
+
+template <int KIND, int D>
+__global__ void __launch_bounds__(32 * kAppendWarps) append_many_kernel(const AppendParams p) {
+    constexpr int U = D / 256, held_row = 2 * (D + kP);
+    extern __shared__ uint8_t held_raw[];
+    griddep_wait();
+    griddep_launch_dependents();
+    const int lane = threadIdx.x & 31;
+    const int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kAppendWarps + (threadIdx.x >> 5)) * kMany;
+    if (t0 >= p.total) return;
+    const int m = static_cast<int>(min(static_cast<int64_t>(kMany), p.total - t0));
+    uint8_t* held = held_raw + (threadIdx.x >> 5) * kMany * held_row;
+    for (int n = 0; n < m; ++n) {
+        const __nv_bfloat16* src = p.latent + (t0 + n) * p.lat_st + lane * 8;
+        const uint32_t dst = smem_u32(held + n * held_row) + lane * 16;
+#pragma unroll
+        for (int k = 0; k < U; ++k) a_cp16(dst + 512 * k, src + 256 * k);
+        if (lane < 8) a_cp16(dst + 2 * D, p.k_pe + (t0 + n) * p.pe_st + lane * 8);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    F2 w[U][4];
+#pragma unroll
+    for (int k = 0; k < U; ++k) weights8(p, a_unit<KIND>(lane, k), w[k]);
+    __shared__ Where ways[kAppendWarps][kMany];
+    const Where mine = locate<KIND, D>(p, t0 + min(lane, m - 1));
+    Where* way = ways[threadIdx.x >> 5];
+    if (lane < m) way[lane] = mine;
+    if (__any_sync(0xffffffffu, mine.named && mine.row < 0) && lane == 0 && p.status) atomicOr(p.status, kErrBadBlock);
+    Angle<1> angle;
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncwarp();
+#pragma unroll 1
+    for (int n = 0; n < m; ++n) {
+        const Where at = way[n];
+        if (!at.named) continue;
+        const uint4* src = reinterpret_cast<const uint4*>(held + n * held_row);
+        uint4 lat[U];
+#pragma unroll
+        for (int k = 0; k < U; ++k) lat[k] = src[a_unit<KIND>(lane, k)];
+        const uint32_t pair = load_pair(src + D / 8, p.interleaved, lane);
+        put_token<KIND, D>(p, t0 + n, at, lat, w, angle.turn(p, pair, at.pos, lane), lane);
+    }
 }
 
 // ------------------------------------------------------------------ page rows
 
-constexpr int kHold = 8;  // new tokens of a page that a warp keeps in registers
+constexpr int kHold = 8;                    // new tokens of a page that a warp keeps
+constexpr int kHeldRow = 2 * (kD + kP);     // bytes of one
+constexpr int kPageSmem = kAppendWarps * kHold * kHeldRow;
 
 // The least power of two s with top <= 448 s, within 2^-40 .. 2^40: top =
 // m 2^e with m in [1, 2), and 448 = 1.75 * 2^8.
@@ -209,9 +387,10 @@ __device__ __forceinline__ float finite_abs(float x) {
 // or more of them, from item cu[b] / page_size + 2 b on, which is as many as
 // the pages its tokens can touch; those past its last page have nothing to do.
 template <int W>
-__global__ void __launch_bounds__(32 * kAppendWarps) append_page_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(32 * kAppendWarps, 3) append_page_kernel(const AppendParams p) {
     constexpr int kItems = kAppendWarps / W;  // pages a CTA
-    __shared__ float tops[kAppendWarps];
+    extern __shared__ uint8_t held_raw[];
+    __shared__ float tops[kAppendWarps], factors[kAppendWarps][kHold];
     griddep_wait();
     griddep_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, wi = warp % W, grp = warp / W;
@@ -228,7 +407,7 @@ __global__ void __launch_bounds__(32 * kAppendWarps) append_page_kernel(const Ap
     if (n <= 0) return;  // (the whole group leaves)
     // places p0 .. p1 - 1 are new; those below 0 have none
     const int64_t p1 = max(__ldg(p.seq_lens + b), 0), p0 = p1 - n;
-    const int64_t pi = max(p0, static_cast<int64_t>(0)) / ps + (item - first_item(b));
+    const int64_t pi = static_cast<int>(max(p0, static_cast<int64_t>(0))) / ps + (item - first_item(b));
     const bool none = p0 < 0 && item == first_item(b);  // this item also sees to the tokens without a place
     if (none && lane == 0 && wi == 0 && p.status) atomicOr(p.status, kErrBadBlock);
     int64_t j0 = max(pi * ps, max(p0, static_cast<int64_t>(0)));
@@ -237,44 +416,75 @@ __global__ void __launch_bounds__(32 * kAppendWarps) append_page_kernel(const Ap
     if (j0 >= j1) return;
     const int64_t t0 = c0 + (j0 - p0);  // the first token's row
     const int m = static_cast<int>(j1 - j0);
-    // the token at index x of the item, 0 <= x < m, is warp x % W's
-    Raw<kD> raw[kHold];
-#pragma unroll
-    for (int k = 0; k < kHold; ++k)
-        if (wi + k * W < m) load_raw<kD>(p, t0 + wi + k * W, lane, raw[k]);
+    // the token at index x of the item, 0 <= x < m, is warp x % W's. The first
+    // kHold of each are on their way to shared memory while the page is looked up.
+    uint8_t* held = held_raw + warp * kHold * kHeldRow;
+    for (int k = 0, x = wi; k < kHold && x < m; ++k, x += W) {
+        const __nv_bfloat16* src = p.latent + (t0 + x) * p.lat_st + lane * 8;
+        const uint32_t dst = smem_u32(held + k * kHeldRow) + lane * 16;
+        a_cp16(dst, src);
+        a_cp16(dst + 512, src + 256);
+        if (lane < 8) a_cp16(dst + 1024, p.k_pe + (t0 + x) * p.pe_st + lane * 8);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
     const int64_t page = a_page(p, b, pi);
     const bool bad = page < 0 && j1 > max(pi * ps, static_cast<int64_t>(0));
     if (bad && lane == 0 && wi == 0 && p.status) atomicOr(p.status, kErrBadBlock);
     const int64_t off = max(p0, static_cast<int64_t>(0)) - pi * ps;  // rows of the page that were there before (if > 0)
     const float old = page >= 0 && off > 0 ? __ldcg(p.scales + page) : 0.f;
-    float factor[kHold];
-    float2 pe[kHold];
+    F2 w[2][4];
+    weights8(p, lane, w[0]);
+    weights8(p, lane + 32, w[1]);
     float top = 0.f;
-    auto position = [&](int x) -> int64_t { return p.positions ? __ldg(p.positions + t0 + x) : j0 + x; };
-    auto largest = [&](const Raw<kD>& r, float fac, float2 e, int x) {
-        if (j0 + x < 0) return;
-        top = fmaxf(top, fmaxf(finite_abs(e.x), finite_abs(e.y)));
+    Angle<W> angle;
+    auto position = [&](int x) { return p.positions ? __ldg(p.positions + t0 + x) : static_cast<int>(j0) + x; };
+    // a token's values times the weights (times its factor they are normalised);
+    // returns the factor
+    auto weighed = [&](uint4 a, uint4 c, F2 (&f)[2][4], bool want) {
+        unpack8(a, f[0]);
+        unpack8(c, f[1]);
+        if (!p.norm) return 1.f;
+        const float fac = want ? norm_factor(squares(squares(f2(0.f, 0.f), f[0]), f[1]), 1.f / kD, p.eps) : 0.f;
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            float f[8];
-            latent8<kD>(p, r, u, lane, fac, f);
+        for (int u = 0; u < 2; ++u)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) top = fmaxf(top, finite_abs(f[i]));
-        }
+            for (int i = 0; i < 4; ++i) f[u][i] = mul2(f[u][i], w[u][i]);
+        return fac;
     };
+    // the largest magnitude of a token's finite values
+    auto largest = [&](const F2 (&f)[2][4], float fac, float2 e, int x) {
+        if (j0 + x < 0) return;
+        float a = most_abs(most_abs(0.f, f[0]), f[1]) * fac;  // (rounding keeps the order)
+        a = fmaxf(a, fmaxf(fabsf(e.x), fabsf(e.y)));
+        if (!(a < INFINITY)) {
+            a = fmaxf(finite_abs(e.x), finite_abs(e.y));
 #pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 v = un2(f[u][i]);
+                    a = fmaxf(a, fmaxf(finite_abs(v.x * fac), finite_abs(v.y * fac)));
+                }
+        }
+        top = fmaxf(top, a);
+    };
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncwarp();
+#pragma unroll 2
     for (int k = 0; k < kHold; ++k) {
         const int x = wi + k * W;
-        if (x < m) {
-            factor[k] = norm_factor<kD>(p, raw[k]);
-            pe[k] = turned(p, raw[k].pe, position(x), lane);
-            largest(raw[k], factor[k], pe[k], x);
-        }
+        if (x >= m) break;
+        const uint4* lat = reinterpret_cast<const uint4*>(held + k * kHeldRow);
+        F2 f[2][4];
+        const float fac = weighed(lat[lane], lat[lane + 32], f, true);
+        if (lane == 0) factors[warp][k] = fac;
+        largest(f, fac, angle.turn(p, load_pair(lat + 64, p.interleaved, lane), position(x), lane), x);
     }
     for (int x = wi + kHold * W; x < m; x += W) {  // pages of more rows than the warps hold: read twice
-        Raw<kD> r;
-        load_raw<kD>(p, t0 + x, lane, r);
-        largest(r, norm_factor<kD>(p, r), turned(p, r.pe, position(x), lane), x);
+        const uint4* lat = reinterpret_cast<const uint4*>(p.latent + (t0 + x) * p.lat_st);
+        F2 f[2][4];
+        const float fac = weighed(lat[lane], lat[lane + 32], f, true);
+        largest(f, fac, angle.turn(p, load_pair(p.k_pe + (t0 + x) * p.pe_st, p.interleaved, lane), position(x), lane), x);
     }
     top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));  // (not negative: ordered as its bits)
     if constexpr (W > 1) {
@@ -292,14 +502,14 @@ __global__ void __launch_bounds__(32 * kAppendWarps) append_page_kernel(const Ap
             uint8_t* rows = p.cache + page * ps * static_cast<int64_t>(kRowPage);
             for (int64_t u = wi * 32 + lane; u < off * (kRowPage / 16); u += 32 * W) {
                 uint4 v = reinterpret_cast<const uint4*>(rows)[u];
-                uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+                uint32_t* v4 = reinterpret_cast<uint32_t*>(&v);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const __half2_raw h01 = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w[i] & 0xFFFFu), __NV_E4M3);
-                    const __half2_raw h23 = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w[i] >> 16), __NV_E4M3);
+                    const __half2_raw h01 = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(v4[i] & 0xFFFFu), __NV_E4M3);
+                    const __half2_raw h23 = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(v4[i] >> 16), __NV_E4M3);
                     const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&h01));
                     const float2 c = __half22float2(*reinterpret_cast<const __half2*>(&h23));
-                    w[i] = codes4(a.x * ratio, a.y * ratio, c.x * ratio, c.y * ratio);
+                    v4[i] = codes4(f2(a.x * ratio, a.y * ratio), f2(c.x * ratio, c.y * ratio));
                 }
                 reinterpret_cast<uint4*>(rows)[u] = v;
             }
@@ -307,64 +517,92 @@ __global__ void __launch_bounds__(32 * kAppendWarps) append_page_kernel(const Ap
         if (lane == 0 && wi == 0 && scale != old) p.scales[page] = scale;
     }
     const float inv = 1.f / scale;  // exact: a power of two
-    auto write = [&](const Raw<kD>& r, float fac, float2 e, int x) {
-        const bool put = page >= 0 && j0 + x >= 0;
-        __nv_bfloat16* dense = p.rows ? p.rows + (t0 + x) * p.rows_st : nullptr;
-        uint8_t* row = p.cache + (page * ps + (j0 + x - pi * ps)) * static_cast<int64_t>(kRowPage);
+    auto write = [&](const F2 (&f)[2][4], float fac, float2 e, int x) {
+        if (p.rows) {
+            uint4* dense = reinterpret_cast<uint4*>(p.rows + (t0 + x) * p.rows_st);
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            float f[8];
-            latent8<kD>(p, r, u, lane, fac, f);
-            if (dense) reinterpret_cast<uint4*>(dense)[lane + 32 * u] = pack8(f);
-            if (put)
-                reinterpret_cast<uint2*>(row)[lane + 32 * u] =
-                    make_uint2(codes4(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv),
-                               codes4(f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv));
-        }
-        if (dense) store_pe(p, dense + kD, e, lane);
-        if (put) {
-            const uint32_t v = codes4(e.x * inv, e.y * inv, 0.f, 0.f);
-            if (p.interleaved) {
-                reinterpret_cast<unsigned short*>(row + kD)[lane] = static_cast<unsigned short>(v);
-            } else {
-                row[kD + lane] = static_cast<uint8_t>(v);
-                row[kD + 32 + lane] = static_cast<uint8_t>(v >> 8);
+            for (int u = 0; u < 2; ++u) {
+                F2 y[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) y[i] = mul2(f[u][i], f2(fac, fac));
+                dense[lane + 32 * u] = pack8(y);
             }
+            store_pe(p, dense + kD / 8, e, lane);
+        }
+        if (page < 0 || j0 + x < 0) return;
+        uint8_t* row = p.cache + (page * ps + (j0 + x - pi * ps)) * static_cast<int64_t>(kRowPage);
+        const F2 c = f2(fac * inv, fac * inv);  // (inv is a power of two: the same as two multiplications)
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+            reinterpret_cast<uint2*>(row)[lane + 32 * u] =
+                make_uint2(codes4(mul2(f[u][0], c), mul2(f[u][1], c)), codes4(mul2(f[u][2], c), mul2(f[u][3], c)));
+        const uint32_t v = codes4(f2(e.x * inv, e.y * inv), 0ull);
+        if (p.interleaved) {
+            reinterpret_cast<unsigned short*>(row + kD)[lane] = static_cast<unsigned short>(v);
+        } else {
+            row[kD + lane] = static_cast<uint8_t>(v);
+            row[kD + 32 + lane] = static_cast<uint8_t>(v >> 8);
         }
     };
-#pragma unroll
+    angle.left = min(angle.left, 0);  // (as the first time: the largest value is among these)
+#pragma unroll 2
     for (int k = 0; k < kHold; ++k) {
         const int x = wi + k * W;
-        if (x < m) write(raw[k], factor[k], pe[k], x);
+        if (x >= m) break;
+        const uint4* lat = reinterpret_cast<const uint4*>(held + k * kHeldRow);
+        F2 f[2][4];
+        weighed(lat[lane], lat[lane + 32], f, false);
+        write(f, factors[warp][k], angle.turn(p, load_pair(lat + 64, p.interleaved, lane), position(x), lane), x);
     }
     for (int x = wi + kHold * W; x < m; x += W) {
-        Raw<kD> r;
-        load_raw<kD>(p, t0 + x, lane, r);
-        write(r, norm_factor<kD>(p, r), turned(p, r.pe, position(x), lane), x);
+        const uint4* lat = reinterpret_cast<const uint4*>(p.latent + (t0 + x) * p.lat_st);
+        F2 f[2][4];
+        const float fac = weighed(lat[lane], lat[lane + 32], f, true);
+        write(f, fac, angle.turn(p, load_pair(p.k_pe + (t0 + x) * p.pe_st, p.interleaved, lane), position(x), lane), x);
     }
 }
 
 }  // namespace
 
-cudaError_t launch_append(const AppendParams& p, int kind, int lat_dim, cudaStream_t stream) {
+cudaError_t launch_append(const AppendParams& p, int kind, int lat_dim, int sms, cudaStream_t stream) {
     cudaLaunchAttribute attr[1];
     if (kind == MLA_CACHE_FP8_PAGE_576) {
         const int W = p.page_size <= 8 ? 1 : p.page_size <= 16 ? 2 : p.page_size <= 32 ? 4 : 8;
         const int64_t items = p.total / p.page_size + 2 * static_cast<int64_t>(p.B);
         const int64_t blocks = (items + kAppendWarps / W - 1) / (kAppendWarps / W);
-        cudaLaunchConfig_t cfg = pdl_config(dim3(static_cast<unsigned>(blocks)), 32 * kAppendWarps, 0, stream, attr);
-        return W == 1   ? cudaLaunchKernelEx(&cfg, append_page_kernel<1>, p)
-               : W == 2 ? cudaLaunchKernelEx(&cfg, append_page_kernel<2>, p)
-               : W == 4 ? cudaLaunchKernelEx(&cfg, append_page_kernel<4>, p)
-                        : cudaLaunchKernelEx(&cfg, append_page_kernel<8>, p);
+        static std::atomic<uint64_t> done[4];
+        auto go = [&](auto* k, int i) {
+            const cudaError_t e = attribute_once(done[i], reinterpret_cast<const void*>(k),
+                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, kPageSmem);
+            if (e != cudaSuccess) return e;
+            cudaLaunchConfig_t cfg = pdl_config(dim3(static_cast<unsigned>(blocks)), 32 * kAppendWarps, kPageSmem, stream, attr);
+            return cudaLaunchKernelEx(&cfg, k, p);
+        };
+        return W == 1   ? go(append_page_kernel<1>, 0)
+               : W == 2 ? go(append_page_kernel<2>, 1)
+               : W == 4 ? go(append_page_kernel<4>, 2)
+                        : go(append_page_kernel<8>, 3);
     }
-    const int64_t blocks = (p.total + kAppendWarps - 1) / kAppendWarps;
-    cudaLaunchConfig_t cfg = pdl_config(dim3(static_cast<unsigned>(blocks)), 32 * kAppendWarps, 0, stream, attr);
-    if (kind == MLA_CACHE_FP8_DS_MLA_656) return cudaLaunchKernelEx(&cfg, append_kernel<MLA_CACHE_FP8_DS_MLA_656, 512>, p);
-    return lat_dim == 256   ? cudaLaunchKernelEx(&cfg, append_kernel<MLA_CACHE_BF16_576, 256>, p)
-           : lat_dim == 512 ? cudaLaunchKernelEx(&cfg, append_kernel<MLA_CACHE_BF16_576, 512>, p)
-           : lat_dim == 768 ? cudaLaunchKernelEx(&cfg, append_kernel<MLA_CACHE_BF16_576, 768>, p)
-                            : cudaLaunchKernelEx(&cfg, append_kernel<MLA_CACHE_BF16_576, 1792>, p);
+    // eight tokens a warp where every SM still gets its 24 warps
+    const bool many = p.total >= static_cast<int64_t>(kMany) * 24 * sms && lat_dim <= 768;
+    const int64_t per = static_cast<int64_t>(kAppendWarps) * (many ? kMany : 1), blocks = (p.total + per - 1) / per;
+    static std::atomic<uint64_t> done[4];
+    auto go = [&](auto* k, int smem, int i) {
+        if (smem > 0) {
+            const cudaError_t e = attribute_once(done[i], reinterpret_cast<const void*>(k),
+                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+            if (e != cudaSuccess) return e;
+        }
+        cudaLaunchConfig_t cfg = pdl_config(dim3(static_cast<unsigned>(blocks)), 32 * kAppendWarps, smem, stream, attr);
+        return cudaLaunchKernelEx(&cfg, k, p);
+    };
+#define MLA_APPEND(K, DV, I) (many ? go(append_many_kernel<K, DV>, many_smem<DV>(), I) : go(append_kernel<K, DV>, 0, I))
+    if (kind == MLA_CACHE_FP8_DS_MLA_656) return MLA_APPEND(MLA_CACHE_FP8_DS_MLA_656, 512, 0);
+    return lat_dim == 256   ? MLA_APPEND(MLA_CACHE_BF16_576, 256, 1)
+           : lat_dim == 512 ? MLA_APPEND(MLA_CACHE_BF16_576, 512, 2)
+           : lat_dim == 768 ? MLA_APPEND(MLA_CACHE_BF16_576, 768, 3)
+                            : go(append_kernel<MLA_CACHE_BF16_576, 1792>, 0, 0);
+#undef MLA_APPEND
 }
 
 }  // namespace mla

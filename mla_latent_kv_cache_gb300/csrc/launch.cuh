@@ -263,6 +263,6 @@ struct AppendParams {
     int64_t rows_st;
     int* status;
 };
-cudaError_t launch_append(const AppendParams& p, int kind, int lat_dim, cudaStream_t stream);
+cudaError_t launch_append(const AppendParams& p, int kind, int lat_dim, int sms, cudaStream_t stream);
 
 }  // namespace mla

@@ -172,6 +172,22 @@ def test_a_step_of_many_requests(kind, n):
     run(Case([n] * 150, list(range(150)), 64, kind, seed=n, given=True, dense=False))
 
 
+@pytest.mark.parametrize("kind,D", [(BF16, 512), (FP8, 512), (PAGE, 512), (BF16, 256), (BF16, 768), (BF16, 1792)])
+def test_long_prompts(kind, D):
+    """Enough tokens for every kernel's form for prompts, odd numbers of them, one request without any."""
+    run(Case([20001, 0, 3, 14999, 1], [0, 9, 100, 7, 0], 64, kind, D=D, seed=D + kind, pad=3, dense=kind != FP8))
+
+
+@pytest.mark.parametrize("kind", [BF16, FP8])
+def test_long_prompts_without_norm_equal_the_separate_calls(kind):
+    c = Case([30011, 77], [0, 60], 16, kind, norm=False, turn=False, seed=12)
+    other = c.cache.clone()
+    c.go()
+    slots = np.concatenate([c.slots(b, np.arange(p, p + n)) for b, (n, p) in enumerate(zip(c.new, c.before))])
+    m.mla_cache_write(c.proj[:, :512], c.proj[:, 512:], torch.from_numpy(slots).to(DEV), other, kind)
+    assert torch.equal(c.cache, other)
+
+
 @pytest.mark.parametrize("D", [256, 768, 1792])
 def test_other_latent_widths(D):
     run(Case([5, 70, 1], [0, 9, 100], 16, BF16, D=D, seed=D))
