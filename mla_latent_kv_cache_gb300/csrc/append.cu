@@ -14,6 +14,8 @@
 // once. The scale is a power of two: e4m3 values keep their 4 significant bits
 // whatever it is, and when a later token makes it grow, the codes before it are
 // divided by a power of two, which changes only those that become subnormal.
+#include <climits>
+
 #include "launch.cuh"
 #include "mla.h"
 #include "mla_common.cuh"
@@ -315,7 +317,7 @@ __global__ void __launch_bounds__(32 * kAppendWarps) append_kernel(const AppendP
 
 // Prompts: a warp kMany consecutive tokens, all of them on their way to shared
 // memory while lane n looks up where the n-th goes.
-constexpr int kMany = 8;
+constexpr int kMany = 4;
 template <int D>
 constexpr int many_smem() {
     return kAppendWarps * kMany * 2 * (D + kP);
@@ -419,12 +421,14 @@ __global__ void __launch_bounds__(32 * kAppendWarps, 3) append_page_kernel(const
     // the token at index x of the item, 0 <= x < m, is warp x % W's. The first
     // kHold of each are on their way to shared memory while the page is looked up.
     uint8_t* held = held_raw + warp * kHold * kHeldRow;
-    for (int k = 0, x = wi; k < kHold && x < m; ++k, x += W) {
-        const __nv_bfloat16* src = p.latent + (t0 + x) * p.lat_st + lane * 8;
-        const uint32_t dst = smem_u32(held + k * kHeldRow) + lane * 16;
-        a_cp16(dst, src);
-        a_cp16(dst + 512, src + 256);
-        if (lane < 8) a_cp16(dst + 1024, p.k_pe + (t0 + x) * p.pe_st + lane * 8);
+    {
+        const __nv_bfloat16 *src = p.latent + (t0 + wi) * p.lat_st + lane * 8, *pe = p.k_pe + (t0 + wi) * p.pe_st + lane * 8;
+        uint32_t dst = smem_u32(held) + lane * 16;
+        for (int x = wi; x < min(m, kHold * W); x += W, src += W * p.lat_st, pe += W * p.pe_st, dst += kHeldRow) {
+            a_cp16(dst, src);
+            a_cp16(dst + 512, src + 256);
+            if (lane < 8) a_cp16(dst + 1024, pe);
+        }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
     const int64_t page = a_page(p, b, pi);
@@ -452,8 +456,9 @@ __global__ void __launch_bounds__(32 * kAppendWarps, 3) append_page_kernel(const
         return fac;
     };
     // the largest magnitude of a token's finite values
+    const int skip = static_cast<int>(max(-j0, static_cast<int64_t>(0)));  // tokens of the item without a place
     auto largest = [&](const F2 (&f)[2][4], float fac, float2 e, int x) {
-        if (j0 + x < 0) return;
+        if (x < skip) return;
         float a = most_abs(most_abs(0.f, f[0]), f[1]) * fac;  // (rounding keeps the order)
         a = fmaxf(a, fmaxf(fabsf(e.x), fabsf(e.y)));
         if (!(a < INFINITY)) {
@@ -517,32 +522,38 @@ __global__ void __launch_bounds__(32 * kAppendWarps, 3) append_page_kernel(const
         if (lane == 0 && wi == 0 && scale != old) p.scales[page] = scale;
     }
     const float inv = 1.f / scale;  // exact: a power of two
+    // the dense row and the cached row of token wi; those of the warp's next are W rows further
+    __nv_bfloat16* dense = p.rows ? p.rows + (t0 + wi) * p.rows_st : nullptr;
+    uint8_t* row = p.cache + (page * ps + (j0 + wi - pi * ps)) * static_cast<int64_t>(kRowPage);
+    const int from = page >= 0 ? skip : INT_MAX;  // tokens below this are not cached
     auto write = [&](const F2 (&f)[2][4], float fac, float2 e, int x) {
-        if (p.rows) {
-            uint4* dense = reinterpret_cast<uint4*>(p.rows + (t0 + x) * p.rows_st);
+        if (dense) {
+            uint4* d = reinterpret_cast<uint4*>(dense);
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 F2 y[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) y[i] = mul2(f[u][i], f2(fac, fac));
-                dense[lane + 32 * u] = pack8(y);
+                d[lane + 32 * u] = pack8(y);
             }
-            store_pe(p, dense + kD / 8, e, lane);
+            store_pe(p, d + kD / 8, e, lane);
+            dense += W * p.rows_st;
         }
-        if (page < 0 || j0 + x < 0) return;
-        uint8_t* row = p.cache + (page * ps + (j0 + x - pi * ps)) * static_cast<int64_t>(kRowPage);
-        const F2 c = f2(fac * inv, fac * inv);  // (inv is a power of two: the same as two multiplications)
+        if (x >= from) {
+            const F2 c = f2(fac * inv, fac * inv);  // (inv is a power of two: the same as two multiplications)
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
-            reinterpret_cast<uint2*>(row)[lane + 32 * u] =
-                make_uint2(codes4(mul2(f[u][0], c), mul2(f[u][1], c)), codes4(mul2(f[u][2], c), mul2(f[u][3], c)));
-        const uint32_t v = codes4(f2(e.x * inv, e.y * inv), 0ull);
-        if (p.interleaved) {
-            reinterpret_cast<unsigned short*>(row + kD)[lane] = static_cast<unsigned short>(v);
-        } else {
-            row[kD + lane] = static_cast<uint8_t>(v);
-            row[kD + 32 + lane] = static_cast<uint8_t>(v >> 8);
+            for (int u = 0; u < 2; ++u)
+                reinterpret_cast<uint2*>(row)[lane + 32 * u] =
+                    make_uint2(codes4(mul2(f[u][0], c), mul2(f[u][1], c)), codes4(mul2(f[u][2], c), mul2(f[u][3], c)));
+            const uint32_t v = __nv_cvt_float2_to_fp8x2(make_float2(e.x * inv, e.y * inv), __NV_SATFINITE, __NV_E4M3);
+            if (p.interleaved) {
+                reinterpret_cast<unsigned short*>(row + kD)[lane] = static_cast<unsigned short>(v);
+            } else {
+                row[kD + lane] = static_cast<uint8_t>(v);
+                row[kD + 32 + lane] = static_cast<uint8_t>(v >> 8);
+            }
         }
+        row += W * kRowPage;
     };
     angle.left = min(angle.left, 0);  // (as the first time: the largest value is among these)
 #pragma unroll 2
@@ -583,8 +594,9 @@ cudaError_t launch_append(const AppendParams& p, int kind, int lat_dim, int sms,
                : W == 4 ? go(append_page_kernel<4>, 2)
                         : go(append_page_kernel<8>, 3);
     }
-    // eight tokens a warp where every SM still gets its 24 warps
-    const bool many = p.total >= static_cast<int64_t>(kMany) * 24 * sms && lat_dim <= 768;
+    // four tokens a warp where every SM still gets its 32 warps (with eight, fewer
+    // fit an SM: 98,304 tokens 44 us, against 36)
+    const bool many = p.total >= static_cast<int64_t>(kMany) * 32 * sms && lat_dim <= 768;
     const int64_t per = static_cast<int64_t>(kAppendWarps) * (many ? kMany : 1), blocks = (p.total + per - 1) / per;
     static std::atomic<uint64_t> done[4];
     auto go = [&](auto* k, int smem, int i) {
