@@ -42,6 +42,8 @@ namespace mla {
 
 namespace {
 
+using F2 = packed2;
+
 constexpr int kTok = 128;             // tokens a tile
 constexpr int kBlk = kTok * 128;      // bytes of a latent block
 constexpr int kRopeBlk = kTok * 64;   // and of the rotary part
@@ -94,10 +96,12 @@ struct P8Ctrl {
     int t_begin, t_end, b0, j0;
     alignas(16) float sc[kScs][kTok];   // scales of a tile: one for each run of rows in a page, or each row
     alignas(16) float kq[kQGens][64];   // what turns a column's sum into log2 units (without the token's scale)
-    alignas(16) float mm[64];           // running maximum - kTop
+    alignas(16) float m[64];            // running maximum (kNoMax: nothing seen yet)
+    alignas(16) float nm[64];           // kTop - m (0 where m is kNoMax)
     alignas(16) float alpha[64];
     alignas(16) float red[4][64];
     alignas(16) float inv[64];
+    int unset[2];                       // a softmax group has columns without a maximum
 };
 
 template <int NP>
@@ -129,6 +133,20 @@ __device__ __forceinline__ float p8_scale(const DecodeParams& p, int page) {
 
 __device__ __forceinline__ void p8_cp16(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// 16 columns from each of two places in TMEM, one wait for both.
+__device__ __forceinline__ void p8_ld_pair(uint32_t at0, uint32_t at1, uint32_t (&a)[16], uint32_t (&b)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%32];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%33];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3]), "=r"(a[4]), "=r"(a[5]), "=r"(a[6]), "=r"(a[7]), "=r"(a[8]),
+          "=r"(a[9]), "=r"(a[10]), "=r"(a[11]), "=r"(a[12]), "=r"(a[13]), "=r"(a[14]), "=r"(a[15]), "=r"(b[0]), "=r"(b[1]),
+          "=r"(b[2]), "=r"(b[3]), "=r"(b[4]), "=r"(b[5]), "=r"(b[6]), "=r"(b[7]), "=r"(b[8]), "=r"(b[9]), "=r"(b[10]),
+          "=r"(b[11]), "=r"(b[12]), "=r"(b[13]), "=r"(b[14]), "=r"(b[15])
+        : "r"(at0), "r"(at1)
+        : "memory");
 }
 
 // Two values as e4m3 codes (low byte the first) and what is left of them.
@@ -180,6 +198,7 @@ __global__ void __launch_bounds__(P8Cfg<NP>::kThreads, 1)
         for (int i = 0; i < kQGens; ++i) mbar_init(&ctrl->q_full[i], 4);
         mbar_init(&ctrl->q_empty, 1);
         for (int i = 0; i < kScs; ++i) mbar_init(&ctrl->sc_full[i], LSU ? 4 : 1);
+        for (int c = 0; c < 64; ++c) ctrl->nm[c] = 0.f;
         ctrl->abort = 0;
         fence_mbar_init();
     }
@@ -412,9 +431,15 @@ __global__ void __launch_bounds__(P8Cfg<NP>::kThreads, 1)
                 }
                 drain_mma(&ctrl->fin[1]);
             }
-        } else if (!LSU && warp == 1) {
+        } else if (!LSU && (warp == 1 || warp == 2)) {
             // ------------------------------------------------------------ loads
             // Lane r owns run r of a tile: BR rows that lie next to each other in a page.
+            // Warp 1 loads blocks 0 and 1 and the rotary part, warp 2 blocks 2 and 3 (a tile
+            // of 16-token pages is 40 boxes). A refill waits for the block 1 ring before by
+            // its parity, which could not tell it from the one 2 rings before; but the warp's
+            // last wait was for block u - 1 - kSlots or later, and products end in order, so
+            // that one is long done.
+            const int kb0 = warp == 1 ? 0 : 2;
             const int BR = p.run_rows;
             const uint64_t pol = gridDim.y > 1 ? l2_policy_evict_normal() : l2_policy_evict_first();
             bool bad = false, ok = true;
@@ -426,36 +451,40 @@ __global__ void __launch_bounds__(P8Cfg<NP>::kThreads, 1)
                 return p8_slot(p, p.block_table + static_cast<int64_t>(t.b) * p.bt_stride, t.j * kTok + lane * BR, page, bad);
             };
             int page_next, y_next = run_of(it, page_next);
-            float s_next = p8_scale(p, page_next);
-            uint32_t u = 0, armed = 0, parity = 0;  // blocks so far; slots whose barrier is armed, and their last parity
+            float s_next = warp == 1 ? p8_scale(p, page_next) : 1.f;
+            uint32_t armed = 0;  // blocks whose barrier this warp has armed
             int rope_armed = 0;
             for (; i < ntiles && ok; ++i) {
                 const int valid = min(kTok, it.T - it.j * kTok);
                 const int nruns = (valid + BR - 1) / BR;
                 const int y = y_next;
-                // (its slot: the loads of tile i are behind the value product of tile i - 3,
-                // which read nothing later than the scales of tile i - 3 did)
-                if (lane < nruns) ctrl->sc[i % kScs][lane] = s_next;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&ctrl->sc_full[i % kScs]);
+                if (warp == 1) {
+                    // (its slot: the loads of tile i are behind the value product of tile i - 3,
+                    // which read nothing later than the scales of tile i - 3 did)
+                    if (lane < nruns) ctrl->sc[i % kScs][lane] = s_next;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&ctrl->sc_full[i % kScs]);
+                }
                 it.next(p.seq_lens, p.B);
                 if (i + 1 < ntiles) {
                     y_next = run_of(it, page_next);
-                    s_next = p8_scale(p, page_next);
+                    if (warp == 1) s_next = p8_scale(p, page_next);
                 }
-                const int rr = i % kRopes;
-                if (i >= kRopes && !__all_sync(0xffffffffu, mbar_wait(&ctrl->rope_empty[rr], ((i / kRopes) - 1) & 1, abort))) {
-                    ok = false;
-                    site = kSiteTmaRopeEmpty;
-                    break;
+                if (warp == 1) {
+                    const int rr = i % kRopes;
+                    if (i >= kRopes && !__all_sync(0xffffffffu, mbar_wait(&ctrl->rope_empty[rr], ((i / kRopes) - 1) & 1, abort))) {
+                        ok = false;
+                        site = kSiteTmaRopeEmpty;
+                        break;
+                    }
+                    if (lane == 0) mbar_arrive_expect_tx(&ctrl->rope_full[rr], static_cast<uint32_t>(nruns * BR * 64));
+                    __syncwarp();
+                    rope_armed = i + 1;
+                    if (lane < nruns)
+                        tma_load_2d(rope_ring + rr * kRopeBlk + lane * BR * 64, &maps.rope, &ctrl->rope_full[rr], kD, y, pol);
                 }
-                if (lane == 0) mbar_arrive_expect_tx(&ctrl->rope_full[rr], static_cast<uint32_t>(nruns * BR * 64));
-                __syncwarp();
-                rope_armed = i + 1;
-                if (lane < nruns)
-                    tma_load_2d(rope_ring + rr * kRopeBlk + lane * BR * 64, &maps.rope, &ctrl->rope_full[rr], kD, y, pol);
-                for (int kb = 0; kb < 4; ++kb, ++u) {
-                    const uint32_t slot = u % C::kSlots, fill = u / C::kSlots;
+                for (int kb = kb0; kb < kb0 + 2; ++kb) {
+                    const uint32_t u = 4u * i + kb, slot = u % C::kSlots, fill = u / C::kSlots;
                     if (fill > 0 && !__all_sync(0xffffffffu, mbar_wait(&ctrl->blk_empty[slot], (fill - 1) & 1, abort))) {
                         ok = false;
                         site = kSiteTmaPairEmpty;
@@ -463,8 +492,7 @@ __global__ void __launch_bounds__(P8Cfg<NP>::kThreads, 1)
                     }
                     if (lane == 0) mbar_arrive_expect_tx(&ctrl->blk_full[slot], static_cast<uint32_t>(nruns * BR * 128));
                     __syncwarp();
-                    armed |= 1u << slot;
-                    parity = (parity & ~(1u << slot)) | ((fill & 1u) << slot);
+                    armed = u + 1;
                     if (lane < nruns)
                         tma_load_2d(ring + slot * kBlk + lane * BR * 128, &maps.lat, &ctrl->blk_full[slot], kb * 128, y, pol);
                 }
@@ -473,13 +501,21 @@ __global__ void __launch_bounds__(P8Cfg<NP>::kThreads, 1)
                 fail(p, ctrl, kErrWaitTimeout, site, i);
                 report(p, kRoleTma, site, i);
             }
-            // no copy may arrive after the CTA is gone: wait (bounded, whatever the abort
-            // flag says) for the last fill of every barrier armed here
-            volatile int never = 0;
-            for (int s = 0; s < C::kSlots; ++s)
-                if (armed >> s & 1) mbar_wait(&ctrl->blk_full[s], parity >> s & 1, &never);
-            for (int k = max(0, rope_armed - kRopes); k < rope_armed; ++k)
-                mbar_wait(&ctrl->rope_full[k % kRopes], (k / kRopes) & 1, &never);
+            if (lane == 0 && *abort) {
+                // Copies armed here may still be on their way: let them land before the CTA
+                // leaves (otherwise the score product has waited for every one). A slot that
+                // the other loader filled since cannot be told by its parity and waits out
+                // the deadline, one for all.
+                const unsigned long long t0 = globaltimer_ns();
+                auto land = [&](uint64_t* bar, uint32_t par) {
+                    while (!mbar_try_wait(bar, par) && globaltimer_ns() - t0 < kWaitLimitNs) {
+                    }
+                };
+                const uint32_t from = armed > static_cast<uint32_t>(C::kSlots) ? armed - C::kSlots : 0;
+                for (uint32_t u = from; u < armed; ++u)
+                    if ((u & 2) == static_cast<uint32_t>(kb0)) land(&ctrl->blk_full[u % C::kSlots], (u / C::kSlots) & 1);
+                for (int k = max(0, rope_armed - kRopes); k < rope_armed; ++k) land(&ctrl->rope_full[k % kRopes], (k / kRopes) & 1);
+            }
             if (bad) atomicOr(status_rec(p), kErrBadBlock);
         } else if (warp >= C::kQWarp) {
             // ---------------------------------------------------------- queries
@@ -588,7 +624,8 @@ __global__ void __launch_bounds__(P8Cfg<NP>::kThreads, 1)
             const int bar = 1 + grp;
             const uint32_t lane_base = static_cast<uint32_t>(wq * 32) << 16;
             const int run_shift = LSU ? 0 : 31 - __clz(p.run_rows);  // (a power of two)
-            float l[CW];
+            F2 l[CW / 2];          // this token's share of the columns' sums
+            bool unset = false;
             int seg = -1, start_j = 0, T = 0, qt = 0, rows = 0;
             bool failed = false;
             int site = 0, i = 0;
@@ -607,7 +644,7 @@ __global__ void __launch_bounds__(P8Cfg<NP>::kThreads, 1)
                     qt = req_qt(p, it.b);
                     rows = req_rows_in_group(p, it.b, gy);
 #pragma unroll
-                    for (int c = 0; c < CW; ++c) l[c] = 0.f;
+                    for (int c = 0; c < CW / 2; ++c) l[c] = 0ull;
                     wait(&ctrl->q_full[seg % kQGens], (seg / kQGens) & 1, kSiteQFull);
                 }
                 const float* kq = ctrl->kq[seg % kQGens] + cb;
@@ -617,32 +654,43 @@ __global__ void __launch_bounds__(P8Cfg<NP>::kThreads, 1)
                 const float lv = log2f(vs), inv_vs = 1.f / vs;
                 wait(&ctrl->s_full[i & 1], (i >> 1) & 1, kSiteSFull);
                 tc_fence_after();
-                float x[CW];
+                // y = log2 of P before any limit: score and scale in log2 units, less the maximum, and kTop
+                F2 y[CW / 2];
                 {
                     const uint32_t tS = tmem + C::kColS + (i & 1) * 2 * NP + lane_base + cb;
+                    const F2 vs2 = f2(vs, vs), lv2 = f2(lv, lv), old2 = fresh ? 0ull : f2(1.f, 1.f);
 #pragma unroll
                     for (int c0 = 0; c0 < CW; c0 += 16) {
                         uint32_t h[16], lo[16];
-                        tmem_ld_x16(tS + c0, h);
-                        tmem_ld_x16(tS + NP + c0, lo);
+                        p8_ld_pair(tS + c0, tS + NP + c0, h, lo);
 #pragma unroll
-                        for (int c = 0; c < 16; ++c) x[c0 + c] = fmaf(__uint_as_float(lo[c]), 0x1p-5f, __uint_as_float(h[c]));
+                        for (int c = 0; c < 16; c += 4) {
+                            const float4 k = *reinterpret_cast<const float4*>(kq + c0 + c);
+                            const float4 nm = *reinterpret_cast<const float4*>(ctrl->nm + cb + c0 + c);
+                            const F2 a = fma2(f2(__uint_as_float(lo[c]), __uint_as_float(lo[c + 1])), f2(0x1p-5f, 0x1p-5f),
+                                              f2(__uint_as_float(h[c]), __uint_as_float(h[c + 1])));
+                            const F2 b = fma2(f2(__uint_as_float(lo[c + 2]), __uint_as_float(lo[c + 3])), f2(0x1p-5f, 0x1p-5f),
+                                              f2(__uint_as_float(h[c + 2]), __uint_as_float(h[c + 3])));
+                            y[(c0 + c) / 2] = fma2(mul2(a, vs2), f2(k.x, k.y), fma2(f2(nm.x, nm.y), old2, lv2));
+                            y[(c0 + c) / 2 + 1] = fma2(mul2(b, vs2), f2(k.z, k.w), fma2(f2(nm.z, nm.w), old2, lv2));
+                        }
                     }
                 }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&ctrl->s_free[i & 1]);
                 bool clear = tk >= valid;  // the row's codes must not meet the value product
-#pragma unroll
-                for (int c = 0; c < CW; ++c) x[c] = fmaf(x[c] * vs, kq[c], lv);
                 if (it.j * kTok + valid > T - qt || valid < kTok) {
                     // columns from c0 on see the token: query t sees tokens up to T - qt + t
                     const int c0 = tk < valid ? max(0, tok - (T - qt)) * p.Hq - gy * 64 - cb : INT_MAX;
                     bool nan = true;
 #pragma unroll
-                    for (int c = 0; c < CW; ++c) {
-                        nan = nan && x[c] != x[c];
-                        if (c < c0) x[c] = -INFINITY;
+                    for (int c = 0; c < CW; c += 2) {
+                        float2 v = un2(y[c / 2]);
+                        nan = nan && v.x != v.x && v.y != v.y;
+                        if (c < c0) v.x = -INFINITY;
+                        if (c + 1 < c0) v.y = -INFINITY;
+                        y[c / 2] = f2(v.x, v.y);
                     }
                     // a NaN code would pass a weight of 0: rows that some queries do not see are
                     // cleared if they hold one (those that do see it have NaN for a weight)
@@ -657,34 +705,43 @@ __global__ void __launch_bounds__(P8Cfg<NP>::kThreads, 1)
                         }
                     }
                 }
-                bool need = fresh || failed;
+                float top = -INFINITY;
 #pragma unroll
-                for (int c = 0; c < CW; ++c) need = need || x[c] > ctrl->mm[cb + c] + (kTop + kSlack);
-                if (named_bar_or(bar, 128, need)) {
+                for (int c = 0; c < CW / 2; ++c) {
+                    const float2 v = un2(y[c]);
+                    top = fmaxf(top, fmaxf(v.x, v.y));
+                }
+                if (named_bar_or(bar, 128, fresh || failed || unset || top > kTop + kSlack)) {
                     // the maxima move: every column's goes to the tile's if that is larger
-                    float most[CW];
+                    int most[CW];
 #pragma unroll
                     for (int c = 0; c < CW; ++c) {
                         // order-preserving whole numbers; NaN counts as nothing
-                        const float v = fmaxf(x[c], kNoMax);
-                        const int k = __float_as_int(v);
-                        const int r = __reduce_max_sync(0xffffffffu, k < 0 ? k ^ 0x7FFFFFFF : k);
-                        most[c] = __int_as_float(r < 0 ? r ^ 0x7FFFFFFF : r);
+                        const float2 v = un2(y[c / 2]);
+                        const int k = __float_as_int(fmaxf(c & 1 ? v.y : v.x, kNoMax));
+                        most[c] = __reduce_max_sync(0xffffffffu, k < 0 ? k ^ 0x7FFFFFFF : k);
                     }
                     if (lane == 0) {
 #pragma unroll
-                        for (int c = 0; c < CW; ++c) ctrl->red[wq][cb + c] = most[c];
+                        for (int c = 0; c < CW; ++c) ctrl->red[wq][cb + c] = __int_as_float(most[c] < 0 ? most[c] ^ 0x7FFFFFFF : most[c]);
                     }
+                    float before[CW];  // the kTop - m that y holds
+#pragma unroll
+                    for (int c = 0; c < CW; ++c) before[c] = fresh ? 0.f : ctrl->nm[cb + c];
                     named_bar_sync(bar, 128);
                     if (tk < CW) {
                         const int c = cb + tk;
-                        const float old = fresh ? kNoMax : ctrl->mm[c] + kTop;
-                        const float top = fmaxf(fmaxf(ctrl->red[0][c], ctrl->red[1][c]), fmaxf(ctrl->red[2][c], ctrl->red[3][c]));
-                        const float m = fmaxf(old, top);
-                        ctrl->mm[c] = m - kTop;
+                        const float old = fresh ? kNoMax : ctrl->m[c], shift = fresh ? 0.f : ctrl->nm[c];
+                        const float t = fmaxf(fmaxf(ctrl->red[0][c], ctrl->red[1][c]), fmaxf(ctrl->red[2][c], ctrl->red[3][c]));
+                        const float m = t > kNoMax ? fmaxf(old, t - shift) : old;
+                        ctrl->m[c] = m;
+                        ctrl->nm[c] = m > kNoMax ? kTop - m : 0.f;
                         ctrl->alpha[c] = ex2(old - m);
+                        const unsigned none = __ballot_sync(CW == 32 ? 0xffffffffu : 0xffffu, !(m > kNoMax));
+                        if (tk == 0) ctrl->unset[grp] = none != 0;
                     }
                     if (named_bar_or(bar, 128, failed)) break;
+                    unset = ctrl->unset[grp] != 0;
                     if (!fresh) {
                         wait(&ctrl->o_done[(i - 1) & 1], ((i - 1) >> 1) & 1, kSiteORescale);
                         tc_fence_after();
@@ -704,28 +761,41 @@ __global__ void __launch_bounds__(P8Cfg<NP>::kThreads, 1)
                                     tmem_st_x16(at, o);
                                 }
                         tmem_wait_st();
+                    }
 #pragma unroll
-                        for (int c = 0; c < CW; ++c) l[c] *= ctrl->alpha[cb + c];
+                    for (int c = 0; c < CW; c += 2) {
+                        const float2 a = *reinterpret_cast<const float2*>(ctrl->alpha + cb + c);
+                        const float2 nm = *reinterpret_cast<const float2*>(ctrl->nm + cb + c);
+                        if (!fresh) l[c / 2] = mul2(l[c / 2], f2(a.x, a.y));
+                        float2 v = un2(y[c / 2]);
+                        v.x += nm.x - before[c];
+                        v.y += nm.y - before[c + 1];
+                        y[c / 2] = f2(v.x, v.y);
                     }
                 }
                 // P and its place: free when the value product that read it last is done
                 if (i >= C::kPBufs)
                     wait(&ctrl->o_done[(i - C::kPBufs) & 1], ((i - C::kPBufs) >> 1) & 1, kSiteOPbuf);
                 uint32_t hc[CW / 4], lc[CW / 4];
+                const F2 inv2 = f2(inv_vs, inv_vs);
 #pragma unroll
                 for (int c = 0; c < CW; c += 2) {
-                    const float a = ex2(x[c] - ctrl->mm[cb + c]), b = ex2(x[c + 1] - ctrl->mm[cb + c + 1]);
-                    l[c] = fmaf(a, inv_vs, l[c]);
-                    l[c + 1] = fmaf(b, inv_vs, l[c + 1]);
-                    float ra, rb;
-                    const uint32_t h = p8_split(a, b, ra, rb);
-                    const uint32_t lo = C::kStack ? p8_codes(ra * 32.f, rb * 32.f) : p8_codes(ra, rb);
+                    const float2 v = un2(y[c / 2]);
+                    const float a = ex2(v.x), b = ex2(v.y);
+                    l[c / 2] = fma2(f2(a, b), inv2, l[c / 2]);
+                    // in f16 (11 bits, of which the two codes hold 8) the rest is one packed subtraction
+                    const __half2 ph = __floats2half2_rn(a, b);
+                    const uint32_t h = __nv_cvt_halfraw2_to_fp8x2(*reinterpret_cast<const __half2_raw*>(&ph), __NV_SATFINITE, __NV_E4M3);
+                    const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(h), __NV_E4M3);
+                    __half2 rest = __hsub2(ph, *reinterpret_cast<const __half2*>(&hr));
+                    if (C::kStack) rest = __hmul2(rest, __float2half2_rn(32.f));
+                    const uint32_t lo = __nv_cvt_halfraw2_to_fp8x2(*reinterpret_cast<const __half2_raw*>(&rest), __NV_SATFINITE, __NV_E4M3);
                     if (c & 2) {
                         hc[c >> 2] |= h << 16;
                         lc[c >> 2] |= lo << 16;
                     } else {
-                        hc[c >> 2] = h;
-                        lc[c >> 2] = lo;
+                        hc[c >> 2] = h & 0xFFFFu;
+                        lc[c >> 2] = lo & 0xFFFFu;
                     }
                 }
                 uint8_t* prow = pbufs + (i % C::kPBufs) * C::kPBytes + tk * C::kPRow;
@@ -756,7 +826,10 @@ __global__ void __launch_bounds__(P8Cfg<NP>::kThreads, 1)
                 // ------------------------------------------- the segment's end
                 float sum[CW];
 #pragma unroll
-                for (int c = 0; c < CW; ++c) sum[c] = warp_sum(l[c]);
+                for (int c = 0; c < CW; ++c) {
+                    const float2 v = un2(l[c / 2]);
+                    sum[c] = warp_sum(c & 1 ? v.y : v.x);
+                }
                 if (lane == 0) {
 #pragma unroll
                     for (int c = 0; c < CW; ++c) ctrl->red[wq][cb + c] = sum[c];
@@ -770,7 +843,7 @@ __global__ void __launch_bounds__(P8Cfg<NP>::kThreads, 1)
                     const float s = ctrl->red[0][c] + ctrl->red[1][c] + ctrl->red[2][c] + ctrl->red[3][c];
                     // (a NaN sum is not nothing)
                     ctrl->inv[c] = s == 0.f ? 0.f : 1.f / s;
-                    const float L = s == 0.f ? -INFINITY : (ctrl->mm[c] + log2f(s)) * kLn2f;
+                    const float L = s == 0.f ? -INFINITY : (ctrl->m[c] - kTop + log2f(s)) * kLn2f;
                     if (c < rows) {
                         if (whole) p.lse[row0 + c] = L;
                         // (the merge leaves a NaN out of its maximum, and of an infinity it makes NaN)
@@ -788,13 +861,14 @@ __global__ void __launch_bounds__(P8Cfg<NP>::kThreads, 1)
                     for (int c0 = 0; c0 < CW; c0 += 16) {
                         const uint32_t at = tmem + lane_base + mt * C::kPRow + cb + c0;
                         uint32_t o[16];
-                        tmem_ld_x16(at, o);
-                        if (C::kStack) {
+                        if constexpr (C::kStack) {
                             uint32_t lo[16];
-                            tmem_ld_x16(at + NP, lo);
+                            p8_ld_pair(at, at + NP, o, lo);
 #pragma unroll
                             for (int c = 0; c < 16; ++c)
                                 o[c] = __float_as_uint(fmaf(__uint_as_float(lo[c]), 0x1p-5f, __uint_as_float(o[c])));
+                        } else {
+                            tmem_ld_x16(at, o);
                         }
 #pragma unroll
                         for (int c = 0; c < 16; ++c) {
