@@ -47,18 +47,26 @@ using F2 = packed2;
 constexpr int kTok = 128;             // tokens a tile
 constexpr int kBlk = kTok * 128;      // bytes of a latent block
 constexpr int kRopeBlk = kTok * 64;   // and of the rotary part
-constexpr int kRopes = 2;
 constexpr int kQGens = 4;             // generations of query scales that may be in use at once
 constexpr int kScs = 4;               // tiles' scales
-constexpr float kTop = 6.f;           // P of the maximum itself is 2^6
-constexpr float kSlack = 2.f;         // which a score may pass by so much before the maximum is raised: P <= 2^8
+// P of the maximum itself is 2^3, and a score may pass it by 2^5 before the maximum
+// is raised (O rescaled, a few thousand cycles): with 2^6 and 2^2 that was every
+// other of the first dozen tiles of a request.
+constexpr float kTop = 3.f, kSlack = 5.f;
 constexpr float kNoMax = -1e30f;
 constexpr float kLn2f = 0.69314718055994530942f;
 
-template <int NP>
+// Shared memory decides the rate: a block is held from its load to its value
+// product, so the ring's slots are what is in flight. At 64 rows the last block
+// of a tile would wait for the value product of the tile before with seven slots
+// (a chain of 4,700 cycles a tile); with eight it does not, and they fit beside
+// one rotary slot (free again after the first two products of a tile).
+template <int NP, bool LSU>
 struct P8Cfg {
     static constexpr bool kStack = NP <= 32;            // P's parts in columns of their own
-    static constexpr int kSlots = NP == 16 ? 11 : NP == 32 ? 9 : 7;
+    static constexpr int kSlots = NP == 16 ? 11 : NP == 32 ? 9 : LSU ? 7 : 8;
+    static constexpr int kRopes = NP == 64 && !LSU ? 1 : 2;
+    static constexpr int kScW = LSU ? kTok : 16;        // scales of a tile: one for each row, or run of rows
     static constexpr int kPBufs = NP == 64 ? 1 : 2;
     static constexpr int kGroups = NP == 16 ? 1 : 2;    // softmax groups of four warps
     static constexpr int kCW = NP / kGroups;            // columns of a group
@@ -68,10 +76,15 @@ struct P8Cfg {
     static constexpr int kPBytes = 2 * NP * kTok;
     static constexpr uint32_t kPSw = kPRow == 32 ? kSw32 : kSw64;
     static constexpr int kOffRope = kSlots * kBlk;
-    static constexpr int kOffQ = kOffRope + kRopes * kRopeBlk;
+    static constexpr int kOffQ = kOffRope + kRopes * kRopeBlk;  // (swizzle atoms: all of these lie at multiples of 1024)
     static constexpr int kOffP = kOffQ + kQBytes;
     static constexpr int kOffCtrl = kOffP + kPBufs * kPBytes;
-    static constexpr int kQWarp = 4 + 4 * kGroups;      // first of the four query warps
+    static constexpr int kQWarp = 4 + 4 * kGroups;      // first of the query warps
+    // loading warps: 1 and 2, and at 16 rows, where two warps are enough for the
+    // queries, two more (a tile of 16-token pages is 40 boxes, about 75 cycles each to
+    // the warp that issues them)
+    static constexpr int kLoaders = LSU ? 0 : NP == 16 ? 4 : 2;
+    static constexpr int kQWarps = kLoaders == 4 ? 2 : 4;
     static constexpr int kThreads = 32 * (kQWarp + 4);
     static constexpr int kOCols = 4 * (kStack ? 2 * NP : NP);
     static constexpr int kColS = kOCols;                // two S buffers of 2 NP columns
@@ -80,9 +93,10 @@ struct P8Cfg {
     static_assert(kQBlk % 1024 == 0 && (2 * NP * 64) % 1024 == 0 && kPBytes % 1024 == 0, "alignment of the swizzle atoms");
 };
 
+template <class C>
 struct P8Ctrl {
-    uint64_t blk_full[12], blk_empty[12];
-    uint64_t rope_full[kRopes], rope_empty[kRopes];
+    uint64_t blk_full[C::kSlots], blk_empty[C::kSlots];
+    uint64_t rope_full[C::kRopes], rope_empty[C::kRopes];
     uint64_t s_full[2], s_free[2];
     // tile t's hand-off is p_full[t & 1], its products' end o_done[t & 1]: the
     // softmax may be a tile ahead of a slow issuer, which a single barrier's
@@ -94,21 +108,24 @@ struct P8Ctrl {
     uint32_t tmem_base;
     int abort;
     int t_begin, t_end, b0, j0;
-    alignas(16) float sc[kScs][kTok];   // scales of a tile: one for each run of rows in a page, or each row
-    alignas(16) float kq[kQGens][64];   // what turns a column's sum into log2 units (without the token's scale)
-    alignas(16) float m[64];            // running maximum (kNoMax: nothing seen yet)
-    alignas(16) float nm[64];           // kTop - m (0 where m is kNoMax)
-    alignas(16) float alpha[64];
-    alignas(16) float red[4][64];
-    alignas(16) float inv[64];
-    int unset[2];                       // a softmax group has columns without a maximum
+    int unset[2];                         // a softmax group has columns without a maximum
+    alignas(16) float sc[kScs][C::kScW];  // scales of a tile
+    alignas(16) float kq[kQGens][64];     // what turns a column's sum into log2 units (without the token's scale)
+    alignas(16) float m[64];              // running maximum (kNoMax: nothing seen yet)
+    alignas(16) float nm[64];             // kTop - m (0 where m is kNoMax)
+    alignas(16) float dy[64];             // how much nm changed; at a segment's end 1 / sum
+    alignas(16) int most[64];             // largest of a tile, as an ordered whole number (INT_MIN: not raised)
 };
 
-template <int NP>
+// (no slack for alignment: dynamic shared memory begins at a multiple of 1024,
+// which the kernel checks)
+template <int NP, bool LSU>
 constexpr int p8_smem() {
-    return P8Cfg<NP>::kOffCtrl + (static_cast<int>(sizeof(P8Ctrl)) + 15) / 16 * 16 + 1024;
+    return P8Cfg<NP, LSU>::kOffCtrl + (static_cast<int>(sizeof(P8Ctrl<P8Cfg<NP, LSU>>)) + 15) / 16 * 16;
 }
-static_assert(p8_smem<16>() <= 232448 && p8_smem<32>() <= 232448 && p8_smem<64>() <= 232448, "shared memory");
+static_assert(p8_smem<16, false>() <= 232448 && p8_smem<32, false>() <= 232448 && p8_smem<64, false>() <= 232448 &&
+                  p8_smem<16, true>() <= 232448 && p8_smem<32, true>() <= 232448 && p8_smem<64, true>() <= 232448,
+              "shared memory");
 
 // Page and slot of token tok of the request with this table row; page 0 and a
 // flag for an entry outside the pool or the row.
@@ -133,6 +150,34 @@ __device__ __forceinline__ float p8_scale(const DecodeParams& p, int page) {
 
 __device__ __forceinline__ void p8_cp16(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// N columns (16 or 32) of 32 lanes to one number each: lane c gets column c's (16
+// columns: lanes c and c + 16). Each step hands half of what a lane holds to
+// its partner, N - 1 or N shuffles in all; a redux for each column took some 100 cycles.
+template <int N, class Op>
+__device__ __forceinline__ float across_lanes(const F2 (&y)[N / 2], int lane, Op op) {
+    float v[N / 2];
+    {
+        constexpr int h = N / 2;
+        const bool up = (lane & h) != 0;
+#pragma unroll
+        for (int c = 0; c < h; c += 2) {
+            const float2 lo = un2(y[c / 2]), hi = un2(y[(c + h) / 2]);
+            v[c] = op(up ? hi.x : lo.x, __shfl_xor_sync(0xffffffffu, up ? lo.x : hi.x, h));
+            v[c + 1] = op(up ? hi.y : lo.y, __shfl_xor_sync(0xffffffffu, up ? lo.y : hi.y, h));
+        }
+    }
+#pragma unroll
+    for (int h = N / 4; h > 0; h >>= 1) {
+        const bool up = (lane & h) != 0;
+#pragma unroll
+        for (int c = 0; c < h; ++c) {
+            const float lo = v[c], hi = v[c + h];
+            v[c] = op(up ? hi : lo, __shfl_xor_sync(0xffffffffu, up ? lo : hi, h));
+        }
+    }
+    return N == 16 ? op(v[0], __shfl_xor_sync(0xffffffffu, v[0], 16)) : v[0];
 }
 
 // 16 columns from each of two places in TMEM, one wait for both.
@@ -163,18 +208,18 @@ __device__ __forceinline__ uint32_t p8_codes(float a, float b) {
 }
 
 template <int NP, bool LSU>
-__global__ void __launch_bounds__(P8Cfg<NP>::kThreads, 1)
+__global__ void __launch_bounds__(P8Cfg<NP, LSU>::kThreads, 1)
     mla_decode_page8_kernel(const __grid_constant__ DecodeMaps maps, const DecodeParams p) {
-    using C = P8Cfg<NP>;
+    using C = P8Cfg<NP, LSU>;
+    using Ctrl = P8Ctrl<C>;
     using It = TileItT<7>;
-    constexpr int CW = C::kCW;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    constexpr int CW = C::kCW, kRopes = C::kRopes;
+    extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t* ring = smem;
     uint8_t* rope_ring = smem + C::kOffRope;
     uint8_t* qs = smem + C::kOffQ;
     uint8_t* pbufs = smem + C::kOffP;
-    P8Ctrl* ctrl = reinterpret_cast<P8Ctrl*>(smem + C::kOffCtrl);
+    Ctrl* ctrl = reinterpret_cast<Ctrl*>(smem + C::kOffCtrl);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = blockIdx.x, G = gridDim.x, gy = blockIdx.y;
     volatile int* abort = &ctrl->abort;
@@ -185,7 +230,7 @@ __global__ void __launch_bounds__(P8Cfg<NP>::kThreads, 1)
             mbar_init(&ctrl->blk_empty[i], 1);
         }
         for (int i = 0; i < kRopes; ++i) {
-            mbar_init(&ctrl->rope_full[i], LSU ? 4 : 1);
+            mbar_init(&ctrl->rope_full[i], LSU ? 4 : C::kLoaders);
             mbar_init(&ctrl->rope_empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -195,10 +240,9 @@ __global__ void __launch_bounds__(P8Cfg<NP>::kThreads, 1)
             mbar_init(&ctrl->o_done[i], 1);
             mbar_init(&ctrl->fin[i], 1);
         }
-        for (int i = 0; i < kQGens; ++i) mbar_init(&ctrl->q_full[i], 4);
+        for (int i = 0; i < kQGens; ++i) mbar_init(&ctrl->q_full[i], C::kQWarps);
         mbar_init(&ctrl->q_empty, 1);
         for (int i = 0; i < kScs; ++i) mbar_init(&ctrl->sc_full[i], LSU ? 4 : 1);
-        for (int c = 0; c < 64; ++c) ctrl->nm[c] = 0.f;
         ctrl->abort = 0;
         fence_mbar_init();
     }
@@ -228,11 +272,17 @@ __global__ void __launch_bounds__(P8Cfg<NP>::kThreads, 1)
             ctrl->j0 = r.j0;
         }
     }
+    if (threadIdx.x >= 128 && threadIdx.x < 192) {
+        ctrl->nm[threadIdx.x - 128] = 0.f;
+        ctrl->most[threadIdx.x - 128] = INT_MIN;
+    }
+    const bool misplaced = (smem_u32(smem) & 1023u) != 0;  // (cannot happen)
+    if (misplaced && threadIdx.x == 0) atomicOr(status_rec(p), kErrWaitTimeout);
     __syncthreads();
     if (threadIdx.x == 0) griddep_launch_dependents();  // the merge grid may be scheduled as CTAs retire
     tc_fence_after();
     const uint32_t tmem = ctrl->tmem_base;
-    const int ntiles = ctrl->t_end - ctrl->t_begin;
+    const int ntiles = misplaced ? 0 : ctrl->t_end - ctrl->t_begin;
     if (ntiles == 0 && ctrl->j0 > 0 && threadIdx.x < 64) {
         // an empty range strictly inside request b0 (more workers than tiles):
         // the merge of b0 counts this worker's slot, so mark it empty
@@ -241,19 +291,19 @@ __global__ void __launch_bounds__(P8Cfg<NP>::kThreads, 1)
     It it;
     if (ntiles > 0) it.init(p.seq_lens, ctrl->b0, ctrl->j0);
 
-    // the query rows of request b in this row group as h and l codes, and their scales; four warps
+    // the query rows of request b in this row group as h and l codes, and their scales; the query warps
     auto load_q = [&](int b, int gen) {
         const int wq = warp - C::kQWarp;
         const int rows = req_rows_in_group(p, b, gy);
         const int64_t row0 = req_row0(p, b) + gy * 64;
         uint8_t* qr = qs + 4 * C::kQBlk;
 #pragma unroll 1
-        for (int r4 = wq; r4 < NP; r4 += 16) {  // four rows at a time, loads first
+        for (int r4 = wq; r4 < NP; r4 += 4 * C::kQWarps) {  // four rows at a time, loads first
             uint4 x[4][2];
             uint32_t e[4];
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
-                const int r = r4 + 4 * n;
+                const int r = r4 + C::kQWarps * n;
                 const uint4 z = make_uint4(0u, 0u, 0u, 0u);
                 // lane holds latent values 16 lane .. 16 lane + 15 and rotary values 2 lane, 2 lane + 1
                 const uint4* ql = reinterpret_cast<const uint4*>(p.q_lat + (row0 + r) * kD) + 2 * lane;
@@ -263,7 +313,7 @@ __global__ void __launch_bounds__(P8Cfg<NP>::kThreads, 1)
             }
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
-                const int r = r4 + 4 * n;
+                const int r = r4 + C::kQWarps * n;
                 const __nv_bfloat162* xb = reinterpret_cast<const __nv_bfloat162*>(x[n]);
                 const float2 pe = make_float2(__uint_as_float(e[n] << 16), __uint_as_float(e[n] & 0xFFFF0000u));
                 float mx = fmaxf(fabsf(pe.x), fabsf(pe.y));
@@ -392,7 +442,7 @@ __global__ void __launch_bounds__(P8Cfg<NP>::kThreads, 1)
             // --------------------------------------------------- value product
             const bool leader = elect_lane();
             const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-            const uint32_t id = idesc_f8(128, C::kPRow, 0, 0, true);
+            const uint32_t id = idesc_f8(128, C::kPRow, 0, 0, true), id_l = idesc_f8(128, C::kPRow, 0, 1, true);
             const uint64_t dring = smem_desc(smem_u32(ring), kBlk, 1024, kSw128);
             const uint64_t dp0 = smem_desc(smem_u32(pbufs), C::kPBytes, 8 * C::kPRow, C::kPSw);
             uint32_t slot = 0;
@@ -414,7 +464,7 @@ __global__ void __launch_bounds__(P8Cfg<NP>::kThreads, 1)
                             // tokens 32 kk .. 32 kk + 31
                             umma_f8(tO, da + kk * (32 * 128 >> 4), dp + kk * (32 * C::kPRow >> 4), id, !(fresh && kk == 0));
                             if (!C::kStack)
-                                umma_f8(tO, da + kk * (32 * 128 >> 4), dp + ((NP * kTok + kk * 32 * C::kPRow) >> 4), id, 1u);
+                                umma_f8(tO, da + kk * (32 * 128 >> 4), dp + ((NP * kTok + kk * 32 * C::kPRow) >> 4), id_l, 1u);
                         }
                         umma_commit(&ctrl->blk_empty[slot]);
                     }
@@ -431,27 +481,40 @@ __global__ void __launch_bounds__(P8Cfg<NP>::kThreads, 1)
                 }
                 drain_mma(&ctrl->fin[1]);
             }
-        } else if (!LSU && (warp == 1 || warp == 2)) {
+        } else if (!LSU && (warp == 1 || warp == 2 || warp >= C::kQWarp + C::kQWarps)) {
             // ------------------------------------------------------------ loads
             // Lane r owns run r of a tile: BR rows that lie next to each other in a page.
-            // Warp 1 loads blocks 0 and 1 and the rotary part, warp 2 blocks 2 and 3 (a tile
-            // of 16-token pages is 40 boxes). A refill waits for the block 1 ring before by
-            // its parity, which could not tell it from the one 2 rings before; but the warp's
-            // last wait was for block u - 1 - kSlots or later, and products end in order, so
-            // that one is long done.
-            const int kb0 = warp == 1 ? 0 : 2;
+            // Each loading warp has its blocks of every tile and a share of the rotary part's
+            // runs. A refill waits for the block 1 ring before by its parity, which could not
+            // tell it from the one 2 rings before; but the warp's last wait was for a block
+            // at most 4 earlier, and products end in order, so that one is long done.
+            constexpr int kMine = LSU ? 4 : 4 / C::kLoaders;  // blocks of a warp
+            const int me = warp < 4 ? warp - 1 : 2 + warp - C::kQWarp - C::kQWarps, kb0 = me * kMine;
             const int BR = p.run_rows;
             const uint64_t pol = gridDim.y > 1 ? l2_policy_evict_normal() : l2_policy_evict_first();
             bool bad = false, ok = true;
             int site = 0, i = 0;
-            auto run_of = [&](const It& t, int& page) -> int {
-                page = 0;
-                const int valid = min(kTok, t.T - t.j * kTok);
-                if (lane * BR >= valid) return 0;
-                return p8_slot(p, p.block_table + static_cast<int64_t>(t.b) * p.bt_stride, t.j * kTok + lane * BR, page, bad);
+            // the table is read two tiles ahead and the scales one, so that neither load is
+            // waited for where it is made
+            auto entry = [&](const It& t) -> int {
+                const int tok = t.j * kTok + lane * BR, pi = tok / p.page_size;
+                return tok < t.T && lane * BR < kTok && pi < p.bt_cols
+                           ? __ldg(p.block_table + static_cast<int64_t>(t.b) * p.bt_stride + pi) : -1;
             };
-            int page_next, y_next = run_of(it, page_next);
+            auto run_of = [&](const It& t, int pg, int& page) -> int {
+                page = 0;
+                const int tok = t.j * kTok + lane * BR;
+                if (lane * BR >= min(kTok, t.T - t.j * kTok)) return 0;
+                if (pg < 0 || (static_cast<int64_t>(pg) + 1) * p.page_size > p.num_slots) bad = true;
+                else page = pg;
+                const int64_t s = static_cast<int64_t>(page) * p.page_size + tok % p.page_size;
+                return static_cast<int>(s < p.num_slots ? s : 0);
+            };
+            int page_next, y_next = run_of(it, entry(it), page_next);
             float s_next = warp == 1 ? p8_scale(p, page_next) : 1.f;
+            It it1 = it;  // the tile after the one that is loaded
+            if (ntiles > 1) it1.next(p.seq_lens, p.B);
+            int e_next = ntiles > 1 ? entry(it1) : -1;
             uint32_t armed = 0;  // blocks whose barrier this warp has armed
             int rope_armed = 0;
             for (; i < ntiles && ok; ++i) {
@@ -465,25 +528,33 @@ __global__ void __launch_bounds__(P8Cfg<NP>::kThreads, 1)
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&ctrl->sc_full[i % kScs]);
                 }
-                it.next(p.seq_lens, p.B);
+                it = it1;
                 if (i + 1 < ntiles) {
-                    y_next = run_of(it, page_next);
+                    const int e = e_next;
+                    if (i + 2 < ntiles) {
+                        it1.next(p.seq_lens, p.B);
+                        e_next = entry(it1);
+                    }
+                    y_next = run_of(it, e, page_next);
                     if (warp == 1) s_next = p8_scale(p, page_next);
                 }
-                if (warp == 1) {
+                {
                     const int rr = i % kRopes;
                     if (i >= kRopes && !__all_sync(0xffffffffu, mbar_wait(&ctrl->rope_empty[rr], ((i / kRopes) - 1) & 1, abort))) {
                         ok = false;
                         site = kSiteTmaRopeEmpty;
                         break;
                     }
-                    if (lane == 0) mbar_arrive_expect_tx(&ctrl->rope_full[rr], static_cast<uint32_t>(nruns * BR * 64));
+                    // the runs of lanes me, me + kLoaders, ..
+                    constexpr int kL = C::kLoaders > 0 ? C::kLoaders : 1;
+                    const int share = (nruns - me + kL - 1) / kL;
+                    if (lane == 0) mbar_arrive_expect_tx(&ctrl->rope_full[rr], static_cast<uint32_t>(share * BR * 64));
                     __syncwarp();
                     rope_armed = i + 1;
-                    if (lane < nruns)
+                    if (lane < nruns && lane % kL == me)
                         tma_load_2d(rope_ring + rr * kRopeBlk + lane * BR * 64, &maps.rope, &ctrl->rope_full[rr], kD, y, pol);
                 }
-                for (int kb = kb0; kb < kb0 + 2; ++kb) {
+                for (int kb = kb0; kb < kb0 + kMine; ++kb) {
                     const uint32_t u = 4u * i + kb, slot = u % C::kSlots, fill = u / C::kSlots;
                     if (fill > 0 && !__all_sync(0xffffffffu, mbar_wait(&ctrl->blk_empty[slot], (fill - 1) & 1, abort))) {
                         ok = false;
@@ -513,11 +584,11 @@ __global__ void __launch_bounds__(P8Cfg<NP>::kThreads, 1)
                 };
                 const uint32_t from = armed > static_cast<uint32_t>(C::kSlots) ? armed - C::kSlots : 0;
                 for (uint32_t u = from; u < armed; ++u)
-                    if ((u & 2) == static_cast<uint32_t>(kb0)) land(&ctrl->blk_full[u % C::kSlots], (u / C::kSlots) & 1);
+                    if ((u & 3) / kMine == static_cast<uint32_t>(me)) land(&ctrl->blk_full[u % C::kSlots], (u / C::kSlots) & 1);
                 for (int k = max(0, rope_armed - kRopes); k < rope_armed; ++k) land(&ctrl->rope_full[k % kRopes], (k / kRopes) & 1);
             }
             if (bad) atomicOr(status_rec(p), kErrBadBlock);
-        } else if (warp >= C::kQWarp) {
+        } else if (warp >= C::kQWarp && warp < C::kQWarp + C::kQWarps) {
             // ---------------------------------------------------------- queries
             // (and LSU: the rows, warp w's being 32 w .. 32 w + 31 of a tile)
             bool ok = true, bad = false;
@@ -712,31 +783,25 @@ __global__ void __launch_bounds__(P8Cfg<NP>::kThreads, 1)
                     top = fmaxf(top, fmaxf(v.x, v.y));
                 }
                 if (named_bar_or(bar, 128, fresh || failed || unset || top > kTop + kSlack)) {
-                    // the maxima move: every column's goes to the tile's if that is larger
-                    int most[CW];
-#pragma unroll
-                    for (int c = 0; c < CW; ++c) {
-                        // order-preserving whole numbers; NaN counts as nothing
-                        const float2 v = un2(y[c / 2]);
-                        const int k = __float_as_int(fmaxf(c & 1 ? v.y : v.x, kNoMax));
-                        most[c] = __reduce_max_sync(0xffffffffu, k < 0 ? k ^ 0x7FFFFFFF : k);
+                    // maxima move: of a fresh segment all columns', otherwise of those that a
+                    // score passes by more than kSlack. Lane c finds its warp's largest of
+                    // column c (as an ordered whole number; NaN counts as nothing).
+                    const float best = across_lanes<CW>(y, lane, [](float a, float b) { return fmaxf(a, b); });
+                    if (lane < CW && (fresh || unset || best > kTop + kSlack)) {
+                        const int k = __float_as_int(fmaxf(best, kNoMax));
+                        atomicMax(&ctrl->most[cb + lane], k < 0 ? k ^ 0x7FFFFFFF : k);
                     }
-                    if (lane == 0) {
-#pragma unroll
-                        for (int c = 0; c < CW; ++c) ctrl->red[wq][cb + c] = __int_as_float(most[c] < 0 ? most[c] ^ 0x7FFFFFFF : most[c]);
-                    }
-                    float before[CW];  // the kTop - m that y holds
-#pragma unroll
-                    for (int c = 0; c < CW; ++c) before[c] = fresh ? 0.f : ctrl->nm[cb + c];
                     named_bar_sync(bar, 128);
                     if (tk < CW) {
-                        const int c = cb + tk;
+                        const int c = cb + tk, k = ctrl->most[c];
+                        ctrl->most[c] = INT_MIN;
                         const float old = fresh ? kNoMax : ctrl->m[c], shift = fresh ? 0.f : ctrl->nm[c];
-                        const float t = fmaxf(fmaxf(ctrl->red[0][c], ctrl->red[1][c]), fmaxf(ctrl->red[2][c], ctrl->red[3][c]));
+                        const float t = k == INT_MIN ? kNoMax : __int_as_float(k < 0 ? k ^ 0x7FFFFFFF : k);
                         const float m = t > kNoMax ? fmaxf(old, t - shift) : old;
+                        const float nm = m > kNoMax ? kTop - m : 0.f;
                         ctrl->m[c] = m;
-                        ctrl->nm[c] = m > kNoMax ? kTop - m : 0.f;
-                        ctrl->alpha[c] = ex2(old - m);
+                        ctrl->nm[c] = nm;
+                        ctrl->dy[c] = nm - shift;
                         const unsigned none = __ballot_sync(CW == 32 ? 0xffffffffu : 0xffffu, !(m > kNoMax));
                         if (tk == 0) ctrl->unset[grp] = none != 0;
                     }
@@ -746,36 +811,57 @@ __global__ void __launch_bounds__(P8Cfg<NP>::kThreads, 1)
                         wait(&ctrl->o_done[(i - 1) & 1], ((i - 1) >> 1) & 1, kSiteORescale);
                         tc_fence_after();
                         __syncwarp();
-#pragma unroll 1
-                        for (int part = 0; part < (C::kStack ? 2 : 1); ++part)
-#pragma unroll 1
-                            for (int mt = 0; mt < 4; ++mt)
-#pragma unroll 1
-                                for (int c0 = 0; c0 < CW; c0 += 16) {
-                                    const uint32_t at = tmem + lane_base + mt * C::kPRow + part * NP + cb + c0;
-                                    uint32_t o[16];
-                                    tmem_ld_x16(at, o);
+                    }
 #pragma unroll
-                                    for (int c = 0; c < 16; ++c)
-                                        o[c] = __float_as_uint(__uint_as_float(o[c]) * ctrl->alpha[cb + c0 + c]);
-                                    tmem_st_x16(at, o);
+                    for (int c0 = 0; c0 < CW; c0 += 16) {
+                        float a[16];
+                        bool moved = false;
+#pragma unroll
+                        for (int c = 0; c < 16; c += 4) {
+                            const float4 d = *reinterpret_cast<const float4*>(ctrl->dy + cb + c0 + c);
+                            y[(c0 + c) / 2] = add2(y[(c0 + c) / 2], f2(d.x, d.y));
+                            y[(c0 + c) / 2 + 1] = add2(y[(c0 + c) / 2 + 1], f2(d.z, d.w));
+                            a[c] = d.x;
+                            a[c + 1] = d.y;
+                            a[c + 2] = d.z;
+                            a[c + 3] = d.w;
+                            moved = moved || fminf(fminf(d.x, d.y), fminf(d.z, d.w)) < 0.f;
+                        }
+                        if (fresh || !moved) continue;
+                        // (a column that had nothing yet may go up; there is nothing to scale)
+#pragma unroll
+                        for (int c = 0; c < 16; ++c) a[c] = ex2(fminf(a[c], 0.f));
+#pragma unroll
+                        for (int c = 0; c < 16; c += 2) l[(c0 + c) / 2] = mul2(l[(c0 + c) / 2], f2(a[c], a[c + 1]));
+                        if constexpr (NP == 16) {
+                            // all of O is the group's: 128 columns, h and l of each M-tile side by side
+#pragma unroll 1
+                            for (int half = 0; half < 2; ++half) {
+                                uint32_t o[64];
+                                tmem_ld_x64(tmem + lane_base + half * 64, o);
+#pragma unroll
+                                for (int c = 0; c < 64; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * a[c & 15]);
+                                tmem_st_x64(tmem + lane_base + half * 64, o);
+                            }
+                        } else {
+#pragma unroll 1
+                            for (int mt = 0; mt < 4; ++mt) {
+                                const uint32_t at = tmem + lane_base + mt * C::kPRow + cb + c0;
+                                uint32_t o[16], u[16];
+                                if constexpr (C::kStack) p8_ld_pair(at, at + NP, o, u);
+                                else tmem_ld_x16(at, o);
+#pragma unroll
+                                for (int c = 0; c < 16; ++c) {
+                                    o[c] = __float_as_uint(__uint_as_float(o[c]) * a[c]);
+                                    if (C::kStack) u[c] = __float_as_uint(__uint_as_float(u[c]) * a[c]);
                                 }
+                                tmem_st_x16(at, o);
+                                if (C::kStack) tmem_st_x16(at + NP, u);
+                            }
+                        }
                         tmem_wait_st();
                     }
-#pragma unroll
-                    for (int c = 0; c < CW; c += 2) {
-                        const float2 a = *reinterpret_cast<const float2*>(ctrl->alpha + cb + c);
-                        const float2 nm = *reinterpret_cast<const float2*>(ctrl->nm + cb + c);
-                        if (!fresh) l[c / 2] = mul2(l[c / 2], f2(a.x, a.y));
-                        float2 v = un2(y[c / 2]);
-                        v.x += nm.x - before[c];
-                        v.y += nm.y - before[c + 1];
-                        y[c / 2] = f2(v.x, v.y);
-                    }
                 }
-                // P and its place: free when the value product that read it last is done
-                if (i >= C::kPBufs)
-                    wait(&ctrl->o_done[(i - C::kPBufs) & 1], ((i - C::kPBufs) >> 1) & 1, kSiteOPbuf);
                 uint32_t hc[CW / 4], lc[CW / 4];
                 const F2 inv2 = f2(inv_vs, inv_vs);
 #pragma unroll
@@ -789,7 +875,8 @@ __global__ void __launch_bounds__(P8Cfg<NP>::kThreads, 1)
                     const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(h), __NV_E4M3);
                     __half2 rest = __hsub2(ph, *reinterpret_cast<const __half2*>(&hr));
                     if (C::kStack) rest = __hmul2(rest, __float2half2_rn(32.f));
-                    const uint32_t lo = __nv_cvt_halfraw2_to_fp8x2(*reinterpret_cast<const __half2_raw*>(&rest), __NV_SATFINITE, __NV_E4M3);
+                    const uint32_t lo = __nv_cvt_halfraw2_to_fp8x2(*reinterpret_cast<const __half2_raw*>(&rest), __NV_SATFINITE,
+                                                                   C::kStack ? __NV_E4M3 : __NV_E5M2);
                     if (c & 2) {
                         hc[c >> 2] |= h << 16;
                         lc[c >> 2] |= lo << 16;
@@ -798,6 +885,9 @@ __global__ void __launch_bounds__(P8Cfg<NP>::kThreads, 1)
                         lc[c >> 2] = lo & 0xFFFFu;
                     }
                 }
+                // P's place is free when the value product that read it last is done
+                if (i >= C::kPBufs)
+                    wait(&ctrl->o_done[(i - C::kPBufs) & 1], ((i - C::kPBufs) >> 1) & 1, kSiteOPbuf);
                 uint8_t* prow = pbufs + (i % C::kPBufs) * C::kPBytes + tk * C::kPRow;
                 const int sw = swz_p(tk, C::kPSw);
 #pragma unroll
@@ -824,25 +914,25 @@ __global__ void __launch_bounds__(P8Cfg<NP>::kThreads, 1)
                 it.next(p.seq_lens, p.B);
                 if (i + 1 < ntiles && j + 1 < tiles) continue;
                 // ------------------------------------------- the segment's end
-                float sum[CW];
-#pragma unroll
-                for (int c = 0; c < CW; ++c) {
-                    const float2 v = un2(l[c / 2]);
-                    sum[c] = warp_sum(c & 1 ? v.y : v.x);
-                }
-                if (lane == 0) {
-#pragma unroll
-                    for (int c = 0; c < CW; ++c) ctrl->red[wq][cb + c] = sum[c];
-                }
+                // The warps' sums meet in the group's own part of P, which the last value
+                // product has read: CW / 4 numbers in each row.
+                wait(&ctrl->o_done[i & 1], (i >> 1) & 1, kSiteOFinal);
+                auto sums = [&](int w, int c) -> float* {
+                    const int idx = w * CW + c, row = idx / (CW / 4), at = idx % (CW / 4);
+                    return reinterpret_cast<float*>(pbufs + (i % C::kPBufs) * C::kPBytes + row * C::kPRow +
+                                                    (((cb / 16 + at / 4) ^ swz_p(row, C::kPSw)) << 4)) + at % 4;
+                };
+                const float sum = across_lanes<CW>(l, lane, [](float a, float b) { return a + b; });
+                if (lane < CW) *sums(wq, lane) = sum;
                 named_bar_sync(bar, 128);
                 const bool whole = start_j == 0 && j + 1 == tiles;
                 const int64_t row0 = req_row0(p, b) + gy * 64;
                 const int64_t slot0 = (static_cast<int64_t>(gy) * p.SPG + g + b) * 64;
                 if (tk < CW) {
                     const int c = cb + tk;
-                    const float s = ctrl->red[0][c] + ctrl->red[1][c] + ctrl->red[2][c] + ctrl->red[3][c];
+                    const float s = *sums(0, tk) + *sums(1, tk) + *sums(2, tk) + *sums(3, tk);
                     // (a NaN sum is not nothing)
-                    ctrl->inv[c] = s == 0.f ? 0.f : 1.f / s;
+                    ctrl->dy[c] = s == 0.f ? 0.f : 1.f / s;
                     const float L = s == 0.f ? -INFINITY : (ctrl->m[c] - kTop + log2f(s)) * kLn2f;
                     if (c < rows) {
                         if (whole) p.lse[row0 + c] = L;
@@ -850,7 +940,6 @@ __global__ void __launch_bounds__(P8Cfg<NP>::kThreads, 1)
                         else p.part_lse[slot0 + c] = L != L ? INFINITY : L;
                     }
                 }
-                wait(&ctrl->o_done[i & 1], (i >> 1) & 1, kSiteOFinal);
                 named_bar_sync(bar, 128);
                 tc_fence_after();
                 __syncwarp();
@@ -874,7 +963,7 @@ __global__ void __launch_bounds__(P8Cfg<NP>::kThreads, 1)
                         for (int c = 0; c < 16; ++c) {
                             const int r = cb + c0 + c;
                             if (r >= rows) continue;
-                            const float v = __uint_as_float(o[c]) * ctrl->inv[r];
+                            const float v = __uint_as_float(o[c]) * ctrl->dy[r];
                             if (!whole) p.part_o[(slot0 + r) * kD + d] = v;
                             else if (p.out_f32) static_cast<float*>(p.out)[(row0 + r) * kD + d] = v;
                             else static_cast<__nv_bfloat16*>(p.out)[(row0 + r) * kD + d] = __float2bfloat16_rn(v);
@@ -902,10 +991,10 @@ cudaError_t go(const DecodeMaps& maps, const DecodeParams& p, int W, int GY, cud
     static std::atomic<uint64_t> done;
     const auto k = mla_decode_page8_kernel<NP, LSU>;
     const cudaError_t e = attribute_once(done, reinterpret_cast<const void*>(k), cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         p8_smem<NP>());
+                                         p8_smem<NP, LSU>());
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr[1];
-    cudaLaunchConfig_t cfg = pdl_config(dim3(W, GY), P8Cfg<NP>::kThreads, p8_smem<NP>(), stream, attr);
+    cudaLaunchConfig_t cfg = pdl_config(dim3(W, GY), P8Cfg<NP, LSU>::kThreads, p8_smem<NP, LSU>(), stream, attr);
     return cudaLaunchKernelEx(&cfg, k, maps, p);
 }
 

@@ -399,6 +399,11 @@ __device__ __forceinline__ packed2 mul2(packed2 a, packed2 b) {
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
+__device__ __forceinline__ packed2 add2(packed2 a, packed2 b) {
+    packed2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
 __device__ __forceinline__ packed2 fma2(packed2 a, packed2 b, packed2 c) {
     packed2 r;
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
