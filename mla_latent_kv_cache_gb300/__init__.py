@@ -23,6 +23,8 @@ table of angles that mla_rope and mla_cache_append take.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import math
 import os
 import threading
@@ -31,6 +33,7 @@ import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_lib", "libmla_gb300.so")
+BIND_PATH = os.path.join(_HERE, "_lib", "_mla_bind.so")
 
 MLA_OK, MLA_ERR_INVALID_ARG, MLA_ERR_UNSUPPORTED, MLA_ERR_WORKSPACE, MLA_ERR_CUDA = 0, -1, -2, -3, -4
 MLA_CACHE_BF16_576, MLA_CACHE_FP8_DS_MLA_656, MLA_CACHE_FP8_PAGE_576 = 0, 1, 2
@@ -39,6 +42,8 @@ STATUS_WAIT_TIMEOUT, STATUS_BAD_BLOCK = 1, 2
 
 _lock = threading.Lock()
 _lib = None
+_bind = None       # the checks of the short calls (csrc/bind.cpp)
+_addresses = {}    # the entry points that it calls
 
 
 class MlaError(RuntimeError):
@@ -115,8 +120,21 @@ def load() -> ctypes.CDLL:
             lib.mla_decode_fp8_page.argtypes = [vp, vp, i64, vp, vp, i64, i32, vp, i64, i64, vp, vp, i32, i32, i32, f32,
                                                 vp, i32, vp, vp, sz, i32, vp]
             lib.mla_decode_fp8_page.restype = i32
+            _load_bind(lib)
             _lib = lib
     return _lib
+
+
+def _load_bind(lib) -> None:
+    global _bind
+    if not os.path.exists(BIND_PATH):
+        raise ImportError(f"{BIND_PATH} not built; run: python -c 'import __graft_entry__ as g; g.build()'")
+    spec = importlib.util.spec_from_loader("_mla_bind", importlib.machinery.ExtensionFileLoader("_mla_bind", BIND_PATH))
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    for name in ("mla_rope", "mla_cache_append", "mla_decode_fp8_page"):
+        _addresses[name] = ctypes.cast(getattr(lib, name), ctypes.c_void_p).value
+    _bind = mod
 
 
 # the current stream's handle without a Stream object around it (a few microseconds a call)
@@ -435,8 +453,42 @@ def _row_bytes(where, cache_kind, lat_dim) -> int:
     return rb
 
 
+# the current device's number without a look at whether CUDA is up (it is asked where a CUDA tensor is at hand)
+_get_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
 def _current_device() -> int:
-    return torch.cuda.current_device()
+    return torch.cuda.current_device() if _get_device is None else _get_device()
+
+
+def _entry(name):
+    """A library's entry point for the compiled checks: its address, or what stands in for it."""
+    lib = load()
+    return _addresses[name] if lib is _lib else getattr(lib, name)
+
+
+def _place(where, first, names, tensors, stream):
+    """The device that a call runs on, and its stream's handle."""
+    if not _is_cuda(first):
+        _here(where, names, tensors)
+    dev = _current_device()
+    if stream is None and dev >= 0 and _raw_stream is not None:
+        return dev, _raw_stream(dev)
+    return dev, _stream(stream)
+
+
+def _answered(where, answer, names, tensors, rest=()) -> None:
+    """What the compiled checks said, if not that all is well."""
+    if isinstance(answer, str):
+        _refuse(where, answer)
+    if answer is not None:
+        _check(answer, where)
+        return
+    _here(where, names, tensors)  # says which tensor is missing or elsewhere
+    for name, t in rest:
+        if t is not None and (not _is_cuda(t) or t.device != tensors[0].device):
+            _refuse(where, f"{name} must be a CUDA tensor on {tensors[0].device}")
+    _refuse(where, "the tensors must be strided CUDA tensors on the current device")
 
 
 def _here(where, names, tensors) -> None:
@@ -693,28 +745,12 @@ def mla_rope(x, positions, steps, out, interleaved: bool = False, mscale: float 
     """Rotary positions (include/mla.h): x and out [T, H, R] bf16 or fp32 with
     contiguous last dimensions (views of wider heads, or one and the same tensor),
     positions int32 [T], steps int64 [R / 2] (rope_steps; negated for the way back)."""
-    where = "mla_rope"
-    _here(where, _ROPE_NAMES, (x, positions, steps, out, None))
-    shape = x.shape
-    if len(shape) != 3:
-        _refuse(where, "x must be [T, H, R]")
-    T, H, R = shape
-    f32 = x.dtype is torch.float32
-    if not f32 and x.dtype is not torch.bfloat16:
-        _refuse(where, "x must be bf16 or fp32")
-    if out.shape != shape or out.dtype is not x.dtype:
-        _refuse(where, f"out must be a {x.dtype} tensor of x's shape")
-    if R < 2 or R % 2:
-        _refuse(where, f"{R} values a head: an even number is rotated")
-    sx, so = x.stride(), out.stride()
-    if sx[2] != 1 or so[2] != 1:
-        _refuse(where, "x and out must have contiguous last dimensions")
-    if positions.dtype is not torch.int32 or positions.shape != (T,) or not positions.is_contiguous():
-        _refuse(where, f"positions must be contiguous int32 [{T}]")
-    if steps.dtype is not torch.int64 or steps.shape != (R // 2,) or not steps.is_contiguous():
-        _refuse(where, f"steps must be contiguous int64 [{R // 2}]")
-    _check(load().mla_rope(x.data_ptr(), sx[0], sx[1], positions.data_ptr(), steps.data_ptr(), T, H, R, 1 if f32 else 0,
-                           1 if interleaved else 0, float(mscale), out.data_ptr(), so[0], so[1], _stream(stream)), where)
+    where, tensors = "mla_rope", (x, positions, steps, out, None)
+    dev, s = _place(where, x, _ROPE_NAMES, tensors, stream)
+    entry = _entry(where)
+    st = _bind.rope(entry, s, dev, x, positions, steps, out, interleaved, mscale)
+    if st != 0:
+        _answered(where, st, _ROPE_NAMES, tensors)
 
 
 _APPEND_NAMES = ("latent", "k_pe", "cu_new_lens", "seq_lens", "block_table", "cache", "-")
@@ -731,71 +767,14 @@ def mla_cache_append(latent, k_pe, cu_new_lens, seq_lens, block_table, page_size
     bf16 [lat_dim]; scales fp32 [pages] for MLA_CACHE_FP8_PAGE_576; rows bf16
     [total, >= lat_dim + 64] takes (latent, key) besides. `status` (a device int32
     tensor) collects status bits."""
-    where = "mla_cache_append"
-    _here(where, _APPEND_NAMES, (latent, k_pe, cu_new_lens, seq_lens, block_table, cache, None))
-    dev = latent.get_device()
-    for name, t in (("steps", steps), ("positions", positions), ("norm_weight", norm_weight), ("scales", scales),
-                    ("rows", rows), ("status", status)):
-        if t is not None and (not _is_cuda(t) or t.get_device() != dev):
-            _refuse(where, f"{name} must be a CUDA tensor on {latent.device}")
-    bf16, i32 = torch.bfloat16, torch.int32
-    lat_dim, page_size = int(lat_dim), int(page_size)
-    if cache_kind == MLA_CACHE_FP8_PAGE_576:
-        rb = 576
-        if lat_dim != 512:
-            _refuse(where, "rows of this cache kind have lat_dim 512")
-    else:
-        rb = _row_bytes(where, cache_kind, lat_dim)
-    l_shape, l_strides, k_strides = latent.shape, latent.stride(), k_pe.stride()
-    if latent.dtype is not bf16 or len(l_shape) != 2 or l_shape[1] != lat_dim or l_strides[1] != 1:
-        _refuse(where, f"latent must be bf16 [total, {lat_dim}] with contiguous rows")
-    total = l_shape[0]
-    if k_pe.dtype is not bf16 or k_pe.shape != (total, 64) or k_strides[1] != 1:
-        _refuse(where, f"k_pe must be bf16 [{total}, 64] with contiguous rows")
-    if page_size < 1:
-        _refuse(where, f"page_size {page_size}")
-    if not cache.is_contiguous():
-        _refuse(where, "cache must be contiguous")
-    if block_table.dtype is not i32 or block_table.dim() != 2 or block_table.stride(1) != 1:
-        _refuse(where, "block_table must be a 2-D int32 tensor with contiguous rows")
-    if seq_lens.dtype is not i32 or not seq_lens.is_contiguous():
-        _refuse(where, "seq_lens must be contiguous int32")
-    B = seq_lens.numel()
-    if cu_new_lens.dtype is not i32 or not cu_new_lens.is_contiguous() or cu_new_lens.numel() != B + 1:
-        _refuse(where, f"cu_new_lens must be contiguous int32 with {B + 1} entries")
-    t_rows, t_cols = block_table.shape
-    if t_rows < B:
-        _refuse(where, f"block_table has {t_rows} rows for {B} requests")
-    bt_stride = block_table.stride(0) if t_rows > 1 else t_cols
-    if bt_stride < t_cols:
-        _refuse(where, "block_table's rows overlap")
-    if steps is not None and (steps.dtype is not torch.int64 or steps.shape != (32,) or not steps.is_contiguous()):
-        _refuse(where, "steps must be contiguous int64 [32]")
-    if positions is not None and (positions.dtype is not i32 or positions.shape != (total,) or not positions.is_contiguous()):
-        _refuse(where, f"positions must be contiguous int32 [{total}]")
-    if norm_weight is not None and (norm_weight.dtype is not bf16 or norm_weight.shape != (lat_dim,) or
-                                    not norm_weight.is_contiguous()):
-        _refuse(where, f"norm_weight must be contiguous bf16 [{lat_dim}]")
-    num_slots = cache.nbytes // rb
-    if cache_kind == MLA_CACHE_FP8_PAGE_576:
-        if scales is None or scales.dtype is not torch.float32 or not scales.is_contiguous() or \
-                scales.numel() < num_slots // page_size:
-            _refuse(where, f"scales must be contiguous fp32 of at least {num_slots // page_size} values")
-    elif scales is not None:
-        _refuse(where, "scales belong to rows of MLA_CACHE_FP8_PAGE_576 alone")
-    if rows is not None and (rows.dtype is not bf16 or rows.dim() != 2 or rows.shape[0] < total or
-                             rows.shape[1] < lat_dim + 64 or rows.stride(1) != 1):
-        _refuse(where, f"rows must be bf16 [>= {total}, >= {lat_dim + 64}] with contiguous rows")
-    st = _status_ptr(where, status)
-    one = total <= 1  # (the stride of a dimension of one entry says nothing)
-    _check(load().mla_cache_append(
-        latent.data_ptr(), lat_dim if one else l_strides[0], k_pe.data_ptr(), 64 if one else k_strides[0],
-        cu_new_lens.data_ptr(), seq_lens.data_ptr(), block_table.data_ptr(), bt_stride, t_cols, B, total, page_size,
-        None if positions is None else positions.data_ptr(), None if steps is None else steps.data_ptr(),
-        1 if interleaved else 0, float(mscale), None if norm_weight is None else norm_weight.data_ptr(), float(eps),
-        cache.data_ptr(), int(cache_kind), lat_dim, num_slots, None if scales is None else scales.data_ptr(),
-        None if rows is None else rows.data_ptr(), 0 if rows is None else (lat_dim + 64 if one else rows.stride(0)), st,
-        _stream(stream)), where)
+    where, tensors = "mla_cache_append", (latent, k_pe, cu_new_lens, seq_lens, block_table, cache, None)
+    dev, s = _place(where, latent, _APPEND_NAMES, tensors, stream)
+    entry = _entry(where)
+    st = _bind.append(entry, s, dev, latent, k_pe, cu_new_lens, seq_lens, block_table, page_size, cache, cache_kind, steps,
+                      positions, interleaved, mscale, norm_weight, eps, scales, rows, lat_dim, status)
+    if st != 0:
+        _answered(where, st, _APPEND_NAMES, tensors, (("steps", steps), ("positions", positions), ("norm_weight", norm_weight),
+                                                      ("scales", scales), ("rows", rows), ("status", status)))
 
 
 _PAGE_NAMES = ("q_lat", "q_pe", "cache", "scales", "block_table", "seq_lens", "out", "lse", "workspace", "cu_q_lens")
@@ -809,46 +788,13 @@ def mla_decode_fp8_page(q_lat, q_pe, cache, scales, page_size, block_table, seq_
     [B + 1]) what it counts, at most q_len for each request. workspace:
     mla_decode_workspace_bytes(B, q_len, Hq, num_ctas)."""
     where = "mla_decode_fp8_page"
-    _here(where, _PAGE_NAMES, (q_lat, q_pe, cache, scales, block_table, seq_lens, out, lse, workspace, cu_q_lens))
-    bf16, f32, i32 = torch.bfloat16, torch.float32, torch.int32
-    B, q_len, page_size = seq_lens.numel(), int(q_len), int(page_size)
-    q_shape = q_lat.shape
-    if len(q_shape) != 3 or q_shape[2] != 512 or q_pe.shape != (q_shape[0], q_shape[1], 64):
-        _refuse(where, "q_lat must be [tokens, Hq, 512] and q_pe [tokens, Hq, 64]")
-    tokens, Hq, _ = q_shape
-    if q_lat.dtype is not bf16 or q_pe.dtype is not bf16 or not q_lat.is_contiguous() or not q_pe.is_contiguous():
-        _refuse(where, "q_lat and q_pe must be contiguous bf16")
-    if cu_q_lens is None:
-        if tokens != B * q_len:
-            _refuse(where, f"q_lat holds {tokens} tokens, {B} requests of {q_len} expected")
-    elif cu_q_lens.dtype is not i32 or not cu_q_lens.is_contiguous() or cu_q_lens.numel() != B + 1:
-        _refuse(where, f"cu_q_lens must be contiguous int32 with {B + 1} entries")
-    if out.dtype not in (bf16, f32) or out.shape != q_shape or not out.is_contiguous():
-        _refuse(where, f"out must be a contiguous bf16 or fp32 [{tokens}, {Hq}, 512] tensor")
-    if lse.dtype is not f32 or lse.shape != (tokens, Hq) or not lse.is_contiguous():
-        _refuse(where, f"lse must be a contiguous fp32 [{tokens}, {Hq}] tensor")
-    if not cache.is_contiguous() or not workspace.is_contiguous():
-        _refuse(where, "cache and workspace must be contiguous")
-    if page_size < 1:
-        _refuse(where, f"page_size {page_size}")
-    num_slots = cache.nbytes // 576
-    if scales.dtype is not f32 or not scales.is_contiguous() or scales.numel() < num_slots // page_size:
-        _refuse(where, f"scales must be contiguous fp32 of at least {num_slots // page_size} values")
-    if block_table.dtype is not i32 or block_table.dim() != 2 or block_table.stride(1) != 1:
-        _refuse(where, "block_table must be a 2-D int32 tensor with contiguous rows")
-    t_rows, t_cols = block_table.shape
-    if t_rows < B:
-        _refuse(where, f"block_table has {t_rows} rows for {B} requests")
-    bt_stride = block_table.stride(0) if t_rows > 1 else t_cols
-    if bt_stride < t_cols:
-        _refuse(where, "block_table's rows overlap")
-    if seq_lens.dtype is not i32 or not seq_lens.is_contiguous():
-        _refuse(where, "seq_lens must be contiguous int32")
-    _check(load().mla_decode_fp8_page(
-        q_lat.data_ptr(), q_pe.data_ptr(), tokens, cache.data_ptr(), scales.data_ptr(), num_slots, page_size,
-        block_table.data_ptr(), bt_stride, t_cols, seq_lens.data_ptr(), None if cu_q_lens is None else cu_q_lens.data_ptr(),
-        B, q_len, Hq, float(scale), out.data_ptr(), MLA_OUT_F32 if out.dtype is f32 else MLA_OUT_BF16, lse.data_ptr(),
-        workspace.data_ptr(), workspace.nbytes, int(num_ctas), _stream(stream)), where)
+    tensors = (q_lat, q_pe, cache, scales, block_table, seq_lens, out, lse, workspace, cu_q_lens)
+    dev, s = _place(where, q_lat, _PAGE_NAMES, tensors, stream)
+    entry = _entry(where)
+    st = _bind.decode_page(entry, s, dev, q_lat, q_pe, cache, scales, page_size, block_table, seq_lens, q_len, scale, out, lse,
+                           workspace, cu_q_lens, num_ctas)
+    if st != 0:
+        _answered(where, st, _PAGE_NAMES, tensors)
 
 
 def decode(q_lat, q_pe, cache, cache_kind, page_size, block_table, seq_lens, q_len, scale,

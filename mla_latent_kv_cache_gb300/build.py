@@ -2,20 +2,25 @@
 
 Each translation unit is compiled in parallel; the objects are linked into
 one shared library with the CUDA runtime linked statically, so the library
-loads next to any PyTorch build without an rpath.
+loads next to any PyTorch build without an rpath. ``_lib/_mla_bind.so`` (host code,
+g++) holds the argument checks of the Python binding's short calls; it is built
+against the installed PyTorch.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIBDIR = os.path.join(HERE, "_lib")
 LIB = os.path.join(LIBDIR, "libmla_gb300.so")
+BIND = os.path.join(LIBDIR, "_mla_bind.so")
 SOURCES = ["api.cu", "cache_write.cu", "decode.cu", "prefill.cu", "attn_weights.cu", "evict.cu", "rope.cu", "append.cu",
            "decode_page8.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -42,10 +47,18 @@ def _inputs():
     return deps
 
 
+def _bind_command(out: str) -> list:
+    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+    inc, lib = os.path.join(torch, "include"), os.path.join(torch, "lib")
+    return ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", "-I", INCLUDE, "-I", inc, "-I",
+            os.path.join(inc, "torch", "csrc", "api", "include"), "-I", sysconfig.get_paths()["include"],
+            os.path.join(CSRC, "bind.cpp"), "-o", out, "-L", lib, "-ltorch_python", "-ltorch_cpu", "-lc10"]
+
+
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
     os.makedirs(LIBDIR, exist_ok=True)
     newest = max(os.path.getmtime(p) for p in _inputs())
-    if not force and not ptxas_info and os.path.exists(LIB) and os.path.getmtime(LIB) >= newest:
+    if not force and not ptxas_info and all(os.path.exists(f) and os.path.getmtime(f) >= newest for f in (LIB, BIND)):
         return LIB
     cc = nvcc()
     objs = []
@@ -61,13 +74,23 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
             sys.stderr.write(r.stdout + r.stderr)
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    def compile_bind():
+        tmp = BIND + f".tmp{os.getpid()}"
+        r = subprocess.run(_bind_command(tmp), capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"g++ failed for bind.cpp:\n{r.stdout}\n{r.stderr}")
+        return tmp
+
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        bind = ex.submit(compile_bind)
         objs = list(ex.map(compile_one, SOURCES))
+        bind = bind.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static", "-lpthread", "-ldl", "-lrt"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(bind, BIND)
     os.replace(tmp, LIB)
     return LIB
 

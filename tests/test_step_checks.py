@@ -1,4 +1,4 @@
-"""Refusals of mla_rope and mla_cache_append, and the table of angles (no GPU
+"""Refusals of mla_rope, mla_cache_append and mla_decode_fp8_page, and the table of angles (no GPU
 needed): the library's host checks, which come before any CUDA call, and the
 binding's own checks with a stand-in library."""
 import math
@@ -29,6 +29,7 @@ def fake(monkeypatch, lib):
     monkeypatch.setattr(m, "_current_device", lambda: -1)  # what a host tensor gives as its device
     monkeypatch.setattr(m, "load", lambda: rec)
     monkeypatch.setattr(m, "_stream", lambda s: 0)
+    monkeypatch.setattr(m, "_raw_stream", None)
     return rec
 
 
@@ -153,8 +154,69 @@ def _append(**over):
 PAGE = dict(cache_kind=2, cache=torch.zeros((64, 576), dtype=torch.uint8), scales=torch.zeros(4))
 
 
+DECODE = [("ql", 16), ("qp", 16), ("tokens", 2), ("cache", 16), ("scales", 16), ("slots", 100), ("page", 16), ("bt", 16),
+          ("bts", 4), ("btc", 4), ("sl", 16), ("cu", None), ("B", 2), ("q_len", 1), ("Hq", 8), ("scale", 0.1), ("out", 16),
+          ("odt", 0), ("lse", 16), ("ws", 256), ("wsb", 1 << 24), ("ctas", 0), ("stream", None)]
+
+DECODE_BAD = [
+    dict(B=0), dict(q_len=0), dict(Hq=0), dict(page=0), dict(slots=0), dict(ctas=-1), dict(tokens=0), dict(tokens=3), dict(odt=2),
+    dict(ql=None), dict(qp=None), dict(cache=None), dict(scales=None), dict(bt=None), dict(sl=None), dict(out=None), dict(lse=None),
+    dict(ws=None), dict(ql=8), dict(qp=24), dict(cache=8), dict(out=2), dict(ws=128), dict(scales=2), dict(bt=1), dict(sl=2),
+    dict(cu=3), dict(lse=2), dict(btc=-1), dict(bts=3), dict(scale=float("nan")),
+]
+
+
+@pytest.mark.parametrize("over", DECODE_BAD, ids=str)
+def test_decode_refuses(lib, over):
+    assert lib.mla_decode_fp8_page(*_with(DECODE, **over)) == INVALID
+
+
+def test_decode_limits(lib):
+    for over in (dict(slots=1 << 31), dict(Hq=1 << 21), dict(tokens=1 << 29, cu=16)):
+        assert lib.mla_decode_fp8_page(*_with(DECODE, **over)) == UNSUPPORTED
+
+
+def _decode(**over):
+    a = dict(q_lat=bf(4, 8, 512), q_pe=bf(4, 8, 64), cache=torch.zeros((64, 576), dtype=torch.uint8), scales=torch.zeros(4), page_size=16,
+             block_table=i32(2, 4), seq_lens=i32(2), q_len=2, scale=0.1, out=bf(4, 8, 512), lse=f32(4, 8),
+             workspace=torch.zeros(1024, dtype=torch.uint8))
+    a.update(over)
+    return m.mla_decode_fp8_page(**a)
+
+
+@pytest.mark.parametrize("over,words", [
+    (dict(q_lat=bf(4, 8, 256)), "q_lat must be"), (dict(q_lat=f32(4, 8, 512)), "bf16"), (dict(q_pe=bf(4, 8, 32)), "q_pe"),
+    (dict(q_pe=bf(4, 64, 8).transpose(1, 2)), "contiguous"), (dict(q_len=1), "expected"), (dict(out=bf(4, 8, 256)), "out must be"),
+    (dict(out=bf(4, 8, 512).half()), "out must be"), (dict(lse=f32(4, 7)), "lse must be"), (dict(lse=bf(4, 8)), "lse must be"),
+    (dict(scales=torch.zeros(3)), "scales"), (dict(scales=bf(4)), "scales"), (dict(page_size=0), "page_size"),
+    (dict(page_size=1 << 40), "page_size"), (dict(block_table=i32(1, 4)), "block_table"), (dict(block_table=i32(4, 2).t()), "block_table"),
+    (dict(block_table=i32(8).as_strided((2, 4), (3, 1))), "overlap"), (dict(seq_lens=f32(2)), "seq_lens"),
+    (dict(cu_q_lens=i32(2)), "cu_q_lens"), (dict(cu_q_lens=f32(3)), "cu_q_lens"), (dict(cache=torch.zeros((576, 64), dtype=torch.uint8).t()), "cache"),
+], ids=str)
+def test_decode_binding_refuses(fake, over, words):
+    _refused(lambda: _decode(**over), words)
+    assert fake.calls == []
+
+
+def test_good_decodes_pass_their_arguments_through(fake):
+    _decode()
+    c = fake.calls[-1][1]
+    assert c[2] == 4 and c[5:7] == (64, 16) and c[8:10] == (4, 4) and c[11] is None and c[12:15] == (2, 2, 8) and c[17] == 0 and c[20:22] == (1024, 0)
+    _decode(cu_q_lens=i32(3), out=f32(4, 8, 512), num_ctas=7, q_lat=bf(4, 8, 512))
+    c = fake.calls[-1][1]
+    assert c[11] and c[17] == 1 and c[21] == 7
+
+
+def test_arguments_of_other_types_are_errors(fake):
+    for call, over in ((_rope, dict(mscale="x")), (_append, dict(eps=None)), (_append, dict(page_size=2.5)), (_decode, dict(q_len=None)),
+                       (_decode, dict(scale=[]))):
+        with pytest.raises(TypeError):
+            call(**over)
+    assert fake.calls == []
+
+
 def test_host_tensors_are_refused():
-    for call in (_rope, _append):
+    for call in (_rope, _append, _decode):
         _refused(call, "must be a CUDA tensor")
 
 
@@ -165,8 +227,11 @@ def test_missing_tensors_and_other_devices_are_refused(fake, monkeypatch):
         _refused(lambda: _append(**{name: None}), f"{name} must be a CUDA tensor")
     for name in ("steps", "positions", "norm_weight", "scales", "rows", "status"):
         _refused(lambda: _append(**{name: 5}), f"{name} must be a CUDA tensor")
+    for name in ("q_lat", "scales", "block_table", "lse", "workspace"):
+        _refused(lambda: _decode(**{name: None}), f"{name} must be a CUDA tensor")
+    _refused(lambda: _decode(cu_q_lens=5), "CUDA tensor")
     monkeypatch.setattr(m, "_current_device", lambda: 1)
-    for call in (_rope, _append):
+    for call in (_rope, _append, _decode):
         _refused(call, "the current device is cuda:1")
     assert fake.calls == []
 
