@@ -2653,6 +2653,7 @@ __global__ void __launch_bounds__(128 * RPB * GRP) mla_decode_merge_kernel(const
 #pragma unroll
     for (int w = 0; w < kThreads / 32; ++w) { pre += red_pre[w]; tot += red_tot[w]; }
     griddep_wait();  // the decode grid has finished and its writes are visible
+    griddep_launch_dependents();  // the next call's set-up may begin (it waits for this grid before it reads anything)
 
     if (blockIdx.x == 0 && blockIdx.y == 0 && warp == 0) {
         // status summary: OR of all records; the lowest failing CTA's site,

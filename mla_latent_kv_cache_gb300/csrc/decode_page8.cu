@@ -102,7 +102,7 @@ struct P8Ctrl {
     // softmax may be a tile ahead of a slow issuer, which a single barrier's
     // parity could not tell
     uint64_t p_full[2], o_done[2];
-    uint64_t q_full[kQGens], q_empty;
+    uint64_t q_first, q_full[kQGens], q_empty;  // the first request's queries; those of the later ones
     uint64_t sc_full[kScs];
     uint64_t fin[2];
     uint32_t tmem_base;
@@ -194,17 +194,19 @@ __device__ __forceinline__ void p8_ld_pair(uint32_t at0, uint32_t at1, uint32_t 
         : "memory");
 }
 
-// Two values as e4m3 codes (low byte the first) and what is left of them.
-__device__ __forceinline__ uint32_t p8_split(float a, float b, float& ra, float& rb) {
-    const uint32_t h = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+__device__ __forceinline__ void p8_store(float* to, float v) { *to = v; }
+__device__ __forceinline__ void p8_store(__nv_bfloat16* to, float v) { *to = __float2bfloat16_rn(v); }
+
+// Two values in f16 as e4m3 codes (the first in the low byte), and the codes of
+// what is left of them times `times` (e4m3, or e5m2).
+__device__ __forceinline__ void p8_split(__half2 v, float times, uint32_t& h, uint32_t& l, bool e5m2 = false) {
+    h = __nv_cvt_halfraw2_to_fp8x2(*reinterpret_cast<const __half2_raw*>(&v), __NV_SATFINITE, __NV_E4M3);
     const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(h), __NV_E4M3);
-    const float2 hf = __half22float2(*reinterpret_cast<const __half2*>(&hr));
-    ra = a - hf.x;
-    rb = b - hf.y;
-    return h & 0xFFFFu;
-}
-__device__ __forceinline__ uint32_t p8_codes(float a, float b) {
-    return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3) & 0xFFFFu;
+    __half2 rest = __hsub2(v, *reinterpret_cast<const __half2*>(&hr));
+    if (times != 1.f) rest = __hmul2(rest, __float2half2_rn(times));
+    l = __nv_cvt_halfraw2_to_fp8x2(*reinterpret_cast<const __half2_raw*>(&rest), __NV_SATFINITE, e5m2 ? __NV_E5M2 : __NV_E4M3);
+    h &= 0xFFFFu;
+    l &= 0xFFFFu;
 }
 
 template <int NP, bool LSU>
@@ -240,6 +242,7 @@ __global__ void __launch_bounds__(P8Cfg<NP, LSU>::kThreads, 1)
             mbar_init(&ctrl->o_done[i], 1);
             mbar_init(&ctrl->fin[i], 1);
         }
+        mbar_init(&ctrl->q_first, 4 * C::kGroups);
         for (int i = 0; i < kQGens; ++i) mbar_init(&ctrl->q_full[i], C::kQWarps);
         mbar_init(&ctrl->q_empty, 1);
         for (int i = 0; i < kScs; ++i) mbar_init(&ctrl->sc_full[i], LSU ? 4 : 1);
@@ -263,7 +266,56 @@ __global__ void __launch_bounds__(P8Cfg<NP, LSU>::kThreads, 1)
         tmem_relinquish();
         tc_fence_before();
     }
-    if (warp == 2) {
+    bool split = false;
+    if (p.B <= C::kThreads) {
+        // A thread a request: prefix sums of cost and tiles (the split of scan_range, in the
+        // latency of one load instead of several passes over the lengths; lengths whose sums
+        // might pass 32 bits are left to that).
+        const int t = threadIdx.x;
+        const uint32_t tl = t < p.B ? (static_cast<uint32_t>(max(__ldg(p.seq_lens + t), 0)) + kTok - 1) / kTok : 0u;
+        const uint32_t cost = tl > 0 ? tl + p.wseg : 0u;
+        uint32_t ic = cost, tt = tl;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t vc = __shfl_up_sync(0xffffffffu, ic, o), vt = __shfl_up_sync(0xffffffffu, tt, o);
+            if (lane >= o) {
+                ic += vc;
+                tt += vt;
+            }
+        }
+        uint2* part = reinterpret_cast<uint2*>(pbufs);  // (not in use yet)
+        if (lane == 31) part[warp] = make_uint2(ic, tt);
+        if (t == 0) ctrl->t_begin = ctrl->t_end = ctrl->b0 = ctrl->j0 = 0;
+        split = __syncthreads_or(tl > (1u << 21)) == 0;
+        if (split) {
+            uint32_t all_c = 0, all_t = 0, c0 = ic - cost, t0 = tt - tl;
+#pragma unroll
+            for (int w = 0; w < C::kThreads / 32; ++w) {
+                const uint2 v = part[w];
+                if (w < warp) {
+                    c0 += v.x;
+                    t0 += v.y;
+                }
+                all_c += v.x;
+                all_t += v.y;
+            }
+            auto bound = [&](int k) -> uint32_t {  // k all_c / G
+                return all_c < (1u << 31) / (G + 1) ? k * all_c / static_cast<uint32_t>(G)
+                                                    : static_cast<uint32_t>(static_cast<unsigned long long>(k) * all_c / G);
+            };
+            const uint32_t x0 = bound(g), x1 = bound(g + 1), wseg = p.wseg;
+            if (cost > 0 && c0 <= x0 && x0 < c0 + cost) {
+                const uint32_t j = x0 - c0 > wseg ? x0 - c0 - wseg : 0u;
+                ctrl->t_begin = static_cast<int>(t0 + j);
+                ctrl->b0 = t;
+                ctrl->j0 = static_cast<int>(j);
+            }
+            if (cost > 0 && c0 <= x1 && x1 < c0 + cost)
+                ctrl->t_end = static_cast<int>(t0 + (x1 - c0 > wseg ? x1 - c0 - wseg : 0u));
+            if (t == 0 && g == G - 1) ctrl->t_end = static_cast<int>(all_t);
+        }
+    }
+    if (!split && warp == 2) {
         const TileRange r = scan_range<7>(p, g, G, lane);
         if (lane == 0) {
             ctrl->t_begin = r.tb;
@@ -291,19 +343,20 @@ __global__ void __launch_bounds__(P8Cfg<NP, LSU>::kThreads, 1)
     It it;
     if (ntiles > 0) it.init(p.seq_lens, ctrl->b0, ctrl->j0);
 
-    // the query rows of request b in this row group as h and l codes, and their scales; the query warps
-    auto load_q = [&](int b, int gen) {
-        const int wq = warp - C::kQWarp;
+    // The query rows of request b in this row group as h and l codes, and what undoes
+    // their powers of two: rows w, w + W, .. are this warp's.
+    auto load_q = [&](int b, int gen, int w, int W) {
         const int rows = req_rows_in_group(p, b, gy);
         const int64_t row0 = req_row0(p, b) + gy * 64;
         uint8_t* qr = qs + 4 * C::kQBlk;
+        constexpr int kAt = 4;  // rows at a time, loads first
 #pragma unroll 1
-        for (int r4 = wq; r4 < NP; r4 += 4 * C::kQWarps) {  // four rows at a time, loads first
-            uint4 x[4][2];
-            uint32_t e[4];
+        for (int r4 = w; r4 < NP; r4 += kAt * W) {
+            uint4 x[kAt][2];
+            uint32_t e[kAt];
 #pragma unroll
-            for (int n = 0; n < 4; ++n) {
-                const int r = r4 + C::kQWarps * n;
+            for (int n = 0; n < kAt; ++n) {
+                const int r = r4 + W * n;
                 const uint4 z = make_uint4(0u, 0u, 0u, 0u);
                 // lane holds latent values 16 lane .. 16 lane + 15 and rotary values 2 lane, 2 lane + 1
                 const uint4* ql = reinterpret_cast<const uint4*>(p.q_lat + (row0 + r) * kD) + 2 * lane;
@@ -312,56 +365,52 @@ __global__ void __launch_bounds__(P8Cfg<NP, LSU>::kThreads, 1)
                 e[n] = r < rows ? __ldg(reinterpret_cast<const uint32_t*>(p.q_pe + (row0 + r) * kP) + lane) : 0u;
             }
 #pragma unroll
-            for (int n = 0; n < 4; ++n) {
-                const int r = r4 + C::kQWarps * n;
-                const __nv_bfloat162* xb = reinterpret_cast<const __nv_bfloat162*>(x[n]);
-                const float2 pe = make_float2(__uint_as_float(e[n] << 16), __uint_as_float(e[n] & 0xFFFF0000u));
-                float mx = fmaxf(fabsf(pe.x), fabsf(pe.y));
+            for (int n = 0; n < kAt; ++n) {
+                const int r = r4 + W * n;
+                if (r >= NP) break;
+                const uint32_t v[9] = {x[n][0].x, x[n][0].y, x[n][0].z, x[n][0].w, x[n][1].x,
+                                       x[n][1].y, x[n][1].z, x[n][1].w, e[n]};
+                // the largest magnitude (non-negative floats are ordered as their bits)
+                uint32_t top = 0;
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const float2 f = __bfloat1622float2(xb[k]);
-                    mx = fmaxf(mx, fmaxf(fabsf(f.x), fabsf(f.y)));
+                for (int k = 0; k < 9; ++k) {
+                    // (a NaN is not the largest: its bits would be)
+                    const uint32_t a = v[k] << 16 & 0x7FFFFFFFu, c = v[k] & 0x7FFF0000u;
+                    top = max(top, max(a > 0x7F800000u ? 0u : a, c > 0x7F800000u ? 0u : c));
                 }
-                // (non-negative floats are ordered as their bits)
-                mx = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mx)));
-                // the power of two that brings the largest into [128, 256)
-                const int ex = static_cast<int>(__float_as_uint(mx) >> 23) - 127;
+                top = __reduce_max_sync(0xffffffffu, top);
+                // the power of two that brings it into [128, 256); a row with an infinity, which
+                // 8 bits do not hold, becomes NaN
+                const int ex = static_cast<int>(top >> 23) - 127;
                 const int k2 = max(-120, min(120, 7 - ex));
-                const float up = __uint_as_float(static_cast<uint32_t>(127 + k2) << 23);
-                // (x - x is 0, and NaN for an infinity, which 8 bits do not hold)
-                auto scaled = [&](float v) { return fmaf(v, up, v - v); };
-                uint32_t h[4], l[4];
+                const float up = top == 0x7F800000u ? __uint_as_float(0x7FC00000u) : __uint_as_float(static_cast<uint32_t>(127 + k2) << 23);
+                // in f16, which holds 8 bits of every value that counts: the rest is one subtraction
+                uint32_t h[9], l[9];
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const float2 f = __bfloat1622float2(xb[k]);
-                    float ra, rb;
-                    const uint32_t hc = p8_split(scaled(f.x), scaled(f.y), ra, rb);
-                    const uint32_t lc = p8_codes(ra * 32.f, rb * 32.f);
-                    if (k & 1) {
-                        h[k >> 1] |= hc << 16;
-                        l[k >> 1] |= lc << 16;
-                    } else {
-                        h[k >> 1] = hc;
-                        l[k >> 1] = lc;
-                    }
+                for (int k = 0; k < 9; ++k) {
+                    const float2 f = un2(mul2(f2(__uint_as_float(v[k] << 16), __uint_as_float(v[k] & 0xFFFF0000u)), f2(up, up)));
+                    p8_split(__floats2half2_rn(f.x, f.y), 32.f, h[k], l[k]);
                 }
                 // unit lane % 8 of row r, block lane / 8 (NP is a multiple of 8: rows NP + r swizzle alike)
                 uint8_t* at = qs + (lane >> 3) * C::kQBlk + r * 128 + (((lane & 7) ^ (r & 7)) << 4);
-                *reinterpret_cast<uint4*>(at) = make_uint4(h[0], h[1], h[2], h[3]);
-                *reinterpret_cast<uint4*>(at + NP * 128) = make_uint4(l[0], l[1], l[2], l[3]);
-                float ra, rb;
-                const uint32_t hc = p8_split(scaled(pe.x), scaled(pe.y), ra, rb);
-                const uint32_t lc = p8_codes(ra * 32.f, rb * 32.f);
+                auto pair = [](const uint32_t (&c)[9], int k) { return c[k] | c[k + 1] << 16; };
+                *reinterpret_cast<uint4*>(at) = make_uint4(pair(h, 0), pair(h, 2), pair(h, 4), pair(h, 6));
+                *reinterpret_cast<uint4*>(at + NP * 128) = make_uint4(pair(l, 0), pair(l, 2), pair(l, 4), pair(l, 6));
                 uint8_t* ar = qr + r * 64 + (((lane >> 3) ^ ((r >> 1) & 3)) << 4) + (lane & 7) * 2;
-                *reinterpret_cast<uint16_t*>(ar) = static_cast<uint16_t>(hc);
-                *reinterpret_cast<uint16_t*>(ar + NP * 64) = static_cast<uint16_t>(lc);
+                *reinterpret_cast<uint16_t*>(ar) = static_cast<uint16_t>(h[8]);
+                *reinterpret_cast<uint16_t*>(ar + NP * 64) = static_cast<uint16_t>(l[8]);
                 if (lane == 0)
                     ctrl->kq[gen][r] = __uint_as_float(static_cast<uint32_t>(127 - k2) << 23) * p.scale_log2;
             }
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&ctrl->q_full[gen]);
+    };
+    // the queries of segment seg are there: the softmax warps have made the first ones (there
+    // are more of them than query warps, and nothing else to do yet)
+    auto queries = [&](int seg, volatile int* stop) {
+        return seg == 0 ? mbar_wait(&ctrl->q_first, 0, stop)
+                        : mbar_wait(&ctrl->q_full[(seg - 1) % kQGens], ((seg - 1) / kQGens) & 1, stop);
     };
 
     if (ntiles > 0) {
@@ -381,7 +430,7 @@ __global__ void __launch_bounds__(P8Cfg<NP, LSU>::kThreads, 1)
             for (; i < ntiles; ++i) {
                 if (i == 0 || it.j == 0) {
                     ++seg;
-                    if (!mbar_wait(&ctrl->q_full[seg % kQGens], (seg / kQGens) & 1, abort)) {
+                    if (!queries(seg, abort)) {
                         site = kSiteQFull;
                         break;
                     }
@@ -510,24 +559,19 @@ __global__ void __launch_bounds__(P8Cfg<NP, LSU>::kThreads, 1)
                 const int64_t s = static_cast<int64_t>(page) * p.page_size + tok % p.page_size;
                 return static_cast<int>(s < p.num_slots ? s : 0);
             };
-            int page_next, y_next = run_of(it, entry(it), page_next);
-            float s_next = warp == 1 ? p8_scale(p, page_next) : 1.f;
+            const int e_first = entry(it);
             It it1 = it;  // the tile after the one that is loaded
             if (ntiles > 1) it1.next(p.seq_lens, p.B);
             int e_next = ntiles > 1 ? entry(it1) : -1;
+            int page_next, y_next = run_of(it, e_first, page_next);
+            float s_next = warp == 1 ? p8_scale(p, page_next) : 1.f;
             uint32_t armed = 0;  // blocks whose barrier this warp has armed
             int rope_armed = 0;
             for (; i < ntiles && ok; ++i) {
                 const int valid = min(kTok, it.T - it.j * kTok);
                 const int nruns = (valid + BR - 1) / BR;
                 const int y = y_next;
-                if (warp == 1) {
-                    // (its slot: the loads of tile i are behind the value product of tile i - 3,
-                    // which read nothing later than the scales of tile i - 3 did)
-                    if (lane < nruns) ctrl->sc[i % kScs][lane] = s_next;
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&ctrl->sc_full[i % kScs]);
-                }
+                const float s_now = s_next;
                 it = it1;
                 if (i + 1 < ntiles) {
                     const int e = e_next;
@@ -566,6 +610,13 @@ __global__ void __launch_bounds__(P8Cfg<NP, LSU>::kThreads, 1)
                     armed = u + 1;
                     if (lane < nruns)
                         tma_load_2d(ring + slot * kBlk + lane * BR * 128, &maps.lat, &ctrl->blk_full[slot], kb * 128, y, pol);
+                }
+                if (warp == 1) {
+                    // (its slot: the loads of tile i are behind the value product of tile i - 3,
+                    // which read nothing later than the scales of tile i - 3 did)
+                    if (lane < nruns) ctrl->sc[i % kScs][lane] = s_now;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&ctrl->sc_full[i % kScs]);
                 }
             }
             if (!ok && lane == 0) {
@@ -637,7 +688,10 @@ __global__ void __launch_bounds__(P8Cfg<NP, LSU>::kThreads, 1)
                         while (!ok && !__any_sync(0xffffffffu, *abort));
                         if (!ok) break;  // (another role has said why)
                     }
-                    load_q(it.b, seg % kQGens);
+                    if (seg > 0) {
+                        load_q(it.b, seg % kQGens, w, C::kQWarps);
+                        if (lane == 0) mbar_arrive(&ctrl->q_full[(seg - 1) % kQGens]);
+                    }
                 }
                 if constexpr (LSU) {
                     const int valid = min(kTok, it.T - it.j * kTok);
@@ -695,6 +749,8 @@ __global__ void __launch_bounds__(P8Cfg<NP, LSU>::kThreads, 1)
             const int bar = 1 + grp;
             const uint32_t lane_base = static_cast<uint32_t>(wq * 32) << 16;
             const int run_shift = LSU ? 0 : 31 - __clz(p.run_rows);  // (a power of two)
+            load_q(it.b, 0, warp - 4, 4 * C::kGroups);
+            if (lane == 0) mbar_arrive(&ctrl->q_first);
             F2 l[CW / 2];          // this token's share of the columns' sums
             bool unset = false;
             int seg = -1, start_j = 0, T = 0, qt = 0, rows = 0;
@@ -716,7 +772,10 @@ __global__ void __launch_bounds__(P8Cfg<NP, LSU>::kThreads, 1)
                     rows = req_rows_in_group(p, it.b, gy);
 #pragma unroll
                     for (int c = 0; c < CW / 2; ++c) l[c] = 0ull;
-                    wait(&ctrl->q_full[seg % kQGens], (seg / kQGens) & 1, kSiteQFull);
+                    if (!queries(seg, abort)) {
+                        if (!failed) site = kSiteQFull;
+                        failed = true;
+                    }
                 }
                 const float* kq = ctrl->kq[seg % kQGens] + cb;
                 const int tok = it.j * kTok + tk, valid = min(kTok, T - it.j * kTok);
@@ -869,20 +928,15 @@ __global__ void __launch_bounds__(P8Cfg<NP, LSU>::kThreads, 1)
                     const float2 v = un2(y[c / 2]);
                     const float a = ex2(v.x), b = ex2(v.y);
                     l[c / 2] = fma2(f2(a, b), inv2, l[c / 2]);
-                    // in f16 (11 bits, of which the two codes hold 8) the rest is one packed subtraction
-                    const __half2 ph = __floats2half2_rn(a, b);
-                    const uint32_t h = __nv_cvt_halfraw2_to_fp8x2(*reinterpret_cast<const __half2_raw*>(&ph), __NV_SATFINITE, __NV_E4M3);
-                    const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(h), __NV_E4M3);
-                    __half2 rest = __hsub2(ph, *reinterpret_cast<const __half2*>(&hr));
-                    if (C::kStack) rest = __hmul2(rest, __float2half2_rn(32.f));
-                    const uint32_t lo = __nv_cvt_halfraw2_to_fp8x2(*reinterpret_cast<const __half2_raw*>(&rest), __NV_SATFINITE,
-                                                                   C::kStack ? __NV_E4M3 : __NV_E5M2);
+                    // (f16 holds 11 bits, the two codes 8 of them)
+                    uint32_t h, lo;
+                    p8_split(__floats2half2_rn(a, b), C::kStack ? 32.f : 1.f, h, lo, !C::kStack);
                     if (c & 2) {
                         hc[c >> 2] |= h << 16;
                         lc[c >> 2] |= lo << 16;
                     } else {
-                        hc[c >> 2] = h & 0xFFFFu;
-                        lc[c >> 2] = lo & 0xFFFFu;
+                        hc[c >> 2] = h;
+                        lc[c >> 2] = lo;
                     }
                 }
                 // P's place is free when the value product that read it last is done
@@ -943,33 +997,49 @@ __global__ void __launch_bounds__(P8Cfg<NP, LSU>::kThreads, 1)
                 named_bar_sync(bar, 128);
                 tc_fence_after();
                 __syncwarp();
-#pragma unroll 1
-                for (int mt = 0; mt < 4; ++mt) {
-                    const int d = mt * 128 + tk;  // (lane tk holds a dim here)
+                // lane tk holds dim 128 mt + tk here, of 16 rows at a time
+                auto put = [&](auto* base) {  // row cb of this segment, dim tk
 #pragma unroll 1
                     for (int c0 = 0; c0 < CW; c0 += 16) {
-                        const uint32_t at = tmem + lane_base + mt * C::kPRow + cb + c0;
-                        uint32_t o[16];
-                        if constexpr (C::kStack) {
-                            uint32_t lo[16];
-                            p8_ld_pair(at, at + NP, o, lo);
+                        const int n = rows - cb - c0;  // rows of these 16 that there are
+                        if (n <= 0) break;
+                        float inv[16];
 #pragma unroll
-                            for (int c = 0; c < 16; ++c)
-                                o[c] = __float_as_uint(fmaf(__uint_as_float(lo[c]), 0x1p-5f, __uint_as_float(o[c])));
-                        } else {
-                            tmem_ld_x16(at, o);
+                        for (int c = 0; c < 16; c += 4) {
+                            const float4 v = *reinterpret_cast<const float4*>(ctrl->dy + cb + c0 + c);
+                            inv[c] = v.x;
+                            inv[c + 1] = v.y;
+                            inv[c + 2] = v.z;
+                            inv[c + 3] = v.w;
                         }
+#pragma unroll 1
+                        for (int mt = 0; mt < 4; ++mt) {
+                            const uint32_t at = tmem + lane_base + mt * C::kPRow + cb + c0;
+                            uint32_t o[16];
+                            if constexpr (C::kStack) {
+                                uint32_t lo[16];
+                                p8_ld_pair(at, at + NP, o, lo);
 #pragma unroll
-                        for (int c = 0; c < 16; ++c) {
-                            const int r = cb + c0 + c;
-                            if (r >= rows) continue;
-                            const float v = __uint_as_float(o[c]) * ctrl->dy[r];
-                            if (!whole) p.part_o[(slot0 + r) * kD + d] = v;
-                            else if (p.out_f32) static_cast<float*>(p.out)[(row0 + r) * kD + d] = v;
-                            else static_cast<__nv_bfloat16*>(p.out)[(row0 + r) * kD + d] = __float2bfloat16_rn(v);
+                                for (int c = 0; c < 16; ++c)
+                                    o[c] = __float_as_uint(fmaf(__uint_as_float(lo[c]), 0x1p-5f, __uint_as_float(o[c])));
+                            } else {
+                                tmem_ld_x16(at, o);
+                            }
+                            auto* to = base + c0 * kD + mt * 128;
+                            if (n >= 16) {
+#pragma unroll
+                                for (int c = 0; c < 16; ++c) p8_store(to + c * kD, __uint_as_float(o[c]) * inv[c]);
+                            } else {
+#pragma unroll
+                                for (int c = 0; c < 16; ++c)
+                                    if (c < n) p8_store(to + c * kD, __uint_as_float(o[c]) * inv[c]);
+                            }
                         }
                     }
-                }
+                };
+                if (!whole) put(p.part_o + (slot0 + cb) * kD + tk);
+                else if (p.out_f32) put(static_cast<float*>(p.out) + (row0 + cb) * kD + tk);
+                else put(static_cast<__nv_bfloat16*>(p.out) + (row0 + cb) * kD + tk);
                 tc_fence_before();
             }
             if (failed) {
