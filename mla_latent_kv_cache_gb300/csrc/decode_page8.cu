@@ -27,10 +27,10 @@
 // operand of S = C Q^T (thread = token = TMEM lane) and the MN-major A operand of
 // O^T += C^T P, and its ring slot is free when its own value product is done.
 //
-// Warps: 0 issues S, 3 the value product, 1 loads; 4..7 (and 8..11 from 32 rows
-// on, each group half of the columns) softmax, P and output; the last four turn
-// a request's queries into h and l. Pages that are not a multiple of 8 rows are
-// read row by row by those last four. The split of the work between CTAs, the
+// Warps: 0 issues S, 3 the value product, 1 and 2 load (at 16 rows 8 and 9 too); 4..7
+// (and 8..11 from 32 rows on, each group half of the columns) turn a request's queries
+// into h and l, then softmax, P and output. Pages that are not a multiple of 8 rows are
+// read row by row by four warps behind those. The split of the work between CTAs, the
 // partial results and their merge are those of the other decode kernels.
 #include <climits>
 
@@ -47,7 +47,7 @@ using F2 = packed2;
 constexpr int kTok = 128;             // tokens a tile
 constexpr int kBlk = kTok * 128;      // bytes of a latent block
 constexpr int kRopeBlk = kTok * 64;   // and of the rotary part
-constexpr int kQGens = 4;             // generations of query scales that may be in use at once
+constexpr int kQGens = 4;             // generations of query scales (three may be in use: a group is at most two tiles behind)
 constexpr int kScs = 4;               // tiles' scales
 // P of the maximum itself is 2^3, and a score may pass it by 2^5 before the maximum
 // is raised (O rescaled, a few thousand cycles): with 2^6 and 2^2 that was every
@@ -79,13 +79,12 @@ struct P8Cfg {
     static constexpr int kOffQ = kOffRope + kRopes * kRopeBlk;  // (swizzle atoms: all of these lie at multiples of 1024)
     static constexpr int kOffP = kOffQ + kQBytes;
     static constexpr int kOffCtrl = kOffP + kPBufs * kPBytes;
-    static constexpr int kQWarp = 4 + 4 * kGroups;      // first of the query warps
-    // loading warps: 1 and 2, and at 16 rows, where two warps are enough for the
-    // queries, two more (a tile of 16-token pages is 40 boxes, about 75 cycles each to
-    // the warp that issues them)
+    static constexpr int kMore = 4 + 4 * kGroups;       // first of the warps behind the softmax
+    // loading warps: 1 and 2, and at 16 rows, where there are registers for it, two more
+    // (a tile of 16-token pages is 40 boxes, about 75 cycles each to the warp that issues
+    // them); LSU: four behind the softmax
     static constexpr int kLoaders = LSU ? 0 : NP == 16 ? 4 : 2;
-    static constexpr int kQWarps = kLoaders == 4 ? 2 : 4;
-    static constexpr int kThreads = 32 * (kQWarp + 4);
+    static constexpr int kThreads = 32 * (kMore + (LSU ? 4 : kLoaders - 2));
     static constexpr int kOCols = 4 * (kStack ? 2 * NP : NP);
     static constexpr int kColS = kOCols;                // two S buffers of 2 NP columns
     static_assert(kPRow == 32 || kPRow == 64, "one swizzle row");
@@ -102,7 +101,7 @@ struct P8Ctrl {
     // softmax may be a tile ahead of a slow issuer, which a single barrier's
     // parity could not tell
     uint64_t p_full[2], o_done[2];
-    uint64_t q_first, q_full[kQGens], q_empty;  // the first request's queries; those of the later ones
+    uint64_t q_full;
     uint64_t sc_full[kScs];
     uint64_t fin[2];
     uint32_t tmem_base;
@@ -139,6 +138,16 @@ __device__ __forceinline__ int p8_slot(const DecodeParams& p, const int32_t* btr
     page = static_cast<int>(pg);
     const int64_t s = pg * p.page_size + tok % p.page_size;
     return static_cast<int>(s < p.num_slots ? s : 0);
+}
+
+// L2 prefetch of request b's query rows of row group gy.
+__device__ __forceinline__ void prefetch_queries(const DecodeParams& p, int b, int gy) {
+    const int rows = req_rows_in_group(p, b, gy);
+    const int64_t row0 = req_row0(p, b) + gy * 64;
+    if (rows > 0) {
+        prefetch_l2_bulk(p.q_lat + row0 * kD, static_cast<uint32_t>(rows * kD * 2));
+        prefetch_l2_bulk(p.q_pe + row0 * kP, static_cast<uint32_t>(rows * kP * 2));
+    }
 }
 
 // A page's scale. A pool smaller than a page has no scales (and no rows that count).
@@ -242,9 +251,7 @@ __global__ void __launch_bounds__(P8Cfg<NP, LSU>::kThreads, 1)
             mbar_init(&ctrl->o_done[i], 1);
             mbar_init(&ctrl->fin[i], 1);
         }
-        mbar_init(&ctrl->q_first, 4 * C::kGroups);
-        for (int i = 0; i < kQGens; ++i) mbar_init(&ctrl->q_full[i], C::kQWarps);
-        mbar_init(&ctrl->q_empty, 1);
+        mbar_init(&ctrl->q_full, 4 * C::kGroups);
         for (int i = 0; i < kScs; ++i) mbar_init(&ctrl->sc_full[i], LSU ? 4 : 1);
         ctrl->abort = 0;
         fence_mbar_init();
@@ -405,12 +412,7 @@ __global__ void __launch_bounds__(P8Cfg<NP, LSU>::kThreads, 1)
         }
         fence_proxy_async_smem();
         __syncwarp();
-    };
-    // the queries of segment seg are there: the softmax warps have made the first ones (there
-    // are more of them than query warps, and nothing else to do yet)
-    auto queries = [&](int seg, volatile int* stop) {
-        return seg == 0 ? mbar_wait(&ctrl->q_first, 0, stop)
-                        : mbar_wait(&ctrl->q_full[(seg - 1) % kQGens], ((seg - 1) / kQGens) & 1, stop);
+        if (lane == 0) mbar_arrive(&ctrl->q_full);
     };
 
     if (ntiles > 0) {
@@ -430,7 +432,7 @@ __global__ void __launch_bounds__(P8Cfg<NP, LSU>::kThreads, 1)
             for (; i < ntiles; ++i) {
                 if (i == 0 || it.j == 0) {
                     ++seg;
-                    if (!queries(seg, abort)) {
+                    if (!mbar_wait(&ctrl->q_full, seg & 1, abort)) {
                         site = kSiteQFull;
                         break;
                     }
@@ -470,13 +472,8 @@ __global__ void __launch_bounds__(P8Cfg<NP, LSU>::kThreads, 1)
                     }
                 }
                 if (site) break;
-                It nx = it;
-                nx.next(p.seq_lens, p.B);
-                if (leader) {
-                    umma_commit(&ctrl->s_full[i & 1]);
-                    if (i + 1 == ntiles || nx.j == 0) umma_commit(&ctrl->q_empty);
-                }
-                it = nx;
+                if (leader) umma_commit(&ctrl->s_full[i & 1]);
+                it.next(p.seq_lens, p.B);
             }
             __syncwarp();
             if (leader) {
@@ -530,7 +527,7 @@ __global__ void __launch_bounds__(P8Cfg<NP, LSU>::kThreads, 1)
                 }
                 drain_mma(&ctrl->fin[1]);
             }
-        } else if (!LSU && (warp == 1 || warp == 2 || warp >= C::kQWarp + C::kQWarps)) {
+        } else if (!LSU && (warp == 1 || warp == 2 || warp >= C::kMore)) {
             // ------------------------------------------------------------ loads
             // Lane r owns run r of a tile: BR rows that lie next to each other in a page.
             // Each loading warp has its blocks of every tile and a share of the rotary part's
@@ -538,7 +535,7 @@ __global__ void __launch_bounds__(P8Cfg<NP, LSU>::kThreads, 1)
             // tell it from the one 2 rings before; but the warp's last wait was for a block
             // at most 4 earlier, and products end in order, so that one is long done.
             constexpr int kMine = LSU ? 4 : 4 / C::kLoaders;  // blocks of a warp
-            const int me = warp < 4 ? warp - 1 : 2 + warp - C::kQWarp - C::kQWarps, kb0 = me * kMine;
+            const int me = warp < 4 ? warp - 1 : 2 + warp - C::kMore, kb0 = me * kMine;
             const int BR = p.run_rows;
             const uint64_t pol = gridDim.y > 1 ? l2_policy_evict_normal() : l2_policy_evict_first();
             bool bad = false, ok = true;
@@ -578,6 +575,8 @@ __global__ void __launch_bounds__(P8Cfg<NP, LSU>::kThreads, 1)
                     if (i + 2 < ntiles) {
                         it1.next(p.seq_lens, p.B);
                         e_next = entry(it1);
+                        // (a new request: its queries are wanted as soon as the last one's are done with)
+                        if (it1.j == 0 && warp == 2 && lane == 0) prefetch_queries(p, it1.b, gy);
                     }
                     y_next = run_of(it, e, page_next);
                     if (warp == 1) s_next = p8_scale(p, page_next);
@@ -639,13 +638,13 @@ __global__ void __launch_bounds__(P8Cfg<NP, LSU>::kThreads, 1)
                 for (int k = max(0, rope_armed - kRopes); k < rope_armed; ++k) land(&ctrl->rope_full[k % kRopes], (k / kRopes) & 1);
             }
             if (bad) atomicOr(status_rec(p), kErrBadBlock);
-        } else if (warp >= C::kQWarp && warp < C::kQWarp + C::kQWarps) {
-            // ---------------------------------------------------------- queries
-            // (and LSU: the rows, warp w's being 32 w .. 32 w + 31 of a tile)
-            bool ok = true, bad = false;
-            int seg = -1, site = 0, i = 0;
-            const int w = warp - C::kQWarp;
-            uint64_t *pend = nullptr, *pend2 = nullptr;  // LSU: barriers of the fill before, not yet handed over
+        } else if (warp >= C::kMore) {
+            // -------------------------------------------- loads, row by row (LSU)
+            // Warp w's rows of a tile are 32 w .. 32 w + 31.
+            bool bad = false;
+            int site = 0, i = 0;
+            const int w = warp - C::kMore;
+            uint64_t *pend = nullptr, *pend2 = nullptr;  // barriers of the fill before, not yet handed over
             uint32_t u = 0;
             auto hand_over = [&]() {
                 if (!pend) return;
@@ -657,9 +656,9 @@ __global__ void __launch_bounds__(P8Cfg<NP, LSU>::kThreads, 1)
                 }
                 pend = pend2 = nullptr;
             };
-            // LSU: what waits behind a barrier may need this warp's last fill first
+            // what waits behind a barrier may need this warp's last fill first
             auto wait = [&](uint64_t* bar, uint32_t par, int where) {
-                if (LSU && pend && !__all_sync(0xffffffffu, mbar_try_wait(bar, par))) {
+                if (pend && !__all_sync(0xffffffffu, mbar_try_wait(bar, par))) {
                     asm volatile("cp.async.wait_group 0;" ::: "memory");
                     hand_over();
                 }
@@ -675,24 +674,6 @@ __global__ void __launch_bounds__(P8Cfg<NP, LSU>::kThreads, 1)
                 pend2 = bar2;
             };
             for (; i < ntiles; ++i) {
-                if (i == 0 || it.j == 0) {
-                    ++seg;
-                    if (seg > 0) {
-                        // (the last queries may be in use for long: as long as the products, whose
-                        // own waits end)
-                        if (LSU && pend) {
-                            asm volatile("cp.async.wait_group 0;" ::: "memory");
-                            hand_over();
-                        }
-                        do ok = __all_sync(0xffffffffu, mbar_wait(&ctrl->q_empty, (seg - 1) & 1, abort));
-                        while (!ok && !__any_sync(0xffffffffu, *abort));
-                        if (!ok) break;  // (another role has said why)
-                    }
-                    if (seg > 0) {
-                        load_q(it.b, seg % kQGens, w, C::kQWarps);
-                        if (lane == 0) mbar_arrive(&ctrl->q_full[(seg - 1) % kQGens]);
-                    }
-                }
                 if constexpr (LSU) {
                     const int valid = min(kTok, it.T - it.j * kTok);
                     const int row = w * 32 + lane;
@@ -732,10 +713,8 @@ __global__ void __launch_bounds__(P8Cfg<NP, LSU>::kThreads, 1)
                 }
                 it.next(p.seq_lens, p.B);
             }
-            if (LSU) {
-                asm volatile("cp.async.wait_group 0;" ::: "memory");
-                hand_over();
-            }
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+            hand_over();
             if (site && lane == 0) {
                 fail(p, ctrl, kErrWaitTimeout, site, i);
                 report(p, kRoleLsu0, site, i);
@@ -750,7 +729,6 @@ __global__ void __launch_bounds__(P8Cfg<NP, LSU>::kThreads, 1)
             const uint32_t lane_base = static_cast<uint32_t>(wq * 32) << 16;
             const int run_shift = LSU ? 0 : 31 - __clz(p.run_rows);  // (a power of two)
             load_q(it.b, 0, warp - 4, 4 * C::kGroups);
-            if (lane == 0) mbar_arrive(&ctrl->q_first);
             F2 l[CW / 2];          // this token's share of the columns' sums
             bool unset = false;
             int seg = -1, start_j = 0, T = 0, qt = 0, rows = 0;
@@ -772,10 +750,7 @@ __global__ void __launch_bounds__(P8Cfg<NP, LSU>::kThreads, 1)
                     rows = req_rows_in_group(p, it.b, gy);
 #pragma unroll
                     for (int c = 0; c < CW / 2; ++c) l[c] = 0ull;
-                    if (!queries(seg, abort)) {
-                        if (!failed) site = kSiteQFull;
-                        failed = true;
-                    }
+                    wait(&ctrl->q_full, seg & 1, kSiteQFull);
                 }
                 const float* kq = ctrl->kq[seg % kQGens] + cb;
                 const int tok = it.j * kTok + tk, valid = min(kTok, T - it.j * kTok);
@@ -968,6 +943,9 @@ __global__ void __launch_bounds__(P8Cfg<NP, LSU>::kThreads, 1)
                 it.next(p.seq_lens, p.B);
                 if (i + 1 < ntiles && j + 1 < tiles) continue;
                 // ------------------------------------------- the segment's end
+                // The next request's queries first: the score product has read these, and while
+                // the last value product runs there is nothing else to do.
+                if (i + 1 < ntiles) load_q(it.b, (seg + 1) % kQGens, warp - 4, 4 * C::kGroups);
                 // The warps' sums meet in the group's own part of P, which the last value
                 // product has read: CW / 4 numbers in each row.
                 wait(&ctrl->o_done[i & 1], (i >> 1) & 1, kSiteOFinal);
