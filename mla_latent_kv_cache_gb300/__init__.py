@@ -44,6 +44,7 @@ _lock = threading.Lock()
 _lib = None
 _bind = None       # the checks of the short calls (csrc/bind.cpp)
 _addresses = {}    # the entry points that it calls
+_device = None     # what it takes for the current device instead (tests: tensors of the host)
 
 
 class MlaError(RuntimeError):
@@ -453,28 +454,8 @@ def _row_bytes(where, cache_kind, lat_dim) -> int:
     return rb
 
 
-# the current device's number without a look at whether CUDA is up (it is asked where a CUDA tensor is at hand)
-_get_device = getattr(torch._C, "_cuda_getDevice", None)
-
-
 def _current_device() -> int:
-    return torch.cuda.current_device() if _get_device is None else _get_device()
-
-
-def _entry(name):
-    """A library's entry point for the compiled checks: its address, or what stands in for it."""
-    lib = load()
-    return _addresses[name] if lib is _lib else getattr(lib, name)
-
-
-def _place(where, first, names, tensors, stream):
-    """The device that a call runs on, and its stream's handle."""
-    if not _is_cuda(first):
-        _here(where, names, tensors)
-    dev = _current_device()
-    if stream is None and dev >= 0 and _raw_stream is not None:
-        return dev, _raw_stream(dev)
-    return dev, _stream(stream)
+    return torch.cuda.current_device()
 
 
 def _answered(where, answer, names, tensors, rest=()) -> None:
@@ -745,12 +726,11 @@ def mla_rope(x, positions, steps, out, interleaved: bool = False, mscale: float 
     """Rotary positions (include/mla.h): x and out [T, H, R] bf16 or fp32 with
     contiguous last dimensions (views of wider heads, or one and the same tensor),
     positions int32 [T], steps int64 [R / 2] (rope_steps; negated for the way back)."""
-    where, tensors = "mla_rope", (x, positions, steps, out, None)
-    dev, s = _place(where, x, _ROPE_NAMES, tensors, stream)
-    entry = _entry(where)
-    st = _bind.rope(entry, s, dev, x, positions, steps, out, interleaved, mscale)
+    if _bind is None:
+        load()
+    st = _bind.rope(_addresses["mla_rope"], stream, _device, x, positions, steps, out, interleaved, mscale)
     if st != 0:
-        _answered(where, st, _ROPE_NAMES, tensors)
+        _answered("mla_rope", st, _ROPE_NAMES, (x, positions, steps, out, None))
 
 
 _APPEND_NAMES = ("latent", "k_pe", "cu_new_lens", "seq_lens", "block_table", "cache", "-")
@@ -767,14 +747,14 @@ def mla_cache_append(latent, k_pe, cu_new_lens, seq_lens, block_table, page_size
     bf16 [lat_dim]; scales fp32 [pages] for MLA_CACHE_FP8_PAGE_576; rows bf16
     [total, >= lat_dim + 64] takes (latent, key) besides. `status` (a device int32
     tensor) collects status bits."""
-    where, tensors = "mla_cache_append", (latent, k_pe, cu_new_lens, seq_lens, block_table, cache, None)
-    dev, s = _place(where, latent, _APPEND_NAMES, tensors, stream)
-    entry = _entry(where)
-    st = _bind.append(entry, s, dev, latent, k_pe, cu_new_lens, seq_lens, block_table, page_size, cache, cache_kind, steps,
-                      positions, interleaved, mscale, norm_weight, eps, scales, rows, lat_dim, status)
+    if _bind is None:
+        load()
+    st = _bind.append(_addresses["mla_cache_append"], stream, _device, latent, k_pe, cu_new_lens, seq_lens, block_table, page_size,
+                      cache, cache_kind, steps, positions, interleaved, mscale, norm_weight, eps, scales, rows, lat_dim, status)
     if st != 0:
-        _answered(where, st, _APPEND_NAMES, tensors, (("steps", steps), ("positions", positions), ("norm_weight", norm_weight),
-                                                      ("scales", scales), ("rows", rows), ("status", status)))
+        _answered("mla_cache_append", st, _APPEND_NAMES, (latent, k_pe, cu_new_lens, seq_lens, block_table, cache, None),
+                  (("steps", steps), ("positions", positions), ("norm_weight", norm_weight), ("scales", scales), ("rows", rows),
+                   ("status", status)))
 
 
 _PAGE_NAMES = ("q_lat", "q_pe", "cache", "scales", "block_table", "seq_lens", "out", "lse", "workspace", "cu_q_lens")
@@ -787,14 +767,13 @@ def mla_decode_fp8_page(q_lat, q_pe, cache, scales, page_size, block_table, seq_
     fp32 [num_slots / page_size]; tokens is B * q_len, or with cu_q_lens (int32
     [B + 1]) what it counts, at most q_len for each request. workspace:
     mla_decode_workspace_bytes(B, q_len, Hq, num_ctas)."""
-    where = "mla_decode_fp8_page"
-    tensors = (q_lat, q_pe, cache, scales, block_table, seq_lens, out, lse, workspace, cu_q_lens)
-    dev, s = _place(where, q_lat, _PAGE_NAMES, tensors, stream)
-    entry = _entry(where)
-    st = _bind.decode_page(entry, s, dev, q_lat, q_pe, cache, scales, page_size, block_table, seq_lens, q_len, scale, out, lse,
-                           workspace, cu_q_lens, num_ctas)
+    if _bind is None:
+        load()
+    st = _bind.decode_page(_addresses["mla_decode_fp8_page"], stream, _device, q_lat, q_pe, cache, scales, page_size, block_table,
+                           seq_lens, q_len, scale, out, lse, workspace, cu_q_lens, num_ctas)
     if st != 0:
-        _answered(where, st, _PAGE_NAMES, tensors)
+        _answered("mla_decode_fp8_page", st, _PAGE_NAMES,
+                  (q_lat, q_pe, cache, scales, block_table, seq_lens, out, lse, workspace, cu_q_lens))
 
 
 def decode(q_lat, q_pe, cache, cache_kind, page_size, block_table, seq_lens, q_len, scale,

@@ -52,7 +52,8 @@ def _bind_command(out: str) -> list:
     inc, lib = os.path.join(torch, "include"), os.path.join(torch, "lib")
     return ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", "-I", INCLUDE, "-I", inc, "-I",
             os.path.join(inc, "torch", "csrc", "api", "include"), "-I", sysconfig.get_paths()["include"],
-            os.path.join(CSRC, "bind.cpp"), "-o", out, "-L", lib, "-ltorch_python", "-ltorch_cpu", "-lc10"]
+            "-I", os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include"), os.path.join(CSRC, "bind.cpp"), "-o", out, "-L", lib,
+            "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:

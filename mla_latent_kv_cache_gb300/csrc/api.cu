@@ -657,7 +657,8 @@ int mla_rope(const void* x, int64_t x_stride_t, int64_t x_stride_h, const int32_
     const uintptr_t es = f32 ? 4 : 2, xa = reinterpret_cast<uintptr_t>(x), oa = reinterpret_cast<uintptr_t>(out);
     if (xa % es || oa % es || !aligned4(positions) || (reinterpret_cast<uintptr_t>(steps) & 7u)) return MLA_ERR_INVALID_ARG;
     // a grid has a CTA for at least 256 pairs, or for four tokens
-    if (T > INT32_MAX || rot_dim > (1 << 20) || H > (1 << 20) || T * H > (256LL * INT32_MAX) / rot_dim)
+    if (T > INT32_MAX || rot_dim > (1 << 20) || H > (1 << 20) || T * H > (256LL * INT32_MAX) / rot_dim ||
+        static_cast<int64_t>(H) * rot_dim > INT32_MAX)
         return MLA_ERR_UNSUPPORTED;
     mla::RopeParams p;
     // (the stride of a dimension of one entry says nothing)

@@ -5,12 +5,13 @@
 // done here: a call in 17 us became one in 5.
 //
 // Each function takes the library's entry point (its address, or a callable that
-// gets the arguments instead), the stream, the current device (-1: tensors
-// without one) and the call's arguments. It returns the library's status, a text
-// where an argument is refused, or None where one is not a tensor of that device
-// (the binding then says which).
+// gets the arguments instead), the stream (None: PyTorch's current one), a device
+// that stands in for the current one (None as a rule) and the call's arguments. It
+// returns the library's status, a text where an argument is refused, or None where
+// one is not a tensor of the current device (the binding then says which).
 #include <Python.h>
 
+#include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cstdint>
@@ -48,6 +49,33 @@ float real(PyObject* o) {
     const double v = PyFloat_AsDouble(o);
     if (v == -1.0 && PyErr_Occurred()) throw Raised{};
     return static_cast<float>(v);
+}
+
+// Where a call runs: the current device, if `first` is on one.
+struct Place {
+    int64_t dev;
+    void* stream;
+};
+Place place(PyObject* stream, PyObject* dev, PyObject* first) {
+    Place p{};
+    if (dev != Py_None) {
+        p.dev = whole(dev);
+    } else {
+        if (!THPVariable_Check(first) || !THPVariable_Unpack(first).is_cuda()) throw NotThere{};
+        p.dev = c10::cuda::current_device();
+    }
+    if (stream == Py_None) {
+        if (dev == Py_None) p.stream = c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(p.dev)).stream();
+    } else if (PyLong_Check(stream)) {
+        p.stream = PyLong_AsVoidPtr(stream);
+    } else {
+        PyObject* h = PyObject_GetAttrString(stream, "cuda_stream");
+        if (!h) throw Raised{};
+        p.stream = PyLong_AsVoidPtr(h);
+        Py_DECREF(h);
+    }
+    if (PyErr_Occurred()) throw Raised{};
+    return p;
 }
 
 const Tensor& tensor(PyObject* o, int64_t dev) {
@@ -144,10 +172,11 @@ PyObject* guarded(Py_ssize_t n, Py_ssize_t want, F f) {
     }
 }
 
-// call, stream, device, x, positions, steps, out, interleaved, mscale
+// entry, stream, device, x, positions, steps, out, interleaved, mscale
 PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded(n, 9, [&] {
-        const int64_t dev = whole(a[2]);
+        const Place at = place(a[1], a[2], a[3]);
+        const int64_t dev = at.dev;
         const Tensor &x = tensor(a[3], dev), &pos = tensor(a[4], dev), &steps = tensor(a[5], dev), &y = tensor(a[6], dev);
         need(x.dim() == 3, "x must be [T, H, R]");
         const int64_t T = x.size(0), H = x.size(1), R = x.size(2);
@@ -163,15 +192,16 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
         need(H <= INT32_MAX && R <= INT32_MAX, "x must be [T, H, R]");
         return enter(a[0], &mla_rope, x.const_data_ptr(), x.stride(0), x.stride(1), in<int32_t>(pos), in<int64_t>(steps), T,
                      static_cast<int>(H), static_cast<int>(R), f32 ? 1 : 0, small(a[7], "interleaved") ? 1 : 0, real(a[8]), out(y),
-                     y.stride(0), y.stride(1), PyLong_AsVoidPtr(a[1]));
+                     y.stride(0), y.stride(1), at.stream);
     });
 }
 
-// call, stream, device, latent, k_pe, cu_new_lens, seq_lens, block_table, page_size, cache,
+// entry, stream, device, latent, k_pe, cu_new_lens, seq_lens, block_table, page_size, cache,
 // cache_kind, steps, positions, interleaved, mscale, norm_weight, eps, scales, rows, lat_dim, status
 PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded(n, 21, [&] {
-        const int64_t dev = whole(a[2]);
+        const Place at = place(a[1], a[2], a[3]);
+        const int64_t dev = at.dev;
         const Tensor &lat = tensor(a[3], dev), &pe = tensor(a[4], dev), &cu = tensor(a[5], dev), &sl = tensor(a[6], dev),
                      &bt = tensor(a[7], dev), &cache = tensor(a[9], dev);
         const Tensor *steps = maybe(a[11], dev), *pos = maybe(a[12], dev), *norm = maybe(a[15], dev), *scales = maybe(a[17], dev),
@@ -222,15 +252,16 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
                      total, page, in<int32_t>(pos), in<int64_t>(steps), small(a[13], "interleaved") ? 1 : 0, real(a[14]),
                      norm ? norm->const_data_ptr() : nullptr, real(a[16]), out(cache), kind, D, slots,
                      static_cast<float*>(out(scales)), out(rows), rows ? (one ? D + 64 : rows->stride(0)) : 0, st,
-                     PyLong_AsVoidPtr(a[1]));
+                     at.stream);
     });
 }
 
-// call, stream, device, q_lat, q_pe, cache, scales, page_size, block_table, seq_lens, q_len, scale, out, lse,
+// entry, stream, device, q_lat, q_pe, cache, scales, page_size, block_table, seq_lens, q_len, scale, out, lse,
 // workspace, cu_q_lens, num_ctas
 PyObject* decode_page(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded(n, 17, [&] {
-        const int64_t dev = whole(a[2]);
+        const Place at = place(a[1], a[2], a[3]);
+        const int64_t dev = at.dev;
         const Tensor &ql = tensor(a[3], dev), &qp = tensor(a[4], dev), &cache = tensor(a[5], dev), &scales = tensor(a[6], dev),
                      &bt = tensor(a[8], dev), &sl = tensor(a[9], dev), &o = tensor(a[12], dev), &lse = tensor(a[13], dev),
                      &ws = tensor(a[14], dev);
@@ -264,7 +295,7 @@ PyObject* decode_page(PyObject*, PyObject* const* a, Py_ssize_t n) {
                      in<float>(scales), slots, page, tb.at, tb.stride, tb.cols, in<int32_t>(sl), in<int32_t>(cu),
                      static_cast<int>(B), q_len, static_cast<int>(Hq), real(a[11]), out(o),
                      static_cast<int>(f32 ? MLA_OUT_F32 : MLA_OUT_BF16), static_cast<float*>(out(lse)), out(ws), ws.nbytes(), ctas,
-                     PyLong_AsVoidPtr(a[1]));
+                     at.stream);
     });
 }
 

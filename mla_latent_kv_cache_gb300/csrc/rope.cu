@@ -7,6 +7,8 @@
 // the values go through shared memory. A lane holds 16 values of a head in
 // 16-byte vectors placed so that neighbouring lanes read neighbouring vectors
 // (of both halves, or of the interleaved pairs).
+#include <algorithm>
+
 #include "launch.cuh"
 #include "mla_common.cuh"
 #include "rope.cuh"
@@ -74,19 +76,27 @@ __global__ void __launch_bounds__(32 * kRopeWarps) rope_kernel(const RopeParams 
         return NV == 2 ? o + v * half_units : o + (v & 1) * lph + (v >> 1) * half_units;
     };
     Vec<E> a[NV];
-    const int first = i0 + lane;
-    auto load = [&](int it) {
-        const int h = it / lph, o = it - h * lph;
+    // item it is lane o of head h; the warp's next 32 items on
+    const int first = i0 + lane, step_h = 32 / lph, step_o = 32 - step_h * lph;
+    auto next = [&](int& h, int& o) {
+        h += step_h;
+        o += step_o;
+        if (o >= lph) {
+            o -= lph;
+            ++h;
+        }
+    };
+    auto load = [&](int h, int o) {
         const E* src = xt + static_cast<int64_t>(h) * p.x_h;
 #pragma unroll
         for (int v = 0; v < NV; ++v) a[v].raw = reinterpret_cast<const uint4*>(src)[unit(o, v)];
     };
-    if (first < i1) load(first);
+    int h = first / lph, o = first - h * lph;
+    if (first < i1) load(h, o);
     const int64_t pos = __ldg(p.positions + t);
     for (int i = lane; i < p.R / 2; i += 32) table[wl][i] = rope_cos_sin(pos, __ldg(p.steps + i), p.mscale);
     __syncwarp();
     for (int it = first; it < i1; it += 32) {
-        const int h = it / lph, o = it - h * lph;
         E* dst = ot + static_cast<int64_t>(h) * p.o_h;
         Vec<E> y[NV];
         if constexpr (INTER) {
@@ -122,30 +132,40 @@ __global__ void __launch_bounds__(32 * kRopeWarps) rope_kernel(const RopeParams 
                 y[v + NV / 2].pack(g);
             }
         }
-        if (it + 32 < i1) load(it + 32);
+        const int o_now = o;
+        next(h, o);
+        if (it + 32 < i1) load(h, o);
 #pragma unroll
-        for (int v = 0; v < NV; ++v) reinterpret_cast<uint4*>(dst)[unit(o, v)] = y[v].raw;
+        for (int v = 0; v < NV; ++v) reinterpret_cast<uint4*>(dst)[unit(o_now, v)] = y[v].raw;
     }
 }
 
-// Any even R and any alignment: a thread a pair.
+// Any even R and any alignment: a lane a pair at a time, value by value.
 template <typename E>
-__global__ void __launch_bounds__(256) rope_any_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(32 * kRopeWarps) rope_any_kernel(const RopeParams p) {
+    __shared__ float2 table[kRopeWarps][kRopeMostPairs];
     griddep_wait();
     griddep_launch_dependents();
-    const int half = p.R / 2;
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-    if (i >= p.T * p.H * half) return;
-    const int64_t t = i / (static_cast<int64_t>(p.H) * half);
-    const int64_t r = i - t * p.H * half;
-    const int h = static_cast<int>(r / half), k = static_cast<int>(r - static_cast<int64_t>(h) * half);
-    const float2 cs = rope_cos_sin(__ldg(p.positions + t), __ldg(p.steps + k), p.mscale);
-    const E* x = static_cast<const E*>(p.x) + t * p.x_t + h * p.x_h;
-    E* y = static_cast<E*>(p.out) + t * p.o_t + h * p.o_h;
-    const int ia = p.interleaved ? 2 * k : k, ib = p.interleaved ? 2 * k + 1 : k + half;
-    const float a = static_cast<float>(x[ia]), b = static_cast<float>(x[ib]);
-    y[ia] = static_cast<E>(a * cs.x - b * cs.y);
-    y[ib] = static_cast<E>(a * cs.y + b * cs.x);
+    const int lane = threadIdx.x & 31, wl = threadIdx.x >> 5, half = p.R / 2;
+    const int64_t w = static_cast<int64_t>(blockIdx.x) * kRopeWarps + wl;
+    const int64_t t = w / p.chunks;
+    if (t >= p.T) return;
+    const int i0 = static_cast<int>(w - t * p.chunks) * p.items_chunk, i1 = min(p.H * half, i0 + p.items_chunk);
+    const int64_t pos = __ldg(p.positions + t);
+    for (int k = lane; k < min(half, kRopeMostPairs); k += 32) table[wl][k] = rope_cos_sin(pos, __ldg(p.steps + k), p.mscale);
+    __syncwarp();
+    const E* xt = static_cast<const E*>(p.x) + t * p.x_t;
+    E* yt = static_cast<E*>(p.out) + t * p.o_t;
+    for (int i = i0 + lane; i < i1; i += 32) {
+        const int h = i / half, k = i - h * half;
+        const float2 cs = k < kRopeMostPairs ? table[wl][k] : rope_cos_sin(pos, __ldg(p.steps + k), p.mscale);
+        const E* x = xt + static_cast<int64_t>(h) * p.x_h;
+        E* y = yt + static_cast<int64_t>(h) * p.o_h;
+        const int ia = p.interleaved ? 2 * k : k, ib = p.interleaved ? 2 * k + 1 : k + half;
+        const float a = static_cast<float>(x[ia]), b = static_cast<float>(x[ib]);
+        y[ia] = static_cast<E>(a * cs.x - b * cs.y);
+        y[ib] = static_cast<E>(a * cs.y + b * cs.x);
+    }
 }
 
 template <typename E>
@@ -155,20 +175,17 @@ cudaError_t launch(RopeParams& p, int sms, cudaStream_t stream) {
     auto aligned = [&](const void* base, int64_t st, int64_t sh) {
         return reinterpret_cast<uintptr_t>(base) % 16 == 0 && st % n == 0 && sh % n == 0;
     };
-    if (p.R % 16 || p.R > 2 * kRopeMostPairs || !aligned(p.x, p.x_t, p.x_h) || !aligned(p.out, p.o_t, p.o_h)) {
-        const int64_t blocks = (p.T * p.H * (p.R / 2) + 255) / 256;
-        cudaLaunchConfig_t cfg = pdl_config(dim3(static_cast<unsigned>(blocks)), 256, 0, stream, attr);
-        return cudaLaunchKernelEx(&cfg, rope_any_kernel<E>, p);
-    }
+    const bool any = p.R % 16 || p.R > 2 * kRopeMostPairs || !aligned(p.x, p.x_t, p.x_h) || !aligned(p.out, p.o_t, p.o_h);
     // a token's heads are shared out between as many warps as fill the GPU twice
-    const int64_t items = static_cast<int64_t>(p.H) * (p.R / 16);
+    const int64_t items = static_cast<int64_t>(p.H) * (any ? p.R / 2 : p.R / 16);
     const int64_t turns = (items + 31) / 32;
-    const int64_t want = (static_cast<int64_t>(sms) * 32 + p.T - 1) / p.T;
-    const int64_t per = (turns + (want < turns ? want : turns) - 1) / (want < turns ? want : turns);
+    const int64_t want = std::min((static_cast<int64_t>(sms) * 32 + p.T - 1) / p.T, turns);
+    const int64_t per = (turns + want - 1) / want;
     p.items_chunk = static_cast<int>(per * 32);
     p.chunks = static_cast<int>((turns + per - 1) / per);
     const int64_t blocks = (p.T * p.chunks + kRopeWarps - 1) / kRopeWarps;
     cudaLaunchConfig_t cfg = pdl_config(dim3(static_cast<unsigned>(blocks)), 32 * kRopeWarps, 0, stream, attr);
+    if (any) return cudaLaunchKernelEx(&cfg, rope_any_kernel<E>, p);
     return p.interleaved ? cudaLaunchKernelEx(&cfg, rope_kernel<E, true>, p)
                          : cudaLaunchKernelEx(&cfg, rope_kernel<E, false>, p);
 }

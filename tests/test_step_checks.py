@@ -29,7 +29,8 @@ def fake(monkeypatch, lib):
     monkeypatch.setattr(m, "_current_device", lambda: -1)  # what a host tensor gives as its device
     monkeypatch.setattr(m, "load", lambda: rec)
     monkeypatch.setattr(m, "_stream", lambda s: 0)
-    monkeypatch.setattr(m, "_raw_stream", None)
+    monkeypatch.setattr(m, "_device", -1)
+    monkeypatch.setattr(m, "_addresses", {n: getattr(rec, n) for n in ("mla_rope", "mla_cache_append", "mla_decode_fp8_page")})
     return rec
 
 
@@ -96,7 +97,7 @@ def test_rope_refuses(lib, over):
 def test_rope_limits_and_empty_calls(lib):
     assert lib.mla_rope(*_with(ROPE, T=0, x=None)) == OK
     assert lib.mla_rope(*_with(ROPE, H=0, x=None)) == OK
-    for over in (dict(T=1 << 31), dict(R=(1 << 20) + 2), dict(H=(1 << 20) + 1), dict(x_t=(1 << 30) + 8), dict(T=1 << 30, H=1 << 10)):
+    for over in (dict(T=1 << 31), dict(R=(1 << 20) + 2), dict(H=(1 << 20) + 1), dict(x_t=(1 << 30) + 8), dict(T=1 << 30, H=1 << 10), dict(T=1, H=1 << 20, R=1 << 12)):
         assert lib.mla_rope(*_with(ROPE, **over)) == UNSUPPORTED
 
 
@@ -231,6 +232,7 @@ def test_missing_tensors_and_other_devices_are_refused(fake, monkeypatch):
         _refused(lambda: _decode(**{name: None}), f"{name} must be a CUDA tensor")
     _refused(lambda: _decode(cu_q_lens=5), "CUDA tensor")
     monkeypatch.setattr(m, "_current_device", lambda: 1)
+    monkeypatch.setattr(m, "_device", 1)
     for call in (_rope, _append, _decode):
         _refused(call, "the current device is cuda:1")
     assert fake.calls == []
