@@ -377,13 +377,16 @@ __global__ void __launch_bounds__(32 * kAppendWarps, 3) append_page_kernel(const
     const int64_t item = static_cast<int64_t>(blockIdx.x) * kItems + grp;
     const int ps = p.page_size;
     auto first_item = [&](int b) { return static_cast<int64_t>(a_cu(p, b) / ps) + 2 * static_cast<int64_t>(b); };
-    int lo = 0, hi = p.B;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (first_item(mid) <= item) lo = mid;
-        else hi = mid;
+    // the last b with first_item(b) <= item, 32 probes at a time
+    int b = 0;
+    for (int left = p.B; left > 1;) {
+        const int step = (left + 31) / 32, off = lane * step;
+        const int hits = __popc(__ballot_sync(0xffffffffu, off < left && first_item(b + off) <= item));
+        const int at = max(hits - 1, 0) * step;
+        b += at;
+        left = min(step, left - at);
     }
-    const int b = lo, c0 = a_cu(p, b), n = a_cu(p, b + 1) - c0;
+    const int c0 = a_cu(p, b), n = a_cu(p, b + 1) - c0;
     if (n <= 0) return;  // (the whole group leaves)
     // places p0 .. p1 - 1 are new; those below 0 have none
     const int64_t p1 = max(__ldg(p.seq_lens + b), 0), p0 = p1 - n;
