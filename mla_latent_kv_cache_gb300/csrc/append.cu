@@ -67,6 +67,30 @@ __device__ __forceinline__ F2 squares(F2 s, const F2 (&f)[4]) {
     return s;
 }
 
+// One step of a sum of several numbers over a warp at once: a lane keeps half of its
+// N numbers and hands the other half to the lane `bit` away, so that all of them
+// together take N - 1 shuffles until a lane has one, where one by one they take five each.
+template <int N>
+__device__ __forceinline__ void halve(float (&v)[N], int bit, int lane) {
+    const bool up = (lane & bit) != 0;
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+        const float keep = up ? v[i + N / 2] : v[i], give = up ? v[i] : v[i + N / 2];
+        v[i] = keep + __shfl_xor_sync(0xffffffffu, give, bit);
+    }
+}
+
+// The sums over a warp of eight numbers: lane L gets number L / 4's.
+__device__ __forceinline__ float sums_of(float (&v)[8], int lane) {
+    halve(v, 16, lane);
+    float a[4] = {v[0], v[1], v[2], v[3]};
+    halve(a, 8, lane);
+    float b[2] = {a[0], a[1]};
+    halve(b, 4, lane);
+    float r = b[0] + __shfl_xor_sync(0xffffffffu, b[0], 2);
+    return r + __shfl_xor_sync(0xffffffffu, r, 1);
+}
+
 // 1 / rms from a lane's sum of squares; a whole warp.
 __device__ __forceinline__ float norm_factor(F2 squares, float per, float eps) {
     const float2 v = un2(squares);
@@ -370,7 +394,8 @@ template <int W>
 __global__ void __launch_bounds__(32 * kAppendWarps, 3) append_page_kernel(const AppendParams p) {
     constexpr int kItems = kAppendWarps / W;  // pages a CTA
     extern __shared__ uint8_t held_raw[];
-    __shared__ float tops[kAppendWarps], factors[kAppendWarps][kHold];
+    __shared__ float tops[kAppendWarps];
+    __shared__ alignas(16) float factors[kAppendWarps][kHold];
     griddep_wait();
     griddep_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, wi = warp % W, grp = warp / W;
@@ -456,15 +481,49 @@ __global__ void __launch_bounds__(32 * kAppendWarps, 3) append_page_kernel(const
     };
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     __syncwarp();
-#pragma unroll 2
+    // Sums of squares and largest magnitudes of the held tokens: one pass, and one
+    // reduction for all of them.
+    float sq[kHold], mx[kHold];
+#pragma unroll
     for (int k = 0; k < kHold; ++k) {
         const int x = wi + k * W;
-        if (x >= m) break;
+        sq[k] = mx[k] = 0.f;
+        if (x >= m) continue;
         const uint4* lat = reinterpret_cast<const uint4*>(held + k * kHeldRow);
         F2 f[2][4];
-        const float fac = weighed(lat[lane], lat[lane + 32], f, true);
-        if (lane == 0) factors[warp][k] = fac;
-        largest(f, fac, angle.turn(p, load_pair(lat + 64, p.interleaved, lane), position(x), lane), x);
+        unpack8(lat[lane], f[0]);
+        unpack8(lat[lane + 32], f[1]);
+        if (p.norm) {
+            const float2 v = un2(squares(squares(f2(0.f, 0.f), f[0]), f[1]));
+            sq[k] = v.x + v.y;
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) f[u][i] = mul2(f[u][i], w[u][i]);
+        }
+        const float2 e = angle.turn(p, load_pair(lat + 64, p.interleaved, lane), position(x), lane);
+        if (x < skip) continue;
+        mx[k] = most_abs(most_abs(0.f, f[0]), f[1]);
+        top = fmaxf(top, fmaxf(fabsf(e.x), fabsf(e.y)));
+    }
+    {
+        const float total = sums_of(sq, lane);  // lane L: token L / 4's
+        if ((lane & 3) == 0) factors[warp][lane >> 2] = p.norm ? rsqrtf(total * (1.f / kD) + p.eps) : 1.f;
+        __syncwarp();
+        const float4 a = *reinterpret_cast<const float4*>(factors[warp]), c = *reinterpret_cast<const float4*>(factors[warp] + 4);
+        const float fac[8] = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
+#pragma unroll
+        for (int k = 0; k < kHold; ++k) top = fmaxf(top, mx[k] * fac[k]);  // (rounding keeps the order; NaN is left out)
+        if (__any_sync(0xffffffffu, !(top < INFINITY))) {
+            // an infinity among them: the largest of the finite ones, value by value
+            top = 0.f;
+            for (int k = 0, x = wi; k < kHold && x < m; ++k, x += W) {
+                const uint4* lat = reinterpret_cast<const uint4*>(held + k * kHeldRow);
+                F2 f[2][4];
+                weighed(lat[lane], lat[lane + 32], f, false);
+                largest(f, factors[warp][k], angle.turn(p, load_pair(lat + 64, p.interleaved, lane), position(x), lane), x);
+            }
+        }
     }
     for (int x = wi + kHold * W; x < m; x += W) {  // pages of more rows than the warps hold: read twice
         const uint4* lat = reinterpret_cast<const uint4*>(p.latent + (t0 + x) * p.lat_st);
