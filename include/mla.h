@@ -593,7 +593,7 @@ MLA_API int mla_static_scratch_status(int32_t* dst, int n, void* stream);
 
 /*
  * mla_test_hold_next_decode - test support for the device-side failure path.
- * The next mla_decode call in this process withholds its first hand-off from
+ * The next mla_decode (or mla_decode_fp8_page) call in this process withholds its first hand-off from
  * the softmax warps to the PV issuers, so their bounded wait gives up after
  * about one second: the call's status word then has bit 1 set (words 1..11
  * name the wait site and role), its outputs are invalid, and the device

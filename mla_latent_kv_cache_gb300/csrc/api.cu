@@ -104,7 +104,7 @@ int ws_ctas(int num_ctas, int sms) { return num_ctas > 0 ? (num_ctas < 2 ? 2 : n
 size_t decode_ws_bytes(int B, int HQ, int ctas, int D = 512) { return decode_ws_layout(B, HQ, ctas, D).total; }
 
 // Set by mla_test_hold_next_decode (1) or mla_test_slow_pv_next_decode (2),
-// consumed by the next mla_decode.
+// consumed by the next mla_decode or mla_decode_fp8_page.
 std::atomic<int> g_test_hold{0};
 
 // Set by mla_test_limit_next_evict, consumed by the next mla_cache_evict.
@@ -861,6 +861,7 @@ int mla_decode_fp8_page(const void* q_lat, const void* q_pe, int64_t total_q_tok
     p.total_q = static_cast<int>(total_q_tokens);
     p.lat_dim = mla::kD;
     p.rope_dim = mla::kP;
+    p.test_hold = g_test_hold.exchange(0);
     const cudaError_t e = mla::launch_decode_page8(maps, p, NP, lsu, W, GY, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }

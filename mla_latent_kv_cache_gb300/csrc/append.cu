@@ -158,11 +158,11 @@ __device__ __forceinline__ uint32_t codes4(F2 a, F2 b) {
     return lo | hi << 16;
 }
 
-// x / s correctly rounded for s within 2^-100 .. 2^100, with y = 1 / s correctly
+// x / s correctly rounded for s within 2^-89 .. 2^82, with y = 1 / s correctly
 // rounded, by Markstein's correction (P. Markstein, Computation of elementary
 // functions on the IBM RISC System/6000 processor, 1990): the remainder of
 // x y is exact in one fused step. It is taken as q s - x, so that a zero keeps its
-// sign. (Where x is so small that the remainder underflows, the code is 0 anyway.)
+// sign. (Where x is so small that the remainder is not exact, below 2^-10 s, the code is 0 anyway.)
 __device__ __forceinline__ F2 div2(F2 x, F2 minus_x, F2 s, F2 y, F2 minus_y) {
     const F2 q = mul2(x, y);
     return fma2(fma2(q, s, minus_x), minus_y, q);
@@ -256,7 +256,7 @@ __device__ __forceinline__ void put_token(const AppendParams& p, int64_t t, cons
         for (int o = 1; o < 8; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
         float scale;
         uint32_t code[4];
-        if (top > 0x1p-90f && top < 0x1p90f) {
+        if (top > 0x1p-80f && top < 0x1p90f) {
             const float q = top * (1.f / 448.f);
             scale = fmaf(fmaf(q, 448.f, -top), -1.f / 448.f, q);  // top / 448, correctly rounded (see div2)
             if (p.norm) {

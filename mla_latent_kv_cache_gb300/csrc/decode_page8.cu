@@ -938,7 +938,7 @@ __global__ void __launch_bounds__(P8Cfg<NP, LSU>::kThreads, 1)
                 fence_proxy_async_smem();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&ctrl->p_full[i & 1]);
+                if (lane == 0 && (p.test_hold != 1 || i > 0)) mbar_arrive(&ctrl->p_full[i & 1]);  // (test hook: a hand-off that never comes)
                 const int b = it.b, tiles = it.tiles, j = it.j;
                 it.next(p.seq_lens, p.B);
                 if (i + 1 < ntiles && j + 1 < tiles) continue;

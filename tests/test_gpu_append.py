@@ -281,7 +281,7 @@ def test_values_that_are_not_finite():
 @pytest.mark.parametrize("kind", [BF16, FP8, PAGE])
 def test_zeros_and_extremes(kind):
     """Rows of zeros, the smallest and the largest values of a trained layer."""
-    for loud in (0.0, 2.0 ** -60, 2.0 ** -30, 2.0 ** 30):
+    for loud in (0.0, 2.0 ** -110, 2.0 ** -75, 2.0 ** -30, 2.0 ** 30):
         run(Case([40, 1], [0, 3], 16, kind, norm=False, turn=False, seed=8, loud=loud))
     run(Case([40, 1], [0, 3], 16, kind, norm=True, seed=8, loud=0.0))
 
@@ -330,6 +330,32 @@ def test_tokens_without_a_place(kind):
             touched = np.unique(slots // 8)
             other = np.setdiff1d(np.arange(c.pages), touched)
             assert np.array_equal(c.scales.cpu().numpy()[other], scales0.cpu().numpy()[other])
+
+
+@pytest.mark.parametrize("kind", [BF16, FP8, PAGE])
+def test_thousands_of_requests(kind):
+    """More of them than one round of probes looks at, most without a token."""
+    r = np.random.default_rng(7)
+    new = r.choice([0, 0, 0, 1, 2, 17], size=2500)
+    run(Case(list(new), list(r.integers(0, 40, size=2500)), 16, kind, seed=7, dense=False))
+
+
+@pytest.mark.parametrize("norm", [True, False])
+def test_small_and_large_blocks_of_one_row(norm):
+    """656-byte rows whose blocks lie hundreds of powers of two apart, zeros of both signs among them."""
+    c = Case([40], [0], 16, FP8, norm=norm, turn=False, seed=13)
+    x = torch.randn((40, 4, 128), device=DEV) * torch.tensor([2.0 ** -118, 2.0 ** -84, 1.0, 2.0 ** 50], device=DEV)[:, None]
+    if norm:
+        x = x[:, [0, 1, 1, 1]]
+    x[3, 1, 7], x[4, 2, 9] = -0.0, 0.0
+    c.proj[:, :512] = x.reshape(40, 512).to(torch.bfloat16)
+    if norm:
+        run(c)
+        return
+    other = c.cache.clone()
+    c.go()
+    m.mla_cache_write(c.proj[:, :512], c.proj[:, 512:], torch.from_numpy(c.slots(0, np.arange(40))).to(DEV), other, FP8)
+    assert torch.equal(c.cache, other)
 
 
 def test_padded_batches_and_empty_calls():

@@ -120,7 +120,7 @@ class Batch:
                 off = np.abs(got_o[r] - want_o[r])
                 assert (off <= room + half * np.abs(want_o[r])).all(), (b, r, (off / np.maximum(room, 1e-300)).max())
                 assert abs(got_l[r] - want_l[r]) <= ds + 2.0 ** -20 * abs(want_l[r]) + 2.0 ** -20, (b, r, got_l[r], want_l[r], ds)
-                worst = max(worst, (off / room).max())
+                worst = max(worst, (off / np.maximum(room, 1e-300)).max())
         return worst
 
 
@@ -300,6 +300,51 @@ def test_offsets_past_32_bits():
     a.dev["table"] = torch.where(a.dev["table"] >= 0, a.dev["table"] + shift, a.dev["table"])
     a.dev["cache"] = big
     assert torch.equal(a.go()[0], out)
+
+
+@pytest.mark.parametrize("B", [319, 321, 700])
+@pytest.mark.parametrize("Hq,q_len", [(16, 1), (64, 1)])
+def test_many_requests(B, Hq, q_len):
+    """More requests than a CTA has threads, and as many."""
+    r = np.random.default_rng(B)
+    run(Batch(list(r.choice([0, 1, 5, 130, 300], size=B)), Hq, q_len, 16, seed=B))
+
+
+def test_rows_that_no_request_names_are_left_as_they_were():
+    b = Batch([300, 2, 129], 16, 4, 16, seed=15, q_lens=[1, 4, 2])
+    d = b.upload()
+    pad = 5
+    for name in ("q_lat", "q_pe", "out", "lse"):
+        t = d[name]
+        d[name] = torch.cat([t, torch.full((pad, *t.shape[1:]), 7.0, dtype=t.dtype, device=DEV)])
+    out, lse, ws = b.go()
+    torch.cuda.synchronize()
+    assert m.device_status(ws) == 0
+    b.check(out, lse)
+    assert bool((out[-pad:] == 7.0).all()) and bool((lse[-pad:] == 7.0).all())
+
+
+def test_a_workspace_that_is_too_small_is_refused():
+    b = Batch([300], 16, 1, 16, seed=16)
+    need = m.mla_decode_workspace_bytes(1, 1, 16)
+    with pytest.raises(m.MlaError) as e:
+        b.go(ws=torch.empty(need - 256, dtype=torch.uint8, device=DEV))
+    assert e.value.status == m.MLA_ERR_WORKSPACE
+
+
+@pytest.mark.parametrize("Hq,page", [(16, 16), (32, 16), (64, 64), (16, 3)])
+def test_a_wait_that_runs_out_is_reported(Hq, page):
+    """A hand-off that never comes: the call ends after about a second with status bit 1,
+    and the next one is right."""
+    b = Batch([3000, 700], Hq, 1, page, seed=17)
+    want = b.go()[0].clone()
+    m.test_hold_next_decode()
+    ws = b.go()[2]
+    torch.cuda.synchronize()
+    assert m.device_status(ws) & 1
+    out, _, ws = b.go()
+    torch.cuda.synchronize()
+    assert m.device_status(ws) == 0 and torch.equal(out, want)
 
 
 def test_one_long_request():
