@@ -671,19 +671,19 @@ int mla_rope(const void* x, int64_t x_stride_t, int64_t x_stride_h, const int32_
         if (s > (1LL << 30)) return MLA_ERR_UNSUPPORTED;
     }
     // heads of a token, then tokens, or the other way round: rows apart either way
-    auto rows_apart = [&](int64_t st, int64_t sh) {
-        return T == 1 || H == 1 || st >= sh * (H - 1) + rot_dim || sh >= st * (T - 1) + rot_dim;
+    auto rows_apart = [&](int64_t st, int64_t sh, int64_t width) {
+        return T == 1 || H == 1 || st >= sh * (H - 1) + width || sh >= st * (T - 1) + width;
     };
-    if (!rows_apart(p.x_t, p.x_h) || !rows_apart(p.o_t, p.o_h)) return MLA_ERR_INVALID_ARG;
+    if (!rows_apart(p.x_t, p.x_h, rot_dim) || !rows_apart(p.o_t, p.o_h, rot_dim)) return MLA_ERR_INVALID_ARG;
     if (xa != oa || p.x_t != p.o_t || p.x_h != p.o_h) {
         // not the same view: apart, or other values of the same heads
         const uintptr_t xe = xa + es * ((T - 1) * p.x_t + (H - 1) * p.x_h + rot_dim);
         const uintptr_t oe = oa + es * ((T - 1) * p.o_t + (H - 1) * p.o_h + rot_dim);
         if (xa < oe && oa < xe) {
-            const uintptr_t d = (xa > oa ? xa - oa : oa - xa) / es;
+            const int64_t d = static_cast<int64_t>((xa > oa ? xa - oa : oa - xa) / es);
             const int64_t step = H > 1 ? (T > 1 ? std::min(p.x_t, p.x_h) : p.x_h) : p.x_t;
-            if (p.x_t != p.o_t || p.x_h != p.o_h || (xa - oa) % es || d < static_cast<uintptr_t>(rot_dim) ||
-                d + rot_dim > static_cast<uintptr_t>(step))
+            if (p.x_t != p.o_t || p.x_h != p.o_h || d < rot_dim || d + rot_dim > step ||
+                !rows_apart(p.x_t, p.x_h, d + rot_dim))
                 return MLA_ERR_INVALID_ARG;
         }
     }

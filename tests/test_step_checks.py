@@ -86,6 +86,8 @@ ROPE_BAD = [
     dict(out=4096 + 64), dict(out=4096 + 128), dict(out=4096, o_h=128, o_t=1024),             # overlaps its input
     dict(out=4096 + 2 * 65, x_h=192, o_h=192, x_t=1536, o_t=1536, R=66),
     dict(out=4096 + 2 * 150, x_h=192, o_h=192, x_t=1536, o_t=1536),                            # runs into the next head
+    dict(out=4096 + 2 * 64, x_h=192, o_h=192, x_t=1408, o_t=1408),                             # or a token's last into the next token
+    dict(out=4096 + 2 * 64, x_h=1792, o_h=1792, x_t=192, o_t=192),                             # (heads outermost)
 ]
 
 
