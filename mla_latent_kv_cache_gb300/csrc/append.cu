@@ -9,14 +9,14 @@
 // go out before the request, its length and its page are looked up.
 //
 // Prompts are near the rate at which instructions issue as well (unpacking, the
-// norm, the rotation and the rounding are some 290 of them a token), hence packed
+// norm, the rotation and the rounding are some 260 of them a token), hence packed
 // fp32 instructions, a reduction for several tokens at once, one sine and cosine
 // for four positions, and tokens that wait in shared memory instead of registers.
-// Measured: 98,304 tokens into 656-byte rows 36 us (4.9 TB/s, 0.73 of the copy
+// Measured: 98,304 tokens into 656-byte rows 31 us (5.7 TB/s, 0.84 of the copy
 // rate), 52,106 tokens of 16 prompts into page rows, with dense rows besides, 34 us
 // (0.65, issue slots 57% busy), 64 requests with a token each 3.7 us.
 //
-// bf16 and fp8_ds_mla rows: a warp a token, or four for prompts. Page rows (one scale for all rows of
+// bf16 and fp8_ds_mla rows: a warp a token, or for prompts a stream of them. Page rows (one scale for all rows of
 // a page): the warps of a page hold its new tokens in registers, meet for the
 // largest value, and write when the scale is known, so a token's input is read
 // once. The scale is a power of two: e4m3 values keep their 4 significant bits
@@ -105,7 +105,7 @@ __device__ __forceinline__ float norm_factor(F2 squares, float per, float eps) {
     float s = v.x + v.y;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    return rsqrtf(s * per + eps);
+    return rsqrtf(fmaf(s, per, eps));
 }
 
 // A lane's norm weights of the 16-byte unit u (1 without a norm).
@@ -122,10 +122,15 @@ __device__ __forceinline__ uint32_t load_pair(const void* pe, int interleaved, i
     return a | b << 16;
 }
 
+__device__ __forceinline__ float2 turned(float a, float b, float2 cs) {
+    return make_float2(fmaf(a, cs.x, -__fmul_rn(b, cs.y)), fmaf(a, cs.y, __fmul_rn(b, cs.x)));
+}
+
 // The angles of a warp's tokens, every DELTA-th, for the lane's pair. Most
 // positions follow each other, and a turn by DELTA positions more is four
 // instructions instead of another sine and cosine. It is off by some 2^-22 each
 // time, so every fourth is formed anew.
+// (The fused steps are written out, so that every kernel rounds alike.)
 template <int DELTA>
 struct Angle {
     int pos;
@@ -135,7 +140,7 @@ struct Angle {
         const float a = bf16_lo(pe), b = bf16_hi(pe);
         if (!p.steps) return make_float2(a, b);
         if (left > 0 && at == pos + DELTA) {
-            cs = make_float2(cs.x * step.x - cs.y * step.y, cs.x * step.y + cs.y * step.x);
+            cs = turned(cs.x, cs.y, step);
             --left;
         } else {
             const int64_t f = __ldg(p.steps + lane);
@@ -144,7 +149,7 @@ struct Angle {
             left = 3;
         }
         pos = at;
-        return make_float2(a * cs.x - b * cs.y, a * cs.y + b * cs.x);
+        return turned(a, b, cs);
     }
 };
 
@@ -325,54 +330,73 @@ __global__ void __launch_bounds__(32 * kAppendWarps) append_kernel(const AppendP
     put_token<KIND, D>(p, t, at, lat, w, angle.turn(p, pair, at.pos, lane), lane);
 }
 
-// Prompts: a warp kMany consecutive tokens, all of them on their way to shared
-// memory while lane n looks up where the n-th goes.
-constexpr int kMany = 4;
+// Prompts: a CTA a run of tokens, as long as lets all CTAs run at once, its warps
+// every eighth of it. Each has kMany on their way to shared memory, and looks 32 up at
+// once, a lane each. (98,304 tokens into 656-byte rows: 31.1 us; with a run a warp
+// 31.7; runs for twice as many CTAs 37 against 35.4; kMany 2 31.1, 4 31.9; four CTAs
+// an SM, whose 64 registers a thread spill, 34.8; a CTA for every 32 tokens, all of
+// them asked for at once, 36.)
+constexpr int kMany = 3;
 template <int D>
 constexpr int many_smem() {
     return kAppendWarps * kMany * 2 * (D + kP);
 }
+constexpr int kManyCtas = 3;  // CTAs an SM holds
 
 template <int KIND, int D>
-__global__ void __launch_bounds__(32 * kAppendWarps) append_many_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(32 * kAppendWarps, kManyCtas) append_many_kernel(const AppendParams p, int per) {
     constexpr int U = D / 256, held_row = 2 * (D + kP);
     extern __shared__ uint8_t held_raw[];
+    __shared__ Where ways[kAppendWarps][32];
     griddep_wait();
     griddep_launch_dependents();
     const int lane = threadIdx.x & 31;
-    const int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kAppendWarps + (threadIdx.x >> 5)) * kMany;
-    if (t0 >= p.total) return;
-    const int m = static_cast<int>(min(static_cast<int64_t>(kMany), p.total - t0));
-    uint8_t* held = held_raw + (threadIdx.x >> 5) * kMany * held_row;
-    for (int n = 0; n < m; ++n) {
-        const __nv_bfloat16* src = p.latent + (t0 + n) * p.lat_st + lane * 8;
-        const uint32_t dst = smem_u32(held + n * held_row) + lane * 16;
+    // token n of the warp is t0 + n kAppendWarps
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * per, t0 = first + (threadIdx.x >> 5);
+    const int m = static_cast<int>((min(first + per, p.total) - t0 + kAppendWarps - 1) / kAppendWarps);
+    if (m <= 0) return;
+    const uint8_t* held = held_raw + (threadIdx.x >> 5) * kMany * held_row;
+    const uint32_t to = smem_u32(held) + lane * 16;
+    const __nv_bfloat16 *lat_at = p.latent + t0 * p.lat_st + lane * 8, *pe_at = p.k_pe + t0 * p.pe_st + lane * 8;
+    int fetched = 0;
+    auto fetch = [&]() {  // the next token, if any
+        if (fetched < m) {
+            const uint32_t dst = to + (fetched % kMany) * held_row;
 #pragma unroll
-        for (int k = 0; k < U; ++k) a_cp16(dst + 512 * k, src + 256 * k);
-        if (lane < 8) a_cp16(dst + 2 * D, p.k_pe + (t0 + n) * p.pe_st + lane * 8);
-    }
-    asm volatile("cp.async.commit_group;" ::: "memory");
+            for (int k = 0; k < U; ++k) a_cp16(dst + 512 * k, lat_at + 256 * k);
+            if (lane < 8) a_cp16(dst + 2 * D, pe_at);
+            lat_at += kAppendWarps * p.lat_st;
+            pe_at += kAppendWarps * p.pe_st;
+            ++fetched;
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll
+    for (int n = 0; n < kMany; ++n) fetch();
     F2 w[U][4];
 #pragma unroll
     for (int k = 0; k < U; ++k) weights8(p, a_unit<KIND>(lane, k), w[k]);
-    __shared__ Where ways[kAppendWarps][kMany];
-    const Where mine = locate<KIND, D>(p, t0 + min(lane, m - 1));
     Where* way = ways[threadIdx.x >> 5];
-    if (lane < m) way[lane] = mine;
-    if (__any_sync(0xffffffffu, mine.named && mine.row < 0) && lane == 0 && p.status) atomicOr(p.status, kErrBadBlock);
-    Angle<1> angle;
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
-    __syncwarp();
+    Angle<kAppendWarps> angle;
 #pragma unroll 1
     for (int n = 0; n < m; ++n) {
-        const Where at = way[n];
-        if (!at.named) continue;
-        const uint4* src = reinterpret_cast<const uint4*>(held + n * held_row);
+        if ((n & 31) == 0) {
+            const Where mine = locate<KIND, D>(p, t0 + min(n + lane, m - 1) * kAppendWarps);
+            way[lane] = mine;
+            if (__any_sync(0xffffffffu, mine.named && mine.row < 0) && lane == 0 && p.status) atomicOr(p.status, kErrBadBlock);
+        }
+        asm volatile("cp.async.wait_group %0;" ::"n"(kMany - 1) : "memory");
+        __syncwarp();
+        const Where at = way[n & 31];
+        const uint4* src = reinterpret_cast<const uint4*>(held + (n % kMany) * held_row);
         uint4 lat[U];
 #pragma unroll
         for (int k = 0; k < U; ++k) lat[k] = src[a_unit<KIND>(lane, k)];
         const uint32_t pair = load_pair(src + D / 8, p.interleaved, lane);
-        put_token<KIND, D>(p, t0 + n, at, lat, w, angle.turn(p, pair, at.pos, lane), lane);
+        __syncwarp();
+        fetch();
+        if (!at.named) continue;
+        put_token<KIND, D>(p, t0 + n * kAppendWarps, at, lat, w, angle.turn(p, pair, at.pos, lane), lane);
     }
 }
 
@@ -516,7 +540,7 @@ __global__ void __launch_bounds__(32 * kAppendWarps, 3) append_page_kernel(const
     }
     {
         const float total = sums_of(sq, lane);  // lane L: token L / 4's
-        if ((lane & 3) == 0) factors[warp][lane >> 2] = p.norm ? rsqrtf(total * (1.f / kD) + p.eps) : 1.f;
+        if ((lane & 3) == 0) factors[warp][lane >> 2] = p.norm ? rsqrtf(fmaf(total, 1.f / kD, p.eps)) : 1.f;
         __syncwarp();
         const float4 a = *reinterpret_cast<const float4*>(factors[warp]), c = *reinterpret_cast<const float4*>(factors[warp] + 4);
         const float fac[8] = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
@@ -642,21 +666,23 @@ cudaError_t launch_append(const AppendParams& p, int kind, int lat_dim, int sms,
                : W == 4 ? go(append_page_kernel<4>, 2)
                         : go(append_page_kernel<8>, 3);
     }
-    // four tokens a warp where every SM still gets its 32 warps (with eight, fewer
-    // fit an SM: 98,304 tokens 44 us, against 36)
-    const bool many = p.total >= static_cast<int64_t>(kMany) * 32 * sms && lat_dim <= 768;
-    const int64_t per = static_cast<int64_t>(kAppendWarps) * (many ? kMany : 1), blocks = (p.total + per - 1) / per;
+    // Runs where every warp that fits gets kMany tokens or more (11,008 tokens into
+    // 656-byte rows: 5.9 us, 6.1 with a warp a token; 4,096: 4.0 and 3.7)
+    const int64_t held = static_cast<int64_t>(sms) * kManyCtas, share = (p.total + held - 1) / held;
+    const bool many = share >= kAppendWarps * kMany && lat_dim <= 768;
+    const int64_t each = many ? share : kAppendWarps, blocks = (p.total + each - 1) / each;
     static std::atomic<uint64_t> done[4];
-    auto go = [&](auto* k, int smem, int i) {
+    auto go = [&](auto* k, int smem, int i, auto... more) {
         if (smem > 0) {
             const cudaError_t e = attribute_once(done[i], reinterpret_cast<const void*>(k),
                                                  cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
             if (e != cudaSuccess) return e;
         }
         cudaLaunchConfig_t cfg = pdl_config(dim3(static_cast<unsigned>(blocks)), 32 * kAppendWarps, smem, stream, attr);
-        return cudaLaunchKernelEx(&cfg, k, p);
+        return cudaLaunchKernelEx(&cfg, k, p, more...);
     };
-#define MLA_APPEND(K, DV, I) (many ? go(append_many_kernel<K, DV>, many_smem<DV>(), I) : go(append_kernel<K, DV>, 0, I))
+#define MLA_APPEND(K, DV, I) \
+    (many ? go(append_many_kernel<K, DV>, many_smem<DV>(), I, static_cast<int>(share)) : go(append_kernel<K, DV>, 0, I))
     if (kind == MLA_CACHE_FP8_DS_MLA_656) return MLA_APPEND(MLA_CACHE_FP8_DS_MLA_656, 512, 0);
     return lat_dim == 256   ? MLA_APPEND(MLA_CACHE_BF16_576, 256, 1)
            : lat_dim == 512 ? MLA_APPEND(MLA_CACHE_BF16_576, 512, 2)

@@ -188,6 +188,48 @@ def test_long_prompts_without_norm_equal_the_separate_calls(kind):
     assert torch.equal(c.cache, other)
 
 
+@pytest.mark.parametrize("kind,D", [(BF16, 256), (BF16, 512), (BF16, 768), (FP8, 512)])
+def test_a_very_long_call_equals_short_ones(kind, D):
+    """Tokens are independent of each other in these rows: one call for 130,000 of them
+    and calls for pieces give the same bits (positions that do not follow each
+    other, so every angle is formed for itself). Rows behind the last token stay."""
+    c = Case([90001, 0, 39000, 17], [5, 9, 0, 300], 64, kind, D=D, seed=13, pad=700, given=True)
+    other, rows = c.cache.clone(), c.rows.clone()
+    c.go()
+    t = 0
+    for b, (n, p) in enumerate(zip(c.new.tolist(), c.before.tolist())):
+        for i in range(0, n, 9000):
+            k = min(9000, n - i)
+            cu = torch.tensor([0, k], dtype=torch.int32, device=DEV)
+            lens = torch.tensor([p + i + k], dtype=torch.int32, device=DEV)
+            at = slice(t + i, t + i + k)
+            m.mla_cache_append(c.proj[at, :D], c.proj[at, D:], cu, lens, c.table[b:b + 1], 64, other, kind, steps=c.steps,
+                               positions=c.pos[at], mscale=c.ms, norm_weight=c.w, eps=EPS, rows=rows[at], lat_dim=D,
+                               status=c.status)
+        t += n
+    assert torch.equal(c.cache, other) and torch.equal(c.rows, rows) and int(c.status) == 0
+    assert bool((rows[t:] == 7.0).all())
+
+
+@pytest.mark.parametrize("kind", [BF16, FP8])
+def test_a_very_long_call_with_pages_outside_the_pool(kind):
+    """The tokens of a bad page are left out and reported, the others are written."""
+    c = Case([40000], [0], 64, kind, seed=17, given=True)
+    good = Case([40000], [0], 64, kind, seed=17, given=True)
+    good.go()
+    cache0 = c.cache.clone()
+    bad = [3, 77, 400, 624]
+    for i, pi in enumerate(bad):
+        c.table[0, pi] = [-1, c.pages, 1 << 30, -(1 << 31)][i]
+    c.go()
+    assert int(c.status) == 2 and int(good.status) == 0
+    hit = torch.zeros(c.pages, dtype=torch.bool, device=DEV)
+    hit[torch.from_numpy(c.bt[0, bad].astype(np.int64)).to(DEV)] = True
+    slots = hit.repeat_interleave(64)
+    assert torch.equal(c.cache[slots], cache0[slots]) and torch.equal(c.cache[~slots], good.cache[~slots])
+    assert torch.equal(c.rows, good.rows)
+
+
 @pytest.mark.parametrize("D", [256, 768, 1792])
 def test_other_latent_widths(D):
     run(Case([5, 70, 1], [0, 9, 100], 16, BF16, D=D, seed=D))
