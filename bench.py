@@ -99,7 +99,7 @@ def measured_peaks():
 
 
 KERNEL_HEADERS = [os.path.join(ROOT, "mla_latent_kv_cache_gb300", "csrc", f)
-                  for f in ("launch.cuh", "mla_common.cuh", "tmem_ldst.inc")]
+                  for f in ("launch.cuh", "mla_common.cuh", "tmem_ldst.inc", "decode_split.cuh")]
 
 
 def _code_only(text):
