@@ -9,7 +9,7 @@
 // go out before the request, its length and its page are looked up.
 //
 // Prompts are near the rate at which instructions issue as well (unpacking, the
-// norm, the rotation and the rounding are some 260 of them a token), hence packed
+// norm, the rotation and the rounding are some 240 of them a token), hence packed
 // fp32 instructions, a reduction for several tokens at once, one sine and cosine
 // for four positions, and tokens that wait in shared memory instead of registers.
 // Measured: 98,304 tokens into 656-byte rows 31 us (5.7 TB/s, 0.84 of the copy
