@@ -2609,31 +2609,34 @@ __device__ __forceinline__ void merge_row(const float* po, int64_t o_stride, con
     if (lane == 0 && lse_out) *lse_out = L;
 }
 
-// Decode merge: RPB rows of one request per block, GRP groups of 128 threads
+// Decode merge: RPB rows of one request per block, GRP groups of TPR threads
 // per row; thread t of group grp holds dims 4t .. 4t+3 of the row's partial
 // slots k = grp (mod GRP), and the groups' sums meet in shared memory (GRP = 4
 // when rows have dozens of slots, 1 otherwise). Rows of requests that one
 // worker held whole were written by the decode kernel; rows of requests cut
 // across workers g0..g1 combine their partial slots g + b; rows of empty
-// requests get (0, -inf). Block (0, 0) also folds the per-CTA status records
-// of the decode grid into the workspace header.
-// VP float4 columns per thread: thread t of a row owns dims 4t + 512v, v < VP,
+// requests get (0, -inf). The last block (row 0) folds the per-CTA status records
+// of the decode grid into the workspace header; it has no rows, so that nothing
+// waits for it.
+// VP float4 columns per thread: thread t of a row owns dims 4t + 4 TPR v, v < VP,
 // below the latent width (VP = 2 for 768).
-template <int RPB, int GRP, int VP>
-__global__ void __launch_bounds__(128 * RPB * GRP) mla_decode_merge_kernel(const DecodeParams p, int G, int nrec) {
-    constexpr int kThreads = 128 * RPB * GRP;
+// Bound: latency, from the decode grid's end to the next call's beginning; what
+// depends on the lengths alone is found before the wait for the decode grid.
+template <int RPB, int GRP, int VP, int TPR = 128>
+__global__ void __launch_bounds__(TPR * RPB * GRP, VP * TPR <= 128 ? 1024 / (TPR * RPB * GRP) : 1) mla_decode_merge_kernel(const DecodeParams p, int G, int nrec) {
+    constexpr int kThreads = TPR * RPB * GRP;
     const int64_t D = p.lat_dim;
     MLA_MTRACE(0);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int RB = (min(64, p.HQ) + RPB - 1) / RPB;  // blocks per (request, row group)
     const int b = blockIdx.x / RB, gy = blockIdx.y;
-    const int rb = tid / (128 * GRP);
+    const int rb = tid / (TPR * GRP);
     const int n = (blockIdx.x - b * RB) * RPB + rb;
-    const int t = tid & 127, grp = (tid >> 7) % GRP;
+    const int t = tid % TPR, grp = (tid / TPR) % GRP;
     // cost coordinate of request b's first tile, and the total cost (the
     // decode kernel's work split)
     __shared__ long long red_pre[kThreads / 32], red_tot[kThreads / 32];
-    __shared__ float4 part[GRP > 1 ? GRP - 1 : 1][VP][128];
+    __shared__ float4 part[GRP > 1 ? GRP - 1 : 1][VP][TPR];
     long long pre = 0, tot = 0;
     for (int i = tid; i < p.B; i += kThreads) {
         const long long tl = (max(__ldg(p.seq_lens + i), 0) + (1 << p.tile_shift) - 1) >> p.tile_shift;
@@ -2652,10 +2655,31 @@ __global__ void __launch_bounds__(128 * RPB * GRP) mla_decode_merge_kernel(const
     tot = 0;
 #pragma unroll
     for (int w = 0; w < kThreads / 32; ++w) { pre += red_pre[w]; tot += red_tot[w]; }
+    const bool has_row = b < p.B && n < req_rows_in_group(p, b, gy);  // the same for the whole block when it holds one row
+    int nseg = 0;
+    int64_t row = 0;
+    const float *pl = nullptr, *po = nullptr;
+    const int d = 4 * t;
+    bool whole = false;
+    if (has_row) {
+        const int tiles_b = (max(__ldg(p.seq_lens + b), 0) + (1 << p.tile_shift) - 1) >> p.tile_shift;
+        row = req_row0(p, b) + gy * 64 + n;
+        if (tiles_b > 0) {
+            // the workers holding the first and last tile: the largest g with
+            // floor(g * tot / G) <= cost coordinate of the tile
+            const long long g0 = ((pre + 1) * G - 1) / tot;
+            const long long g1 = ((pre + tiles_b) * G - 1) / tot;
+            whole = g0 == g1;  // one worker held the whole request and wrote the output
+            nseg = static_cast<int>(g1 - g0 + 1);
+            const int64_t slot0 = static_cast<int64_t>(gy) * p.SPG + g0 + b;
+            pl = p.part_lse + slot0 * 64 + n;
+            po = p.part_o + (slot0 * 64 + n) * D + d;
+        }
+    }
     griddep_wait();  // the decode grid has finished and its writes are visible
     griddep_launch_dependents();  // the next call's set-up may begin (it waits for this grid before it reads anything)
 
-    if (blockIdx.x == 0 && blockIdx.y == 0 && warp == 0) {
+    if (blockIdx.x == gridDim.x - 1 && blockIdx.y == 0 && warp == 0) {
         // status summary: OR of all records; the lowest failing CTA's site,
         // tile, index and role reports
         int bits = 0, first = INT_MAX;
@@ -2681,32 +2705,19 @@ __global__ void __launch_bounds__(128 * RPB * GRP) mla_decode_merge_kernel(const
         }
     }
 
-    if (b >= p.B) return;
-    if (n >= req_rows_in_group(p, b, gy)) return;  // the same for the whole block when it holds one row
-    const int tiles_b = (max(__ldg(p.seq_lens + b), 0) + (1 << p.tile_shift) - 1) >> p.tile_shift;
-    const int64_t row = req_row0(p, b) + gy * 64 + n;
-    const int d = 4 * t;
+    if (!has_row || whole) return;
     bool dv[VP];
 #pragma unroll
-    for (int v = 0; v < VP; ++v) dv[v] = d + 512 * v < D;
+    for (int v = 0; v < VP; ++v) dv[v] = d + 4 * TPR * v < D;
     float4 acc[VP];
 #pragma unroll
     for (int v = 0; v < VP; ++v) acc[v] = make_float4(0.f, 0.f, 0.f, 0.f);
     float L = -INFINITY;
-    if (tiles_b > 0) {
-        // the workers holding the first and last tile: the largest g with
-        // floor(g * tot / G) <= cost coordinate of the tile
-        const long long g0 = ((pre + 1) * G - 1) / tot;
-        const long long g1 = ((pre + tiles_b) * G - 1) / tot;
-        if (g0 == g1) return;  // one worker held the whole request and wrote the output
-        const int nseg = static_cast<int>(g1 - g0 + 1);
-        const int64_t slot0 = static_cast<int64_t>(gy) * p.SPG + g0 + b;
-        const float* pl = p.part_lse + slot0 * 64 + n;
-        const float* po = p.part_o + (slot0 * 64 + n) * D + d;
+    if (nseg > 0) {
         // this group's slots k = grp, grp + GRP, ...: the first kSpec of them are
         // requested before the weights are known, so the loads overlap the LSE
         // round trip (empty slots hold stale values and get weight 0)
-        constexpr int kSpec = GRP > 1 ? 4 : 8;
+        constexpr int kSpec = GRP > 1 || TPR < 128 ? 4 : 8, kMore = TPR < 128 ? 4 : 8;
         const int nmine = nseg > grp ? (nseg - grp + GRP - 1) / GRP : 0;
         float4 ov[kSpec][VP];
 #pragma unroll
@@ -2714,23 +2725,30 @@ __global__ void __launch_bounds__(128 * RPB * GRP) mla_decode_merge_kernel(const
 #pragma unroll
             for (int v = 0; v < VP; ++v)
                 if (k < nmine && dv[v])
-                    ov[k][v] = *reinterpret_cast<const float4*>(po + static_cast<int64_t>(grp + GRP * k) * 64 * D + 512 * v);
+                    ov[k][v] = *reinterpret_cast<const float4*>(po + static_cast<int64_t>(grp + GRP * k) * 64 * D + 4 * TPR * v);
         // the slot LSEs, 32 at a time, one per lane (every warp computes the
-        // same weights)
-        float mx = -INFINITY;
-        for (int c0 = 0; c0 < nseg; c0 += 32)
+        // same weights); the first 32 stay with their lanes
+        const float mine = lane < nseg ? pl[lane * 64] : -INFINITY;
+        float mx = mine;
+        for (int c0 = 32; c0 < nseg; c0 += 32)
             mx = fmaxf(mx, c0 + lane < nseg ? pl[(c0 + lane) * 64] : -INFINITY);
         mx = warp_max(mx);
         if (mx != -INFINITY) {
-            float ws = 0.f;
-            for (int c0 = 0; c0 < nseg; c0 += 32) {
+            float ws = mine != -INFINITY ? expf(mine - mx) : 0.f;
+            for (int c0 = 32; c0 < nseg; c0 += 32) {
                 const float v = c0 + lane < nseg ? pl[(c0 + lane) * 64] : -INFINITY;
                 ws += v != -INFINITY ? expf(v - mx) : 0.f;
             }
             L = mx + logf(warp_sum(ws));
+            const float weight = mine != -INFINITY ? expf(mine - L) : 0.f;
             auto add = [&](int k, const float4 (&o)[VP]) {
-                const float lv = pl[k * 64];
-                const float w = lv != -INFINITY ? expf(lv - L) : 0.f;
+                float w;
+                if (k < 32) {
+                    w = __shfl_sync(0xffffffffu, weight, k);
+                } else {
+                    const float lv = pl[k * 64];
+                    w = lv != -INFINITY ? expf(lv - L) : 0.f;
+                }
                 if (w != 0.f) {
 #pragma unroll
                     for (int v = 0; v < VP; ++v) {
@@ -2745,18 +2763,18 @@ __global__ void __launch_bounds__(128 * RPB * GRP) mla_decode_merge_kernel(const
 #pragma unroll
             for (int k = 0; k < kSpec; ++k)
                 if (k < nmine) add(grp + GRP * k, ov[k]);
-            // the rest, 8 loads in flight at a time
-            for (int k0 = kSpec; k0 < nmine; k0 += 8) {
-                float4 o8[8][VP];
+            // the rest, kMore loads in flight at a time
+            for (int k0 = kSpec; k0 < nmine; k0 += kMore) {
+                float4 o8[kMore][VP];
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
+                for (int k = 0; k < kMore; ++k)
 #pragma unroll
                     for (int v = 0; v < VP; ++v)
                         if (k0 + k < nmine && dv[v])
                             o8[k][v] = *reinterpret_cast<const float4*>(
-                                po + static_cast<int64_t>(grp + GRP * (k0 + k)) * 64 * D + 512 * v);
+                                po + static_cast<int64_t>(grp + GRP * (k0 + k)) * 64 * D + 4 * TPR * v);
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
+                for (int k = 0; k < kMore; ++k)
                     if (k0 + k < nmine) add(grp + GRP * (k0 + k), o8[k]);
             }
         }
@@ -2785,15 +2803,17 @@ __global__ void __launch_bounds__(128 * RPB * GRP) mla_decode_merge_kernel(const
     for (int v = 0; v < VP; ++v) {
         if (!dv[v]) continue;
         if (p.out_f32) {
-            *reinterpret_cast<float4*>(static_cast<float*>(p.out) + row * D + d + 512 * v) = acc[v];
+            *reinterpret_cast<float4*>(static_cast<float*>(p.out) + row * D + d + 4 * TPR * v) = acc[v];
         } else {
-            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + row * D + d + 512 * v) =
+            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + row * D + d + 4 * TPR * v) =
                 make_uint2(pack_bf16x2(acc[v].x, acc[v].y), pack_bf16x2(acc[v].z, acc[v].w));
         }
     }
     if (t == 0) p.lse[row] = L;
     MLA_MTRACE(1);
 }
+
+constexpr int64_t kMergeRowsAtOnce = 8 * 152;  // 4 blocks of two rows for each SM
 
 // Public split-KV combine: part_o [S, N, 512], part_lse [S, N]. One warp per row.
 __global__ void __launch_bounds__(256) mla_merge_lse_kernel(const float* __restrict__ part_o,
@@ -2810,14 +2830,17 @@ __global__ void __launch_bounds__(256) mla_merge_lse_kernel(const float* __restr
 
 // The merge grid for G workers: rows whose requests are cut into dozens of
 // slots (workers >= 8 per request) get four thread groups each; otherwise two
-// rows share a block of one group each.
+// rows share a block of one group each, or four a block with half the threads,
+// where more rows than the GPU holds at once (4 blocks an SM) would make a second wave.
 cudaError_t launch_decode_merge(const DecodeParams& p, int G, int nrec, int GY, cudaStream_t stream) {
     const bool wide = G >= 8 * p.B;
     const int rows = min(64, p.HQ);
-    const int RB = wide ? rows : (rows + 1) / 2;
+    const bool packed = !wide && p.lat_dim <= 512 && static_cast<int64_t>(p.B) * rows * GY > kMergeRowsAtOnce;
+    const int RB = wide ? rows : packed ? (rows + 3) / 4 : (rows + 1) / 2;
     cudaLaunchAttribute attr[1];
     cudaLaunchConfig_t cfg =
-        pdl_config(dim3(static_cast<unsigned>(p.B) * RB, GY), wide ? 512 : 256, 0, stream, attr);
+        pdl_config(dim3(static_cast<unsigned>(p.B) * RB + 1, GY), wide ? 512 : 256, 0, stream, attr);
+    if (packed) return cudaLaunchKernelEx(&cfg, mla_decode_merge_kernel<4, 1, 2, 64>, p, G, nrec);
     if (p.lat_dim > 1024)
         return wide ? cudaLaunchKernelEx(&cfg, mla_decode_merge_kernel<1, 4, 4>, p, G, nrec)
                     : cudaLaunchKernelEx(&cfg, mla_decode_merge_kernel<2, 1, 4>, p, G, nrec);
