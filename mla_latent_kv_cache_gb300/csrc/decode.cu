@@ -2717,7 +2717,9 @@ __global__ void __launch_bounds__(TPR * RPB * GRP, VP * TPR <= 128 ? 1024 / (TPR
         // this group's slots k = grp, grp + GRP, ...: the first kSpec of them are
         // requested before the weights are known, so the loads overlap the LSE
         // round trip (empty slots hold stale values and get weight 0)
-        constexpr int kSpec = GRP > 1 || TPR < 128 ? 4 : 8, kMore = TPR < 128 ? 4 : 8;
+        // (4 groups: 5 at a time do not spill, and 39 slots take two rounds: 105 us with the
+        // decode before it, 107 with 4 and then 8)
+        constexpr int kSpec = GRP > 1 ? 5 : TPR < 128 ? 4 : 8, kMore = kSpec;
         const int nmine = nseg > grp ? (nseg - grp + GRP - 1) / GRP : 0;
         float4 ov[kSpec][VP];
 #pragma unroll
@@ -2831,7 +2833,9 @@ __global__ void __launch_bounds__(256) mla_merge_lse_kernel(const float* __restr
 // The merge grid for G workers: rows whose requests are cut into dozens of
 // slots (workers >= 8 per request) get four thread groups each; otherwise two
 // rows share a block of one group each, or four a block with half the threads,
-// where more rows than the GPU holds at once (4 blocks an SM) would make a second wave.
+// where more rows than the GPU holds at once (4 blocks an SM) would make a second wave
+// (2,048 rows: 105 us with the decode before it, 108 with two a block; 1,024 rows,
+// which fit: 39.1 us with four a block, 38.0 with two).
 cudaError_t launch_decode_merge(const DecodeParams& p, int G, int nrec, int GY, cudaStream_t stream) {
     const bool wide = G >= 8 * p.B;
     const int rows = min(64, p.HQ);
