@@ -13,8 +13,8 @@
 // fp32 instructions, a reduction for several tokens at once, one sine and cosine
 // for four positions, and tokens that wait in shared memory instead of registers.
 // Measured: 98,304 tokens into 656-byte rows 31 us (5.7 TB/s, 0.84 of the copy
-// rate), 52,106 tokens of 16 prompts into page rows, with dense rows besides, 34 us
-// (0.65, issue slots 57% busy), 64 requests with a token each 3.7 us.
+// rate), 52,106 tokens of 16 prompts into page rows, with dense rows besides, 33 us
+// (0.68, issue slots 55% busy), 64 requests with a token each 3.7 us.
 //
 // bf16 and fp8_ds_mla rows: a warp a token, or for prompts a stream of them. Page rows (one scale for all rows of
 // a page): the warps of a page hold its new tokens in registers, meet for the
@@ -516,6 +516,7 @@ __global__ void __launch_bounds__(32 * kAppendWarps, 3) append_page_kernel(const
     // Sums of squares and largest magnitudes of the held tokens: one pass, and one
     // reduction for all of them.
     float sq[kHold], mx[kHold];
+    float2 es[kHold];  // the turned pairs (16 prompts 32.6 us; turned again when they are written 34.2)
 #pragma unroll
     for (int k = 0; k < kHold; ++k) {
         const int x = wi + k * W;
@@ -533,7 +534,7 @@ __global__ void __launch_bounds__(32 * kAppendWarps, 3) append_page_kernel(const
 #pragma unroll
                 for (int i = 0; i < 4; ++i) f[u][i] = mul2(f[u][i], w[u][i]);
         }
-        const float2 e = angle.turn(p, load_pair(lat + 64, p.interleaved, lane), position(x), lane);
+        const float2 e = es[k] = angle.turn(p, load_pair(lat + 64, p.interleaved, lane), position(x), lane);
         if (x < skip) continue;
         mx[k] = most_abs(most_abs(0.f, f[0]), f[1]);
         top = fmaxf(top, fmaxf(fabsf(e.x), fabsf(e.y)));
@@ -557,6 +558,7 @@ __global__ void __launch_bounds__(32 * kAppendWarps, 3) append_page_kernel(const
             }
         }
     }
+    angle.left = min(angle.left, 0);
     for (int x = wi + kHold * W; x < m; x += W) {  // pages of more rows than the warps hold: read twice
         const uint4* lat = reinterpret_cast<const uint4*>(p.latent + (t0 + x) * p.lat_st);
         F2 f[2][4];
@@ -627,16 +629,16 @@ __global__ void __launch_bounds__(32 * kAppendWarps, 3) append_page_kernel(const
         }
         row += W * kRowPage;
     };
-    angle.left = min(angle.left, 0);  // (as the first time: the largest value is among these)
-#pragma unroll 2
+#pragma unroll
     for (int k = 0; k < kHold; ++k) {
         const int x = wi + k * W;
         if (x >= m) break;
         const uint4* lat = reinterpret_cast<const uint4*>(held + k * kHeldRow);
         F2 f[2][4];
         weighed(lat[lane], lat[lane + 32], f, false);
-        write(f, factors[warp][k], angle.turn(p, load_pair(lat + 64, p.interleaved, lane), position(x), lane), x);
+        write(f, factors[warp][k], es[k], x);
     }
+    angle.left = min(angle.left, 0);  // (as the first time: the largest value is among these)
     for (int x = wi + kHold * W; x < m; x += W) {
         const uint4* lat = reinterpret_cast<const uint4*>(p.latent + (t0 + x) * p.lat_st);
         F2 f[2][4];
