@@ -855,7 +855,7 @@ int mla_decode_fp8_page(const void* q_lat, const void* q_pe, int64_t total_q_tok
     p.out_f32 = out_dtype == MLA_OUT_F32;
     p.SPG = W + B;
     // what a request boundary costs a worker, in tiles: its queries, the drain before them
-    // (128 rows: 131 us with 2, 126 with 4; 16 rows 39.9 with 2, 41 with 4)
+    // (128 rows: 127 us with 2, 122 with 4 and 5; 64 rows 107.7, 105.0, 105.7; 16 rows 38.5 with 2, 39.5 with 1, 39.3 with 3)
     p.wseg = NP == 64 ? 4 : NP == 32 ? 3 : 2;
     p.cu_q = cu_q_lens;
     p.total_q = static_cast<int>(total_q_tokens);
