@@ -469,8 +469,11 @@ __global__ void __launch_bounds__(32 * kAppendWarps, 3) append_page_kernel(const
         }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
-    const int64_t page = a_page(p, b, pi);
-    const bool bad = page < 0 && j1 > max(pi * ps, static_cast<int64_t>(0));
+    // Tokens without a place touch no page: of a request without any (its length 0 in a padded
+    // batch) the table's first entry is no page of its own, and its scale another request's.
+    const bool placed = j1 > max(j0, static_cast<int64_t>(0));
+    const int64_t page = placed ? a_page(p, b, pi) : -1;
+    const bool bad = placed && page < 0;
     if (bad && lane == 0 && wi == 0 && p.status) atomicOr(p.status, kErrBadBlock);
     const int64_t off = max(p0, static_cast<int64_t>(0)) - pi * ps;  // rows of the page that were there before (if > 0)
     const float old = page >= 0 && off > 0 ? __ldcg(p.scales + page) : 0.f;

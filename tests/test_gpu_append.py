@@ -374,6 +374,40 @@ def test_tokens_without_a_place(kind):
             assert np.array_equal(c.scales.cpu().numpy()[other], scales0.cpu().numpy()[other])
 
 
+@pytest.mark.parametrize("n,length", [(1, 0), (1, -3), (20, 0), (20, -1), (70, 0)])
+@pytest.mark.parametrize("kind", [BF16, FP8, PAGE])
+def test_requests_without_any_place_leave_the_pages_their_table_names(kind, n, length):
+    """A padding request of a batch of fixed size: new tokens, no length, and a table row that
+    names pages of other requests. Page and scale of those stay, and what a live request
+    appends to them in the same call is there, whichever comes first."""
+    for live in (False, True):
+        c = Case([n, 3, n], [0, 5, 0], 16, kind, seed=21)
+        if not live:
+            c.cu = torch.tensor([0, n, n, 2 * n], dtype=torch.int32, device=DEV)
+        c.table[0] = c.table[1]
+        c.table[2] = c.table[1]
+        c.lens[0] = c.lens[2] = length
+        cache0, scales0 = c.cache.clone(), None if c.scales is None else c.scales.clone()
+        c.go()
+        torch.cuda.synchronize()
+        assert int(c.status) == 2
+        cache1, scales1 = cache0.clone(), None if scales0 is None else scales0.clone()
+        if live:  # the same tokens alone
+            d = Case([n, 3, n], [0, 5, 0], 16, kind, seed=21)
+            d.cache, d.scales = cache1, scales1
+            d.cu = torch.tensor([0, 3], dtype=torch.int32, device=DEV)
+            d.proj, d.rows = c.proj[n:n + 3], None
+            d.lens, d.table = c.lens[1:2].clone(), c.table[1:2].clone()
+            d.go()
+            torch.cuda.synchronize()
+            assert int(d.status) == 0
+        assert torch.equal(c.cache, cache1)
+        if kind == PAGE:
+            assert torch.equal(c.scales, scales1)
+        # the dense rows are there all the same
+        assert not bool((c.rows[:n] == 7.0).all(1).any())
+
+
 @pytest.mark.parametrize("kind", [BF16, FP8, PAGE])
 def test_thousands_of_requests(kind):
     """More of them than one round of probes looks at, most without a token."""
