@@ -501,9 +501,13 @@ MLA_API int mla_cache_append(const void* latent, int64_t latent_stride, const vo
  *   out[r]  = sum_j softmax_j(score) s(j) code_j[0:512],   lse[r] = ln sum_j exp(score_j).
  * The codes go to the tensor cores as they are. A query value is the sum of two
  * e4m3 values of different scale: those below 2^-15 of their row's largest are
- * rounded, by at most 2^-22 of it. A probability times s(j) is held likewise
- * (up to 32 query rows: rounded by at most 2^-8 of itself or 2^-20 of the largest;
- * above, 2^-8 or 2^-16). Sums are fp32.
+ * rounded, by at most 2^-22 of it. A probability times s(j) is rounded to f16 (2^-11
+ * of itself) and held likewise: up to 32 query rows rounded by at most 2^-8 of itself
+ * or 2^-20 of the largest; above, 2^-8 or 2^-16. Those below 2^-14 of the largest are
+ * rounded up or down by the token's position, as often up as the part of a step that
+ * is rounded, so that over many tokens they keep their sum: weights alike, however small
+ * (to 2^-28 of the largest), are off by a few steps in all, not by one each. Sums are
+ * fp32; the sum that divides takes the unrounded weights.
  *   scales       device, fp32 [num_slots / page_size], positive; one outside 2^-40 ..
  *                2^40 counts as the nearer bound.
  *   block_table  device, int32 [B, block_table_cols], block_table_stride >=

@@ -17,8 +17,18 @@
 // bits). h and l are two columns of the B operand, so the score product reads
 // the tile once, and the two sums meet in fp32. P in (0, 256] is split the same
 // way. Up to 32 query rows its two parts are columns too, with accumulators of
-// their own; at 64 rows TMEM has no room for them, and the parts (l not scaled
-// there) go into the same accumulator one after the other.
+// their own; at 64 rows TMEM has no room for them, and the parts (l not scaled and
+// e5m2 there) go into the same accumulator one after the other.
+//
+// Small weights. Under 2^-6, where h is at its finest step, l is a rounding up or down by
+// the token's number in the golden-section sequence, up as often as the part of a step that
+// is rounded: many weights of a long tail, each less than a step, add up to their sum
+// (l's own sum takes them unrounded, so a tail rounded to nothing would be missing from
+// the output). Up to 32 rows a fraction of l's one step there is added before it is rounded to
+// the nearest, at 64 rows to the bits of f16 below those of e5m2 before they are cut off.
+// 65,536 tokens alike 12.5 nats below one of them: these roundings put the tail's part of the output
+// off by 2^-11, to the nearest by 2%, and with the largest weight at 2^3 all of it was missing. Time with
+// both: 4 x 262,144 tokens at 32 rows 106.2 -> 107.0 us, 64 requests 39.3 -> 39.7, 64 rows 107.9 -> 108.6.
 //
 // Bound: HBM, 576 bytes a token; at 16 query rows the products take a third of
 // the time the bytes do, at 64 rows about as long (S 1,150 cycles a tile, the value
@@ -54,10 +64,6 @@ constexpr int kBlk = kTok * 128;      // bytes of a latent block
 constexpr int kRopeBlk = kTok * 64;   // and of the rotary part
 constexpr int kQGens = 4;             // generations of query scales (three may be in use: a group is at most two tiles behind)
 constexpr int kScs = 4;               // tiles' scales
-// P of the maximum itself is 2^3, and a score may pass it by 2^5 before the maximum
-// is raised (O rescaled, a few thousand cycles): with 2^6 and 2^2 that was every
-// other of the first dozen tiles of a request.
-constexpr float kTop = 3.f, kSlack = 5.f;
 constexpr float kNoMax = -1e30f;
 constexpr float kLn2f = 0.69314718055994530942f;
 
@@ -73,6 +79,13 @@ struct P8Cfg {
     static constexpr int kRopes = NP == 64 && !LSU ? 1 : 2;
     static constexpr int kScW = LSU ? kTok : 16;        // scales of a tile: one for each row, or run of rows
     static constexpr int kPBufs = NP == 64 ? 1 : 2;
+    // P of the maximum itself is 2^kTop, and a score may pass it by 2^kSlack before the
+    // maximum is raised (O rescaled, a few thousand cycles). What a weight is rounded by, of
+    // the largest: half of l's finest step and as much for the evenly spread part, 2^-14 / 2^kTop =
+    // 2^-20; at 64 rows a step of e5m2 below 2^-10, 2^-13 / 2^kTop = 2^-16. (Raised
+    // rarely, 2^3, up to 32 rows: 2^-17, and 0.5% less time at 32 rows, 0.4% at 16; 2^6
+    // at 64 rows raises it in every other of the first dozen tiles of a request.)
+    static constexpr float kTop = kStack ? 6.f : 3.f, kSlack = 8.f - kTop;
     static constexpr int kGroups = NP == 16 ? 1 : 2;    // softmax groups of four warps
     static constexpr int kCW = NP / kGroups;            // columns of a group
     static constexpr int kQBlk = 2 * NP * 128;          // a 128-dim block of the queries: h rows, then l rows
@@ -211,16 +224,17 @@ __device__ __forceinline__ void p8_ld_pair(uint32_t at0, uint32_t at1, uint32_t 
 __device__ __forceinline__ void p8_store(float* to, float v) { *to = v; }
 __device__ __forceinline__ void p8_store(__nv_bfloat16* to, float v) { *to = __float2bfloat16_rn(v); }
 
-// Two values in f16 as e4m3 codes (the first in the low byte), and the codes of
-// what is left of them times `times` (e4m3, or e5m2).
-__device__ __forceinline__ void p8_split(__half2 v, float times, uint32_t& h, uint32_t& l, bool e5m2 = false) {
-    h = __nv_cvt_halfraw2_to_fp8x2(*reinterpret_cast<const __half2_raw*>(&v), __NV_SATFINITE, __NV_E4M3);
+// Two values in f16 as e4m3 codes (the first in the low byte), and what is left of them.
+__device__ __forceinline__ uint32_t p8_high(__half2 v, __half2& rest) {
+    const uint32_t h = __nv_cvt_halfraw2_to_fp8x2(*reinterpret_cast<const __half2_raw*>(&v), __NV_SATFINITE, __NV_E4M3);
     const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(h), __NV_E4M3);
-    __half2 rest = __hsub2(v, *reinterpret_cast<const __half2*>(&hr));
-    if (times != 1.f) rest = __hmul2(rest, __float2half2_rn(times));
-    l = __nv_cvt_halfraw2_to_fp8x2(*reinterpret_cast<const __half2_raw*>(&rest), __NV_SATFINITE, e5m2 ? __NV_E5M2 : __NV_E4M3);
-    h &= 0xFFFFu;
-    l &= 0xFFFFu;
+    rest = __hsub2(v, *reinterpret_cast<const __half2*>(&hr));
+    return h & 0xFFFFu;
+}
+// rest times 32 plus `more` as e4m3 codes.
+__device__ __forceinline__ uint32_t p8_low(__half2 rest, __half2 more) {
+    rest = __hfma2(rest, __float2half2_rn(32.f), more);
+    return __nv_cvt_halfraw2_to_fp8x2(*reinterpret_cast<const __half2_raw*>(&rest), __NV_SATFINITE, __NV_E4M3) & 0xFFFFu;
 }
 
 template <int NP, bool LSU>
@@ -230,6 +244,7 @@ __global__ void __launch_bounds__(P8Cfg<NP, LSU>::kThreads, 1)
     using Ctrl = P8Ctrl<C>;
     using It = TileItT<7>;
     constexpr int CW = C::kCW, kRopes = C::kRopes;
+    constexpr float kTop = C::kTop, kSlack = C::kSlack;
     extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t* ring = smem;
     uint8_t* rope_ring = smem + C::kOffRope;
@@ -401,7 +416,9 @@ __global__ void __launch_bounds__(P8Cfg<NP, LSU>::kThreads, 1)
 #pragma unroll
                 for (int k = 0; k < 9; ++k) {
                     const float2 f = un2(mul2(f2(__uint_as_float(v[k] << 16), __uint_as_float(v[k] & 0xFFFF0000u)), f2(up, up)));
-                    p8_split(__floats2half2_rn(f.x, f.y), 32.f, h[k], l[k]);
+                    __half2 rest;
+                    h[k] = p8_high(__floats2half2_rn(f.x, f.y), rest);
+                    l[k] = p8_low(rest, __float2half2_rn(0.f));
                 }
                 // unit lane % 8 of row r, block lane / 8 (NP is a multiple of 8: rows NP + r swizzle alike)
                 uint8_t* at = qs + (lane >> 3) * C::kQBlk + r * 128 + (((lane & 7) ^ (r & 7)) << 4);
@@ -903,20 +920,31 @@ __global__ void __launch_bounds__(P8Cfg<NP, LSU>::kThreads, 1)
                 }
                 uint32_t hc[CW / 4], lc[CW / 4];
                 const F2 inv2 = f2(inv_vs, inv_vs);
+                // where this token's roundings of small weights lie: the golden section's multiples,
+                // which any run of tokens covers evenly
+                const uint32_t turn = static_cast<uint32_t>(tok) * 2654435769u;
+                const __half2 dither = __float2half2_rn(static_cast<float>(static_cast<int32_t>(turn)) * 0x1p-41f);
+                const uint32_t up = (turn >> 24) * 0x10001u;
+                uint32_t rests[2];
 #pragma unroll
                 for (int c = 0; c < CW; c += 2) {
                     const float2 v = un2(y[c / 2]);
                     const float a = ex2(v.x), b = ex2(v.y);
                     l[c / 2] = fma2(f2(a, b), inv2, l[c / 2]);
                     // (f16 holds 11 bits, the two codes 8 of them)
-                    uint32_t h, lo;
-                    p8_split(__floats2half2_rn(a, b), C::kStack ? 32.f : 1.f, h, lo, !C::kStack);
-                    if (c & 2) {
-                        hc[c >> 2] |= h << 16;
-                        lc[c >> 2] |= lo << 16;
+                    const __half2 weights = __floats2half2_rn(a, b);
+                    __half2 rest;
+                    const uint32_t h = p8_high(weights, rest);
+                    hc[c >> 2] = c & 2 ? hc[c >> 2] | h << 16 : h;
+                    if constexpr (C::kStack) {
+                        const uint32_t lo = p8_low(rest, dither);
+                        lc[c >> 2] = c & 2 ? lc[c >> 2] | lo << 16 : lo;
                     } else {
-                        hc[c >> 2] = h;
-                        lc[c >> 2] = lo;
+                        // e5m2 is the upper byte of f16: half a step added and cut off rounds to the
+                        // nearest, any part of a step rounds up that often
+                        const uint32_t small = __hlt2_mask(weights, __float2half2_rn(0x1p-6f));
+                        rests[(c >> 1) & 1] = *reinterpret_cast<const uint32_t*>(&rest) + ((up & small) | (0x00800080u & ~small));
+                        if (c & 2) lc[c >> 2] = __byte_perm(rests[0], rests[1], 0x7531);
                     }
                 }
                 // P's place is free when the value product that read it last is done

@@ -350,3 +350,112 @@ def test_a_wait_that_runs_out_is_reported(Hq, page):
 def test_one_long_request():
     b = Batch([100003], 16, 1, 64, seed=14)
     run(b)
+
+
+class Sink:
+    """One token far above a long tail. Rotary codes alone make the scores (the latent part
+    of the queries is 0), so a token's value may be anything: the tail's is 8 in dims 0 .. 127,
+    random in the rest, the sink's is 0 in dims 0 .. 127. Head h puts the sink nats[h] above
+    the tail's middle; `wide` is the tail's width in nats (0: all alike)."""
+
+    def __init__(self, lens, at, Hq, q_len, nats, wide, seed=0, page=64):
+        r = np.random.default_rng(seed)
+        self.lens, self.Hq, self.q_len, self.page = lens, Hq, q_len, page
+        T, rows, B = max(lens), Hq * q_len, len(lens)
+        need = -(-T // page)
+        self.table = np.arange(B * need, dtype=np.int32).reshape(B, need)
+        x = np.zeros((B * need * page, 576), dtype=np.float32)
+        x[:, 128:512] = r.standard_normal((len(x), 384)) * 60
+        x[:, :128] = 8.0
+        x[:, 513:517] = r.standard_normal((len(x), 4)) * 60
+        for b in range(B):
+            j = b * need * page + at
+            x[j, :128], x[j, 512], x[j, 513:517] = 0.0, 448.0, 0.0
+        self.codes = torch.from_numpy(x).clamp(-448, 448).to(torch.float8_e4m3fn)
+        q = np.zeros((B * q_len, Hq, 576), dtype=np.float32)
+        q[..., 512] = np.resize(nats, Hq)[None] / 448.0
+        q[..., 513:517] = wide / 120.0
+        self.q = torch.from_numpy(q).to(torch.bfloat16)
+
+    def bounds(self, cache, q):
+        """For each row: the output in 64 bits and how far each value may be off, lse and its room."""
+        fine = self.Hq * self.q_len <= 32  # the codes of small weights (include/mla.h)
+        need, page = self.table.shape[1], self.page
+        for b, n in enumerate(self.lens):
+            code = cache[b * need * page:b * need * page + n].view(torch.float8_e4m3fn).double()
+            mag = code[:, :512].abs()
+            sq = mag * mag
+            for r in range(self.q_len * self.Hq):
+                see = n - self.q_len + r // self.Hq + 1
+                c, a, a2 = code[:see], mag[:see], sq[:see]
+                qr = q[b * self.q_len + r // self.Hq, r % self.Hq].double()
+                z = c[:, 512:] @ qr[512:]
+                top = z.max()
+                e = torch.exp(z - top)
+                want = (e @ c[:, :512]) / e.sum()
+                # in units of the weights as they are held, the largest of them 2^kTop or more
+                # (where it is more, every step below is smaller beside it)
+                P = e * (64.0 if fine else 8.0)
+                Pa = P @ a
+                # f16, and codes above 2^-6 (2^-8 where the largest may be held as 2^8)
+                big = torch.where(e * 256.0 >= 2.0 ** -6, P, 0.0)
+                room = 2.0 ** -11 * Pa + 2.0 ** -8 * (big @ a)
+                # below: a rounding of mean 0 within a step. Over tokens of equal weight the
+                # positions that are rounded up are evenly spread (a dozen steps at most); over
+                # others the roundings are independent, of deviation half a step at most.
+                step = torch.full_like(P, 2.0 ** -14) if fine else torch.clamp(P * 0.25, 2.0 ** -16, 2.0 ** -13)
+                step = torch.where(P < 2.0 ** -6, step, 0.0)
+                room = room + 7 * 0.5 * torch.sqrt((step * step) @ a2) + 12 * 448 * step.max()
+                # scores, fp32 sums of a CTA's tiles (32 tokens a step, truncated) and of its weights
+                ds = 2.0 ** -22 * qr.abs().max() * c[:, 512:].abs().sum(1).max() + 2.0 ** -19 * (c[:, 512:].abs() @ qr[512:].abs()).max()
+                room = room + (2 * ds + n / 32 * 2.0 ** -23 + 2.0 ** -13) * Pa
+                yield want, room / P.sum(), top + torch.log(e.sum()), ds + 2.0 ** -13
+
+    def check(self, *num_ctas):
+        B, page, Hq, q_len = len(self.lens), self.page, self.Hq, self.q_len
+        pages = len(self.codes) // page
+        t = lambda a: torch.from_numpy(np.ascontiguousarray(a)).to(DEV)  # noqa: E731
+        cache, q = self.codes.view(torch.uint8).to(DEV), self.q.to(DEV)
+        want, room, want_l, room_l = (torch.stack(x) for x in zip(*self.bounds(cache, q)))
+        for n in num_ctas:
+            out = torch.empty((B * q_len, Hq, 512), dtype=torch.float32, device=DEV)
+            lse = torch.empty((B * q_len, Hq), device=DEV)
+            ws = torch.empty(m.mla_decode_workspace_bytes(B, q_len, Hq, n), dtype=torch.uint8, device=DEV)
+            m.mla_decode_fp8_page(q[..., :512].contiguous(), q[..., 512:].contiguous(), cache, torch.ones(pages, device=DEV), page,
+                                  t(self.table), t(np.array(self.lens, dtype=np.int32)), q_len, 1.0, out, lse, ws, num_ctas=n)
+            assert m.device_status(ws) == 0
+            off = (out.double().reshape(-1, 512) - want).abs()
+            assert bool((off <= room).all()), (n, float((off / room).max()))
+            assert bool(((lse.double().reshape(-1) - want_l).abs() <= room_l).all()), n
+
+
+@pytest.mark.parametrize("wide", [0.0, 1.0])
+@pytest.mark.parametrize("Hq,q_len", [(16, 1), (32, 1), (16, 4), (32, 4)])
+@pytest.mark.parametrize("where", ["first", "middle", "last"])
+def test_a_token_far_above_a_long_tail(Hq, q_len, wide, where):
+    """The tail's share counts although each of its weights is 2^-9 to 2^-23 of the largest."""
+    T = 65536
+    at = {"first": 3, "middle": T // 2 + 77, "last": T - q_len - 2}[where]
+    nats = [6.5, 8.0, 9.3, 10.0, 10.7, 11.4, 12.1, 12.5, 12.9, 13.3, 13.7, 14.1, 14.5, 15.0, 15.5, 16.0]
+    Sink([T], at, Hq, q_len, nats, wide, seed=31).check(1)
+
+
+@pytest.mark.parametrize("Hq,q_len", [(16, 1), (32, 1), (16, 4)])
+@pytest.mark.parametrize("wide", [0.0, 1.0])
+def test_a_token_above_a_tail_of_the_longest_contexts(Hq, q_len, wide):
+    """262,144 tokens, whole and cut between CTAs."""
+    Sink([262144, 262001], 131000, Hq, q_len, [10.0, 11.0, 12.0, 12.54, 13.0, 14.0, 15.0, 17.0], wide, seed=32).check(1, 5, 0)
+
+
+@pytest.mark.parametrize("Hq,q_len", [(16, 2), (16, 4), (16, 8)])
+def test_weights_of_nothing_stay_nothing(Hq, q_len):
+    """Rounding small weights gives none to a token that a query does not see: its value may be anything."""
+    b, c = Batch([700, 300], Hq, q_len, 16, seed=33), Batch([700, 300], Hq, q_len, 16, seed=33)
+    for x in range(2):
+        n = int(b.lens[x])
+        b.codes[b.slots(x, np.arange(n - q_len + 1, n)), :512] = 0x7E  # 448, in tokens that query 0 does not see
+    out, lse, _ = b.go()
+    want, want_l, _ = c.go()
+    torch.cuda.synchronize()
+    for x in range(2):
+        assert torch.equal(out[x * q_len], want[x * q_len]) and torch.equal(lse[x * q_len], want_l[x * q_len])
