@@ -517,8 +517,8 @@ MLA_API int mla_cache_append(const void* latent, int64_t latent_stride, const vo
  *                number of query tokens, at most q_len, as in mla_decode_varlen.
  *   total_q_tokens  query tokens in q_lat, q_pe, out and lse (B * q_len without
  *                cu_q_lens).
- * A NaN in a row makes NaN of the query rows that see it, and of no others. Every
- * other argument, the rows without a visible token, the workspace
+ * A NaN in a row, or in the scale of its page, makes NaN of the query rows that see
+ * it, and of no others. Every other argument, the rows without a visible token, the workspace
  * (mla_decode_workspace_bytes(B, q_len, Hq, num_ctas)) and the status words are as
  * in mla_decode and mla_decode_varlen. Up to 64 query rows (Hq * q_len) the cache
  * is read once per request; each further 64 rows read it again, at the same time.

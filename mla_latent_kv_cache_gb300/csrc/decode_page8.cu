@@ -778,7 +778,8 @@ __global__ void __launch_bounds__(P8Cfg<NP, LSU>::kThreads, 1)
                 const int tok = it.j * kTok + tk, valid = min(kTok, T - it.j * kTok);
                 wait(&ctrl->sc_full[i % kScs], (i / kScs) & 1, kSiteSFull);
                 const float vs = tk < valid ? ctrl->sc[i % kScs][tk >> run_shift] : 1.f;
-                const float lv = log2f(vs), inv_vs = 1.f / vs;
+                // (a scale that is NaN makes NaN of the weights that count, and must not of a weight of 0)
+                const float lv = log2f(vs), inv_vs = vs == vs ? 1.f / vs : 1.f;
                 wait(&ctrl->s_full[i & 1], (i >> 1) & 1, kSiteSFull);
                 tc_fence_after();
                 // y = log2 of P before any limit: score and scale in log2 units, less the maximum, and kTop

@@ -459,3 +459,17 @@ def test_weights_of_nothing_stay_nothing(Hq, q_len):
     torch.cuda.synchronize()
     for x in range(2):
         assert torch.equal(out[x * q_len], want[x * q_len]) and torch.equal(lse[x * q_len], want_l[x * q_len])
+
+
+@pytest.mark.parametrize("Hq,q_len,page", [(8, 4, 16), (16, 4, 16), (16, 8, 16), (16, 4, 3)])
+def test_a_page_scale_that_is_not_a_number_reaches_only_the_queries_that_see_the_page(Hq, q_len, page):
+    n = 18 * 16 * 3 + 1
+    b, c = Batch([n, 40], Hq, q_len, page, seed=34), Batch([n, 40], Hq, q_len, page, seed=34)
+    b.scales[b.bt[0, n // page]] = np.nan  # the page of the last token alone
+    out, lse, _ = b.go()
+    want, want_l, _ = c.go()
+    torch.cuda.synchronize()
+    last = q_len - 1
+    assert torch.equal(out[:last], want[:last]) and torch.equal(lse[:last], want_l[:last])
+    assert torch.equal(out[q_len:], want[q_len:]) and torch.equal(lse[q_len:], want_l[q_len:])
+    assert bool(lse[last].isnan().all()) and bool(out[last].isnan().all())
