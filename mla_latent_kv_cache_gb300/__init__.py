@@ -121,21 +121,30 @@ def load() -> ctypes.CDLL:
             lib.mla_decode_fp8_page.argtypes = [vp, vp, i64, vp, vp, i64, i32, vp, i64, i64, vp, vp, i32, i32, i32, f32,
                                                 vp, i32, vp, vp, sz, i32, vp]
             lib.mla_decode_fp8_page.restype = i32
-            _load_bind(lib)
+            for name in ("mla_rope", "mla_cache_append", "mla_decode_fp8_page"):
+                _addresses[name] = ctypes.cast(getattr(lib, name), ctypes.c_void_p).value
             _lib = lib
     return _lib
 
 
-def _load_bind(lib) -> None:
+def _load_bind() -> None:
+    """The library and the compiled checks, at the first call that needs them: the
+    other calls go without."""
     global _bind
-    if not os.path.exists(BIND_PATH):
-        raise ImportError(f"{BIND_PATH} not built; run: python -c 'import __graft_entry__ as g; g.build()'")
-    spec = importlib.util.spec_from_loader("_mla_bind", importlib.machinery.ExtensionFileLoader("_mla_bind", BIND_PATH))
-    mod = importlib.util.module_from_spec(spec)
-    spec.loader.exec_module(mod)
-    for name in ("mla_rope", "mla_cache_append", "mla_decode_fp8_page"):
-        _addresses[name] = ctypes.cast(getattr(lib, name), ctypes.c_void_p).value
-    _bind = mod
+    load()
+    from . import build
+    with _lock:
+        if _bind is not None:
+            return
+        if not os.path.exists(BIND_PATH):
+            raise ImportError(f"{BIND_PATH} is missing: build it with `python -m mla_latent_kv_cache_gb300.build`")
+        if build.bind_built_for() != build.bind_key():
+            raise ImportError(f"{BIND_PATH} was built against {build.bind_built_for() or 'something else'}, this is "
+                              f"{build.bind_key()}: build it anew with `python -m mla_latent_kv_cache_gb300.build`")
+        spec = importlib.util.spec_from_loader("_mla_bind", importlib.machinery.ExtensionFileLoader("_mla_bind", BIND_PATH))
+        mod = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(mod)
+        _bind = mod
 
 
 # the current stream's handle without a Stream object around it (a few microseconds a call)
@@ -727,7 +736,7 @@ def mla_rope(x, positions, steps, out, interleaved: bool = False, mscale: float 
     contiguous last dimensions (views of wider heads, or one and the same tensor),
     positions int32 [T], steps int64 [R / 2] (rope_steps; negated for the way back)."""
     if _bind is None:
-        load()
+        _load_bind()
     st = _bind.rope(_addresses["mla_rope"], stream, _device, x, positions, steps, out, interleaved, mscale)
     if st != 0:
         _answered("mla_rope", st, _ROPE_NAMES, (x, positions, steps, out, None))
@@ -748,7 +757,7 @@ def mla_cache_append(latent, k_pe, cu_new_lens, seq_lens, block_table, page_size
     [total, >= lat_dim + 64] takes (latent, key) besides. `status` (a device int32
     tensor) collects status bits."""
     if _bind is None:
-        load()
+        _load_bind()
     st = _bind.append(_addresses["mla_cache_append"], stream, _device, latent, k_pe, cu_new_lens, seq_lens, block_table, page_size,
                       cache, cache_kind, steps, positions, interleaved, mscale, norm_weight, eps, scales, rows, lat_dim, status)
     if st != 0:
@@ -768,7 +777,7 @@ def mla_decode_fp8_page(q_lat, q_pe, cache, scales, page_size, block_table, seq_
     [B + 1]) what it counts, at most q_len for each request. workspace:
     mla_decode_workspace_bytes(B, q_len, Hq, num_ctas)."""
     if _bind is None:
-        load()
+        _load_bind()
     st = _bind.decode_page(_addresses["mla_decode_fp8_page"], stream, _device, q_lat, q_pe, cache, scales, page_size, block_table,
                            seq_lens, q_len, scale, out, lse, workspace, cu_q_lens, num_ctas)
     if st != 0:

@@ -292,3 +292,67 @@ def test_evicting_page_rows_is_refused(fake):
         torch.zeros((64, 576), dtype=torch.uint8), 2, 16, i32(2, 4), i32(2), f32(2, 50), i32(2, 50), i32(2), 1, 2, i32(2), f32(2, 50),
         i32(2, 50), i32(2, 52)), "cache kind")
     assert fake.calls == []
+
+
+# ------------------------------------------------------------ the compiled checks
+
+def _three_calls():
+    lens, cu, table = i32(2), i32(3), i32(2, 4)
+    x = bf(4, 2, 64)
+    return (lambda: m.mla_rope(x, i32(4), i64(32), torch.empty_like(x)),
+            lambda: m.mla_cache_append(bf(4, 512), bf(4, 64), cu, lens, table, 16, torch.zeros((64, 576), dtype=torch.uint8),
+                                       m.MLA_CACHE_FP8_PAGE_576, scales=f32(4)),
+            lambda: m.mla_decode_fp8_page(bf(2, 8, 512), bf(2, 8, 64), torch.zeros((64, 576), dtype=torch.uint8), f32(4), 16,
+                                          table, lens, 1, 0.1, f32(2, 8, 512), f32(2, 8), torch.zeros(1 << 16, dtype=torch.uint8)))
+
+
+@pytest.mark.parametrize("what", ["missing", "another PyTorch", "no record"])
+def test_only_the_calls_that_need_the_compiled_checks_go_without_them(monkeypatch, tmp_path, lib, what):
+    """The library loads and answers; the three calls name what is wrong."""
+    monkeypatch.setattr(m, "_bind", None)
+    monkeypatch.setattr(m, "_lib", None)
+    key = tmp_path / "key"
+    if what == "missing":
+        monkeypatch.setattr(m, "BIND_PATH", str(tmp_path / "_mla_bind.so"))
+    else:
+        if what == "another PyTorch":
+            key.write_text("torch 1.0 other\n")
+        monkeypatch.setattr(mbuild, "BIND_KEY", str(key))
+    assert m.mla_row_bytes(m.MLA_CACHE_BF16_576) == 1152
+    with pytest.raises(m.MlaError):  # an earlier call's own checks
+        m.mla_merge_lse(f32(1, 1, 512), f32(1, 1), f32(1, 512))
+    for call in _three_calls():
+        with pytest.raises(ImportError, match="missing" if what == "missing" else "built against"):
+            call()
+
+
+def test_the_compiled_checks_load_with_the_first_call(monkeypatch, lib):
+    for call in _three_calls():
+        monkeypatch.setattr(m, "_bind", None)
+        with pytest.raises(m.MlaError):  # (host tensors)
+            call()
+        assert m._bind is not None
+
+
+def test_the_compiled_checks_are_built_anew_for_another_pytorch(monkeypatch, tmp_path):
+    """A record of another PyTorch has them built again, and the library not; where that fails,
+    the library stands, and the old ones do not."""
+    mbuild.build()
+    at, key = tmp_path / "bind.so", tmp_path / "key"
+    at.write_bytes(b"")
+    key.write_text(mbuild.bind_key() + "\n")
+    monkeypatch.setattr(mbuild, "BIND", str(at))
+    monkeypatch.setattr(mbuild, "BIND_KEY", str(key))
+    made = []
+    monkeypatch.setattr(mbuild, "_bind_command", lambda out: made.append(out) or ["cp", mbuild.LIB, out])
+    monkeypatch.setattr(mbuild, "nvcc", lambda: pytest.fail("the library is as it should be"))
+    mbuild.build()
+    assert not made
+    key.write_text("torch 1.0 other\n")
+    mbuild.build()
+    assert len(made) == 1 and at.stat().st_size > 0 and key.read_text().strip() == mbuild.bind_key()
+    key.write_text("torch 1.0 other\n")
+    monkeypatch.setattr(mbuild, "_bind_command", lambda out: ["false"])
+    with pytest.warns(UserWarning, match="cannot be called"):
+        assert mbuild.build() == mbuild.LIB
+    assert not at.exists() and not key.exists()
