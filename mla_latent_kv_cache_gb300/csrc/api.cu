@@ -364,6 +364,7 @@ int decode_impl(const void* q_lat, const void* q_pe, int64_t total_q, const void
     p.cu_q = cu_q;
     p.total_q = static_cast<int>(total_q);  // total_q * Hq < 2^31 (checked above)
     p.lat_dim = D;
+    p.sms = di.sms;
     p.rope_dim = mla::kP;
     cudaError_t e = fold ? mla::launch_decode_fold(maps, p, NP, cache_kind, W, GY, s)
                          : mla::launch_decode(maps, p, NP, lsu, cache_kind, W, GY, s);
@@ -860,6 +861,7 @@ int mla_decode_fp8_page(const void* q_lat, const void* q_pe, int64_t total_q_tok
     p.cu_q = cu_q_lens;
     p.total_q = static_cast<int>(total_q_tokens);
     p.lat_dim = mla::kD;
+    p.sms = di.sms;
     p.rope_dim = mla::kP;
     p.test_hold = g_test_hold.exchange(0);
     const cudaError_t e = mla::launch_decode_page8(maps, p, NP, lsu, W, GY, static_cast<cudaStream_t>(stream));

@@ -2815,8 +2815,6 @@ __global__ void __launch_bounds__(TPR * RPB * GRP, VP * TPR <= 128 ? 1024 / (TPR
     MLA_MTRACE(1);
 }
 
-constexpr int64_t kMergeRowsAtOnce = 8 * 152;  // 4 blocks of two rows for each SM
-
 // Public split-KV combine: part_o [S, N, 512], part_lse [S, N]. One warp per row.
 __global__ void __launch_bounds__(256) mla_merge_lse_kernel(const float* __restrict__ part_o,
                                                             const float* __restrict__ part_lse, int S, int64_t N,
@@ -2839,7 +2837,7 @@ __global__ void __launch_bounds__(256) mla_merge_lse_kernel(const float* __restr
 cudaError_t launch_decode_merge(const DecodeParams& p, int G, int nrec, int GY, cudaStream_t stream) {
     const bool wide = G >= 8 * p.B;
     const int rows = min(64, p.HQ);
-    const bool packed = !wide && p.lat_dim <= 512 && static_cast<int64_t>(p.B) * rows * GY > kMergeRowsAtOnce;
+    const bool packed = !wide && p.lat_dim <= 512 && static_cast<int64_t>(p.B) * rows * GY > 8 * static_cast<int64_t>(p.sms);
     const int RB = wide ? rows : packed ? (rows + 3) / 4 : (rows + 1) / 2;
     cudaLaunchAttribute attr[1];
     cudaLaunchConfig_t cfg =

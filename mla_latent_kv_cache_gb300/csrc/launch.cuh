@@ -72,6 +72,7 @@ struct DecodeParams {
     int total_q;          // query tokens in q_lat, q_pe, out and lse; cu_q is clamped to [0, total_q]
     int lat_dim;       // latent width D: 512 (576-value rows), or 256 / 768 / 1792 (folded tiles, bf16)
     int rope_dim;      // rotary width P: 64
+    int sms;           // of the device
     int64_t bt_cols;       // page-scaled rows: columns of the table
     const float* scales;   // and the pages' scales
 };
