@@ -57,7 +57,8 @@ enum { MLA_OUT_BF16 = 0, MLA_OUT_F32 = 1 };
 
 /*
  * A third kind of rows, with the scale outside of them (mla_cache_append and
- * mla_decode_fp8_page alone take it; the other calls refuse it):
+ * mla_decode_fp8_page alone take it; the other calls refuse it, but for
+ * mla_cache_evict, which knows rows by their bytes: see there):
  *   MLA_CACHE_FP8_PAGE_576   576 bytes: the e4m3 codes of c[0:512] / s and
  *                            k_pe[0:64] / s, with one fp32 scale s for all rows
  *                            of a page, in an array [pages] of the caller's. s
@@ -389,7 +390,10 @@ MLA_API int mla_attn_weights(const void* q_lat, const void* q_pe, const float* l
  *                16 .. 65536), 16-byte aligned; written in place. Pages from
  *                the first that loses a token on must not be shared with
  *                another request: n_sink protects a shared prefix of that
- *                many tokens.
+ *                many tokens. Rows are moved as they are: those of
+ *                MLA_CACHE_FP8_PAGE_576, whose scale belongs to their page, are
+ *                not for this call (the C entry cannot tell them; the Python
+ *                module refuses the kind).
  *   weights, positions          device, fp32 / int32 [B, stride]: the score and
  *                the position in its sequence of the token at each place.
  *   new_weights, new_positions  device, [B, stride]: the same for the kept
@@ -453,7 +457,9 @@ MLA_API int mla_rope(const void* x, int64_t x_stride_t, int64_t x_stride_h, cons
  *        k_pe itself without steps)
  * in 32 bits; each cached value is rounded once:
  *   MLA_CACHE_BF16_576        (c', k') in bf16; lat_dim 256, 512, 768 or 1792.
- *   MLA_CACHE_FP8_DS_MLA_656  as mla_cache_write quantises, from the 32-bit values.
+ *   MLA_CACHE_FP8_DS_MLA_656  as mla_cache_write quantises, from the 32-bit values
+ *       (with a weight the norm's factor is divided by the block's scale first: a
+ *       quotient within 2^-21 of the middle between two codes may become either).
  *   MLA_CACHE_FP8_PAGE_576    codes e4m3(x / s), saturated, s the page's scale: the
  *       least power of two with |x| <= 448 s for every finite new value of the
  *       page, and not less than 2^-40. A page entered behind earlier rows keeps

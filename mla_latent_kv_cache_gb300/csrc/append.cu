@@ -12,9 +12,9 @@
 // norm, the rotation and the rounding are some 240 of them a token), hence packed
 // fp32 instructions, a reduction for several tokens at once, one sine and cosine
 // for four positions, and tokens that wait in shared memory instead of registers.
-// Measured: 98,304 tokens into 656-byte rows 31 us (5.7 TB/s, 0.84 of the copy
-// rate), 52,106 tokens of 16 prompts into page rows, with dense rows besides, 33 us
-// (0.68, issue slots 55% busy), 64 requests with a token each 3.7 us.
+// Measured: 98,304 tokens into 656-byte rows 31 to 32 us (5.6 TB/s, 0.81 to 0.84 of the copy
+// rate), into bf16 rows 41 us (0.81), 52,106 tokens of 16 prompts into page rows, with dense rows
+// besides, 33 us (0.67, issue slots 55% busy), 64 requests with a token each 3.7 us (7 as a call).
 //
 // bf16 and fp8_ds_mla rows: a warp a token, or for prompts a stream of them. Page rows (one scale for all rows of
 // a page): the warps of a page hold its new tokens in registers, meet for the

@@ -32,11 +32,11 @@
 //
 // Bound: HBM, 576 bytes a token; at 16 query rows the products take a third of
 // the time the bytes do, at 64 rows about as long (S 1,150 cycles a tile, the value
-// product 1,640; the bytes 2,940). Measured: 4 x 262,144 tokens at 32 rows 105 us (5.8
-// TB/s, 0.85 of the copy rate), 64 requests of 1k to 8k at 16 rows 38 us (0.69: some 10
-// us are start-up, output and merge), 786k tokens at 64 rows 105 us (0.63: two tiles of
-// shared memory, each block held some 6,000 cycles from its load to its value product),
-// 32 requests at 128 rows 123 us. So the kernel is a stream:
+// product 1,640; the bytes 2,940). Measured (among others in a graph): 4 x 262,144 tokens at 32 rows 106 us (5.7
+// TB/s, 0.84 of the copy rate), 64 requests of 1k to 8k at 16 rows 38.5 us (0.68: some 10
+// us are start-up, output and merge; pages read row by row 61 to 74 us), 786k tokens at 64 rows
+// 105 us (0.63: two tiles of shared memory, each block held some 6,000 cycles from its load to
+// its value product), 32 requests at 128 rows 123 us. So the kernel is a stream:
 // 128-token tiles arrive by TMA as four blocks of 128 dims (16 KB, one 128-byte
 // swizzle row a token) and the rotary part (8 KB). A block is the K-major A
 // operand of S = C Q^T (thread = token = TMEM lane) and the MN-major A operand of
