@@ -490,7 +490,8 @@ MLA_API int mla_rope(const void* x, int64_t x_stride_t, int64_t x_stride_h, cons
  *                aligned. May be the inputs' own memory if these are its columns.
  *   status       device int32 or NULL: ORed with 2 if a token had no place (a
  *                request shorter than its new tokens) or its page lay outside
- *                the pool or the table row. Such a token is not cached.
+ *                the pool or the table row. Such a token is not cached, and changes
+ *                no page and no scale.
  */
 MLA_API int mla_cache_append(const void* latent, int64_t latent_stride, const void* k_pe, int64_t k_pe_stride,
                              const int32_t* cu_new_lens, const int32_t* seq_lens, const int32_t* block_table,
@@ -508,12 +509,12 @@ MLA_API int mla_cache_append(const void* latent, int64_t latent_stride, const vo
  * The codes go to the tensor cores as they are. A query value is the sum of two
  * e4m3 values of different scale: those below 2^-15 of their row's largest are
  * rounded, by at most 2^-22 of it. A probability times s(j) is rounded to f16 (2^-11
- * of itself) and held likewise: up to 32 query rows rounded by at most 2^-8 of itself
- * or 2^-20 of the largest; above, 2^-8 or 2^-16. Those below 2^-14 of the largest are
- * rounded up or down by the token's position, as often up as the part of a step that
- * is rounded, so that over many tokens they keep their sum: weights alike, however small
- * (to 2^-28 of the largest), are off by a few steps in all, not by one each. Sums are
- * fp32; the sum that divides takes the unrounded weights.
+ * of itself or 2^-31 of the largest; above 32 query rows 2^-28) and held likewise: up
+ * to 32 rows rounded by at most 2^-8 of itself or 2^-20 of the largest; above, 2^-8 or
+ * 2^-16. This second rounding takes those below 2^-14 of the largest up or down by the
+ * token's position, as often up as the part of a step that is rounded, so that over many
+ * tokens they keep their sum: weights alike are off by a few steps in all, not by a part
+ * of one each. Sums are fp32; the sum that divides takes the unrounded weights.
  *   scales       device, fp32 [num_slots / page_size], positive; one outside 2^-40 ..
  *                2^40 counts as the nearer bound.
  *   block_table  device, int32 [B, block_table_cols], block_table_stride >=
